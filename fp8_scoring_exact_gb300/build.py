@@ -23,7 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_indexer.so")
-SOURCES = ["api.cu", "score_kernel.cu", "select_kernels.cu", "sparse_attn.cu"]
+SOURCES = ["api.cu", "score_kernel.cu", "select_kernels.cu", "sparse_attn.cu", "latent_api.cu", "latent_attn.cu",
+           "latent_prefill.cu", "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", CSRC, "-I", INCLUDE]

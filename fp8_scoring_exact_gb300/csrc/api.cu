@@ -24,6 +24,7 @@
 #include "dsa_indexer.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "latent.h"
 
 using namespace dsa;
 
@@ -651,6 +652,12 @@ int host_stage_init(HostStage& hs, const HostLayout& L, cudaStream_t stream) {
 }
 
 }  // namespace
+
+namespace dsa {
+uint64_t option_wait_ns() { return read_opts().wait_ns; }
+int option_grid() { return read_opts().grid; }
+void count_launch() { g_launches.fetch_add(1); }
+}  // namespace dsa
 
 // =================================================================== C ABI ==
 extern "C" {
@@ -1348,6 +1355,7 @@ int64_t dsa_indexer_launch_count(void) { return g_launches.load(); }
 const char* dsa_indexer_version(void) { return "dsa_indexer 0.1 (sm_103a, tcgen05 + TMA)"; }
 
 int dsa_indexer_release(void) {
+  release_latent_scratch();
   // lock order of the library: g_host_mu before g_mu
   std::lock_guard<std::mutex> hl(g_host_mu);
   for (auto& kv : g_host) {

@@ -1,0 +1,85 @@
+// latent.h -- parameters and host launchers of the latent-attention operators:
+// dense attention over the paged latent cache (latent_attn.cu), eviction from
+// that cache (cache_evict.cu) and prefill in the expanded form
+// (latent_prefill.cu).  Their entry points are in latent_api.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace dsa {
+
+constexpr int LA_DC = 512;             // compressed dims of a latent key (keys and values)
+constexpr int LA_DP = 64;              // its rope dims (keys only)
+constexpr int LA_DN = 128, LA_DV = 128;  // expanded form: no-rope key dims and value dims of a head
+
+// Process-wide options and the launch counter (api.cu).
+uint64_t option_wait_ns();
+int option_grid();  // CTAs of the persistent kernels: the option, else the SM count
+void count_launch();
+// Frees the scratch of the latent operators (latent_api.cu); called by dsa_indexer_release.
+void release_latent_scratch();
+
+// Attention of every sequence's next_n query tokens over its cached keys, in
+// the absorbed form; with a prefix, over the prefix keys and then its own.
+struct LatentAttnParams {
+  const __nv_bfloat16* q_nope;  // [B, next_n, H, 512]
+  const __nv_bfloat16* q_pe;    // [B, next_n, H, 64]
+  const __nv_bfloat16* ckv;     // slot-major, ckv_stride elements per slot
+  const __nv_bfloat16* kpe;
+  int64_t ckv_stride, kpe_stride;
+  const int32_t* prefix_table;  // [prefix_pages] (null: no prefix)
+  const int32_t* prefix_len;    // [1]
+  int prefix_pages;
+  const int32_t* block_table;   // [B, max_pages]
+  const int32_t* seq_lens;      // [B]
+  int B, next_n, H, max_pages, num_pages;
+  float scale_log2;             // sm_scale * log2(e)
+  __nv_bfloat16* out;           // [B, next_n, H, 512]
+  float* lse;                   // [B, next_n, H]
+  float* weights;               // [B, ld_weights] or null: += the softmax weight of every key
+  int64_t ld_weights;
+  int* status;
+};
+
+// Eviction in place: every sequence of more than `budget` keys keeps its last
+// `recent` keys and the budget - recent others with the largest weights.
+struct EvictParams {
+  uint8_t* ckv;                 // slot-major rows of 1024 bytes, ckv_stride bytes apart
+  uint8_t* kpe;                 // rows of 128 bytes
+  int64_t ckv_stride, kpe_stride;
+  uint8_t* k_cache;             // indexer keys [P, 64, 128] or null
+  float* k_scale;               // [P, 64] or null
+  float* weights;               // [B, ld_weights]
+  int64_t ld_weights;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int B, max_pages, num_pages, budget, recent;
+  int32_t* kept;                // [B, budget]
+  int32_t* new_lens;            // [B]
+  int32_t* old_lens;            // [B] scratch: the validated lengths (new_lens may be seq_lens itself)
+  int* status;
+};
+
+// Causal attention of a ragged batch in the expanded form (a key of a head:
+// 128 dims of its own and 64 rope dims shared by the heads).
+struct PrefillParams {
+  const __nv_bfloat16 *q, *k_nope, *k_pe, *v;
+  int64_t q_st, q_sh, kn_st, kn_sh, kp_st, v_st, v_sh;  // strides per token and per head, in elements
+  const int32_t *cu_q, *cu_k;   // [S + 1]
+  int S, Tq, Tk, H, causal;
+  float scale_log2;
+  __nv_bfloat16* out;           // [Tq, H, 128]
+  float* lse;                   // [Tq, H]
+  int* status;
+};
+
+cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t s);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t s);
+
+}  // namespace dsa

@@ -1,0 +1,263 @@
+// latent_api.cu -- C ABI of the latent-attention operators
+// (include/dsa_indexer.h): argument validation, per-(device, stream) scratch
+// with the status word, and the launches.
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
+#include <vector>
+
+#include "dsa_indexer.h"
+#include "latent.h"
+
+using namespace dsa;
+
+namespace {
+
+// Scratch of one (device, stream): the status word in its first 256 bytes,
+// then what the call lays out.  A buffer that has become too small is kept
+// until dsa_indexer_release: a captured graph may still hold its address, and
+// growing by half at least bounds what is kept to twice the last size.
+struct Scratch {
+  uint8_t* base = nullptr;
+  size_t cap = 0;
+  std::vector<uint8_t*> outgrown;
+};
+std::mutex g_mu;
+std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
+
+constexpr size_t HEAD = 256;
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Scratch with room for `need` bytes past the head; its status word is
+// zeroed on the stream.  Null on an error.
+uint8_t* get_scratch(cudaStream_t stream, size_t need) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  Scratch& a = g_scratch[{dev, stream}];
+  if (a.cap < HEAD + need) {
+    const size_t want = align_up(std::max(HEAD + need, a.cap + a.cap / 2), 1 << 20);
+    uint8_t* p = nullptr;
+    if (cudaMalloc(&p, want) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    if (a.base) a.outgrown.push_back(a.base);
+    a.base = p;
+    a.cap = want;
+  }
+  if (cudaMemsetAsync(a.base, 0, sizeof(int), stream) != cudaSuccess) return nullptr;
+  return a.base;
+}
+
+// sm_scale * log2(e) has to be a positive finite number
+bool usable_scale(float s) { return s > 0.f && s <= 3.4e38f; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+template <class T>
+const __nv_bfloat16* bf(const T* p) {
+  return reinterpret_cast<const __nv_bfloat16*>(p);
+}
+
+// Arguments shared by the two forms of cached attention.
+int check_cached(const LatentAttnParams& p) {
+  if (!p.q_nope || !p.q_pe || !p.ckv || !p.kpe || !p.block_table || !p.seq_lens || !p.out || !p.lse) return DSA_ERR_ARG;
+  if (p.B <= 0 || p.next_n <= 0 || p.H <= 0 || p.max_pages <= 0 || p.num_pages <= 0) return DSA_ERR_ARG;
+  if (!usable_scale(p.scale_log2) || p.ckv_stride < LA_DC || p.kpe_stride < LA_DP || (p.ckv_stride & 7) || (p.kpe_stride & 7))
+    return DSA_ERR_ARG;
+  if (!aligned16(p.q_nope) || !aligned16(p.q_pe) || !aligned16(p.ckv) || !aligned16(p.kpe) || !aligned16(p.out))
+    return DSA_ERR_ARG;
+  if (p.weights && p.ld_weights < (int64_t)p.max_pages * PAGE) return DSA_ERR_ARG;
+  if ((int64_t)p.B * p.next_n * p.H >= (1ll << 31) / 64 || p.next_n > 65535 || (int64_t)p.max_pages * PAGE >= (1ll << 30) ||
+      (int64_t)p.prefix_pages * PAGE >= (1ll << 30) || (int64_t)p.num_pages * PAGE >= (1ll << 31) || p.B > 65535)
+    return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+int run_cached(LatentAttnParams& p, cudaStream_t stream) {
+  const int rc = check_cached(p);
+  if (rc != DSA_OK) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  uint8_t* base = get_scratch(stream, 0);
+  if (!base) return DSA_ERR_CUDA;
+  p.status = reinterpret_cast<int*>(base);
+  return launch_latent_attn(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace dsa {
+void release_latent_scratch() {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_scratch.empty()) cudaDeviceSynchronize();
+  for (auto& kv : g_scratch) {
+    int cur = 0;
+    cudaGetDevice(&cur);
+    cudaSetDevice(kv.first.first);
+    if (kv.second.base) cudaFree(kv.second.base);
+    for (uint8_t* q : kv.second.outgrown) cudaFree(q);
+    cudaSetDevice(cur);
+  }
+  g_scratch.clear();
+}
+}  // namespace dsa
+
+extern "C" {
+
+int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* ckv, int64_t ckv_stride,
+                               const uint16_t* kpe, int64_t kpe_stride, const int32_t* block_table,
+                               const int32_t* seq_lens, int B, int next_n, int H, int max_pages, int num_pages,
+                               float sm_scale, uint16_t* out, float* lse, float* weights, int64_t ld_weights,
+                               dsa_stream_t stream) {
+  LatentAttnParams p{};
+  p.q_nope = bf(q_nope);
+  p.q_pe = bf(q_pe);
+  p.ckv = bf(ckv);
+  p.kpe = bf(kpe);
+  p.ckv_stride = ckv_stride;
+  p.kpe_stride = kpe_stride;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.B = B;
+  p.next_n = next_n;
+  p.H = H;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.weights = weights;
+  p.ld_weights = ld_weights;
+  return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* ckv,
+                                       int64_t ckv_stride, const uint16_t* kpe, int64_t kpe_stride,
+                                       const int32_t* prefix_table, const int32_t* prefix_len, int prefix_pages,
+                                       const int32_t* block_table, const int32_t* seq_lens, int B, int next_n, int H,
+                                       int max_pages, int num_pages, float sm_scale, uint16_t* out, float* lse,
+                                       dsa_stream_t stream) {
+  if (!prefix_table || !prefix_len || prefix_pages <= 0) return DSA_ERR_ARG;
+  LatentAttnParams p{};
+  p.q_nope = bf(q_nope);
+  p.q_pe = bf(q_pe);
+  p.ckv = bf(ckv);
+  p.kpe = bf(kpe);
+  p.ckv_stride = ckv_stride;
+  p.kpe_stride = kpe_stride;
+  p.prefix_table = prefix_table;
+  p.prefix_len = prefix_len;
+  p.prefix_pages = prefix_pages;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.B = B;
+  p.next_n = next_n;
+  p.H = H;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride, uint8_t* k_cache,
+                           float* k_cache_scale, float* weights, int64_t ld_weights, const int32_t* block_table,
+                           const int32_t* seq_lens, int B, int max_pages, int num_pages, int budget, int recent,
+                           int32_t* kept, int32_t* new_lens, dsa_stream_t stream_) {
+  if (!ckv || !kpe || !weights || !block_table || !seq_lens || !kept || !new_lens || !k_cache != !k_cache_scale)
+    return DSA_ERR_ARG;
+  if (B <= 0 || max_pages <= 0 || num_pages <= 0 || budget <= 0 || recent < 0 || recent > budget) return DSA_ERR_ARG;
+  if (ckv_stride < LA_DC || kpe_stride < LA_DP || (ckv_stride & 7) || (kpe_stride & 7) ||
+      ld_weights < (int64_t)max_pages * PAGE)
+    return DSA_ERR_ARG;
+  if (!aligned16(ckv) || !aligned16(kpe) || !aligned16(k_cache)) return DSA_ERR_ARG;
+  if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535)
+    return DSA_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  std::lock_guard<std::mutex> lk(g_mu);
+  uint8_t* base = get_scratch(stream, (size_t)B * 4);
+  if (!base) return DSA_ERR_CUDA;
+  EvictParams p{};
+  p.ckv = reinterpret_cast<uint8_t*>(ckv);
+  p.kpe = reinterpret_cast<uint8_t*>(kpe);
+  p.ckv_stride = 2 * ckv_stride;
+  p.kpe_stride = 2 * kpe_stride;
+  p.k_cache = k_cache;
+  p.k_scale = k_cache_scale;
+  p.weights = weights;
+  p.ld_weights = ld_weights;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.budget = budget;
+  p.recent = recent;
+  p.kept = kept;
+  p.new_lens = new_lens;
+  p.old_lens = reinterpret_cast<int32_t*>(base + HEAD);
+  p.status = reinterpret_cast<int*>(base);
+  return launch_evict(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 const uint16_t* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+                                 const uint16_t* k_pe, int64_t kp_token_stride, const uint16_t* v,
+                                 int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                 const int32_t* cu_k, int S, int Tq, int Tk, int H, int causal, float sm_scale,
+                                 uint16_t* out, float* lse, dsa_stream_t stream_) {
+  if (!q || !k_nope || !k_pe || !v || !cu_q || !cu_k || !out || !lse) return DSA_ERR_ARG;
+  if (S <= 0 || Tq <= 0 || Tk <= 0 || H <= 0 || !usable_scale(sm_scale * 1.4426950408889634f)) return DSA_ERR_ARG;
+  const int64_t strides[] = {q_token_stride, q_head_stride, kn_token_stride, kn_head_stride,
+                             kp_token_stride, v_token_stride, v_head_stride};
+  for (int64_t x : strides)
+    if (x <= 0 || (x & 7) || x >= (1ll << 38)) return DSA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_pe) || !aligned16(v) || !aligned16(out)) return DSA_ERR_ARG;
+  if (H > 65535 || S > 65535 || (int64_t)Tq * H >= (1ll << 31) || Tq >= (1 << 30) || Tk >= (1 << 30))
+    return DSA_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  std::lock_guard<std::mutex> lk(g_mu);
+  uint8_t* base = get_scratch(stream, 0);
+  if (!base) return DSA_ERR_CUDA;
+  PrefillParams p{};
+  p.q = bf(q);
+  p.k_nope = bf(k_nope);
+  p.k_pe = bf(k_pe);
+  p.v = bf(v);
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.kn_st = kn_token_stride;
+  p.kn_sh = kn_head_stride;
+  p.kp_st = kp_token_stride;
+  p.v_st = v_token_stride;
+  p.v_sh = v_head_stride;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.S = S;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.H = H;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = reinterpret_cast<int*>(base);
+  return launch_prefill(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int dsa_latent_last_status(dsa_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return DSA_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  auto it = g_scratch.find({dev, stream});
+  if (it == g_scratch.end() || !it->second.base) return DSA_OK;
+  int st = 0;
+  if (cudaMemcpy(&st, it->second.base, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
+  if (st & ST_TIMEOUT) return DSA_ERR_TIMEOUT;
+  return (st & ST_RANGE) ? DSA_ERR_RANGE : DSA_OK;
+}
+
+}  // extern "C"

@@ -252,6 +252,120 @@ DSA_API int dsa_sparse_attention(const uint16_t* q_nope, const uint16_t* q_pe,
 DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
 
 /*
+ * Latent attention (keys and values from one shared latent vector a token).
+ *
+ * The four operators below share one cache: per slot a 512-dim compressed
+ * vector ckv (the key's no-rope part and the value) and a 64-dim rope part
+ * kpe, bf16, in pages of 64 slots; logical key s of sequence b lives in slot
+ * block_table[b][s / 64] * 64 + s % 64, as in dsa_indexer_topk_paged.
+ * ckv_stride and kpe_stride are the elements between slots (at least 512 and
+ * 64, multiples of 8), so one [P, 64, 576] cache serves as both.  bf16 arrays
+ * are passed as their 16-bit patterns, 16-byte aligned.
+ *
+ * Products are bf16 with fp32 accumulation; softmax statistics are fp32;
+ * weights are rounded to bf16 for the weighted sum, outputs to bf16.  A row
+ * that sees no key gets zeros and lse = -inf.  A value read with weight 0 for
+ * one row of a sequence still has to be finite if another row of it sees it;
+ * slots past a sequence's length are never used, whatever they hold.
+ *
+ * Errors the device detects are read by dsa_latent_last_status: a length
+ * outside [0, 64 * its table's pages] (the sequence counts as empty), a used
+ * table entry outside [0, num_pages) (its keys read as zeros; eviction leaves
+ * its slots alone), a cumulative length outside the arrays (that sequence is
+ * skipped), all DSA_ERR_RANGE; a pipeline wait that gave up: DSA_ERR_TIMEOUT.
+ * Scratch is owned by the library per (device, stream) and grown on demand;
+ * an outgrown buffer lives until dsa_indexer_release, so a captured graph
+ * stays valid.
+ */
+
+/*
+ * Decode in the absorbed form: for token i of sequence b and head h, over the
+ * logical keys s in [0, seq_lens[b] - next_n + i + 1),
+ *
+ *     u_s = sm_scale * log2(e) * (q_nope[b, i, h] . ckv[s] + q_pe[b, i, h] . kpe[s])
+ *     lse[b, i, h] = log2(sum_s 2^u_s),   out[b, i, h] = sum_s 2^(u_s - lse) ckv[s]
+ *
+ * and, if `weights` is not null, weights[b, s] += sum over (i, h) that see s
+ * of 2^(u_s - lse) for s in [0, seq_lens[b]): the attention weight that the
+ * key has received, which dsa_latent_cache_evict goes by.  The sum's order is
+ * fixed.
+ *
+ *   q_nope [B, next_n, H, 512] bf16   q_pe [B, next_n, H, 64] bf16 (any H)
+ *   block_table [B, max_pages]        seq_lens [B] int32
+ *   out [B, next_n, H, 512] bf16      lse [B, next_n, H] fp32
+ *   weights [B, ld_weights] fp32 or null, ld_weights >= 64 * max_pages
+ */
+DSA_API int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe,
+                                       const uint16_t* ckv, int64_t ckv_stride,
+                                       const uint16_t* kpe, int64_t kpe_stride,
+                                       const int32_t* block_table, const int32_t* seq_lens,
+                                       int B, int next_n, int H, int max_pages, int num_pages, float sm_scale,
+                                       uint16_t* out, float* lse,
+                                       float* weights, int64_t ld_weights, dsa_stream_t stream);
+
+/*
+ * Decode of a batch whose sequences share a prefix: every row sees the
+ * prefix_len[0] keys behind prefix_table and then its own sequence's keys as
+ * above (seq_lens counts those alone).  The prefix is read and multiplied once
+ * for the rows of all sequences.  prefix_table [prefix_pages] and prefix_len
+ * [1] are device arrays.
+ */
+DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q_pe,
+                                               const uint16_t* ckv, int64_t ckv_stride,
+                                               const uint16_t* kpe, int64_t kpe_stride,
+                                               const int32_t* prefix_table, const int32_t* prefix_len,
+                                               int prefix_pages,
+                                               const int32_t* block_table, const int32_t* seq_lens,
+                                               int B, int next_n, int H, int max_pages, int num_pages,
+                                               float sm_scale, uint16_t* out, float* lse, dsa_stream_t stream);
+
+/*
+ * Eviction in place: a sequence with more than `budget` keys keeps its last
+ * `recent` keys and, of the others, the budget - recent with the largest
+ * weights (equal weights: the lowest index; NaN counts as the largest), moved
+ * together into logical slots [0, budget) in their old order, with their
+ * weights; weights in [budget, seq_lens[b]) become 0.  Other sequences stay as
+ * they are.  No two sequences may share a page here.
+ *
+ *   k_cache, k_cache_scale: the indexer's keys [P, 64, 128] and scales [P, 64]
+ *                           of the same pages, moved along, or both null
+ *   kept [B, budget] int32: the old logical index of each kept key, ascending,
+ *                           then -1
+ *   new_lens [B] int32:     min(seq_lens[b], budget) (may be seq_lens itself)
+ */
+DSA_API int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride,
+                                   uint8_t* k_cache, float* k_cache_scale,
+                                   float* weights, int64_t ld_weights,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   int B, int max_pages, int num_pages, int budget, int recent,
+                                   int32_t* kept, int32_t* new_lens, dsa_stream_t stream);
+
+/*
+ * Prefill in the expanded form: S sequences, of which z has queries [cu_q[z],
+ * cu_q[z + 1]) and keys [cu_k[z], cu_k[z + 1]); the key of head h at token s
+ * is (k_nope[s, h] | k_pe[s]), the value v[s, h].  With `causal`, query i of n
+ * sees the first m - n + i + 1 of the m keys (the last query all of them);
+ * without it, all.  Softmax and lse in base 2 as above.
+ *
+ *   q [Tq, H, 192] (128 no-rope dims, then 64 rope dims)   k_nope, v [Tk, H, 128]   k_pe [Tk, 64]
+ *   strides in elements, per token and per head, multiples of 8 (k_nope and v
+ *   may be halves of one [Tk, H, 256] array)
+ *   cu_q, cu_k [S + 1] int32, ascending, within [0, Tq] and [0, Tk]
+ *   out [Tq, H, 128] bf16     lse [Tq, H] fp32 (rows outside every sequence are not written)
+ */
+DSA_API int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                         const uint16_t* k_nope, int64_t kn_token_stride, int64_t kn_head_stride,
+                                         const uint16_t* k_pe, int64_t kp_token_stride,
+                                         const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                                         const int32_t* cu_q, const int32_t* cu_k,
+                                         int S, int Tq, int Tk, int H, int causal, float sm_scale,
+                                         uint16_t* out, float* lse, dsa_stream_t stream);
+
+/* Synchronises `stream`; the device status of the most recent latent
+ * operator on it: DSA_OK, DSA_ERR_RANGE or DSA_ERR_TIMEOUT. */
+DSA_API int dsa_latent_last_status(dsa_stream_t stream);
+
+/*
  * Math-only control (a measurement, not an operator; section 5.2 of the
  * indexer study, "Math-only control"): the fused operator's plan and its main
  * scorer with the same work units, tile loads, tcgen05 MMAs and barriers, but

@@ -1,0 +1,471 @@
+"""GPU parity of the latent-attention operators against the float64 oracle.
+
+Tolerances, from the kernels' arithmetic (D products per logit):
+  logits   bf16 products are exact in fp32; a sum of D fp32 additions errs by
+           at most D 2^-23 of the sum of magnitudes (2^-23: a tensor core's
+           additions may truncate), the scale and the exponent's argument by
+           2^-22 of the same: du = (D + 2) 2^-23 spread, in base-2 units
+  weights  p errs by a relative r = 2 ln(2) du + 2^-20 (its own logit and the
+           normaliser's; 2^-20: the exponentials and the fp32 sums)
+  out      bf16 weights: half a step, 2^-8 of the magnitude; bf16 output: 2^-8
+           of the value; r of the magnitude for the logits
+  lse      du + 2^-20 + 2^-22 |lse|"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import latent_attention as la
+
+pytestmark = pytest.mark.gpu
+
+BF = 2.0 ** -8
+SCALE = 1.0 / np.sqrt(192.0)
+
+
+@pytest.fixture(scope="module")
+def B():
+    from fp8_scoring_exact_gb300 import binding
+    binding.lib()
+    return binding
+
+
+def _check_rows(out, lse, ref, D, p_sum=None):
+    """out [R, E], lse [R] (numpy float64) against rows_over_keys' tuple."""
+    o, l, p, mag, spread = ref
+    du = (D + 2) * 2.0 ** -23 * spread
+    r = 2 * np.log(2.0) * du + 2.0 ** -20
+    none = np.isneginf(l)
+    assert np.array_equal(none, np.isneginf(lse))
+    assert np.all(out[none] == 0)
+    tol = BF * np.abs(o) + (BF + r)[:, None] * mag * (1 + BF)
+    err = np.abs(out - o)
+    assert np.all(err <= tol + 1e-30), float((err / (tol + 1e-30)).max())
+    el = np.abs(lse[~none] - l[~none])
+    tl = du[~none] + 2.0 ** -20 + 2.0 ** -22 * np.abs(l[~none])
+    assert np.all(el <= tl), float((el / tl).max())
+    if p_sum is not None:
+        want, got = p.sum(0), p_sum
+        tol = (p * r[:, None]).sum(0) + 2.0 ** -20 * want
+        assert np.all(np.abs(got - want) <= tol + 2.0 ** -24), float(np.abs(got - want).max())
+
+
+class Cache:
+    """A random latent cache with shuffled pages; slots past a sequence hold NaN."""
+
+    def __init__(self, lens, seed, prefix=0, joint=False, spare=3, scale=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.lens = list(lens)
+        n = [-(-x // 64) for x in lens]
+        pp = -(-prefix // 64)
+        self.P = sum(n) + pp + spare
+        order = torch.randperm(self.P, generator=g).tolist()
+        maxp = max(1, max(n)) + 1
+        self.table = torch.full((len(lens), maxp), -1, dtype=torch.int32)
+        data = torch.full((self.P, 64, 576), float("nan"), dtype=torch.bfloat16)
+        at = 0
+
+        def fill(pages, length):
+            x = (torch.randn((length, 576), generator=g) * scale).to(torch.bfloat16)
+            for j, pg in enumerate(pages):
+                part = x[64 * j:64 * j + 64]
+                data[pg, :len(part)] = part
+
+        for b, c in enumerate(n):
+            self.table[b, :c] = torch.tensor(order[at:at + c], dtype=torch.int32)
+            fill(order[at:at + c], lens[b])
+            at += c
+        self.prefix = prefix
+        self.prefix_table = torch.tensor(order[at:at + pp] or [0], dtype=torch.int32)
+        fill(order[at:at + pp], prefix)
+        self.data = data
+        self.joint = joint
+
+    def device(self):
+        d = self.data.cuda()
+        self.dev = d
+        if self.joint:
+            return d[..., :512], d[..., 512:]
+        return d[..., :512].contiguous(), d[..., 512:].contiguous()
+
+    def flat(self):
+        x = torch.nan_to_num(self.data.double()).numpy().reshape(-1, 576)
+        return x[:, :512], x[:, 512:]
+
+
+def _queries(nB, nn, H, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return ((torch.randn((nB, nn, H, 512), generator=g) * scale).to(torch.bfloat16),
+            (torch.randn((nB, nn, H, 64), generator=g) * scale).to(torch.bfloat16))
+
+
+def _ints(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+def _decode(B, c, qn, qp, seq_lens=None, weights=None, **kw):
+    ck, kp = c.device()
+    lens = _ints(c.lens if seq_lens is None else seq_lens)
+    if c.prefix or kw.get("force_prefix"):
+        out, lse = B.latent_attention_shared_prefix(qn.cuda(), qp.cuda(), ck, kp, c.prefix_table.cuda(),
+                                                    _ints([c.prefix]), c.table.cuda(), lens, SCALE)
+    else:
+        out, lse = B.latent_attention_paged(qn.cuda(), qp.cuda(), ck, kp, c.table.cuda(), lens, SCALE,
+                                            weights=weights)
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def _check_decode(c, qn, qp, out, lse, only=None, weights=None, prefix=None):
+    ckv, kpe = c.flat()
+    use = c.prefix > 0 if prefix is None else prefix
+    ref = la.decode(qn.double().numpy(), qp.double().numpy(), ckv, kpe, c.table.numpy(), c.lens, SCALE,
+                    prefix_table=c.prefix_table.numpy() if use else None, prefix_len=c.prefix)
+    for b in range(len(c.lens)) if only is None else only:
+        R = qn.shape[1] * qn.shape[2]
+        _check_rows(out[b].reshape(R, 512), lse[b].reshape(R), ref[b], 576,
+                    None if weights is None else weights[b, :c.lens[b]])
+
+
+DECODE = [
+    # nn, H, lens
+    (1, 16, [1]), (1, 16, [0]), (1, 16, [200]), (1, 1, [1, 64, 65, 0, 130]), (2, 16, [0, 1, 2, 63, 64, 65, 129, 700]),
+    (1, 5, [777, 3, 64]), (3, 7, [2, 1, 500, 64, 66]), (4, 16, [1, 5, 1000]), (1, 64, [300, 1, 128]),
+    (1, 100, [257, 64]), (1, 128, [513, 1, 2100]), (2, 128, [129, 1]), (1, 32, [4100, 90]), (2, 24, [640, 641, 639]),
+    (1, 16, [30000]), (1, 16, list(range(0, 1200, 7))), (5, 33, [2, 300]),
+]
+
+
+@pytest.mark.parametrize("joint", [False, True])
+@pytest.mark.parametrize("nn,H,lens", DECODE)
+def test_decode_matches_oracle(B, nn, H, lens, joint):
+    c = Cache(lens, seed=nn * 100 + H + len(lens), joint=joint)
+    qn, qp = _queries(len(lens), nn, H, seed=H)
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == 0
+    _check_decode(c, qn, qp, out, lse)
+
+
+@pytest.mark.parametrize("nn,H,lens", DECODE)
+def test_key_weights_match_oracle(B, nn, H, lens):
+    c = Cache(lens, seed=nn * 100 + H + len(lens) + 1)
+    qn, qp = _queries(len(lens), nn, H, seed=H + 1)
+    W = c.table.shape[1] * 64 + 5
+    w = torch.zeros((len(lens), W), device="cuda")
+    out, lse = _decode(B, c, qn, qp, weights=w)
+    got = w.cpu()
+    _check_decode(c, qn, qp, out, lse, weights=got.double().numpy())
+    for b, L in enumerate(lens):
+        assert torch.all(got[b, L:] == 0)
+    # they are added to what is there, in a fixed order
+    w2 = torch.zeros_like(w)
+    _decode(B, c, qn, qp, weights=w2)
+    assert torch.equal(w2.cpu(), got)
+    _decode(B, c, qn, qp, weights=w2)
+    assert torch.equal(w2.cpu(), got + got)
+
+
+@pytest.mark.parametrize("nn,H,prefix,lens", [
+    (1, 16, 1, [0, 0]), (1, 16, 64, [1, 0, 65]), (1, 16, 1000, [5, 200, 64]), (2, 16, 300, [0, 1, 2, 90]),
+    (1, 5, 129, [1] * 30), (1, 128, 640, [1, 100]), (2, 20, 5000, [3, 700, 40, 1, 1]), (1, 16, 2000, [33] * 70)])
+def test_shared_prefix_matches_oracle(B, nn, H, prefix, lens):
+    c = Cache(lens, seed=prefix + H, prefix=prefix)
+    qn, qp = _queries(len(lens), nn, H, seed=H + 2)
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == 0
+    _check_decode(c, qn, qp, out, lse)
+
+
+def test_shared_prefix_of_no_keys(B):
+    c = Cache([0, 1, 100], seed=3)
+    qn, qp = _queries(3, 1, 16, seed=4)
+    out, lse = _decode(B, c, qn, qp, force_prefix=True)
+    _check_decode(c, qn, qp, out, lse)
+
+
+@pytest.mark.parametrize("H,scale,grow", [(16, 20.0, False), (16, 1.0, True), (64, 1.0, True), (16, 1e-3, False)])
+def test_decode_far_logits(B, H, scale, grow):
+    """Logits over thousands of units (one-hot rows), and ones that keep growing along the keys, so
+    that the running maximum moves in every tile."""
+    c = Cache([1500, 70], seed=5)
+    if grow:
+        for b in range(2):
+            for j in range(-(-c.lens[b] // 64)):
+                c.data[c.table[b, j]] *= 1.0 + 0.5 * j
+    qn, qp = _queries(2, 1, H, seed=6, scale=scale)
+    out, lse = _decode(B, c, qn, qp)
+    _check_decode(c, qn, qp, out, lse)
+
+
+def test_decode_reports_bad_pages_and_lengths(B):
+    c = Cache([200, 200, 200, 200], seed=7)
+    good = c.table.clone()
+    c.table[1, 2] = c.P + 5
+    qn, qp = _queries(4, 1, 16, seed=8)
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == B.DSA_ERR_RANGE
+    c.table = good
+    _check_decode(c, qn, qp, out, lse, only=[0, 2, 3])
+    assert np.all(np.isfinite(out[1]))
+    for bad in (-1, c.table.shape[1] * 64 + 1):
+        out, lse = _decode(B, c, qn, qp, seq_lens=[200, 200, bad, 200])
+        assert B.latent_last_status() == B.DSA_ERR_RANGE
+        _check_decode(c, qn, qp, out, lse, only=[0, 1, 3])
+        assert np.all(out[2] == 0) and np.all(np.isneginf(lse[2]))
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == 0
+
+
+def test_decode_on_a_side_stream_and_from_a_graph(B):
+    a, b = Cache([300, 64, 1000], seed=9), Cache([65, 900, 1], seed=10)
+    maxp = max(a.table.shape[1], b.table.shape[1])
+    P = max(a.P, b.P)
+
+    def widen(c):
+        t = torch.full((3, maxp), -1, dtype=torch.int32)
+        t[:, :c.table.shape[1]] = c.table
+        c.table = t
+        d = torch.full((P, 64, 576), float("nan"), dtype=torch.bfloat16)
+        d[:c.P] = c.data
+        c.data, c.P = d, P
+
+    widen(a)
+    widen(b)
+    qa, qb = _queries(3, 2, 16, seed=11), _queries(3, 2, 16, seed=12)
+    s = torch.cuda.Stream()
+    ck, kp = a.device()
+    qn, qp, table, lens = qa[0].cuda(), qa[1].cuda(), a.table.cuda(), _ints(a.lens)
+    w = torch.zeros((3, maxp * 64), device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out, lse = B.latent_attention_paged(qn, qp, ck, kp, table, lens, SCALE, weights=w)
+    torch.cuda.synchronize()
+    _check_decode(a, *qa, out.double().cpu().numpy(), lse.double().cpu().numpy(), weights=w.double().cpu().numpy())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        B.latent_attention_paged(qn, qp, ck, kp, table, lens, SCALE, out=out, lse=lse, weights=w)
+    # a larger call between capture and replay outgrows the scratch
+    big = Cache([5000] * 6, seed=13)
+    with torch.cuda.stream(s):
+        qbig = _queries(6, 4, 64, seed=14)
+        B.latent_attention_paged(qbig[0].cuda(), qbig[1].cuda(), *big.device(), big.table.cuda(), _ints(big.lens), SCALE,
+                                 weights=torch.zeros((6, big.table.shape[1] * 64), device="cuda"))
+    torch.cuda.synchronize()
+    for dst, src in ((ck, b.data[..., :512]), (kp, b.data[..., 512:]), (qn, qb[0]), (qp, qb[1]), (table, b.table)):
+        dst.copy_(src)
+    lens.copy_(_ints(b.lens))
+    w.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    _check_decode(b, *qb, out.double().cpu().numpy(), lse.double().cpu().numpy(), weights=w.double().cpu().numpy())
+
+
+def test_decode_leaves_its_inputs_alone(B):
+    c = Cache([130, 64], seed=15)
+    ck, kp = c.device()
+    qn, qp = (x.cuda() for x in _queries(2, 1, 16, seed=16))
+    before = [x.clone() for x in (ck, kp, qn, qp)]
+    B.latent_attention_paged(qn, qp, ck, kp, c.table.cuda(), _ints(c.lens), SCALE)
+    torch.cuda.synchronize()
+    for x, y in zip((ck, kp, qn, qp), before):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+# ------------------------------------------------------------------ eviction --
+@pytest.mark.parametrize("budget,recent,lens,kind", [
+    (64, 8, [0, 1, 64, 65, 300], "random"), (100, 0, [1000, 99, 101], "ties"), (1, 1, [500, 1, 0], "random"),
+    (1, 0, [500, 2], "random"), (256, 256, [1000, 257], "random"), (2048, 100, [9000, 2049, 2047], "ties"),
+    (300, 10, [1300, 777], "zero"), (300, 10, [1300, 777], "nan"), (5000, 37, [70000, 5001], "random"),
+    (40, 4, list(range(0, 400, 3)), "ties"), (20000, 1000, [33000], "signed")])
+@pytest.mark.parametrize("indexer,joint,alias", [(False, False, False), (True, True, True)])
+def test_evict_matches_oracle(B, budget, recent, lens, kind, indexer, joint, alias):
+    c = Cache(lens, seed=budget + recent, joint=joint)
+    g = torch.Generator().manual_seed(budget)
+    nb, maxp = len(lens), c.table.shape[1]
+    w = torch.randn((nb, maxp * 64 + 3), generator=g)
+    if kind == "random":
+        w = w.abs()
+    elif kind == "ties":
+        w = torch.randint(0, 3, w.shape, generator=g).float()
+    elif kind == "zero":
+        w = torch.where(w > 0, 0.0, -0.0)
+    elif kind == "nan":
+        w = torch.where(w > 1, float("nan"), torch.where(w < -1, float("inf"), w))
+        w[:, ::7] = -float("nan")
+    kc = torch.randint(0, 256, (c.P, 64, 128), generator=g, dtype=torch.uint8) if indexer else None
+    ks = torch.rand((c.P, 64), generator=g) if indexer else None
+    ck, kp = c.device()
+    dw, dl = w.cuda(), _ints(lens)
+    dk, ds = (kc.cuda(), ks.cuda()) if indexer else (None, None)
+    kept, new = B.latent_cache_evict(ck, kp, dw, c.table.cuda(), dl, budget, recent, k_cache=dk, k_cache_scale=ds,
+                                     new_lens=dl if alias else None)
+    assert B.latent_last_status() == 0
+    kept, new = kept.cpu().numpy(), new.cpu().numpy()
+    # what the arrays have to hold now, bit for bit
+    want = c.data.clone().view(torch.int16).reshape(-1, 576)
+    old = want.clone()
+    ww = w.clone()
+    wk, ws = (kc.clone().reshape(-1, 128), ks.clone().reshape(-1)) if indexer else (None, None)
+    for b, L in enumerate(lens):
+        rows = la.kept_keys(w[b].numpy(), L, budget, recent)
+        n = len(rows)
+        assert new[b] == n and np.array_equal(kept[b, :n], rows) and np.all(kept[b, n:] == -1), b
+        if L <= budget:
+            continue
+        slots = torch.from_numpy(la.slots_of(c.table[b].numpy(), L))
+        want[slots[:n]] = old[slots[rows]]
+        ww[b, :n] = w[b, rows]
+        ww[b, n:L] = 0.0
+        if indexer:
+            wk[slots[:n]] = kc.reshape(-1, 128)[slots[rows]]
+            ws[slots[:n]] = ks.reshape(-1)[slots[rows]]
+    assert torch.equal(ck.cpu().contiguous().view(torch.int16).reshape(-1, 512), want[:, :512])
+    assert torch.equal(kp.cpu().contiguous().view(torch.int16).reshape(-1, 64), want[:, 512:])
+    assert torch.equal(dw.cpu().view(torch.int32), ww.view(torch.int32))
+    if indexer:
+        assert torch.equal(dk.cpu().reshape(-1, 128), wk) and torch.equal(ds.cpu().reshape(-1), ws)
+
+
+def test_evict_reports_bad_pages_and_lengths(B):
+    c = Cache([300, 300, 300], seed=20)
+    w = torch.rand((3, c.table.shape[1] * 64), generator=torch.Generator().manual_seed(1))
+    bad = c.table.clone()
+    bad[1, 0] = -7
+    ck, kp = c.device()
+    dw = w.cuda()
+    kept, new = B.latent_cache_evict(ck, kp, dw, bad.cuda(), _ints([300, 300, 10 ** 6]), 100, 10)
+    assert B.latent_last_status() == B.DSA_ERR_RANGE
+    assert new.tolist() == [100, 100, 0] and torch.all(kept[2] == -1)
+    for b in (0, 1):
+        assert np.array_equal(kept[b].cpu().numpy(), la.kept_keys(w[b].numpy(), 300, 100, 10))
+    old = c.data.view(torch.int16).reshape(-1, 576)
+    slots = la.slots_of(c.table[0].numpy(), 300)
+    got = ck.cpu().view(torch.int16).reshape(-1, 512)
+    assert torch.equal(got[slots[:100]], old[slots[la.kept_keys(w[0].numpy(), 300, 100, 10)], :512])
+    page = int(c.table[1, 0])  # not named by the bad table: untouched
+    assert torch.equal(got[page * 64:page * 64 + 64], old[page * 64:page * 64 + 64, :512])
+    assert torch.equal(dw[2].cpu(), w[2])
+
+
+# ------------------------------------------------------------------- prefill --
+def _prefill_inputs(qs, ks, H, seed, joint, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+
+    def bf(*shape):
+        return (torch.randn(shape, generator=g) * scale).to(torch.bfloat16)
+
+    Tq, Tk = max(1, sum(qs)), max(1, sum(ks))
+    q, kv, kp = bf(Tq, H, 192), bf(Tk, H, 256), bf(Tk, 64)
+    dq, dkv, dp = q.cuda(), kv.cuda(), kp.cuda()
+    dk, dv = (dkv[..., :128], dkv[..., 128:]) if joint else (dkv[..., :128].contiguous(), dkv[..., 128:].contiguous())
+    cu = [np.concatenate([[0], np.cumsum(x)]) for x in (qs, ks)]
+    return q, kv, kp, (dq, dk, dp, dv, _ints(cu[0]), _ints(cu[1])), cu
+
+
+def _check_prefill(q, kv, kp, cu, out, lse, causal, skip=()):
+    H = q.shape[1]
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for z in range(len(cu[0]) - 1):
+        if z in skip:
+            continue
+        (a, b), (c, d) = cu[0][z:z + 2], cu[1][z:z + 2]
+        sees = np.maximum(0, (d - c) - (b - a) + 1 + np.arange(b - a)) if causal else np.full(b - a, d - c)
+        for h in range(H):
+            k = np.concatenate([kv[c:d, h, :128].double().numpy(), kp[c:d].double().numpy()], 1)
+            ref = la.rows_over_keys(q[a:b, h].double().numpy(), k, kv[c:d, h, 128:].double().numpy(), sees, SCALE)
+            _check_rows(out[a:b, h], lse[a:b, h], ref, 192)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,qs,ks,joint", [
+    (1, [1], [1], False), (16, [100], [100], True), (2, [128, 1, 129], [128, 1, 129], True),
+    (3, [0, 5, 64, 0, 300], [7, 5, 200, 0, 301], False), (2, [10, 200], [3, 0], True), (4, [1] * 9, list(range(1, 250, 28)), True),
+    (1, [700], [1500], False), (2, [127, 257, 511], [640, 257, 1000], True), (31, [40], [77], True)])
+def test_prefill_matches_oracle(B, H, qs, ks, joint, causal):
+    q, kv, kp, dev, cu = _prefill_inputs(qs, ks, H, seed=sum(qs) + H, joint=joint)
+    out, lse = B.latent_attention_prefill(*dev, SCALE, causal=causal)
+    assert B.latent_last_status() == 0
+    _check_prefill(q, kv, kp, cu, out, lse, causal)
+
+
+@pytest.mark.parametrize("scale,grow", [(12.0, False), (1.0, True), (1e-3, False)])
+def test_prefill_far_logits(B, scale, grow):
+    q, kv, kp, dev, cu = _prefill_inputs([300], [700], 2, seed=31, joint=True, scale=scale)
+    if grow:
+        f = (1.0 + 0.01 * torch.arange(700)).to(torch.bfloat16)
+        kv[:, :, :128] *= f[:, None, None]
+        dev[1].copy_(kv[..., :128])
+    out, lse = B.latent_attention_prefill(*dev, SCALE)
+    _check_prefill(q, kv, kp, cu, out, lse, True)
+
+
+def test_prefill_reports_bad_lengths(B):
+    q, kv, kp, dev, cu = _prefill_inputs([50, 60, 70], [50, 60, 70], 2, seed=32, joint=False)
+    out = torch.full((180, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((180, 2), 7.0, device="cuda")
+    bad = torch.tensor([0, 50, 110, 1000], dtype=torch.int32, device="cuda")
+    B.latent_attention_prefill(*dev[:5], bad, SCALE, out=out, lse=lse)
+    assert B.latent_last_status() == B.DSA_ERR_RANGE
+    assert torch.all(out[110:] == 7) and torch.all(lse[110:] == 7)
+    _check_prefill(q, kv, kp, cu, out, lse, True, skip=(2,))
+
+
+def test_prefill_values_past_a_sequence_do_not_leak(B):
+    """Keys of the next sequence share a tile with this one's last: they may hold anything."""
+    q, kv, kp, dev, cu = _prefill_inputs([70, 50], [70, 50], 2, seed=33, joint=True)
+    dev[1][70:] = float("nan")
+    dev[3][70:] = float("inf")
+    dev[2][70:] = float("nan")
+    out, lse = B.latent_attention_prefill(*dev, SCALE)
+    _check_prefill(q, kv, kp, cu, out, lse, True, skip=(1,))
+
+
+def test_prefill_on_a_side_stream_and_from_a_graph(B):
+    q, kv, kp, dev, cu = _prefill_inputs([130, 7], [200, 7], 4, seed=34, joint=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        out, lse = B.latent_attention_prefill(*dev, SCALE)
+    torch.cuda.synchronize()
+    _check_prefill(q, kv, kp, cu, out, lse, True)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        B.latent_attention_prefill(*dev, SCALE, out=out, lse=lse)
+    q2, kv2, kp2, _, cu2 = _prefill_inputs([37, 100], [137, 70], 4, seed=35, joint=True)
+    dev[0].copy_(q2)
+    dev[1].copy_(kv2[..., :128])
+    dev[2].copy_(kp2)
+    dev[3].copy_(kv2[..., 128:])
+    dev[4].copy_(_ints(cu2[0]))
+    dev[5].copy_(_ints(cu2[1]))
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    _check_prefill(q2, kv2, kp2, cu2, out, lse, True)
+
+
+def test_calls_follow_one_another_on_a_stream(B):
+    """Prefill, decode with weights, eviction and decode of what is left, back to back without a
+    synchronisation between: each call's result is what it is alone."""
+    c = Cache([500, 120, 64], seed=40)
+    qn, qp = _queries(3, 1, 16, seed=41)
+    ck, kp = c.device()
+    table, lens = c.table.cuda(), _ints(c.lens)
+    w = torch.zeros((3, c.table.shape[1] * 64), device="cuda")
+    out1, lse1 = B.latent_attention_paged(qn.cuda(), qp.cuda(), ck, kp, table, lens, SCALE, weights=w)
+    w1 = w.clone()
+    kept, new = B.latent_cache_evict(ck, kp, w, table, lens, 100, 20)
+    out2, lse2 = B.latent_attention_paged(qn.cuda(), qp.cuda(), ck, kp, table, new, SCALE)
+    torch.cuda.synchronize()
+    _check_decode(c, qn, qp, out1.double().cpu().numpy(), lse1.double().cpu().numpy(), weights=w1.double().cpu().numpy())
+    kept = kept.cpu().numpy()
+    d = Cache([100, 100, 64], seed=42)
+    d.table, d.P = c.table, c.P
+    d.data = c.data.clone()
+    flat, old = d.data.view(-1, 576), c.data.view(-1, 576)
+    for b in range(3):
+        slots = la.slots_of(c.table[b].numpy(), c.lens[b])
+        rows = la.kept_keys(w1[b].cpu().numpy(), c.lens[b], 100, 20)
+        assert np.array_equal(kept[b, :len(rows)], rows)
+        flat[slots[:len(rows)]] = old[slots[rows]]
+    _check_decode(d, qn, qp, out2.double().cpu().numpy(), lse2.double().cpu().numpy())
