@@ -17,6 +17,16 @@ constexpr int LA_DC = 512;             // compressed dims of a latent key (keys 
 constexpr int LA_DP = 64;              // its rope dims (keys only)
 constexpr int LA_DN = 128, LA_DV = 128;  // expanded form: no-rope key dims and value dims of a head
 
+// Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
+// 64) with the keys its rows see, cut into tiles of one page.  The items'
+// tiles are numbered through, and CTA c of the grid takes tiles [c per, (c + 1)
+// per): a run of them inside one item is a piece, whose id is item + c.
+struct LatentPlan {
+  int per, total;               // tiles per CTA, tiles in all
+  int prefix_len;               // validated
+  int items;
+};
+
 // Process-wide options and the launch counter (api.cu).
 uint64_t option_wait_ns();
 int option_grid();  // CTAs of the persistent kernels: the option, else the SM count
@@ -43,7 +53,19 @@ struct LatentAttnParams {
   float* lse;                   // [B, next_n, H]
   float* weights;               // [B, ld_weights] or null: += the softmax weight of every key
   int64_t ld_weights;
-  int* status;
+  Stats* stats;
+  // the call's row blocks and scratch
+  int n;                        // rows per block
+  int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
+  int items, grid;
+  uint64_t wait_ns;
+  LatentPlan* plan;
+  int32_t* start;               // [items + 1] first tile of each item
+  int32_t* first;               // [grid] item of each CTA's first tile
+  int32_t* lens;                // [B] validated lengths
+  float* part_o;                // [items + grid, n, 512] unnormalised outputs of the pieces
+  float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
+  float* logits;                // [tiles, 64, n] scaled logits (-inf: not seen), for the key weights
 };
 
 // Eviction in place: every sequence of more than `budget` keys keeps its last
@@ -78,7 +100,12 @@ struct PrefillParams {
   int* status;
 };
 
-cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t s);
+// Tensor maps of cached attention: queries [rows, 512] and [rows, 64], caches
+// [slots, 512] and [slots, 64], all bf16 in 128-byte swizzled boxes of 64 dims.
+struct LatentMaps {
+  CUtensorMap q_nope, q_pe, ckv, kpe;
+};
+cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t s);
 

@@ -1,6 +1,8 @@
 // latent_api.cu -- C ABI of the latent-attention operators
 // (include/dsa_indexer.h): argument validation, per-(device, stream) scratch
 // with the status word, and the launches.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -27,11 +29,13 @@ std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
 constexpr size_t HEAD = 256;
+static_assert(sizeof(Stats) <= HEAD, "the status block is the head");
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Scratch with room for `need` bytes past the head; its status word is
-// zeroed on the stream.  Null on an error.
-uint8_t* get_scratch(cudaStream_t stream, size_t need) {
+// Scratch with room for `need` bytes past the head; `zero`: its status block
+// is zeroed on the stream (else the call's first kernel writes it).  Null on
+// an error.
+uint8_t* get_scratch(cudaStream_t stream, size_t need, bool zero) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   Scratch& a = g_scratch[{dev, stream}];
@@ -46,7 +50,7 @@ uint8_t* get_scratch(cudaStream_t stream, size_t need) {
     a.base = p;
     a.cap = want;
   }
-  if (cudaMemsetAsync(a.base, 0, sizeof(int), stream) != cudaSuccess) return nullptr;
+  if (zero && cudaMemsetAsync(a.base, 0, HEAD, stream) != cudaSuccess) return nullptr;
   return a.base;
 }
 
@@ -74,14 +78,76 @@ int check_cached(const LatentAttnParams& p) {
   return DSA_OK;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// bf16 rows `stride` elements apart, `chunks` of 64 dims each: dims (64, rows,
+// chunks), boxes of 64 dims x box_rows x box_chunks in the 128-byte swizzle.
+bool tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t stride, int chunks, int box_rows,
+               int box_chunks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)chunks};
+  const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, chunks > 1 ? 3 : 2, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   const int rc = check_cached(p);
   if (rc != DSA_OK) return rc;
+  const int R = p.next_n * p.H;
+  const int64_t rows = (int64_t)p.B * R;
+  // the rows of a block: a prefix gathers the rows of the whole batch, so its
+  // blocks are full; else the smallest block that holds a sequence's rows
+  p.n = p.prefix_table || R > 32 ? 64 : R > 16 ? 32 : 16;
+  p.blocks = ceil_div(R, p.n);
+  p.prefix_items = p.prefix_table ? (int)((rows + p.n - 1) / p.n) : 0;
+  p.items = p.prefix_items + p.B * p.blocks;
+  p.grid = std::min(option_grid(), 1024);
+  if ((int64_t)p.items * std::max(p.max_pages, p.prefix_pages) >= (1ll << 31) - (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  p.wait_ns = option_wait_ns();
+  LatentMaps m;
+  const int64_t slots = (int64_t)p.num_pages * PAGE;
+  if (!tmap_rows(&m.q_nope, p.q_nope, rows, LA_DC, 8, p.n, 8) || !tmap_rows(&m.q_pe, p.q_pe, rows, LA_DP, 1, p.n, 1) ||
+      !tmap_rows(&m.ckv, p.ckv, slots, p.ckv_stride, 8, PAGE, 2) ||
+      !tmap_rows(&m.kpe, p.kpe, slots, p.kpe_stride, 1, PAGE, 1))
+    return DSA_ERR_CUDA;
+  size_t off = HEAD;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t pieces = (size_t)p.items + p.grid;
+  const size_t o_plan = take(sizeof(LatentPlan)), o_start = take(4 * ((size_t)p.items + 1)), o_first = take(4 * p.grid),
+               o_lens = take(4 * (size_t)p.B), o_ml = take(8 * pieces * p.n), o_po = take(4 * pieces * p.n * LA_DC),
+               o_log = p.weights ? take(4 * (size_t)p.B * p.blocks * p.max_pages * PAGE * p.n) : 0;
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, 0);
+  uint8_t* base = get_scratch(stream, off, false);
   if (!base) return DSA_ERR_CUDA;
-  p.status = reinterpret_cast<int*>(base);
-  return launch_latent_attn(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  p.stats = reinterpret_cast<Stats*>(base);
+  p.plan = reinterpret_cast<LatentPlan*>(base + o_plan);
+  p.start = reinterpret_cast<int32_t*>(base + o_start);
+  p.first = reinterpret_cast<int32_t*>(base + o_first);
+  p.lens = reinterpret_cast<int32_t*>(base + o_lens);
+  p.part_ml = reinterpret_cast<float2*>(base + o_ml);
+  p.part_o = reinterpret_cast<float*>(base + o_po);
+  p.logits = p.weights ? reinterpret_cast<float*>(base + o_log) : nullptr;
+  return launch_latent_attn(m, p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -176,7 +242,7 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, (size_t)B * 4);
+  uint8_t* base = get_scratch(stream, (size_t)B * 4, true);
   if (!base) return DSA_ERR_CUDA;
   EvictParams p{};
   p.ckv = reinterpret_cast<uint8_t*>(ckv);
@@ -218,7 +284,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, 0);
+  uint8_t* base = get_scratch(stream, 0, true);
   if (!base) return DSA_ERR_CUDA;
   PrefillParams p{};
   p.q = bf(q);

@@ -6,161 +6,724 @@
 // kpe[s]) its output is sum_s 2^(u_s - lse) ckv[s], lse = log2(sum_s 2^u_s).
 // A row that sees no key gets zeros and lse = -inf.
 //
-// One CTA per row, one warp per key at a time: lane l holds dims [16 l, + 16)
-// of the query, of the running output and of the key, and 2 rope dims; running
-// maximum and sum in base 2 per warp, joined at the end.
+// A key is 1152 bytes and costs a row 2176 operations, so up to about 128
+// rows a sequence the cache's bandwidth bounds the call, beyond that (a
+// prefix shared by the batch) the tensor cores.  One kernel serves both:
+// blocks of N = 16, 32 or 64 rows against tiles of one page (64 keys), with
+// the products transposed so that the key data, not the few rows, fill the
+// MMA's M side:
+//     S^T [64 keys x N rows]  = K [64 x 576] . Q^T         (36 steps of M = 64)
+//     O^T [512 dims x N rows] += V^T [512 x 64] . P^T      (16 steps of M = 128)
+// K and V are the same shared-memory tile, copied once by TMA: the first
+// product reads it with the dims contiguous, the second with M = dims (the
+// contiguous axis) and K = keys.  O^T (4 x N columns) and two S^T buffers stay
+// in TMEM; nothing but the result leaves the SM.
+//
+// Warps: 0 copies (a ring of 16 KB slots of 128 dims of a page, and 8 KB
+// slots of the rope dims), 1 issues the MMAs (S^T of the next tile before O^T
+// of this one, so the softmax is hidden), 2-5 do the softmax: the 16 x 256b
+// TMEM load leaves a thread two keys and N / 4 rows; the maximum over the 64
+// keys is three shuffle steps and one exchange through shared memory; the
+// weights go to shared memory as bf16 by stmatrix.  The reference maximum of
+// a row only moves when a tile exceeds it by 2^8 (fp32 sums and bf16 weights
+// have the range for that), so O^T is rarely rescaled.
+//
+// Every CTA takes an equal run of the call's tiles, whatever item they
+// belong to; an item cut by a run's border is joined by the merge kernel in
+// the order of its pieces, so results do not depend on timing.
 #include "latent.h"
 
 namespace dsa {
 
 namespace {
-constexpr int LR_WARPS = 8;
-__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* src, float* f) {
-  const uint4* p = reinterpret_cast<const uint4*>(src);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = p[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      f[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
-}
-__device__ __forceinline__ float2 load2(const __nv_bfloat16* src) {
-  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(src));
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+constexpr int LT = PAGE;                       // keys per tile
+constexpr int LA_WARPS = 6;
+constexpr int LA_THREADS = 32 * LA_WARPS;
+constexpr int LA_SM_THREADS = 128;             // softmax warps 2..5
+constexpr uint32_t CHUNK = LT * 128;           // 64 keys x 64 dims, bf16
+constexpr uint32_t PAIR = 2 * CHUNK;           // 64 keys x 128 dims
+constexpr float RESCALE_AT = 8.f;              // a row's reference moves when its maximum passes it by this
 
-// Validated length of sequence b (an invalid one counts as empty and is reported).
-__device__ __forceinline__ int seq_len(const LatentAttnParams& p, int b) {
-  const int len = p.seq_lens[b];
-  if (len >= 0 && len <= (int64_t)p.max_pages * PAGE) return len;
-  atomicOr(p.status, ST_RANGE);
-  return 0;
-}
-__device__ __forceinline__ int prefix_len(const LatentAttnParams& p) {
-  if (!p.prefix_table) return 0;
-  const int len = *p.prefix_len;
-  if (len >= 0 && len <= (int64_t)p.prefix_pages * PAGE) return len;
-  atomicOr(p.status, ST_RANGE);
-  return 0;
-}
-// Slot of logical key s of a table, -1 for a page outside the cache (reported; its keys read as zeros).
-__device__ __forceinline__ int64_t slot_of(const LatentAttnParams& p, const int32_t* table, int s) {
-  const int page = table[s / PAGE];
-  if (page >= 0 && page < p.num_pages) return (int64_t)page * PAGE + s % PAGE;
-  atomicOr(p.status, ST_RANGE);
-  return -1;
-}
-
-struct Key {
-  float c[16];
-  float2 e;
+template <int N>
+struct LA {
+  // Ring depths: what 227 KB leave next to the query block.  64 rows keep
+  // two tiles of ckv and one of the rope part, and one weight buffer.
+  static constexpr int PAIRS = N == 64 ? 8 : N == 32 ? 10 : 11;
+  static constexpr int KPES = N == 64 ? 1 : 2;
+  static constexpr int PBUFS = N == 64 ? 1 : 2;
+  static constexpr uint32_t P_BYTES = N * 128;  // weights of a tile: N rows x 64 keys bf16
+  static constexpr uint32_t OFF_Q = 0;          // 9 chunks of N rows x 64 dims
+  static constexpr uint32_t OFF_P = OFF_Q + 9 * N * 128;
+  static constexpr uint32_t OFF_PAIR = (OFF_P + PBUFS * P_BYTES + 1023) / 1024 * 1024;
+  static constexpr uint32_t OFF_KPE = OFF_PAIR + PAIRS * PAIR;
+  static constexpr uint32_t OFF_MISC = OFF_KPE + KPES * CHUNK;
+  // barriers: pair full/empty, kpe full/empty, q full/empty, S full/empty x 2, P full x 2, PV done x 2, O empty, drain
+  static constexpr int B_PF = 0, B_PE = PAIRS, B_KF = 2 * PAIRS, B_KE = B_KF + KPES, B_QF = B_KE + KPES, B_QE = B_QF + 1,
+                       B_SF = B_QE + 1, B_SE = B_SF + 2, B_WF = B_SE + 2, B_VD = B_WF + 2, B_OE = B_VD + 2,
+                       B_DRAIN = B_OE + 1, N_BARS = B_DRAIN + 1;
+  static constexpr uint32_t OFF_BAR = OFF_MISC;
+  static constexpr uint32_t OFF_RED = OFF_BAR + (N_BARS * 8 + 127) / 128 * 128;  // [4][N] floats
+  static constexpr uint32_t OFF_REF = OFF_RED + 4 * N * 4;                       // [N] reference maxima
+  static constexpr uint32_t OFF_ALPHA = OFF_REF + N * 4;                         // [N] factors
+  static constexpr uint32_t OFF_LIM = OFF_ALPHA + N * 4;                         // [N] visible keys per row
+  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base, rescale
+  static constexpr uint32_t SMEM = OFF_FLAG + 32 + 1024;                         // + alignment
+  static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer
+  static constexpr uint32_t TMEM_COLS = N == 64 ? 512 : N == 32 ? 256 : 128;     // 6 N, to a power of two
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
-__device__ __forceinline__ void load_key(const LatentAttnParams& p, int64_t slot, int lane, Key& k) {
-  if (slot < 0) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) k.c[i] = 0.f;
-    k.e = make_float2(0.f, 0.f);
-    return;
+
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ void stsm_x4_t(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// One item: a block of rows and the keys they see.
+struct Item {
+  int row0, nrows;         // flat query rows
+  int len;                 // keys behind `table`
+  int lim0;                // keys that the block's first row sees; later tokens see one more each
+  int r0;                  // first row within its sequence (-1: a prefix, every row sees all)
+  const int32_t* table;
+};
+__device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
+  Item it;
+  if (w < p.prefix_items) {
+    it.row0 = w * p.n;
+    it.nrows = min(p.n, p.B * p.next_n * p.H - it.row0);
+    it.len = it.lim0 = p.plan->prefix_len;
+    it.r0 = -1;
+    it.table = p.prefix_table;
+    return it;
   }
-  load16(p.ckv + slot * p.ckv_stride + 16 * lane, k.c);
-  k.e = load2(p.kpe + slot * p.kpe_stride + 2 * lane);
+  const int v = w - p.prefix_items, b = v / p.blocks, j = v % p.blocks, R = p.next_n * p.H;
+  it.r0 = j * p.n;
+  it.row0 = b * R + it.r0;
+  it.nrows = min(p.n, R - it.r0);
+  it.len = p.lens[b];
+  it.lim0 = max(0, it.len - p.next_n + 1 + it.r0 / p.H);
+  it.table = p.block_table + (int64_t)b * p.max_pages;
+  return it;
 }
-__device__ __forceinline__ float dot(const Key& a, const Key& b) {
-  float x = a.e.x * b.e.x + a.e.y * b.e.y;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x += a.c[i] * b.c[i];
-  return warp_sum(x);
-}
+
+// The runs of one CTA's tiles: next() gives item w and its tiles [k0, k1).
+struct Runs {
+  int t, t1, w;
+  __device__ __forceinline__ Runs(const LatentAttnParams& p) {
+    const int per = p.plan->per;
+    t = min(p.plan->total, (int)blockIdx.x * per);
+    t1 = min(p.plan->total, t + per);
+    w = t < t1 ? p.first[blockIdx.x] : 0;
+  }
+  __device__ __forceinline__ bool next(const LatentAttnParams& p, int& item, int& k0, int& k1, bool& whole) {
+    if (t >= t1) return false;
+    int s0 = p.start[w], s1 = p.start[w + 1];
+    while (s1 <= t) {
+      ++w;
+      s0 = s1;
+      s1 = p.start[w + 1];
+    }
+    item = w;
+    k0 = t - s0;
+    k1 = min(t1, s1) - s0;
+    whole = k0 == 0 && k1 == s1 - s0;
+    t = s0 + k1;
+    return true;
+  }
+};
+
 }  // namespace
 
-__global__ void __launch_bounds__(32 * LR_WARPS) latent_rows_kernel(const LatentAttnParams p) {
+// Lengths checked, items numbered: start[w], every CTA's first item, the status block.
+constexpr int PLAN_THREADS = 1024;
+__global__ void __launch_bounds__(PLAN_THREADS) latent_plan_kernel(const LatentAttnParams p) {
   pdl_enter();
-  __shared__ float s_m[LR_WARPS], s_l[LR_WARPS], s_o[LR_WARPS][LA_DC];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
-  const int tok = (int)(row / p.H), b = tok / p.next_n, i = tok % p.next_n;
-  const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
-  const int pre = prefix_len(p);
-  const int own = max(0, seq_len(p, b) - p.next_n + i + 1);
-  Key q, k;
-  load16(p.q_nope + row * LA_DC + 16 * lane, q.c);
-  q.e = load2(p.q_pe + row * LA_DP + 2 * lane);
-  float m = neg_inf(), l = 0.f, c = 0.f, o[16];
-#pragma unroll
-  for (int d = 0; d < 16; ++d) o[d] = 0.f;
-  for (int64_t s = warp; s < (int64_t)pre + own; s += LR_WARPS) {
-    load_key(p, s < pre ? slot_of(p, p.prefix_table, (int)s) : slot_of(p, table, (int)(s - pre)), lane, k);
-    const float u = dot(q, k) * p.scale_log2;
-    const float m_new = fmaxf(m, u);
-    const float mm = m_new == neg_inf() ? 0.f : m_new;
-    const float a = exp2f(m - mm), w = exp2f(u - mm);
-    m = m_new;
-    // compensated: over many keys of nearly equal weight a plain sum would
-    // lose the weights' differences
-    l *= a;
-    const float y = w - c * a, sum = l + y;
-    c = (sum - l) - y;
-    l = sum;
-#pragma unroll
-    for (int d = 0; d < 16; ++d) o[d] = o[d] * a + w * k.c[d];
-  }
-#pragma unroll
-  for (int d = 0; d < 16; ++d) s_o[warp][16 * lane + d] = o[d];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  __shared__ int tmp[32];
+  __shared__ int s_status;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_status = 0;
   __syncthreads();
-  float M = neg_inf(), L = 0.f;
-  for (int w = 0; w < LR_WARPS; ++w) M = fmaxf(M, s_m[w]);
-  const float mm = M == neg_inf() ? 0.f : M;
-  for (int w = 0; w < LR_WARPS; ++w) L += exp2f(s_m[w] - mm) * s_l[w];
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  for (int d = threadIdx.x; d < LA_DC; d += blockDim.x) {
-    float x = 0.f;
-    for (int w = 0; w < LR_WARPS; ++w) x += exp2f(s_m[w] - mm) * s_o[w][d];
-    p.out[row * LA_DC + d] = __float2bfloat16(x * inv);
-  }
-  if (threadIdx.x == 0) p.lse[row] = L > 0.f ? M + log2f(L) : neg_inf();
-}
-
-// weights[b, s] += sum over the rows that see key s of 2^(u - lse): one warp per key.
-__global__ void __launch_bounds__(32 * LR_WARPS) latent_weights_kernel(const LatentAttnParams p) {
-  pdl_enter();
-  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = seq_len(p, b);
-  const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
-  for (int s = blockIdx.x * LR_WARPS + warp; s < len; s += gridDim.x * LR_WARPS) {
-    Key k, q;
-    load_key(p, slot_of(p, table, s), lane, k);
-    float sum = 0.f;
-    for (int r = 0; r < p.next_n * p.H; ++r) {
-      if (s >= len - p.next_n + r / p.H + 1) continue;
-      const int64_t row = (int64_t)b * p.next_n * p.H + r;
-      load16(p.q_nope + row * LA_DC + 16 * lane, q.c);
-      q.e = load2(p.q_pe + row * LA_DP + 2 * lane);
-      sum += exp2f(dot(q, k) * p.scale_log2 - p.lse[row]);
+  int pre = 0;
+  if (p.prefix_items) {
+    pre = *p.prefix_len;
+    if (pre < 0 || pre > (int64_t)p.prefix_pages * PAGE) {
+      atomicOr(&s_status, ST_RANGE);
+      pre = 0;
     }
-    if (lane == 0) p.weights[b * p.ld_weights + s] += sum;
+  }
+  int base = 0;
+  for (int i0 = 0; i0 < p.items; i0 += PLAN_THREADS) {
+    const int w = i0 + tid;
+    int tiles = 0;
+    if (w < p.prefix_items) {
+      tiles = ceil_div(pre, LT);
+    } else if (w < p.items) {
+      const int v = w - p.prefix_items, b = v / p.blocks;
+      int len = p.seq_lens[b];
+      if (len < 0 || len > (int64_t)p.max_pages * PAGE) {
+        atomicOr(&s_status, ST_RANGE);
+        len = 0;
+      }
+      if (v % p.blocks == 0) p.lens[b] = len;
+      tiles = ceil_div(len, LT);
+    }
+    int x = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int i = 0; i < 32; ++i) {
+      const int v = tmp[i];
+      if (i < warp) before += v;
+      all += v;
+    }
+    if (w < p.items) p.start[w] = base + before + x - tiles;
+    base += all;
+  }
+  // at least two tiles per CTA: a shorter run costs more in pieces to join
+  // than its parallelism saves
+  const int per = max(2, ceil_div(base, p.grid));
+  if (tid == 0) {
+    p.start[p.items] = base;
+    p.plan->per = per;
+    p.plan->total = base;
+    p.plan->prefix_len = pre;
+    p.plan->items = p.items;
+    p.stats->wait_ns = p.wait_ns;
+  }
+  __syncthreads();  // start[] is written (read back by this CTA only below)
+  if (tid == 0) p.stats->status = s_status;
+  for (int w = tid; w < p.items; w += PLAN_THREADS) {
+    const int s0 = p.start[w], s1 = p.start[w + 1];
+    for (int c = ceil_div(s0, per); c < p.grid && (int64_t)c * per < s1; ++c) p.first[c] = w;
   }
 }
 
-cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t s) {
+template <int N>
+__global__ void __launch_bounds__(LA_THREADS, 1)
+    latent_attn_kernel(const __grid_constant__ LatentMaps maps, const LatentAttnParams p) {
+  using C = LA<N>;
+  pdl_enter();
+  if ((int64_t)blockIdx.x * p.plan->per >= p.plan->total) return;  // uniform over the CTA: no tiles
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * i; };
+  float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
+  float* s_ref = reinterpret_cast<float*>(smem + C::OFF_REF);
+  float* s_alpha = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
+  int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_FLAG);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG + 4);
+  volatile int* s_resc = reinterpret_cast<int*>(smem + C::OFF_FLAG + 8);  // [2]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    s_resc[0] = s_resc[1] = 0;
+    for (int i = 0; i < 2 * C::PAIRS + 2 * C::KPES + 2; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::B_SF + i), 1);
+      mbar_init(bar(C::B_SE + i), 4);
+      mbar_init(bar(C::B_WF + i), 4);
+      mbar_init(bar(C::B_VD + i), 1);
+    }
+    mbar_init(bar(C::B_OE), 4);
+    mbar_init(bar(C::B_DRAIN), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  uint32_t it = 0;       // this CTA's tiles so far
+  uint32_t seg = 0;      // and its pieces
+  uint32_t n_pair = 0, n_kpe = 0, n_q = 0;  // producer: copies armed
+  Runs runs(p);
+  int w, k0, k1;
+  bool whole;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer --
+    bool ok = true;
+    while (ok && runs.next(p, w, k0, k1, whole)) {
+      const Item im = load_item(p, w);
+      if (!(ok = mbar_wait_warp(bar(C::B_QE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(C::B_QF), 9 * N * 128);
+        tma_load_3d(sbase + C::OFF_Q, &maps.q_nope, 0, im.row0, 0, bar(C::B_QF));
+        tma_load_2d(sbase + C::OFF_Q + 8 * N * 128, &maps.q_pe, 0, im.row0, bar(C::B_QF));
+      }
+      ++n_q;
+      ++seg;
+      int pages = 0;  // lane j: page of tile (k & ~31) + j, the page past the cache for an invalid one
+      for (int k = k0; ok && k < k1; ++k) {
+        if (k == k0 || (k & 31) == 0) {
+          const int j = (k & ~31) + lane;
+          bool bad = false;
+          if (j >= k && j < k1) {
+            pages = im.table[j];
+            bad = pages < 0 || pages >= p.num_pages;
+            if (bad) pages = p.num_pages;
+          }
+          if (__ballot_sync(0xffffffffu, bad) && lane == 0) atomicOr(&p.stats->status, ST_RANGE);
+        }
+        const int slot = __shfl_sync(0xffffffffu, pages, k & 31) * PAGE;
+        for (int c = 0; c < 4; ++c, ++n_pair) {
+          const int st = n_pair % C::PAIRS;
+          if (!(ok = mbar_wait_warp(bar(C::B_PE + st), ((n_pair / C::PAIRS) & 1) ^ 1, abort_flag, p.stats))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(C::B_PF + st), PAIR);
+            tma_load_3d(sbase + C::OFF_PAIR + st * PAIR, &maps.ckv, 0, slot, 2 * c, bar(C::B_PF + st));
+          }
+        }
+        if (!ok) break;
+        const int st = n_kpe % C::KPES;
+        if (!(ok = mbar_wait_warp(bar(C::B_KE + st), ((n_kpe / C::KPES) & 1) ^ 1, abort_flag, p.stats))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(C::B_KF + st), CHUNK);
+          tma_load_2d(sbase + C::OFF_KPE + st * CHUNK, &maps.kpe, 0, slot, bar(C::B_KF + st));
+        }
+        ++n_kpe;
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer --
+    if (lane == 0) {
+      constexpr uint32_t ID_S = idesc_bf16_f32(64, N, false, false);
+      constexpr uint32_t ID_O = idesc_bf16_f32(128, N, true, false);
+      bool ok = true;
+      // O^T (+)= V^T P^T of tile i; `first`: the piece's first, which overwrites
+      auto pv = [&](uint32_t i, bool first) {
+        const uint32_t pb = i % C::PBUFS;
+        if (!(ok = mbar_wait(bar(C::B_WF + (i & 1)), (i >> 1) & 1, abort_flag, p.stats))) return;
+        tc_fence_after();
+        const uint64_t pd = sw128_kmajor_desc(sbase + C::OFF_P + pb * C::P_BYTES);
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint32_t st = (4 * i + c) % C::PAIRS;
+          const uint64_t vd = sw128_mnmajor_desc(sbase + C::OFF_PAIR + st * PAIR, CHUNK);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // 16 keys: 2 KB of V, 32 bytes of a P row
+            mma_bf16_ss(tmem + c * N, vd + 128 * k, pd + 2 * k, ID_O, !(first && k == 0));
+          mma_commit(bar(C::B_PE + st));
+        }
+        mma_commit(bar(C::B_VD + (i & 1)));
+      };
+      while (ok && runs.next(p, w, k0, k1, whole)) {
+        if (!(ok = mbar_wait(bar(C::B_QF), seg & 1, abort_flag, p.stats))) break;
+        for (int k = k0; ok && k < k1; ++k, ++it) {
+          const uint32_t sb = it & 1;
+          if (!(ok = mbar_wait(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, p.stats))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + C::TMEM_S + sb * N;
+          const uint64_t qd = sw128_kmajor_desc(sbase + C::OFF_Q);
+          for (uint32_t c = 0; c < 4; ++c) {
+            const uint32_t i = 4 * it + c, st = i % C::PAIRS;
+            if (!(ok = mbar_wait(bar(C::B_PF + st), (i / C::PAIRS) & 1, abort_flag, p.stats))) break;
+            const uint64_t kd = sw128_kmajor_desc(sbase + C::OFF_PAIR + st * PAIR);
+#pragma unroll
+            for (int k2 = 0; k2 < 8; ++k2)
+              mma_bf16_ss(d, kd + (k2 >> 2) * (CHUNK >> 4) + 2 * (k2 & 3),
+                          qd + (2 * c + (k2 >> 2)) * (N * 128 >> 4) + 2 * (k2 & 3), ID_S, c > 0 || k2 > 0);
+          }
+          if (!ok) break;
+          const uint32_t st = it % C::KPES;
+          if (!(ok = mbar_wait(bar(C::B_KF + st), (it / C::KPES) & 1, abort_flag, p.stats))) break;
+          const uint64_t kd = sw128_kmajor_desc(sbase + C::OFF_KPE + st * CHUNK);
+#pragma unroll
+          for (int k2 = 0; k2 < 4; ++k2)
+            mma_bf16_ss(d, kd + 2 * k2, qd + 8 * (N * 128 >> 4) + 2 * k2, ID_S, 1);
+          mma_commit(bar(C::B_KE + st));
+          mma_commit(bar(C::B_SF + sb));
+          if (k == k1 - 1) mma_commit(bar(C::B_QE));
+          if (k == k0) {
+            // the previous piece's O^T has been read out
+            if (!(ok = mbar_wait(bar(C::B_OE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
+          } else {
+            pv(it - 1, k == k0 + 1);
+          }
+        }
+        if (ok) pv(it - 1, k1 == k0 + 1);
+        ++seg;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------- softmax warps --
+    // A wait that gives up does not leave the loop (the other warps of the
+    // exchange would wait for ever): with the abort flag set every later
+    // wait returns at once, and the result is undefined but complete.
+    const int q = warp & 3;                  // TMEM lane quarter: keys [16 q, + 16)
+    const int st_id = threadIdx.x - 64;      // 0 .. 127
+    const int g = lane >> 2, cc = 2 * (lane & 3);
+    constexpr int M8 = N / 8;                // blocks of 8 rows
+    float ref = neg_inf();                   // threads st_id < N: the reference maximum of row st_id
+    while (runs.next(p, w, k0, k1, whole)) {
+      const Item im = load_item(p, w);
+      for (int c = st_id; c < N; c += LA_SM_THREADS)
+        s_lim[c] = c >= im.nrows ? 0 : im.r0 < 0 ? im.len : max(0, im.len - p.next_n + 1 + (im.r0 + c) / p.H);
+      float l[M8][2];                        // this thread's part of each row's sum
+#pragma unroll
+      for (int m = 0; m < M8; ++m) l[m][0] = l[m][1] = 0.f;
+      ref = neg_inf();
+      for (int k = k0; k < k1; ++k, ++it) {
+        const uint32_t sb = it & 1;
+        mbar_wait_warp(bar(C::B_SF + sb), (it >> 1) & 1, abort_flag, p.stats);
+        tc_fence_after();
+        uint32_t s[4 * M8];
+        const uint32_t sa = tmem + C::TMEM_S + sb * N + ((uint32_t)(32 * q) << 16);
+        if constexpr (N == 64) tmem_ld16x256b_x8(sa, s);
+        if constexpr (N == 32) tmem_ld16x256b_x4(sa, s);
+        if constexpr (N == 16) tmem_ld16x256b_x2(sa, s);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_SE + sb));
+        // slots past the sequence may hold anything: their values become 0
+        // in the tile itself (a weight of 0 does not silence a NaN)
+        const int valid = im.len - k * LT;
+        if (valid < LT) {
+          for (int i = st_id; i < (LT - valid) * 64; i += LA_SM_THREADS) {
+            const int row = valid + (i >> 6), ch = (i >> 3) & 7, x = i & 7;  // row, chunk of 64 dims, 16 bytes
+            const uint32_t ps = (4 * it + (ch >> 1)) % C::PAIRS;
+            *reinterpret_cast<uint4*>(smem + C::OFF_PAIR + ps * PAIR + (ch & 1) * CHUNK + row * 128 + 16 * x) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        // u of rows 8 m + cc + {0, 1}, keys 16 q + g and + 8
+        float u[M8][4];
+#pragma unroll
+        for (int i = 0; i < 4 * M8; ++i) u[i >> 2][i & 3] = __uint_as_float(s[i]) * p.scale_log2;
+        const int key = k * LT + 16 * q + g;
+        if ((k + 1) * LT > im.lim0 || im.nrows < N) {
+          __syncwarp();
+          named_bar_sync(1, LA_SM_THREADS);  // s_lim
+#pragma unroll
+          for (int m = 0; m < M8; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int lim = s_lim[8 * m + cc + e];
+              if (key >= lim) u[m][e] = neg_inf();
+              if (key + 8 >= lim) u[m][2 + e] = neg_inf();
+            }
+        }
+        if (p.logits) {
+          float* dst = p.logits + ((int64_t)(p.start[w] + k) * LT + 16 * q + g) * N + cc;
+#pragma unroll
+          for (int m = 0; m < M8; ++m) {
+            *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(u[m][0], u[m][1]);
+            *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2], u[m][3]);
+          }
+        }
+        // maximum over the warp's 16 keys: three steps that halve the rows a
+        // lane holds while they halve the lanes a row is spread over
+        float mx[2 * M8];
+#pragma unroll
+        for (int i = 0; i < 2 * M8; ++i) mx[i] = fmaxf(u[i >> 1][i & 1], u[i >> 1][2 + (i & 1)]);
+#pragma unroll
+        for (int i = 0; i < 2 * M8; ++i) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+        }
+        if (g == 0) {
+#pragma unroll
+          for (int m = 0; m < M8; ++m)
+            *reinterpret_cast<float2*>(&s_red[q * N + 8 * m + cc]) = make_float2(mx[2 * m], mx[2 * m + 1]);
+        }
+        named_bar_sync(1, LA_SM_THREADS);
+        if (st_id < N) {
+          const float top = fmaxf(fmaxf(s_red[st_id], s_red[N + st_id]), fmaxf(s_red[2 * N + st_id], s_red[3 * N + st_id]));
+          float a = 1.f;
+          if (top > ref + RESCALE_AT || (ref == neg_inf() && top > ref)) {
+            a = ex2(ref - top);  // 0 from a reference of -inf
+            ref = top;
+            s_resc[sb] = 1;
+          }
+          s_alpha[st_id] = a;
+          s_ref[st_id] = ref == neg_inf() ? 0.f : ref;
+        }
+        named_bar_sync(1, LA_SM_THREADS);
+        const bool rescale = s_resc[sb] != 0;
+        if (st_id == 0) s_resc[sb ^ 1] = 0;  // the next tile's flag: set after the next barrier at the earliest
+        if (C::PBUFS == 1) {
+          if (it > 0) mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
+        } else if (it > 1) {
+          mbar_wait_warp(bar(C::B_VD + sb), ((it - 2) >> 1) & 1, abort_flag, p.stats);
+        }
+        if (rescale) {
+#pragma unroll
+          for (int m = 0; m < M8; ++m) {
+            l[m][0] *= s_alpha[8 * m + cc];
+            l[m][1] *= s_alpha[8 * m + cc + 1];
+          }
+          if (k > k0) {  // O^T: four blocks of 128 dims, this warp's 32 lanes of each
+            mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 4 * N / 16; ++j) {
+              uint32_t o[16];
+              const uint32_t oa = tmem + 16 * j + ((uint32_t)(32 * q) << 16);
+              tmem_ld16(oa, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * s_alpha[(16 * j + i) % N]);
+              tmem_st16(oa, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
+        // the MMA wants of both operands) into P [row][key]
+        const uint32_t pb = sbase + C::OFF_P + (it % C::PBUFS) * C::P_BYTES;
+#pragma unroll
+        for (int m = 0; m < M8; m += 2) {
+          uint32_t r[4];
+#pragma unroll
+          for (int mm = 0; mm < 2; ++mm) {
+            const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * (m + mm) + cc]);
+            const float a0 = ex2(u[m + mm][0] - f.x), a1 = ex2(u[m + mm][1] - f.y);
+            const float b0 = ex2(u[m + mm][2] - f.x), b1 = ex2(u[m + mm][3] - f.y);
+            l[m + mm][0] += a0 + b0;
+            l[m + mm][1] += a1 + b1;
+            const __nv_bfloat162 pa = __floats2bfloat162_rn(a0, a1), pb2 = __floats2bfloat162_rn(b0, b1);
+            r[2 * mm] = *reinterpret_cast<const uint32_t*>(&pa);
+            r[2 * mm + 1] = *reinterpret_cast<const uint32_t*>(&pb2);
+          }
+          // matrix lane / 8: rows 8 (m + lane / 16), keys 16 q + 8 (lane / 8 % 2)
+          const int row = 8 * (m + (lane >> 4)) + (lane & 7);
+          const int ch = 2 * q + ((lane >> 3) & 1);
+          stsm_x4_t(pb + row * 128 + ((ch ^ (row & 7)) << 4), r);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_WF + sb));
+      }
+      // ---- the piece's result: sums over the warps, then O^T out of TMEM
+#pragma unroll
+      for (int m = 0; m < M8; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], o);
+      named_bar_sync(1, LA_SM_THREADS);  // s_red, s_alpha and s_lim are free
+      if (g == 0) {
+#pragma unroll
+        for (int m = 0; m < M8; ++m)
+          *reinterpret_cast<float2*>(&s_red[q * N + 8 * m + cc]) = make_float2(l[m][0], l[m][1]);
+      }
+      named_bar_sync(1, LA_SM_THREADS);
+      const bool direct = whole && !p.prefix_items;
+      const int64_t piece = (int64_t)w + blockIdx.x;
+      if (st_id < N) {
+        const float sum = (s_red[st_id] + s_red[N + st_id]) + (s_red[2 * N + st_id] + s_red[3 * N + st_id]);
+        if (direct) {
+          s_alpha[st_id] = sum == 0.f ? 0.f : 1.f / sum;
+          if (st_id < im.nrows) p.lse[im.row0 + st_id] = sum == 0.f ? neg_inf() : s_ref[st_id] + log2f(sum);
+        } else {
+          p.part_ml[piece * N + st_id] = make_float2(ref, sum);
+        }
+      }
+      named_bar_sync(1, LA_SM_THREADS);
+      mbar_wait_warp(bar(C::B_VD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
+      tc_fence_after();
+#pragma unroll 1
+      for (int j = 0; j < 4 * N / 16; ++j) {
+        uint32_t o[16];
+        tmem_ld16(tmem + 16 * j + ((uint32_t)(32 * q) << 16), o);
+        tmem_wait_ld();
+        const int dim = 128 * (16 * j / N) + 32 * q + lane, c0 = 16 * j % N;
+        if (direct) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c0 + i < im.nrows)
+              p.out[(int64_t)(im.row0 + c0 + i) * LA_DC + dim] = __float2bfloat16(__uint_as_float(o[i]) * s_alpha[c0 + i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c0 + i < im.nrows) p.part_o[(piece * N + c0 + i) * LA_DC + dim] = __uint_as_float(o[i]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_OE));
+      named_bar_sync(1, LA_SM_THREADS);  // s_alpha has been read
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // before shared memory and TMEM are released, the copies and MMAs
+    // already issued land: the last phase armed on each slot, a last commit
+    if (warp == 0 && lane == 0) {
+      for (uint32_t s = 0; s < C::PAIRS; ++s)
+        if (n_pair > s) mbar_drain(bar(C::B_PF + s), ((n_pair - 1 - s) / C::PAIRS) & 1);
+      for (uint32_t s = 0; s < C::KPES; ++s)
+        if (n_kpe > s) mbar_drain(bar(C::B_KF + s), ((n_kpe - 1 - s) / C::KPES) & 1);
+      if (n_q) mbar_drain(bar(C::B_QF), (n_q - 1) & 1);
+    } else if (warp == 1 && lane == 0) {
+      mma_commit(bar(C::B_DRAIN));
+      mbar_drain(bar(C::B_DRAIN), 0);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the pieces of a row, in their order: one CTA per row.  Rows whose only
+// piece was written by its CTA are left alone.
+constexpr int MG_THREADS = 256;
+constexpr int MG_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
+__global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAttnParams p) {
+  pdl_enter();
+  __shared__ float s_w[MG_MAX];
+  __shared__ float s_part[LA_DC];
+  __shared__ float s_tmp[MG_THREADS / 32];
+  const int64_t row = blockIdx.x;
+  const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = p.plan->per;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int id0[2], cnt[2], col[2], n = 0;  // runs of piece ids, the row's place in its block
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int w = k ? p.prefix_items + b * p.blocks + r / p.n : (int)(row / p.n);
+    cnt[k] = id0[k] = 0;
+    col[k] = k ? r % p.n : (int)(row % p.n);
+    if (k == 0 && !p.prefix_items) continue;
+    const int s0 = p.start[w], s1 = p.start[w + 1];
+    if (s0 == s1) continue;
+    id0[k] = w + s0 / per;
+    cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
+    n += cnt[k];
+  }
+  if (n == 1 && !p.prefix_items) return;
+  auto at = [&](int i) -> int64_t {
+    return i < cnt[0] ? (int64_t)(id0[0] + i) * p.n + col[0] : (int64_t)(id0[1] + i - cnt[0]) * p.n + col[1];
+  };
+  float m = neg_inf();
+  for (int i = tid; i < n; i += MG_THREADS) m = fmaxf(m, p.part_ml[at(i)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_tmp[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MG_THREADS / 32; ++i) m = fmaxf(m, s_tmp[i]);
+  const float mm = m == neg_inf() ? 0.f : m;
+  float sum = 0.f;
+  for (int i = tid; i < n; i += MG_THREADS) {
+    const float2 ml = p.part_ml[at(i)];
+    const float x = ex2(ml.x - mm);
+    s_w[i] = x;
+    sum += x * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncthreads();
+  if (lane == 0) s_tmp[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < MG_THREADS / 32; ++i) sum += s_tmp[i];
+  // two halves of the CTA take every other piece, 4 dims per thread
+  const int half = tid >> 7, d = 4 * (tid & 127);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = half; i < n; i += 2) {
+    const float x = s_w[i];
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(i) * LA_DC + d));
+    if (x != 0.f) {  // a piece without a visible key adds nothing
+      o.x += x * v.x;
+      o.y += x * v.y;
+      o.z += x * v.z;
+      o.w += x * v.w;
+    }
+  }
+  if (half) *reinterpret_cast<float4*>(&s_part[d]) = o;
+  __syncthreads();
+  if (half == 0) {
+    const float4 v = *reinterpret_cast<const float4*>(&s_part[d]);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DC + d);
+    dst[0] = __floats2bfloat162_rn((o.x + v.x) * inv, (o.y + v.y) * inv);
+    dst[1] = __floats2bfloat162_rn((o.z + v.z) * inv, (o.w + v.w) * inv);
+  }
+  if (tid == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+}
+
+// weights[b, s] += sum over the rows that see key s of 2^(u - lse), from the
+// logits that the main kernel left: N / 4 lanes per key, 4 rows per lane.
+constexpr int WT_THREADS = 256;
+template <int N>
+__global__ void __launch_bounds__(WT_THREADS) latent_weights_kernel(const LatentAttnParams p) {
+  pdl_enter();
+  constexpr int LPK = N / 4, KEYS = WT_THREADS / LPK;  // lanes per key, keys per step
+  const int b = blockIdx.y, R = p.next_n * p.H;
+  const int len = p.lens[b], tiles = ceil_div(len, LT), sub = threadIdx.x % LPK, kk = threadIdx.x / LPK;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+#pragma unroll 1
+    for (int k = kk; k < LT; k += KEYS) {
+      float sum = 0.f;
+      for (int j = 0; j < p.blocks; ++j) {
+        const int64_t tile = p.start[b * p.blocks + j] + t;
+        const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
+        const int r = j * N + 4 * sub;
+        const float* lse = p.lse + (int64_t)b * R + r;
+        if (r < R) sum += u.x == neg_inf() ? 0.f : ex2(u.x - lse[0]);
+        if (r + 1 < R) sum += u.y == neg_inf() ? 0.f : ex2(u.y - lse[1]);
+        if (r + 2 < R) sum += u.z == neg_inf() ? 0.f : ex2(u.z - lse[2]);
+        if (r + 3 < R) sum += u.w == neg_inf() ? 0.f : ex2(u.w - lse[3]);
+      }
+#pragma unroll
+      for (int o = 1; o < LPK; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int s = t * LT + k;
+      if (sub == 0 && s < len) p.weights[b * p.ld_weights + s] += sum;
+    }
+  }
+}
+
+template <int N>
+static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
+  static DeviceFlags attr_set;
+  cudaError_t e = set_smem_attr_once(latent_attn_kernel<N>, LA<N>::SMEM, attr_set);
+  if (e != cudaSuccess) return e;
   count_launch();
-  cudaError_t e = launch_pdl(latent_rows_kernel, dim3((unsigned)(p.B * p.next_n * p.H)), dim3(32 * LR_WARPS), 0, s, p);
+  e = launch_pdl(latent_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  e = launch_pdl(latent_attn_kernel<N>, dim3(p.grid), dim3(LA_THREADS), LA<N>::SMEM, s, m, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  e = launch_pdl(latent_merge_kernel, dim3((unsigned)(p.B * p.next_n * p.H)), dim3(MG_THREADS), 0, s, p);
   if (e != cudaSuccess || !p.weights) return e;
   count_launch();
-  return launch_pdl(latent_weights_kernel, dim3(p.max_pages, p.B), dim3(32 * LR_WARPS), 0, s, p);
+  return launch_pdl(latent_weights_kernel<N>, dim3(min(p.max_pages, ceil_div(16 * p.grid, p.B)), p.B), dim3(WT_THREADS),
+                    0, s, p);
+}
+
+cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
+  return p.n == 16 ? launch_n<16>(m, p, s) : p.n == 32 ? launch_n<32>(m, p, s) : launch_n<64>(m, p, s);
 }
 
 }  // namespace dsa
