@@ -364,13 +364,15 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Descriptor of an operand whose M (or N) axis is the contiguous one, in the
-// same 128-byte swizzled rows (64 bf16 of M per row, one row per K index): the
-// leading-byte offset is the distance between blocks of 64 along M, the
-// stride-byte offset that between groups of 8 along K (1024).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t block_bytes) {
-  return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(block_bytes >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Low words of descriptors for mma_bf16_ss, 128-byte swizzled rows of 64 bf16.
+// K-major (rows are M or N, K contiguous): the address.  MN-major (a row per K
+// index, M or N contiguous): the leading-byte offset is the distance between
+// blocks of 64 along M, the stride-byte offset that between groups of 8 along K.
+__device__ __forceinline__ uint32_t desc_lo_kmajor(uint32_t smem_addr) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+__device__ __forceinline__ uint32_t desc_lo_mnmajor(uint32_t smem_addr, uint32_t block_bytes) {
+  return ((smem_addr & 0x3FFFFu) >> 4) | ((block_bytes >> 4) << 16);
 }
 // Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits
 // 7-9, 10-12 = 1), bit 15 / 16 set where A / B has its M / N axis contiguous.
@@ -404,13 +406,34 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem], one M x N x 16 bf16 step.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+// 1 in the lane elect.sync picks, 0 in the others (the warp converged).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// D[tmem] (+)= A[smem] * B[smem], one M x N x 16 bf16 step, issued by the lane
+// with `leader` set; a and b are the low words of the descriptors (the high
+// word of a 128-byte swizzled one with 1024 bytes per group of 8 rows is a
+// constant).  The whole warp runs the code around it, so that addresses can
+// stay in uniform registers: in a single-lane branch each issue had to move
+// them there first and took 75-90 cycles, whatever the step's size.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
                                             uint32_t accumulate) {
+  constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
+      : "memory");
+}
+// The leader's commit: the mbarrier arrives once when all it issued completes.
+__device__ __forceinline__ void mma_commit_warp(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
       : "memory");
 }
 // mbarrier arrives once when every tcgen05 op this thread issued so far completes.

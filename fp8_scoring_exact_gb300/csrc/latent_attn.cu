@@ -38,7 +38,7 @@ namespace dsa {
 namespace {
 
 constexpr int LT = PAGE;                       // keys per tile
-constexpr int LA_WARPS = 6;
+constexpr int LA_WARPS = 7;
 constexpr int LA_THREADS = 32 * LA_WARPS;
 constexpr int LA_SM_THREADS = 128;             // softmax warps 2..5
 constexpr uint32_t CHUNK = LT * 128;           // 64 keys x 64 dims, bf16
@@ -58,10 +58,10 @@ struct LA {
   static constexpr uint32_t OFF_PAIR = (OFF_P + PBUFS * P_BYTES + 1023) / 1024 * 1024;
   static constexpr uint32_t OFF_KPE = OFF_PAIR + PAIRS * PAIR;
   static constexpr uint32_t OFF_MISC = OFF_KPE + KPES * CHUNK;
-  // barriers: pair full/empty, kpe full/empty, q full/empty, S full/empty x 2, P full x 2, PV done x 2, O empty, drain
+  // barriers: pair full/empty, kpe full/empty, q full/empty, S full/empty x 2, P full x 2, PV done x 2, O empty, drain x 2
   static constexpr int B_PF = 0, B_PE = PAIRS, B_KF = 2 * PAIRS, B_KE = B_KF + KPES, B_QF = B_KE + KPES, B_QE = B_QF + 1,
                        B_SF = B_QE + 1, B_SE = B_SF + 2, B_WF = B_SE + 2, B_VD = B_WF + 2, B_OE = B_VD + 2,
-                       B_DRAIN = B_OE + 1, N_BARS = B_DRAIN + 1;
+                       B_DRAIN = B_OE + 1, N_BARS = B_DRAIN + 2;
   static constexpr uint32_t OFF_BAR = OFF_MISC;
   static constexpr uint32_t OFF_RED = OFF_BAR + (N_BARS * 8 + 127) / 128 * 128;  // [4][N] floats
   static constexpr uint32_t OFF_REF = OFF_RED + 4 * N * 4;                       // [N] reference maxima
@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     }
     mbar_init(bar(C::B_OE), 4);
     mbar_init(bar(C::B_DRAIN), 1);
+    mbar_init(bar(C::B_DRAIN + 1), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -306,66 +307,66 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
-      constexpr uint32_t ID_S = idesc_bf16_f32(64, N, false, false);
-      constexpr uint32_t ID_O = idesc_bf16_f32(128, N, true, false);
-      bool ok = true;
-      // O^T (+)= V^T P^T of tile i; `first`: the piece's first, which overwrites
-      auto pv = [&](uint32_t i, bool first) {
-        const uint32_t pb = i % C::PBUFS;
-        if (!(ok = mbar_wait(bar(C::B_WF + (i & 1)), (i >> 1) & 1, abort_flag, p.stats))) return;
+    // --------------------------------------------------------- S^T issuer --
+    constexpr uint32_t ID_S = idesc_bf16_f32(64, N, false, false);
+    const uint32_t leader = elect_one();
+    const uint32_t q_lo = desc_lo_kmajor(sbase + C::OFF_Q);
+    bool ok = true;
+    while (ok && runs.next(p, w, k0, k1, whole)) {
+      if (!(ok = mbar_wait_warp(bar(C::B_QF), seg & 1, abort_flag, p.stats))) break;
+      for (int k = k0; ok && k < k1; ++k, ++it) {
+        const uint32_t sb = it & 1;
+        if (!(ok = mbar_wait_warp(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, p.stats))) break;
         tc_fence_after();
-        const uint64_t pd = sw128_kmajor_desc(sbase + C::OFF_P + pb * C::P_BYTES);
+        const uint32_t d = tmem + C::TMEM_S + sb * N;
         for (uint32_t c = 0; c < 4; ++c) {
-          const uint32_t st = (4 * i + c) % C::PAIRS;
-          const uint64_t vd = sw128_mnmajor_desc(sbase + C::OFF_PAIR + st * PAIR, CHUNK);
+          const uint32_t i = 4 * it + c, st = i % C::PAIRS;
+          if (!(ok = mbar_wait_warp(bar(C::B_PF + st), (i / C::PAIRS) & 1, abort_flag, p.stats))) break;
+          const uint32_t k_lo = desc_lo_kmajor(sbase + C::OFF_PAIR + st * PAIR);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 16 keys: 2 KB of V, 32 bytes of a P row
-            mma_bf16_ss(tmem + c * N, vd + 128 * k, pd + 2 * k, ID_O, !(first && k == 0));
-          mma_commit(bar(C::B_PE + st));
+          for (int j = 0; j < 8; ++j)
+            mma_bf16_ss(leader, d, k_lo + (j >> 2) * (CHUNK >> 4) + 2 * (j & 3),
+                        q_lo + (2 * c + (j >> 2)) * (N * 128 >> 4) + 2 * (j & 3), ID_S, c > 0 || j > 0);
         }
-        mma_commit(bar(C::B_VD + (i & 1)));
-      };
-      while (ok && runs.next(p, w, k0, k1, whole)) {
-        if (!(ok = mbar_wait(bar(C::B_QF), seg & 1, abort_flag, p.stats))) break;
-        for (int k = k0; ok && k < k1; ++k, ++it) {
-          const uint32_t sb = it & 1;
-          if (!(ok = mbar_wait(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, p.stats))) break;
-          tc_fence_after();
-          const uint32_t d = tmem + C::TMEM_S + sb * N;
-          const uint64_t qd = sw128_kmajor_desc(sbase + C::OFF_Q);
-          for (uint32_t c = 0; c < 4; ++c) {
-            const uint32_t i = 4 * it + c, st = i % C::PAIRS;
-            if (!(ok = mbar_wait(bar(C::B_PF + st), (i / C::PAIRS) & 1, abort_flag, p.stats))) break;
-            const uint64_t kd = sw128_kmajor_desc(sbase + C::OFF_PAIR + st * PAIR);
+        if (!ok) break;
+        const uint32_t st = it % C::KPES;
+        if (!(ok = mbar_wait_warp(bar(C::B_KF + st), (it / C::KPES) & 1, abort_flag, p.stats))) break;
+        const uint32_t k_lo = desc_lo_kmajor(sbase + C::OFF_KPE + st * CHUNK);
 #pragma unroll
-            for (int k2 = 0; k2 < 8; ++k2)
-              mma_bf16_ss(d, kd + (k2 >> 2) * (CHUNK >> 4) + 2 * (k2 & 3),
-                          qd + (2 * c + (k2 >> 2)) * (N * 128 >> 4) + 2 * (k2 & 3), ID_S, c > 0 || k2 > 0);
-          }
-          if (!ok) break;
-          const uint32_t st = it % C::KPES;
-          if (!(ok = mbar_wait(bar(C::B_KF + st), (it / C::KPES) & 1, abort_flag, p.stats))) break;
-          const uint64_t kd = sw128_kmajor_desc(sbase + C::OFF_KPE + st * CHUNK);
-#pragma unroll
-          for (int k2 = 0; k2 < 4; ++k2)
-            mma_bf16_ss(d, kd + 2 * k2, qd + 8 * (N * 128 >> 4) + 2 * k2, ID_S, 1);
-          mma_commit(bar(C::B_KE + st));
-          mma_commit(bar(C::B_SF + sb));
-          if (k == k1 - 1) mma_commit(bar(C::B_QE));
-          if (k == k0) {
-            // the previous piece's O^T has been read out
-            if (!(ok = mbar_wait(bar(C::B_OE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
-          } else {
-            pv(it - 1, k == k0 + 1);
-          }
-        }
-        if (ok) pv(it - 1, k1 == k0 + 1);
-        ++seg;
+        for (int j = 0; j < 4; ++j)
+          mma_bf16_ss(leader, d, k_lo + 2 * j, q_lo + 8 * (N * 128 >> 4) + 2 * j, ID_S, 1);
+        mma_commit_warp(leader, bar(C::B_KE + st));
+        mma_commit_warp(leader, bar(C::B_SF + sb));
+        if (k == k1 - 1) mma_commit_warp(leader, bar(C::B_QE));
       }
+      ++seg;
     }
-    __syncwarp();
+  } else if (warp == 6) {
+    // --------------------------------------------------------- O^T issuer --
+    // A warp of its own: a tile's weights are ready while the next tile's data
+    // are still on their way, and its slots should come free then.
+    constexpr uint32_t ID_O = idesc_bf16_f32(128, N, true, false);
+    const uint32_t leader = elect_one();
+    bool ok = true;
+    while (ok && runs.next(p, w, k0, k1, whole)) {
+      // the previous piece's O^T has been read out
+      if (!(ok = mbar_wait_warp(bar(C::B_OE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
+      for (int k = k0; k < k1; ++k, ++it) {
+        if (!(ok = mbar_wait_warp(bar(C::B_WF + (it & 1)), (it >> 1) & 1, abort_flag, p.stats))) break;
+        tc_fence_after();
+        const uint32_t p_lo = desc_lo_kmajor(sbase + C::OFF_P + (it % C::PBUFS) * C::P_BYTES);
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint32_t st = (4 * it + c) % C::PAIRS;
+          const uint32_t v_lo = desc_lo_mnmajor(sbase + C::OFF_PAIR + st * PAIR, CHUNK);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // 16 keys: 2 KB of V, 32 bytes of a P row
+            mma_bf16_ss(leader, tmem + c * N, v_lo + 128 * j, p_lo + 2 * j, ID_O, k > k0 || j > 0);
+          mma_commit_warp(leader, bar(C::B_PE + st));
+        }
+        mma_commit_warp(leader, bar(C::B_VD + (it & 1)));
+      }
+      ++seg;
+    }
   } else {
     // ----------------------------------------------------- softmax warps --
     // A wait that gives up does not leave the loop (the other warps of the
@@ -581,9 +582,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       for (uint32_t s = 0; s < C::KPES; ++s)
         if (n_kpe > s) mbar_drain(bar(C::B_KF + s), ((n_kpe - 1 - s) / C::KPES) & 1);
       if (n_q) mbar_drain(bar(C::B_QF), (n_q - 1) & 1);
-    } else if (warp == 1 && lane == 0) {
-      mma_commit(bar(C::B_DRAIN));
-      mbar_drain(bar(C::B_DRAIN), 0);
+    } else if (warp == 1 || warp == 6) {
+      const uint32_t db = bar(C::B_DRAIN + (warp == 6));
+      mma_commit_warp(elect_one(), db);  // (elect.sync picks the lane that issued: it is deterministic)
+      mbar_drain(db, 0);
     }
     __syncthreads();
   }
