@@ -60,10 +60,15 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
   const int b = blockIdx.x, tid = threadIdx.x;
   int L = p.seq_lens[b];
   if (L < 0 || L > (int64_t)p.max_pages * PAGE) {
-    if (tid == 0) atomicOr(p.status, ST_RANGE);
+    if (tid == 0) atomicOr(&p.status->now, ST_RANGE);
     L = 0;
   }
   __syncthreads();  // every thread has its length: new_lens may be seq_lens
+  if (L > p.budget)  // the pages the move reads and writes
+    for (int i = tid; i < ceil_div(L, PAGE); i += ES_THREADS) {
+      const int page = p.block_table[(int64_t)b * p.max_pages + i];
+      if (page < 0 || page >= p.num_pages) atomicOr(&p.status->now, ST_RANGE);
+    }
   const int n = min(L, p.budget);
   int32_t* kept = p.kept + (int64_t)b * p.budget;
   for (int i = n + tid; i < p.budget; i += ES_THREADS) kept[i] = -1;
@@ -115,15 +120,17 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
 __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParams p) {
   pdl_enter();
   const int b = blockIdx.y, col = blockIdx.x, tid = threadIdx.x;
+  if (b == 0 && col == 0 && tid == 0) {  // the call's last kernel
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
   const int L = p.old_lens[b], n = min(L, p.budget);
   if (L <= p.budget) return;
   const int32_t* kept = p.kept + (int64_t)b * p.budget;
   const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
   auto slot = [&](int s) -> int64_t {
     const int page = table[s / PAGE];
-    if (page >= 0 && page < p.num_pages) return (int64_t)page * PAGE + s % PAGE;
-    atomicOr(p.status, ST_RANGE);
-    return -1;
+    return page >= 0 && page < p.num_pages ? (int64_t)page * PAGE + s % PAGE : -1;  // (reported by the selection)
   };
   if (col == 9) {
     float* w = p.weights + (int64_t)b * p.ld_weights;

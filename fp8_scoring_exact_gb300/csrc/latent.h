@@ -17,15 +17,20 @@ constexpr int LA_DC = 512;             // compressed dims of a latent key (keys 
 constexpr int LA_DP = 64;              // its rope dims (keys only)
 constexpr int LA_DN = 128, LA_DV = 128;  // expanded form: no-rope key dims and value dims of a head
 
-// Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
-// 64) with the keys its rows see, cut into tiles of one page.  The items'
-// tiles are numbered through, and CTA c of the grid takes tiles [c per, (c + 1)
-// per): a run of them inside one item is a piece, whose id is item + c.
-struct LatentPlan {
-  int per, total;               // tiles per CTA, tiles in all
-  int prefix_len;               // validated
-  int items;
+// Status of a latent operator's call: its kernels OR into `now`; the last one
+// moves it to `last` and leaves `now` zero for the next call (also when the
+// call is replayed from a graph).
+struct LatentStatus {
+  int now, last;
 };
+
+// Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
+// 64) with the keys its rows see, cut into tiles of one page.  An item with
+// tiles counts LA_ITEM_UNITS units and one per tile; the items' units are
+// numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
+// tiles in one item are a piece, whose id is item + c.
+constexpr int LA_ITEM_UNITS = 2;  // what starting and ending a piece costs, in tiles
+constexpr int LA_MIN_UNITS = LA_ITEM_UNITS + 2;  // of a CTA
 
 // Process-wide options and the launch counter (api.cu).
 uint64_t option_wait_ns();
@@ -53,19 +58,17 @@ struct LatentAttnParams {
   float* lse;                   // [B, next_n, H]
   float* weights;               // [B, ld_weights] or null: += the softmax weight of every key
   int64_t ld_weights;
-  Stats* stats;
+  LatentStatus* status;
   // the call's row blocks and scratch
   int n;                        // rows per block
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
   int items, grid;
   uint64_t wait_ns;
-  LatentPlan* plan;
-  int32_t* start;               // [items + 1] first tile of each item
-  int32_t* first;               // [grid] item of each CTA's first tile
-  int32_t* lens;                // [B] validated lengths
+  int32_t* per;                 // [1] units per CTA
+  int32_t* start;               // [grid, items + 1] first unit of each item, worked out by every CTA for itself
   float* part_o;                // [items + grid, n, 512] unnormalised outputs of the pieces
   float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
-  float* logits;                // [tiles, 64, n] scaled logits (-inf: not seen), for the key weights
+  float* logits;                // [B, blocks, max_pages, 64, n] scaled logits (-inf: not seen), for the key weights
 };
 
 // Eviction in place: every sequence of more than `budget` keys keeps its last
@@ -84,7 +87,7 @@ struct EvictParams {
   int32_t* kept;                // [B, budget]
   int32_t* new_lens;            // [B]
   int32_t* old_lens;            // [B] scratch: the validated lengths (new_lens may be seq_lens itself)
-  int* status;
+  LatentStatus* status;
 };
 
 // Causal attention of a ragged batch in the expanded form (a key of a head:
@@ -97,7 +100,7 @@ struct PrefillParams {
   float scale_log2;
   __nv_bfloat16* out;           // [Tq, H, 128]
   float* lse;                   // [Tq, H]
-  int* status;
+  LatentStatus* status;
 };
 
 // Tensor maps of cached attention: queries [rows, 512] and [rows, 64], caches

@@ -16,8 +16,8 @@ using namespace dsa;
 
 namespace {
 
-// Scratch of one (device, stream): the status word in its first 256 bytes,
-// then what the call lays out.  A buffer that has become too small is kept
+// Scratch of one (device, stream): the status in its first 256 bytes, then
+// what the call lays out.  A buffer that has become too small is kept
 // until dsa_indexer_release: a captured graph may still hold its address, and
 // growing by half at least bounds what is kept to twice the last size.
 struct Scratch {
@@ -29,28 +29,29 @@ std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
 constexpr size_t HEAD = 256;
-static_assert(sizeof(Stats) <= HEAD, "the status block is the head");
+static_assert(sizeof(LatentStatus) <= HEAD, "the status is the head");
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Scratch with room for `need` bytes past the head; `zero`: its status block
-// is zeroed on the stream (else the call's first kernel writes it).  Null on
-// an error.
-uint8_t* get_scratch(cudaStream_t stream, size_t need, bool zero) {
+// Scratch with room for `need` bytes, the status first.  Null on an error.
+uint8_t* get_scratch(cudaStream_t stream, size_t need) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   Scratch& a = g_scratch[{dev, stream}];
-  if (a.cap < HEAD + need) {
-    const size_t want = align_up(std::max(HEAD + need, a.cap + a.cap / 2), 1 << 20);
+  if (a.cap < need) {
+    const size_t want = align_up(std::max(need, a.cap + a.cap / 2), 1 << 20);
     uint8_t* p = nullptr;
     if (cudaMalloc(&p, want) != cudaSuccess) {
       cudaGetLastError();
+      return nullptr;
+    }
+    if (cudaMemsetAsync(p, 0, HEAD, stream) != cudaSuccess) {
+      cudaFree(p);
       return nullptr;
     }
     if (a.base) a.outgrown.push_back(a.base);
     a.base = p;
     a.cap = want;
   }
-  if (zero && cudaMemsetAsync(a.base, 0, HEAD, stream) != cudaSuccess) return nullptr;
   return a.base;
 }
 
@@ -118,7 +119,7 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   p.prefix_items = p.prefix_table ? (int)((rows + p.n - 1) / p.n) : 0;
   p.items = p.prefix_items + p.B * p.blocks;
   p.grid = std::min(option_grid(), 1024);
-  if ((int64_t)p.items * std::max(p.max_pages, p.prefix_pages) >= (1ll << 31) - (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  if ((int64_t)p.items * (std::max(p.max_pages, p.prefix_pages) + LA_ITEM_UNITS) >= (1ll << 31) - (1 << 20)) return DSA_ERR_UNSUPPORTED;
   p.wait_ns = option_wait_ns();
   LatentMaps m;
   const int64_t slots = (int64_t)p.num_pages * PAGE;
@@ -133,17 +134,15 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
     return o;
   };
   const size_t pieces = (size_t)p.items + p.grid;
-  const size_t o_plan = take(sizeof(LatentPlan)), o_start = take(4 * ((size_t)p.items + 1)), o_first = take(4 * p.grid),
-               o_lens = take(4 * (size_t)p.B), o_ml = take(8 * pieces * p.n), o_po = take(4 * pieces * p.n * LA_DC),
+  const size_t o_per = take(4), o_start = take(4 * ((size_t)p.items + 1) * p.grid), o_ml = take(8 * pieces * p.n),
+               o_po = take(4 * pieces * p.n * LA_DC),
                o_log = p.weights ? take(4 * (size_t)p.B * p.blocks * p.max_pages * PAGE * p.n) : 0;
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, off, false);
+  uint8_t* base = get_scratch(stream, off);
   if (!base) return DSA_ERR_CUDA;
-  p.stats = reinterpret_cast<Stats*>(base);
-  p.plan = reinterpret_cast<LatentPlan*>(base + o_plan);
+  p.status = reinterpret_cast<LatentStatus*>(base);
+  p.per = reinterpret_cast<int32_t*>(base + o_per);
   p.start = reinterpret_cast<int32_t*>(base + o_start);
-  p.first = reinterpret_cast<int32_t*>(base + o_first);
-  p.lens = reinterpret_cast<int32_t*>(base + o_lens);
   p.part_ml = reinterpret_cast<float2*>(base + o_ml);
   p.part_o = reinterpret_cast<float*>(base + o_po);
   p.logits = p.weights ? reinterpret_cast<float*>(base + o_log) : nullptr;
@@ -242,7 +241,7 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, (size_t)B * 4, true);
+  uint8_t* base = get_scratch(stream, HEAD + (size_t)B * 4);
   if (!base) return DSA_ERR_CUDA;
   EvictParams p{};
   p.ckv = reinterpret_cast<uint8_t*>(ckv);
@@ -263,7 +262,7 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   p.kept = kept;
   p.new_lens = new_lens;
   p.old_lens = reinterpret_cast<int32_t*>(base + HEAD);
-  p.status = reinterpret_cast<int*>(base);
+  p.status = reinterpret_cast<LatentStatus*>(base);
   return launch_evict(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -284,7 +283,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, 0, true);
+  uint8_t* base = get_scratch(stream, HEAD);
   if (!base) return DSA_ERR_CUDA;
   PrefillParams p{};
   p.q = bf(q);
@@ -308,7 +307,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.status = reinterpret_cast<int*>(base);
+  p.status = reinterpret_cast<LatentStatus*>(base);
   return launch_prefill(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -320,8 +319,9 @@ int dsa_latent_last_status(dsa_stream_t stream_) {
   std::lock_guard<std::mutex> lk(g_mu);
   auto it = g_scratch.find({dev, stream});
   if (it == g_scratch.end() || !it->second.base) return DSA_OK;
-  int st = 0;
-  if (cudaMemcpy(&st, it->second.base, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
+  LatentStatus s;
+  if (cudaMemcpy(&s, it->second.base, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
+  const int st = s.last;
   if (st & ST_TIMEOUT) return DSA_ERR_TIMEOUT;
   return (st & ST_RANGE) ? DSA_ERR_RANGE : DSA_OK;
 }

@@ -38,15 +38,18 @@ namespace dsa {
 namespace {
 
 constexpr int LT = PAGE;                       // keys per tile
-constexpr int LA_WARPS = 7;
-constexpr int LA_THREADS = 32 * LA_WARPS;
-constexpr int LA_SM_THREADS = 128;             // softmax warps 2..5
 constexpr uint32_t CHUNK = LT * 128;           // 64 keys x 64 dims, bf16
 constexpr uint32_t PAIR = 2 * CHUNK;           // 64 keys x 128 dims
 constexpr float RESCALE_AT = 8.f;              // a row's reference moves when its maximum passes it by this
 
 template <int N>
 struct LA {
+  // Softmax warps: four (a quarter of the TMEM lanes each), for 64 rows eight
+  // (half the rows each), as there the softmax of a tile takes as long as its products.
+  static constexpr int SW = N == 64 ? 8 : 4, ST = 32 * SW;
+  static constexpr int NC = N * 4 / SW;                    // rows per softmax warp
+  static constexpr int W_PV = 2 + SW;                      // the last warp issues the second product
+  static constexpr int THREADS = 32 * (W_PV + 1);
   // Ring depths: what 227 KB leave next to the query block.  64 rows keep
   // two tiles of ckv and one of the rope part, and one weight buffer.
   static constexpr int PAIRS = N == 64 ? 8 : N == 32 ? 10 : 11;
@@ -67,8 +70,9 @@ struct LA {
   static constexpr uint32_t OFF_REF = OFF_RED + 4 * N * 4;                       // [N] reference maxima
   static constexpr uint32_t OFF_ALPHA = OFF_REF + N * 4;                         // [N] factors
   static constexpr uint32_t OFF_LIM = OFF_ALPHA + N * 4;                         // [N] visible keys per row
-  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base, rescale
-  static constexpr uint32_t SMEM = OFF_FLAG + 32 + 1024;                         // + alignment
+  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base, rescale, scan
+  static constexpr uint32_t OFF_STAT = OFF_FLAG + 128;                           // Stats: this CTA's status and wait limit
+  static constexpr uint32_t SMEM = OFF_STAT + 128 + 1024;                        // + alignment
   static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer
   static constexpr uint32_t TMEM_COLS = N == 64 ? 512 : N == 32 ? 256 : 128;     // 6 N, to a power of two
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
@@ -86,6 +90,40 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t addr, const uint32_t* r) {
                : "memory");
 }
 
+// Length of sequence b, and of the prefix; an invalid one counts as 0.
+__device__ __forceinline__ int valid_len(int len, int pages, bool& bad) {
+  bad = len < 0 || len > (int64_t)pages * PAGE;
+  return bad ? 0 : len;
+}
+
+// Reduces a[i] over the lanes that differ in bits 2..4 (the keys of a warp):
+// each step halves what a lane holds and the lanes a row is spread over.  A
+// lane ends with the row own_row() of its warp's, in a[0].
+template <int n, class Op>
+__device__ __forceinline__ void over_keys(float (&a)[n], int lane, Op op) {
+  int h = n;
+#pragma unroll
+  for (int o = 16; o >= 4; o >>= 1) {
+    if (h > 1) {
+      h >>= 1;
+      const bool up = lane & o;
+#pragma unroll
+      for (int i = 0; i < h; ++i) {
+        const float keep = up ? a[i + h] : a[i], send = up ? a[i] : a[i + h];
+        a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      }
+    } else {
+      a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], o));
+    }
+  }
+}
+template <int n>
+__device__ __forceinline__ int own_row(int lane) {
+  static_assert(n == 8 || n == 4, "NC = 32 or 16");
+  const int i = n == 8 ? (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1) : (lane >> 4 & 1) * 2 + (lane >> 3 & 1);
+  return 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
+}
+
 // One item: a block of rows and the keys they see.
 struct Item {
   int row0, nrows;         // flat query rows
@@ -96,10 +134,11 @@ struct Item {
 };
 __device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
   Item it;
+  bool bad;
   if (w < p.prefix_items) {
     it.row0 = w * p.n;
     it.nrows = min(p.n, p.B * p.next_n * p.H - it.row0);
-    it.len = it.lim0 = p.plan->prefix_len;
+    it.len = it.lim0 = valid_len(*p.prefix_len, p.prefix_pages, bad);
     it.r0 = -1;
     it.table = p.prefix_table;
     return it;
@@ -108,74 +147,58 @@ __device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
   it.r0 = j * p.n;
   it.row0 = b * R + it.r0;
   it.nrows = min(p.n, R - it.r0);
-  it.len = p.lens[b];
+  it.len = valid_len(p.seq_lens[b], p.max_pages, bad);
   it.lim0 = max(0, it.len - p.next_n + 1 + it.r0 / p.H);
   it.table = p.block_table + (int64_t)b * p.max_pages;
   return it;
 }
 
-// The runs of one CTA's tiles: next() gives item w and its tiles [k0, k1).
+// The pieces of one CTA: next() gives item w and its tiles [k0, k1).
 struct Runs {
+  const int32_t* start;
   int t, t1, w;
-  __device__ __forceinline__ Runs(const LatentAttnParams& p) {
-    const int per = p.plan->per;
-    t = min(p.plan->total, (int)blockIdx.x * per);
-    t1 = min(p.plan->total, t + per);
-    w = t < t1 ? p.first[blockIdx.x] : 0;
-  }
-  __device__ __forceinline__ bool next(const LatentAttnParams& p, int& item, int& k0, int& k1, bool& whole) {
-    if (t >= t1) return false;
-    int s0 = p.start[w], s1 = p.start[w + 1];
-    while (s1 <= t) {
-      ++w;
-      s0 = s1;
-      s1 = p.start[w + 1];
+  __device__ __forceinline__ bool next(int& item, int& k0, int& k1, bool& whole) {
+    for (;;) {
+      if (t >= t1) return false;
+      int s0 = start[w], s1 = start[w + 1];
+      while (s1 <= t) {
+        ++w;
+        s0 = s1;
+        s1 = start[w + 1];
+      }
+      const int u1 = min(t1, s1) - s0;
+      item = w;
+      k0 = max(0, t - s0 - LA_ITEM_UNITS);
+      k1 = max(0, u1 - LA_ITEM_UNITS);
+      whole = k0 == 0 && u1 == s1 - s0;
+      t = s0 + u1;
+      if (k1 > k0) return true;  // (a run may end before an item's first tile)
     }
-    item = w;
-    k0 = t - s0;
-    k1 = min(t1, s1) - s0;
-    whole = k0 == 0 && k1 == s1 - s0;
-    t = s0 + k1;
-    return true;
   }
 };
 
-}  // namespace
-
-// Lengths checked, items numbered: start[w], every CTA's first item, the status block.
-constexpr int PLAN_THREADS = 1024;
-__global__ void __launch_bounds__(PLAN_THREADS) latent_plan_kernel(const LatentAttnParams p) {
-  pdl_enter();
-  __shared__ int tmp[32];
-  __shared__ int s_status;
+// Numbers the items' units (start[]), the same in every CTA; returns this
+// CTA's units and first item.  tmp: 34 ints of shared memory.
+template <int THREADS>
+__device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, int* status) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_status = 0;
-  __syncthreads();
-  int pre = 0;
-  if (p.prefix_items) {
-    pre = *p.prefix_len;
-    if (pre < 0 || pre > (int64_t)p.prefix_pages * PAGE) {
-      atomicOr(&s_status, ST_RANGE);
-      pre = 0;
-    }
-  }
+  int32_t* start = p.start + (int64_t)blockIdx.x * (p.items + 1);
+  bool bad = false;
+  const int pre = p.prefix_items ? valid_len(*p.prefix_len, p.prefix_pages, bad) : 0;
+  if (bad) atomicOr(status, ST_RANGE);
   int base = 0;
-  for (int i0 = 0; i0 < p.items; i0 += PLAN_THREADS) {
+  for (int i0 = 0; i0 < p.items; i0 += THREADS) {
     const int w = i0 + tid;
-    int tiles = 0;
-    if (w < p.prefix_items) {
-      tiles = ceil_div(pre, LT);
-    } else if (w < p.items) {
-      const int v = w - p.prefix_items, b = v / p.blocks;
-      int len = p.seq_lens[b];
-      if (len < 0 || len > (int64_t)p.max_pages * PAGE) {
-        atomicOr(&s_status, ST_RANGE);
-        len = 0;
+    int units = 0;
+    if (w < p.items) {
+      int len = pre;
+      if (w >= p.prefix_items) {
+        len = valid_len(p.seq_lens[(w - p.prefix_items) / p.blocks], p.max_pages, bad);
+        if (bad) atomicOr(status, ST_RANGE);
       }
-      if (v % p.blocks == 0) p.lens[b] = len;
-      tiles = ceil_div(len, LT);
+      units = len ? ceil_div(len, LT) + LA_ITEM_UNITS : 0;
     }
-    int x = tiles;
+    int x = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -185,40 +208,35 @@ __global__ void __launch_bounds__(PLAN_THREADS) latent_plan_kernel(const LatentA
     if (lane == 31) tmp[warp] = x;
     __syncthreads();
     int before = 0, all = 0;
-    for (int i = 0; i < 32; ++i) {
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
       const int v = tmp[i];
-      if (i < warp) before += v;
+      before += i < warp ? v : 0;
       all += v;
     }
-    if (w < p.items) p.start[w] = base + before + x - tiles;
+    if (w < p.items) start[w] = base + before + x - units;
     base += all;
   }
-  // at least two tiles per CTA: a shorter run costs more in pieces to join
-  // than its parallelism saves
-  const int per = max(2, ceil_div(base, p.grid));
+  const int per = max(LA_MIN_UNITS, ceil_div(base, p.grid));
+  const int t = min((int64_t)base, (int64_t)blockIdx.x * per);
   if (tid == 0) {
-    p.start[p.items] = base;
-    p.plan->per = per;
-    p.plan->total = base;
-    p.plan->prefix_len = pre;
-    p.plan->items = p.items;
-    p.stats->wait_ns = p.wait_ns;
+    start[p.items] = base;
+    tmp[33] = 0;
+    if (blockIdx.x == 0) *p.per = per;
   }
-  __syncthreads();  // start[] is written (read back by this CTA only below)
-  if (tid == 0) p.stats->status = s_status;
-  for (int w = tid; w < p.items; w += PLAN_THREADS) {
-    const int s0 = p.start[w], s1 = p.start[w + 1];
-    for (int c = ceil_div(s0, per); c < p.grid && (int64_t)c * per < s1; ++c) p.first[c] = w;
-  }
+  __syncthreads();
+  for (int w = tid; w < p.items; w += THREADS)
+    if (start[w] <= t && t < start[w + 1]) tmp[33] = w;  // one item at most
+  __syncthreads();
+  return Runs{start, t, min(base, t + per), tmp[33]};
 }
 
+}  // namespace
+
 template <int N>
-__global__ void __launch_bounds__(LA_THREADS, 1)
+__global__ void __launch_bounds__(LA<N>::THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentMaps maps, const LatentAttnParams p) {
   using C = LA<N>;
-  pdl_enter();
-  if ((int64_t)blockIdx.x * p.plan->per >= p.plan->total) return;  // uniform over the CTA: no tiles
-
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -231,18 +249,28 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG + 4);
   volatile int* s_resc = reinterpret_cast<int*>(smem + C::OFF_FLAG + 8);  // [2]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Stats* stats = reinterpret_cast<Stats*>(smem + C::OFF_STAT);
 
+  // before the wait for the previous kernel of the stream: barriers, TMEM
+  // and the tensor maps (the call's own inputs are read after it)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     s_resc[0] = s_resc[1] = 0;
+    stats->status = 0;
+    stats->wait_ns = p.wait_ns;
+    tma_prefetch_desc(&maps.q_nope);
+    tma_prefetch_desc(&maps.q_pe);
+    tma_prefetch_desc(&maps.ckv);
+    tma_prefetch_desc(&maps.kpe);
     for (int i = 0; i < 2 * C::PAIRS + 2 * C::KPES + 2; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_SF + i), 1);
-      mbar_init(bar(C::B_SE + i), 4);
-      mbar_init(bar(C::B_WF + i), 4);
+      mbar_init(bar(C::B_SE + i), C::SW);
+      mbar_init(bar(C::B_WF + i), C::SW);
       mbar_init(bar(C::B_VD + i), 1);
     }
-    mbar_init(bar(C::B_OE), 4);
+    mbar_init(bar(C::B_OE), C::SW);
     mbar_init(bar(C::B_DRAIN), 1);
     mbar_init(bar(C::B_DRAIN + 1), 1);
     fence_mbar_init();
@@ -252,22 +280,25 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  // (the scan's scratch lies in the exchange buffer of the softmax)
+  Runs runs = plan_runs<C::THREADS>(p, reinterpret_cast<int*>(smem + C::OFF_RED), &stats->status);
+  __syncthreads();
   uint32_t it = 0;       // this CTA's tiles so far
   uint32_t seg = 0;      // and its pieces
   uint32_t n_pair = 0, n_kpe = 0, n_q = 0;  // producer: copies armed
-  Runs runs(p);
   int w, k0, k1;
   bool whole;
 
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer --
     bool ok = true;
-    while (ok && runs.next(p, w, k0, k1, whole)) {
+    while (ok && runs.next(w, k0, k1, whole)) {
       const Item im = load_item(p, w);
-      if (!(ok = mbar_wait_warp(bar(C::B_QE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
+      if (!(ok = mbar_wait_warp(bar(C::B_QE), (seg & 1) ^ 1, abort_flag, stats))) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(C::B_QF), 9 * N * 128);
         tma_load_3d(sbase + C::OFF_Q, &maps.q_nope, 0, im.row0, 0, bar(C::B_QF));
@@ -285,25 +316,24 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             bad = pages < 0 || pages >= p.num_pages;
             if (bad) pages = p.num_pages;
           }
-          if (__ballot_sync(0xffffffffu, bad) && lane == 0) atomicOr(&p.stats->status, ST_RANGE);
+          if (__ballot_sync(0xffffffffu, bad) && lane == 0) atomicOr(&stats->status, ST_RANGE);
         }
         const int slot = __shfl_sync(0xffffffffu, pages, k & 31) * PAGE;
+        const int ks = n_kpe % C::KPES;
+        if (!(ok = mbar_wait_warp(bar(C::B_KE + ks), ((n_kpe / C::KPES) & 1) ^ 1, abort_flag, stats))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(C::B_KF + ks), CHUNK);
+          tma_load_2d(sbase + C::OFF_KPE + ks * CHUNK, &maps.kpe, 0, slot, bar(C::B_KF + ks));
+        }
+        ++n_kpe;
         for (int c = 0; c < 4; ++c, ++n_pair) {
           const int st = n_pair % C::PAIRS;
-          if (!(ok = mbar_wait_warp(bar(C::B_PE + st), ((n_pair / C::PAIRS) & 1) ^ 1, abort_flag, p.stats))) break;
+          if (!(ok = mbar_wait_warp(bar(C::B_PE + st), ((n_pair / C::PAIRS) & 1) ^ 1, abort_flag, stats))) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(bar(C::B_PF + st), PAIR);
             tma_load_3d(sbase + C::OFF_PAIR + st * PAIR, &maps.ckv, 0, slot, 2 * c, bar(C::B_PF + st));
           }
         }
-        if (!ok) break;
-        const int st = n_kpe % C::KPES;
-        if (!(ok = mbar_wait_warp(bar(C::B_KE + st), ((n_kpe / C::KPES) & 1) ^ 1, abort_flag, p.stats))) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(C::B_KF + st), CHUNK);
-          tma_load_2d(sbase + C::OFF_KPE + st * CHUNK, &maps.kpe, 0, slot, bar(C::B_KF + st));
-        }
-        ++n_kpe;
       }
     }
   } else if (warp == 1) {
@@ -312,47 +342,48 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     const uint32_t leader = elect_one();
     const uint32_t q_lo = desc_lo_kmajor(sbase + C::OFF_Q);
     bool ok = true;
-    while (ok && runs.next(p, w, k0, k1, whole)) {
-      if (!(ok = mbar_wait_warp(bar(C::B_QF), seg & 1, abort_flag, p.stats))) break;
+    while (ok && runs.next(w, k0, k1, whole)) {
+      if (!(ok = mbar_wait_warp(bar(C::B_QF), seg & 1, abort_flag, stats))) break;
       for (int k = k0; ok && k < k1; ++k, ++it) {
         const uint32_t sb = it & 1;
-        if (!(ok = mbar_wait_warp(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, p.stats))) break;
+        if (!(ok = mbar_wait_warp(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, stats))) break;
         tc_fence_after();
         const uint32_t d = tmem + C::TMEM_S + sb * N;
+        // the rope part first, so that its slot comes free first
+        const uint32_t ks = it % C::KPES;
+        if (!(ok = mbar_wait_warp(bar(C::B_KF + ks), (it / C::KPES) & 1, abort_flag, stats))) break;
+        const uint32_t e_lo = desc_lo_kmajor(sbase + C::OFF_KPE + ks * CHUNK);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_bf16_ss(leader, d, e_lo + 2 * j, q_lo + 8 * (N * 128 >> 4) + 2 * j, ID_S, j > 0);
+        mma_commit_warp(leader, bar(C::B_KE + ks));
         for (uint32_t c = 0; c < 4; ++c) {
           const uint32_t i = 4 * it + c, st = i % C::PAIRS;
-          if (!(ok = mbar_wait_warp(bar(C::B_PF + st), (i / C::PAIRS) & 1, abort_flag, p.stats))) break;
+          if (!(ok = mbar_wait_warp(bar(C::B_PF + st), (i / C::PAIRS) & 1, abort_flag, stats))) break;
           const uint32_t k_lo = desc_lo_kmajor(sbase + C::OFF_PAIR + st * PAIR);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             mma_bf16_ss(leader, d, k_lo + (j >> 2) * (CHUNK >> 4) + 2 * (j & 3),
-                        q_lo + (2 * c + (j >> 2)) * (N * 128 >> 4) + 2 * (j & 3), ID_S, c > 0 || j > 0);
+                        q_lo + (2 * c + (j >> 2)) * (N * 128 >> 4) + 2 * (j & 3), ID_S, 1);
         }
         if (!ok) break;
-        const uint32_t st = it % C::KPES;
-        if (!(ok = mbar_wait_warp(bar(C::B_KF + st), (it / C::KPES) & 1, abort_flag, p.stats))) break;
-        const uint32_t k_lo = desc_lo_kmajor(sbase + C::OFF_KPE + st * CHUNK);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mma_bf16_ss(leader, d, k_lo + 2 * j, q_lo + 8 * (N * 128 >> 4) + 2 * j, ID_S, 1);
-        mma_commit_warp(leader, bar(C::B_KE + st));
         mma_commit_warp(leader, bar(C::B_SF + sb));
         if (k == k1 - 1) mma_commit_warp(leader, bar(C::B_QE));
       }
       ++seg;
     }
-  } else if (warp == 6) {
+  } else if (warp == C::W_PV) {
     // --------------------------------------------------------- O^T issuer --
     // A warp of its own: a tile's weights are ready while the next tile's data
     // are still on their way, and its slots should come free then.
     constexpr uint32_t ID_O = idesc_bf16_f32(128, N, true, false);
     const uint32_t leader = elect_one();
     bool ok = true;
-    while (ok && runs.next(p, w, k0, k1, whole)) {
+    while (ok && runs.next(w, k0, k1, whole)) {
       // the previous piece's O^T has been read out
-      if (!(ok = mbar_wait_warp(bar(C::B_OE), (seg & 1) ^ 1, abort_flag, p.stats))) break;
+      if (!(ok = mbar_wait_warp(bar(C::B_OE), (seg & 1) ^ 1, abort_flag, stats))) break;
       for (int k = k0; k < k1; ++k, ++it) {
-        if (!(ok = mbar_wait_warp(bar(C::B_WF + (it & 1)), (it >> 1) & 1, abort_flag, p.stats))) break;
+        if (!(ok = mbar_wait_warp(bar(C::B_WF + (it & 1)), (it >> 1) & 1, abort_flag, stats))) break;
         tc_fence_after();
         const uint32_t p_lo = desc_lo_kmajor(sbase + C::OFF_P + (it % C::PBUFS) * C::P_BYTES);
         for (uint32_t c = 0; c < 4; ++c) {
@@ -373,27 +404,28 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
     // exchange would wait for ever): with the abort flag set every later
     // wait returns at once, and the result is undefined but complete.
     const int q = warp & 3;                  // TMEM lane quarter: keys [16 q, + 16)
-    const int st_id = threadIdx.x - 64;      // 0 .. 127
-    const int g = lane >> 2, cc = 2 * (lane & 3);
-    constexpr int M8 = N / 8;                // blocks of 8 rows
+    const int half = (warp - 2) >> 2;        // rows [NC half, + NC)
+    const int st_id = threadIdx.x - 64;      // 0 .. ST - 1
+    const int g = lane >> 2, cb = half * C::NC, cc = cb + 2 * (lane & 3);
+    constexpr int M8 = C::NC / 8;            // blocks of 8 rows
+    constexpr int HALVES = C::SW / 4;
     float ref = neg_inf();                   // threads st_id < N: the reference maximum of row st_id
-    while (runs.next(p, w, k0, k1, whole)) {
+    while (runs.next(w, k0, k1, whole)) {
       const Item im = load_item(p, w);
-      for (int c = st_id; c < N; c += LA_SM_THREADS)
+      for (int c = st_id; c < N; c += C::ST)
         s_lim[c] = c >= im.nrows ? 0 : im.r0 < 0 ? im.len : max(0, im.len - p.next_n + 1 + (im.r0 + c) / p.H);
-      float l[M8][2];                        // this thread's part of each row's sum
+      float l[2 * M8];                       // this thread's part of each row's sum
 #pragma unroll
-      for (int m = 0; m < M8; ++m) l[m][0] = l[m][1] = 0.f;
+      for (int i = 0; i < 2 * M8; ++i) l[i] = 0.f;
       ref = neg_inf();
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it & 1;
-        mbar_wait_warp(bar(C::B_SF + sb), (it >> 1) & 1, abort_flag, p.stats);
+        mbar_wait_warp(bar(C::B_SF + sb), (it >> 1) & 1, abort_flag, stats);
         tc_fence_after();
         uint32_t s[4 * M8];
-        const uint32_t sa = tmem + C::TMEM_S + sb * N + ((uint32_t)(32 * q) << 16);
-        if constexpr (N == 64) tmem_ld16x256b_x8(sa, s);
-        if constexpr (N == 32) tmem_ld16x256b_x4(sa, s);
-        if constexpr (N == 16) tmem_ld16x256b_x2(sa, s);
+        const uint32_t sa = tmem + C::TMEM_S + sb * N + cb + ((uint32_t)(32 * q) << 16);
+        if constexpr (M8 == 4) tmem_ld16x256b_x4(sa, s);
+        if constexpr (M8 == 2) tmem_ld16x256b_x2(sa, s);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
@@ -402,21 +434,20 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         // in the tile itself (a weight of 0 does not silence a NaN)
         const int valid = im.len - k * LT;
         if (valid < LT) {
-          for (int i = st_id; i < (LT - valid) * 64; i += LA_SM_THREADS) {
+          for (int i = st_id; i < (LT - valid) * 64; i += C::ST) {
             const int row = valid + (i >> 6), ch = (i >> 3) & 7, x = i & 7;  // row, chunk of 64 dims, 16 bytes
             const uint32_t ps = (4 * it + (ch >> 1)) % C::PAIRS;
             *reinterpret_cast<uint4*>(smem + C::OFF_PAIR + ps * PAIR + (ch & 1) * CHUNK + row * 128 + 16 * x) =
                 make_uint4(0, 0, 0, 0);
           }
         }
-        // u of rows 8 m + cc + {0, 1}, keys 16 q + g and + 8
+        // logits of rows 8 m + cc + {0, 1}, keys 16 q + g and + 8
         float u[M8][4];
 #pragma unroll
-        for (int i = 0; i < 4 * M8; ++i) u[i >> 2][i & 3] = __uint_as_float(s[i]) * p.scale_log2;
+        for (int i = 0; i < 4 * M8; ++i) u[i >> 2][i & 3] = __uint_as_float(s[i]);
         const int key = k * LT + 16 * q + g;
         if ((k + 1) * LT > im.lim0 || im.nrows < N) {
-          __syncwarp();
-          named_bar_sync(1, LA_SM_THREADS);  // s_lim
+          named_bar_sync(1, C::ST);  // s_lim
 #pragma unroll
           for (int m = 0; m < M8; ++m)
 #pragma unroll
@@ -427,31 +458,22 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
             }
         }
         if (p.logits) {
-          float* dst = p.logits + ((int64_t)(p.start[w] + k) * LT + 16 * q + g) * N + cc;
+          float* dst = p.logits + (((int64_t)w * p.max_pages + k) * LT + 16 * q + g) * N + cc;
 #pragma unroll
           for (int m = 0; m < M8; ++m) {
-            *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(u[m][0], u[m][1]);
-            *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2], u[m][3]);
+            *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(u[m][0] * p.scale_log2, u[m][1] * p.scale_log2);
+            *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2] * p.scale_log2, u[m][3] * p.scale_log2);
           }
         }
-        // maximum over the warp's 16 keys: three steps that halve the rows a
-        // lane holds while they halve the lanes a row is spread over
         float mx[2 * M8];
 #pragma unroll
         for (int i = 0; i < 2 * M8; ++i) mx[i] = fmaxf(u[i >> 1][i & 1], u[i >> 1][2 + (i & 1)]);
-#pragma unroll
-        for (int i = 0; i < 2 * M8; ++i) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-        }
-        if (g == 0) {
-#pragma unroll
-          for (int m = 0; m < M8; ++m)
-            *reinterpret_cast<float2*>(&s_red[q * N + 8 * m + cc]) = make_float2(mx[2 * m], mx[2 * m + 1]);
-        }
-        named_bar_sync(1, LA_SM_THREADS);
+        over_keys<2 * M8>(mx, lane, [](float a, float b) { return fmaxf(a, b); });
+        s_red[q * N + own_row<2 * M8>(lane) + cb] = mx[0];
+        named_bar_sync(1, C::ST);
         if (st_id < N) {
-          const float top = fmaxf(fmaxf(s_red[st_id], s_red[N + st_id]), fmaxf(s_red[2 * N + st_id], s_red[3 * N + st_id]));
+          const float top = p.scale_log2 * fmaxf(fmaxf(s_red[st_id], s_red[N + st_id]),
+                                                 fmaxf(s_red[2 * N + st_id], s_red[3 * N + st_id]));
           float a = 1.f;
           if (top > ref + RESCALE_AT || (ref == neg_inf() && top > ref)) {
             a = ex2(ref - top);  // 0 from a reference of -inf
@@ -461,58 +483,57 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           s_alpha[st_id] = a;
           s_ref[st_id] = ref == neg_inf() ? 0.f : ref;
         }
-        named_bar_sync(1, LA_SM_THREADS);
+        named_bar_sync(1, C::ST);
         const bool rescale = s_resc[sb] != 0;
         if (st_id == 0) s_resc[sb ^ 1] = 0;  // the next tile's flag: set after the next barrier at the earliest
-        if (C::PBUFS == 1) {
-          if (it > 0) mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
-        } else if (it > 1) {
-          mbar_wait_warp(bar(C::B_VD + sb), ((it - 2) >> 1) & 1, abort_flag, p.stats);
-        }
+        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
+        // the MMA wants of both operands) for P
         if (rescale) {
 #pragma unroll
-          for (int m = 0; m < M8; ++m) {
-            l[m][0] *= s_alpha[8 * m + cc];
-            l[m][1] *= s_alpha[8 * m + cc + 1];
-          }
-          if (k > k0) {  // O^T: four blocks of 128 dims, this warp's 32 lanes of each
-            mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
-            tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < 4 * N / 16; ++j) {
-              uint32_t o[16];
-              const uint32_t oa = tmem + 16 * j + ((uint32_t)(32 * q) << 16);
-              tmem_ld16(oa, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * s_alpha[(16 * j + i) % N]);
-              tmem_st16(oa, o);
-            }
-            tmem_wait_st();
-          }
+          for (int i = 0; i < 2 * M8; ++i) l[i] *= s_alpha[8 * (i >> 1) + cc + (i & 1)];
         }
-        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
-        // the MMA wants of both operands) into P [row][key]
+        uint32_t r[M8][2];
+#pragma unroll
+        for (int m = 0; m < M8; ++m) {
+          const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * m + cc]);
+          const float a0 = ex2(fmaf(u[m][0], p.scale_log2, -f.x)), a1 = ex2(fmaf(u[m][1], p.scale_log2, -f.y));
+          const float b0 = ex2(fmaf(u[m][2], p.scale_log2, -f.x)), b1 = ex2(fmaf(u[m][3], p.scale_log2, -f.y));
+          l[2 * m] += a0 + b0;
+          l[2 * m + 1] += a1 + b1;
+          const __nv_bfloat162 pa = __floats2bfloat162_rn(a0, a1), pc = __floats2bfloat162_rn(b0, b1);
+          r[m][0] = *reinterpret_cast<const uint32_t*>(&pa);
+          r[m][1] = *reinterpret_cast<const uint32_t*>(&pc);
+        }
+        // the weight buffer is free once the product that read it last is done
+        if (C::PBUFS == 1) {
+          if (it > 0) mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, stats);
+        } else if (it > 1) {
+          mbar_wait_warp(bar(C::B_VD + sb), ((it - 2) >> 1) & 1, abort_flag, stats);
+        }
+        if (rescale && k > k0) {  // O^T: four blocks of 128 dims, 32 lanes of each
+          mbar_wait_warp(bar(C::B_VD + (sb ^ 1)), ((it - 1) >> 1) & 1, abort_flag, stats);
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = half; j < 4 * N / 16; j += HALVES) {
+            uint32_t o[16];
+            const uint32_t oa = tmem + 16 * j + ((uint32_t)(32 * q) << 16);
+            tmem_ld16(oa, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * s_alpha[(16 * j + i) % N]);
+            tmem_st16(oa, o);
+          }
+          tmem_wait_st();
+        }
         const uint32_t pb = sbase + C::OFF_P + (it % C::PBUFS) * C::P_BYTES;
 #pragma unroll
         for (int m = 0; m < M8; m += 2) {
-          uint32_t r[4];
-#pragma unroll
-          for (int mm = 0; mm < 2; ++mm) {
-            const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * (m + mm) + cc]);
-            const float a0 = ex2(u[m + mm][0] - f.x), a1 = ex2(u[m + mm][1] - f.y);
-            const float b0 = ex2(u[m + mm][2] - f.x), b1 = ex2(u[m + mm][3] - f.y);
-            l[m + mm][0] += a0 + b0;
-            l[m + mm][1] += a1 + b1;
-            const __nv_bfloat162 pa = __floats2bfloat162_rn(a0, a1), pb2 = __floats2bfloat162_rn(b0, b1);
-            r[2 * mm] = *reinterpret_cast<const uint32_t*>(&pa);
-            r[2 * mm + 1] = *reinterpret_cast<const uint32_t*>(&pb2);
-          }
           // matrix lane / 8: rows 8 (m + lane / 16), keys 16 q + 8 (lane / 8 % 2)
-          const int row = 8 * (m + (lane >> 4)) + (lane & 7);
+          const int row = cb + 8 * (m + (lane >> 4)) + (lane & 7);
           const int ch = 2 * q + ((lane >> 3) & 1);
-          stsm_x4_t(pb + row * 128 + ((ch ^ (row & 7)) << 4), r);
+          const uint32_t x[4] = {r[m][0], r[m][1], r[m + 1][0], r[m + 1][1]};
+          stsm_x4_t(pb + row * 128 + ((ch ^ (row & 7)) << 4), x);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -520,19 +541,10 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
         if (lane == 0) mbar_arrive(bar(C::B_WF + sb));
       }
       // ---- the piece's result: sums over the warps, then O^T out of TMEM
-#pragma unroll
-      for (int m = 0; m < M8; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) l[m][e] += __shfl_xor_sync(0xffffffffu, l[m][e], o);
-      named_bar_sync(1, LA_SM_THREADS);  // s_red, s_alpha and s_lim are free
-      if (g == 0) {
-#pragma unroll
-        for (int m = 0; m < M8; ++m)
-          *reinterpret_cast<float2*>(&s_red[q * N + 8 * m + cc]) = make_float2(l[m][0], l[m][1]);
-      }
-      named_bar_sync(1, LA_SM_THREADS);
+      over_keys<2 * M8>(l, lane, [](float a, float b) { return a + b; });
+      named_bar_sync(1, C::ST);  // s_red, s_alpha and s_lim are free
+      s_red[q * N + own_row<2 * M8>(lane) + cb] = l[0];
+      named_bar_sync(1, C::ST);
       const bool direct = whole && !p.prefix_items;
       const int64_t piece = (int64_t)w + blockIdx.x;
       if (st_id < N) {
@@ -544,11 +556,11 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
           p.part_ml[piece * N + st_id] = make_float2(ref, sum);
         }
       }
-      named_bar_sync(1, LA_SM_THREADS);
-      mbar_wait_warp(bar(C::B_VD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort_flag, p.stats);
+      named_bar_sync(1, C::ST);
+      mbar_wait_warp(bar(C::B_VD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort_flag, stats);
       tc_fence_after();
 #pragma unroll 1
-      for (int j = 0; j < 4 * N / 16; ++j) {
+      for (int j = half; j < 4 * N / 16; j += HALVES) {
         uint32_t o[16];
         tmem_ld16(tmem + 16 * j + ((uint32_t)(32 * q) << 16), o);
         tmem_wait_ld();
@@ -567,7 +579,7 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::B_OE));
-      named_bar_sync(1, LA_SM_THREADS);  // s_alpha has been read
+      named_bar_sync(1, C::ST);  // s_alpha has been read
     }
   }
 
@@ -582,13 +594,14 @@ __global__ void __launch_bounds__(LA_THREADS, 1)
       for (uint32_t s = 0; s < C::KPES; ++s)
         if (n_kpe > s) mbar_drain(bar(C::B_KF + s), ((n_kpe - 1 - s) / C::KPES) & 1);
       if (n_q) mbar_drain(bar(C::B_QF), (n_q - 1) & 1);
-    } else if (warp == 1 || warp == 6) {
-      const uint32_t db = bar(C::B_DRAIN + (warp == 6));
+    } else if (warp == 1 || warp == C::W_PV) {
+      const uint32_t db = bar(C::B_DRAIN + (warp == C::W_PV));
       mma_commit_warp(elect_one(), db);  // (elect.sync picks the lane that issued: it is deterministic)
       mbar_drain(db, 0);
     }
     __syncthreads();
   }
+  if (threadIdx.x == 0 && stats->status) atomicOr(&p.status->now, stats->status);
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
@@ -605,7 +618,11 @@ __global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAt
   __shared__ float s_part[LA_DC];
   __shared__ float s_tmp[MG_THREADS / 32];
   const int64_t row = blockIdx.x;
-  const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = p.plan->per;
+  if (row == 0 && threadIdx.x == 0 && !p.weights) {  // the call's last kernel
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = *p.per;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int id0[2], cnt[2], col[2], n = 0;  // runs of piece ids, the row's place in its block
 #pragma unroll
@@ -616,7 +633,7 @@ __global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAt
     if (k == 0 && !p.prefix_items) continue;
     const int s0 = p.start[w], s1 = p.start[w + 1];
     if (s0 == s1) continue;
-    id0[k] = w + s0 / per;
+    id0[k] = w + (s0 + LA_ITEM_UNITS) / per;  // the CTA of its first tile
     cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
     n += cnt[k];
   }
@@ -682,13 +699,18 @@ __global__ void __launch_bounds__(WT_THREADS) latent_weights_kernel(const Latent
   pdl_enter();
   constexpr int LPK = N / 4, KEYS = WT_THREADS / LPK;  // lanes per key, keys per step
   const int b = blockIdx.y, R = p.next_n * p.H;
-  const int len = p.lens[b], tiles = ceil_div(len, LT), sub = threadIdx.x % LPK, kk = threadIdx.x / LPK;
+  if (b == 0 && blockIdx.x == 0 && threadIdx.x == 0) {  // the call's last kernel
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  bool bad;
+  const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT), sub = threadIdx.x % LPK, kk = threadIdx.x / LPK;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
 #pragma unroll 1
     for (int k = kk; k < LT; k += KEYS) {
       float sum = 0.f;
       for (int j = 0; j < p.blocks; ++j) {
-        const int64_t tile = p.start[b * p.blocks + j] + t;
+        const int64_t tile = (int64_t)(b * p.blocks + j) * p.max_pages + t;
         const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
         const int r = j * N + 4 * sub;
         const float* lse = p.lse + (int64_t)b * R + r;
@@ -711,10 +733,7 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
   cudaError_t e = set_smem_attr_once(latent_attn_kernel<N>, LA<N>::SMEM, attr_set);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(latent_plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, s, p);
-  if (e != cudaSuccess) return e;
-  count_launch();
-  e = launch_pdl(latent_attn_kernel<N>, dim3(p.grid), dim3(LA_THREADS), LA<N>::SMEM, s, m, p);
+  e = launch_pdl(latent_attn_kernel<N>, dim3(p.grid), dim3(LA<N>::THREADS), LA<N>::SMEM, s, m, p);
   if (e != cudaSuccess) return e;
   count_launch();
   e = launch_pdl(latent_merge_kernel, dim3((unsigned)(p.B * p.next_n * p.H)), dim3(MG_THREADS), 0, s, p);

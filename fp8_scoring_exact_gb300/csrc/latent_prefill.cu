@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(32 * PR_WARPS) prefill_rows_kernel(const Prefi
   if (z >= p.S) return;
   const int q0 = p.cu_q[z], q1 = p.cu_q[z + 1], k0 = p.cu_k[z], k1 = p.cu_k[z + 1];
   if (q0 < 0 || q1 > p.Tq || k0 < 0 || k1 > p.Tk || k0 > k1) {
-    atomicOr(p.status, ST_RANGE);
+    atomicOr(&p.status->now, ST_RANGE);
     return;
   }
   const int n = p.causal ? max(0, (k1 - k0) - (q1 - q0) + (t - q0) + 1) : k1 - k0;
@@ -64,10 +64,19 @@ __global__ void __launch_bounds__(32 * PR_WARPS) prefill_rows_kernel(const Prefi
   if (lane == 0) p.lse[row] = l > 0.f ? m + log2f(l) : -__int_as_float(0x7f800000);
 }
 
+__global__ void prefill_status_kernel(LatentStatus* s) {
+  pdl_enter();
+  s->last = s->now;
+  s->now = 0;
+}
+
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t s) {
   count_launch();
   const int64_t rows = (int64_t)p.Tq * p.H;
-  return launch_pdl(prefill_rows_kernel, dim3((unsigned)((rows + PR_WARPS - 1) / PR_WARPS)), dim3(32 * PR_WARPS), 0, s, p);
+  cudaError_t e = launch_pdl(prefill_rows_kernel, dim3((unsigned)((rows + PR_WARPS - 1) / PR_WARPS)), dim3(32 * PR_WARPS), 0, s, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_pdl(prefill_status_kernel, dim3(1), dim3(1), 0, s, p.status);
 }
 
 }  // namespace dsa
