@@ -93,13 +93,17 @@ struct EvictParams {
 // Causal attention of a ragged batch in the expanded form (a key of a head:
 // 128 dims of its own and 64 rope dims shared by the heads).
 struct PrefillParams {
-  const __nv_bfloat16 *q, *k_nope, *k_pe, *v;
-  int64_t q_st, q_sh, kn_st, kn_sh, kp_st, v_st, v_sh;  // strides per token and per head, in elements
   const int32_t *cu_q, *cu_k;   // [S + 1]
   int S, Tq, Tk, H, causal;
   float scale_log2;
   __nv_bfloat16* out;           // [Tq, H, 128]
   float* lse;                   // [Tq, H]
+  int grid;
+  uint64_t wait_ns;
+  int64_t* per;                 // [1] units per CTA
+  int64_t* start;               // [grid, S + 1] first unit of each sequence, worked out by every CTA for itself
+  float* part_o;                // [2 grid, 256, 128] unnormalised outputs of the pieces of cut blocks
+  float2* part_ml;              // [2 grid, 256]: reference maximum (base-2 units) and sum
   LatentStatus* status;
 };
 
@@ -110,6 +114,11 @@ struct LatentMaps {
 };
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
-cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t s);
+// Tensor maps of the expanded form: q [Tq, H, 192], k_nope and v [Tk, H, 128],
+// boxes of 64 dims x 1 head x 128 tokens; k_pe [Tk, 64].
+struct PrefillMaps {
+  CUtensorMap q, k_nope, k_pe, v;
+};
+cudaError_t launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t s);
 
 }  // namespace dsa

@@ -107,6 +107,19 @@ bool tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t stride, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 [tokens, heads, dims], boxes of 64 dims x 1 head x 128 tokens.
+bool tmap_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int dims_, int64_t token_stride,
+                int64_t head_stride) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dims_, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+  const cuuint32_t box[3] = {64, 1, 128}, one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   const int rc = check_cached(p);
   if (rc != DSA_OK) return rc;
@@ -282,21 +295,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   if (H > 65535 || S > 65535 || (int64_t)Tq * H >= (1ll << 31) || Tq >= (1 << 30) || Tk >= (1 << 30))
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, HEAD);
-  if (!base) return DSA_ERR_CUDA;
   PrefillParams p{};
-  p.q = bf(q);
-  p.k_nope = bf(k_nope);
-  p.k_pe = bf(k_pe);
-  p.v = bf(v);
-  p.q_st = q_token_stride;
-  p.q_sh = q_head_stride;
-  p.kn_st = kn_token_stride;
-  p.kn_sh = kn_head_stride;
-  p.kp_st = kp_token_stride;
-  p.v_st = v_token_stride;
-  p.v_sh = v_head_stride;
   p.cu_q = cu_q;
   p.cu_k = cu_k;
   p.S = S;
@@ -307,8 +306,31 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
+  p.grid = std::min(option_grid(), 1024);
+  p.wait_ns = option_wait_ns();
+  PrefillMaps m;
+  if (!tmap_heads(&m.q, q, Tq, H, LA_DN + LA_DP, q_token_stride, q_head_stride) ||
+      !tmap_heads(&m.k_nope, k_nope, Tk, H, LA_DN, kn_token_stride, kn_head_stride) ||
+      !tmap_heads(&m.v, v, Tk, H, LA_DV, v_token_stride, v_head_stride) ||
+      !tmap_rows(&m.k_pe, k_pe, Tk, kp_token_stride, 1, 128, 1))
+    return DSA_ERR_CUDA;
+  size_t off = HEAD;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t o_per = take(8), o_start = take(8 * ((size_t)S + 1) * p.grid), o_ml = take(8 * 512 * (size_t)p.grid),
+               o_po = take(4 * 512 * (size_t)p.grid * LA_DV);
+  std::lock_guard<std::mutex> lk(g_mu);
+  uint8_t* base = get_scratch(stream, off);
+  if (!base) return DSA_ERR_CUDA;
   p.status = reinterpret_cast<LatentStatus*>(base);
-  return launch_prefill(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  p.per = reinterpret_cast<int64_t*>(base + o_per);
+  p.start = reinterpret_cast<int64_t*>(base + o_start);
+  p.part_ml = reinterpret_cast<float2*>(base + o_ml);
+  p.part_o = reinterpret_cast<float*>(base + o_po);
+  return launch_prefill(m, p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 int dsa_latent_last_status(dsa_stream_t stream_) {

@@ -5,78 +5,573 @@
 // the causal mask); a key of head h is (k_nope[s, h] | k_pe[s]), 192 dims,
 // its value v[s, h], 128 dims.  Softmax in base 2 as in latent_attn.cu.
 //
-// One warp per (query, head): lane l holds 4 key dims, 2 rope dims and 4
-// value dims.
+// 640 operations per (query, key, head): bound by the tensor cores.  A CTA
+// takes blocks of 256 queries of one head, two M = 128 tiles that share every
+// key tile (128 keys) in shared memory; S (128 x 128 fp32 each) and O (128 x
+// 128 each) fill the 512 TMEM columns, the weights go back to TMEM over their
+// logits as bf16 and are the second product's A operand there:
+//     S = Q [128 x 192] . K^T    12 steps, 64 cycles each
+//     O += P [128 x 128] . V      8 steps x 2 halves of the value dims
+// While one tile's softmax runs, the tensor cores work for the other.  Each
+// tile has an issuing warp of its own: its next S may only overwrite P once
+// the product that reads P is done, a wait that must not hold up the other
+// tile.  A softmax thread owns a row: no exchange between threads, and as in
+// latent_attn.cu the reference maximum moves only past 2^8.
+//
+// Every CTA takes an equal run of the call's units (a unit: a key tile of a
+// block, and PF_BLOCK_UNITS more per block); a block cut by a run's border is
+// joined by the merge kernel in the order of its pieces.
 #include "latent.h"
 
 namespace dsa {
 
 namespace {
-constexpr int PR_WARPS = 8;
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* src) {
-  const uint2 v = *reinterpret_cast<const uint2*>(src);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
+
+constexpr int PF_ROWS = 256;           // queries per block: two MMA tiles
+constexpr int PF_KEYS = 128;           // keys per tile
+constexpr int PF_BLOCK_UNITS = 2;      // what starting and ending a block costs, in key tiles
+constexpr uint32_t PF_SLOT = PF_KEYS * 128;  // 128 rows x 64 dims, bf16
+constexpr int PF_SLOTS = 8;            // ring: a key tile takes 3 (128 + 64 dims), its values 2
+constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue, 4-7 and 8-11 softmax
+constexpr int PF_THREADS = 32 * PF_WARPS;
+constexpr float PF_RESCALE_AT = 8.f;
+
+constexpr uint32_t PF_OFF_Q = 0;       // per tile 3 chunks of 128 rows x 64 dims
+constexpr uint32_t PF_OFF_RING = PF_OFF_Q + 6 * PF_SLOT;
+constexpr uint32_t PF_OFF_MISC = PF_OFF_RING + PF_SLOTS * PF_SLOT;
+// barriers: slot full / empty, q full / empty, then per tile S full, P full, PV done, O empty, drain
+constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1, B_P = B_S + 2,
+              B_V = B_P + 2, B_O = B_V + 2, B_DRAIN = B_O + 2, PF_BARS = B_DRAIN + 2;
+constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
+constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
+constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // 12 + 4 int64
+constexpr uint32_t PF_SMEM = PF_OFF_SCAN + 128 + 1024;
+static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128, "shared memory per CTA");
+
+__device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
+
+struct Seq {
+  int q0, n, k0, m;  // first query and queries, first key and keys
+};
+// A sequence outside the arrays counts as empty and is reported.
+__device__ __forceinline__ Seq load_seq(const PrefillParams& p, int z, bool& bad) {
+  const int q0 = p.cu_q[z], q1 = p.cu_q[z + 1], k0 = p.cu_k[z], k1 = p.cu_k[z + 1];
+  bad = q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk;
+  return bad ? Seq{0, 0, 0, 0} : Seq{q0, q1 - q0, k0, k1 - k0};
+}
+// Keys that the first `i` queries of a sequence see at most.
+__device__ __forceinline__ int keys_seen(const PrefillParams& p, const Seq& s, int i) {
+  return p.causal ? max(0, s.m - s.n + min(i, s.n)) : s.m;
+}
+__device__ __forceinline__ int block_tiles(const PrefillParams& p, const Seq& s, int blk) {
+  return ceil_div(keys_seen(p, s, (blk + 1) * PF_ROWS), PF_KEYS);
+}
+
+// One CTA's pieces: next() gives sequence, head, block and key tiles [k0, k1).
+struct Pieces {
+  int64_t t, t1, s0;  // next unit, end, first unit of the current block
+  int z, h, blk;
+  Seq seq;
+
+  __device__ __forceinline__ bool next(const PrefillParams& p, int& k0, int& k1, int& tiles) {
+    for (;;) {
+      if (t >= t1) return false;
+      bool bad;
+      while (blk * PF_ROWS >= seq.n) {  // past the last block: next head or sequence
+        blk = 0;
+        if (++h == p.H) {
+          h = 0;
+          seq = load_seq(p, ++z, bad);
+          if (seq.n == 0) {
+            h = p.H - 1;  // an empty sequence has no units
+            blk = 1;
+          }
+        }
+      }
+      tiles = block_tiles(p, seq, blk);
+      const int units = tiles + PF_BLOCK_UNITS;
+      if (s0 + units <= t) {  // (only on the way to the first block)
+        s0 += units;
+        ++blk;
+        continue;
+      }
+      const int u0 = (int)(t - s0), u1 = (int)(min(t1, s0 + units) - s0);
+      k0 = max(0, u0 - PF_BLOCK_UNITS);
+      k1 = max(0, u1 - PF_BLOCK_UNITS);
+      t = s0 + u1;
+      if (k1 > k0 || (tiles == 0 && u0 == 0)) return true;  // (an empty block: its rows are written once)
+      if (u1 < units) return false;                          // the run ends before the block's first tile
+    }
+  }
+  // what next() left: block `blk` of head h; step past it once its end has been reached
+  __device__ __forceinline__ void step(int tiles) {
+    if (t == s0 + tiles + PF_BLOCK_UNITS) {
+      s0 = t;
+      ++blk;
+    }
+  }
+};
+
+// Numbers the units of all sequences (start[], the same in every CTA); the
+// pieces of units [c per, (c + 1) per) for c = `cta`.
+template <int THREADS>
+__device__ __forceinline__ Pieces plan_pieces(const PrefillParams& p, int64_t* start, int cta, int64_t* tmp, int* status) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t base = 0;
+  for (int z0 = 0; z0 < p.S; z0 += THREADS) {
+    const int z = z0 + tid;
+    int64_t units = 0;
+    if (z < p.S) {
+      bool bad;
+      const Seq s = load_seq(p, z, bad);
+      if (bad && status) atomicOr(status, ST_RANGE);
+      for (int blk = 0; blk * PF_ROWS < s.n; ++blk) units += block_tiles(p, s, blk) + PF_BLOCK_UNITS;
+      units *= p.H;
+    }
+    int64_t x = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      before += i < warp ? tmp[i] : 0;
+      all += tmp[i];
+    }
+    if (z < p.S) start[z] = base + before + x - units;
+    base += all;
+  }
+  const int64_t per = max((int64_t)(PF_BLOCK_UNITS + 1), (base + p.grid - 1) / p.grid);
+  const int64_t t = min(base, cta * per);
+  if (tid == 0) {
+    start[p.S] = base;
+    tmp[12] = 0;
+    if (blockIdx.x == 0) *p.per = per;
+  }
+  __syncthreads();
+  for (int z = tid; z < p.S; z += THREADS)
+    if (start[z] <= t && t < start[z + 1]) tmp[12] = z;
+  __syncthreads();
+  Pieces r;
+  r.t = t;
+  r.t1 = min(base, t + per);
+  r.z = (int)tmp[12];
+  r.s0 = start[r.z];
+  bool bad;
+  r.seq = load_seq(p, r.z, bad);
+  r.h = 0;
+  r.blk = 0;
+  if (r.t < r.t1) {  // the head, then (in next) the block
+    const int64_t head = (start[r.z + 1] - start[r.z]) / p.H;
+    r.h = (int)((t - r.s0) / head);
+    r.s0 += r.h * head;
+  }
+  return r;
+}
+
 }  // namespace
 
-__global__ void __launch_bounds__(32 * PR_WARPS) prefill_rows_kernel(const PrefillParams p) {
-  pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * PR_WARPS + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.Tq * p.H) return;
-  const int t = (int)(row / p.H), h = (int)(row % p.H);
-  int z = 0;
-  while (z < p.S && p.cu_q[z + 1] <= t) ++z;
-  if (z >= p.S) return;
-  const int q0 = p.cu_q[z], q1 = p.cu_q[z + 1], k0 = p.cu_k[z], k1 = p.cu_k[z + 1];
-  if (q0 < 0 || q1 > p.Tq || k0 < 0 || k1 > p.Tk || k0 > k1) {
-    atomicOr(&p.status->now, ST_RANGE);
-    return;
+__global__ void __launch_bounds__(PF_THREADS, 1)
+    prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + PF_OFF_MISC + 8u * i; };
+  volatile int* abort_flag = reinterpret_cast<int*>(smem + PF_OFF_FLAG);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + PF_OFF_FLAG + 4);
+  Stats* stats = reinterpret_cast<Stats*>(smem + PF_OFF_STAT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    stats->status = 0;
+    stats->wait_ns = p.wait_ns;
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.k_nope);
+    tma_prefetch_desc(&maps.k_pe);
+    tma_prefetch_desc(&maps.v);
+    for (int i = 0; i < PF_SLOTS; ++i) {
+      mbar_init(bar(B_FULL + i), 1);
+      mbar_init(bar(B_EMPTY + i), 2);  // both tiles' issuers
+    }
+    mbar_init(bar(B_QF), 1);
+    mbar_init(bar(B_QE), 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_S + i), 1);
+      mbar_init(bar(B_P + i), 4);
+      mbar_init(bar(B_V + i), 1);
+      mbar_init(bar(B_O + i), 4);
+      mbar_init(bar(B_DRAIN + i), 1);
+    }
+    fence_mbar_init();
   }
-  const int n = p.causal ? max(0, (k1 - k0) - (q1 - q0) + (t - q0) + 1) : k1 - k0;
-  const float4 q = load4(p.q + t * p.q_st + h * p.q_sh + 4 * lane);
-  const float2 qe = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.q + t * p.q_st + h * p.q_sh + 128 + 2 * lane));
-  float m = -__int_as_float(0x7f800000), l = 0.f, c = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t s = k0; s < k0 + n; ++s) {
-    const float4 k = load4(p.k_nope + s * p.kn_st + h * p.kn_sh + 4 * lane);
-    const float4 v = load4(p.v + s * p.v_st + h * p.v_sh + 4 * lane);
-    const float2 ke = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p.k_pe + s * p.kp_st + 2 * lane));
-    float x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w + qe.x * ke.x + qe.y * ke.y;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  Pieces pc = plan_pieces<PF_THREADS>(p, p.start + (int64_t)blockIdx.x * (p.S + 1), blockIdx.x,
+                                      reinterpret_cast<int64_t*>(smem + PF_OFF_SCAN), &stats->status);
+  uint32_t n_slot = 0, n_q = 0;  // producer: copies armed
+  int k0, k1, tiles;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- TMA producer --
+    bool ok = true;
+    for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
+      if (k1 <= k0) continue;
+      if (!(ok = mbar_wait_warp(bar(B_QE), (n_q & 1) ^ 1, abort_flag, stats))) break;
+      const int row = pc.seq.q0 + pc.blk * PF_ROWS;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(B_QF), 6 * PF_SLOT);
+        for (int c = 0; c < 6; ++c)
+          tma_load_3d(sbase + PF_OFF_Q + c * PF_SLOT, &maps.q, 64 * (c % 3), pc.h, row + 128 * (c / 3), bar(B_QF));
+      }
+      ++n_q;
+      for (int k = k0; ok && k < k1; ++k) {
+        const int key = pc.seq.k0 + k * PF_KEYS;
+        for (int c = 0; c < 5; ++c, ++n_slot) {  // k_nope, k_nope, k_pe, v, v
+          const int st = n_slot % PF_SLOTS;
+          if (!(ok = mbar_wait_warp(bar(B_EMPTY + st), ((n_slot / PF_SLOTS) & 1) ^ 1, abort_flag, stats))) break;
+          if (lane == 0) {
+            const uint32_t dst = sbase + PF_OFF_RING + st * PF_SLOT;
+            mbar_arrive_expect_tx(bar(B_FULL + st), PF_SLOT);
+            if (c < 2)
+              tma_load_3d(dst, &maps.k_nope, 64 * c, pc.h, key, bar(B_FULL + st));
+            else if (c == 2)
+              tma_load_2d(dst, &maps.k_pe, 0, key, bar(B_FULL + st));
+            else
+              tma_load_3d(dst, &maps.v, 64 * (c - 3), pc.h, key, bar(B_FULL + st));
+          }
+        }
+      }
+    }
+  } else if (warp == 1 || warp == 2) {
+    // ---------------------------------------- the issuer of tile `t` (0, 1) --
+    const uint32_t t = warp - 1;
+    constexpr uint32_t ID_S = idesc_bf16_f32(128, PF_KEYS, false, false);
+    constexpr uint32_t ID_O = idesc_bf16_f32(128, 64, false, true);
+    const uint32_t leader = elect_one();
+    const uint32_t d_s = tmem + 128 * t, d_o = tmem + 256 + 128 * t;
+    const uint32_t q_lo = desc_lo_kmajor(sbase + PF_OFF_Q + t * 3 * PF_SLOT);
+    uint32_t seg = 0, it = 0, slot = 0;  // pieces; this tile's key tiles; ring position of the piece's first key tile
+    bool ok = true;
+    // slots [s, s + n) without reading them (each only once it has been filled:
+    // its barrier counts one arrival of either issuer per filling)
+    auto pass_on = [&](uint32_t s, uint32_t n) {
+      for (uint32_t e = s + n; s < e; ++s) {
+        if (!mbar_wait_warp(bar(B_FULL + s % PF_SLOTS), (s / PF_SLOTS) & 1, abort_flag, stats)) return false;
+        if (lane == 0) mbar_arrive(bar(B_EMPTY + s % PF_SLOTS));
+      }
+      return true;
+    };
+    for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
+      if (k1 <= k0) continue;
+      // key tiles that this query tile sees (the other tile may see one more)
+      const int first = pc.blk * PF_ROWS + 128 * t;
+      const int mine = first < pc.seq.n ? ceil_div(keys_seen(p, pc.seq, first + 128), PF_KEYS) : 0;
+      if (!(ok = mbar_wait_warp(bar(B_QF), seg & 1, abort_flag, stats))) break;
+      for (int k = k0; ok && k < k1; ++k) {
+        {
+          // S of key tile k; P of the tile before it has been read (waited for below)
+          const uint32_t s0 = slot + 5 * (k - k0);
+          if (k < mine) {
+            for (uint32_t c = 0; c < 3; ++c) {
+              const uint32_t st = (s0 + c) % PF_SLOTS;
+              if (!(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + c) / PF_SLOTS) & 1, abort_flag, stats))) break;
+              tc_fence_after();
+              const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    const float u = x * p.scale_log2, m_new = fmaxf(m, u);
-    const float a = exp2f(m - m_new), w = exp2f(u - m_new);
-    m = m_new;
-    // compensated: over many keys of nearly equal weight a plain sum would
-    // lose the weights' differences
-    l *= a;
-    const float y = w - c * a, sum = l + y;
-    c = (sum - l) - y;
-    l = sum;
-    o = make_float4(o.x * a + w * v.x, o.y * a + w * v.y, o.z * a + w * v.z, o.w * a + w * v.w);
+              for (int j = 0; j < 4; ++j)
+                mma_bf16_ss(leader, d_s, q_lo + c * (PF_SLOT >> 4) + 2 * j, k_lo + 2 * j, ID_S, c > 0 || j > 0);
+              mma_commit_warp(leader, bar(B_EMPTY + st));
+            }
+            if (!ok) break;
+            mma_commit_warp(leader, bar(B_S + t));
+          } else {
+            ok = pass_on(s0, 3);
+            if (!ok) break;
+          }
+          if (k == k1 - 1) mma_commit_warp(leader, bar(B_QE));
+        }
+        if (k >= mine) {  // its values are not read either
+          ok = pass_on(slot + 5 * (k - k0) + 3, 2);
+        } else {
+          // O += P V of key tile k
+          const uint32_t s0 = slot + 5 * (k - k0) + 3;
+          if (!(ok = mbar_wait_warp(bar(B_P + t), it & 1, abort_flag, stats))) break;
+          if (k == k0 && !(ok = mbar_wait_warp(bar(B_O + t), (seg & 1) ^ 1, abort_flag, stats))) break;
+          for (uint32_t c = 0; c < 2; ++c) {
+            const uint32_t st = (s0 + c) % PF_SLOTS;
+            if (!(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + c) / PF_SLOTS) & 1, abort_flag, stats))) break;
+            tc_fence_after();
+            const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // 16 keys: 8 columns of P, 2 KB of V
+              mma_bf16_ts(leader, d_o + 64 * c, d_s + 8 * j, v_lo + 128 * j, ID_O, k > k0 || j > 0);
+            mma_commit_warp(leader, bar(B_EMPTY + st));
+          }
+          if (!ok) break;
+          mma_commit_warp(leader, bar(B_V + t));
+          if (!(ok = mbar_wait_warp(bar(B_V + t), it & 1, abort_flag, stats))) break;
+          ++it;
+        }
+      }
+      slot += 5 * (k1 - k0);
+      // a tile without rows or keys here leaves its softmax warps nothing to read
+      ++seg;
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------- softmax warps --
+    // (a wait that gives up leaves the result undefined; the loops still end)
+    const uint32_t t = (warp - 4) >> 2;
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t d_s = tmem + 128 * t + lanes, d_o = tmem + 256 + 128 * t + lanes;
+    uint32_t it = 0, slot = 0;
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
+      const int first = pc.blk * PF_ROWS + 128 * t, i = first + r;  // this row's query within its sequence
+      const int mine = first < pc.seq.n ? ceil_div(keys_seen(p, pc.seq, first + 128), PF_KEYS) : 0;
+      const int lim = i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0;
+      const int lim0 = keys_seen(p, pc.seq, first + 1);  // the tile's first row sees least
+      float ref = neg_inf(), l[4] = {0.f, 0.f, 0.f, 0.f};
+      const int end = min(k1, mine);
+      for (int k = k0; k < end; ++k, ++it) {
+        mbar_wait_warp(bar(B_S + t), it & 1, abort_flag, stats);
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(d_s + 32 * c, s + 32 * c);
+        tmem_wait_ld();
+        if ((k + 1) * PF_KEYS > lim0) {
+          const int left = lim - k * PF_KEYS;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= left) s[c] = 0xff800000u;  // -inf
+          // the next sequence's values share the tile: they become 0 (a
+          // weight of 0 does not silence a NaN)
+          const int valid = pc.seq.m - k * PF_KEYS;
+          if (valid < PF_KEYS) {
+            for (uint32_t c = 3; c < 5; ++c) {
+              const uint32_t n = slot + 5 * (k - k0) + c;
+              mbar_wait_warp(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+              uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + (n % PF_SLOTS) * PF_SLOT);
+              for (int x = valid * 8 + r; x < PF_KEYS * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+        const float top = p.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
+        if (__any_sync(0xffffffffu, moves)) {
+          const float a = moves ? ex2(ref - top) : 1.f;  // 0 from a reference of -inf
+          if (moves) ref = top;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[j] *= a;
+          if (k > k0) {  // (S of this tile was issued after the product before it was done)
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(d_o + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
+              tmem_st16(d_o + 16 * c, o);
+            }
+          }
+        }
+        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
+        // the MMA wants of both operands) over the logits in TMEM
+        const float nr = ref == neg_inf() ? 0.f : -ref;
+        const uint64_t nr2 = pack2(nr, nr);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 x = unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale2, nr2));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            l[2 * (j & 1)] += e0;
+            l[2 * (j & 1) + 1] += e1;
+            const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          tmem_st32(d_s + 32 * c, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P + t));
+      }
+      slot += 5 * (k1 > k0 ? k1 - k0 : 0);
+      // ---- the piece's result
+      const float sum = (l[0] + l[1]) + (l[2] + l[3]);
+      const bool cut = k0 > 0 || k1 < tiles;
+      const int64_t part = 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0);
+      const int64_t prow = part * PF_ROWS + 128 * t + r;
+      const bool here = i < pc.seq.n;
+      const int64_t row = (int64_t)(pc.seq.q0 + i) * p.H + pc.h;
+      if (cut) {
+        p.part_ml[prow] = make_float2(ref, sum);
+      } else if (here) {
+        p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
+      }
+      const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      const bool any = end > k0;
+      if (any) {
+        mbar_wait_warp(bar(B_V + t), (it - 1) & 1, abort_flag, stats);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
+        if (any) {
+          tmem_ld16(d_o + 16 * c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = 0;
+        }
+        if (cut) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * LA_DV + 16 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                                 __uint_as_float(o[4 * j + 3]));
+        } else if (here) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 b =
+                __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * LA_DV + 16 * c);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (k1 > k0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_O + t));
+      }
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DV + 4 * lane);
-  dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-  dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  if (lane == 0) p.lse[row] = l > 0.f ? m + log2f(l) : -__int_as_float(0x7f800000);
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // before shared memory and TMEM are released, the copies and MMAs
+    // already issued land: the last phase armed on each slot, a last commit
+    if (warp == 0 && lane == 0) {
+      for (uint32_t s = 0; s < PF_SLOTS; ++s)
+        if (n_slot > s) mbar_drain(bar(B_FULL + s), ((n_slot - 1 - s) / PF_SLOTS) & 1);
+      if (n_q) mbar_drain(bar(B_QF), (n_q - 1) & 1);
+    } else if (warp == 1 || warp == 2) {
+      mma_commit_warp(elect_one(), bar(B_DRAIN + warp - 1));
+      mbar_drain(bar(B_DRAIN + warp - 1), 0);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0 && stats->status) atomicOr(&p.status->now, stats->status);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
-__global__ void prefill_status_kernel(LatentStatus* s) {
+// Joins the pieces of cut blocks.  CTA (c, y): if the border between the runs
+// of c and c + 1 is the first inside some block, rows [32 y, + 32) of it; one
+// warp per row at a time, 4 dims per lane.
+constexpr int PM_THREADS = 256;
+__global__ void __launch_bounds__(PM_THREADS) prefill_merge_kernel(const PrefillParams p) {
   pdl_enter();
-  s->last = s->now;
-  s->now = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {  // the call's last kernel
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  const int64_t per = *p.per, total = p.start[p.S], t = (blockIdx.x + 1) * per;  // the unit after the border
+  if (t >= total) return;
+  int lo = 0, hi = p.S - 1;  // the last sequence that starts at or before t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.start[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  bool bad;
+  const Seq seq = load_seq(p, lo, bad);
+  int64_t s0 = p.start[lo];
+  const int64_t head = (p.start[lo + 1] - s0) / p.H;
+  const int h = (int)((t - s0) / head);
+  s0 += h * head;
+  int blk = 0, tiles = block_tiles(p, seq, 0);
+  while (s0 + tiles + PF_BLOCK_UNITS <= t) {
+    s0 += tiles + PF_BLOCK_UNITS;
+    tiles = block_tiles(p, seq, ++blk);
+  }
+  // pieces: the CTA of the block's first tile, then every one up to that of its last
+  const int64_t c0 = (s0 + PF_BLOCK_UNITS) / per, c1 = (s0 + PF_BLOCK_UNITS + tiles - 1) / per;
+  if (tiles == 0 || c0 != blockIdx.x || c1 == c0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int r = 32 * blockIdx.y + warp; r < 32 * (int)blockIdx.y + 32; r += PM_THREADS / 32) {
+    const int i = blk * PF_ROWS + r;
+    if (i >= seq.n) return;
+    auto at = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * PF_ROWS + r; };
+    float m = neg_inf();
+    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[at(c)].x);
+    const float mm = m == neg_inf() ? 0.f : m;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t c = c0; c <= c1; ++c) {
+      const float2 ml = p.part_ml[at(c)];
+      const float x = ex2(ml.x - mm);
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(c) * LA_DV) + lane);
+      sum += x * ml.y;
+      if (x != 0.f) {
+        o.x += x * v.x;
+        o.y += x * v.y;
+        o.z += x * v.z;
+        o.w += x * v.w;
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = (int64_t)(seq.q0 + i) * p.H + h;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DV + 4 * lane);
+    dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    if (lane == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+  }
 }
 
-cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t s) {
-  count_launch();
-  const int64_t rows = (int64_t)p.Tq * p.H;
-  cudaError_t e = launch_pdl(prefill_rows_kernel, dim3((unsigned)((rows + PR_WARPS - 1) / PR_WARPS)), dim3(32 * PR_WARPS), 0, s, p);
+cudaError_t launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t s) {
+  static DeviceFlags attr_set;
+  cudaError_t e = set_smem_attr_once(prefill_kernel, PF_SMEM, attr_set);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(prefill_status_kernel, dim3(1), dim3(1), 0, s, p.status);
+  e = launch_pdl(prefill_kernel, dim3(p.grid), dim3(PF_THREADS), PF_SMEM, s, m, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_pdl(prefill_merge_kernel, dim3(p.grid, PF_ROWS / 32), dim3(PM_THREADS), 0, s, p);
 }
 
 }  // namespace dsa
