@@ -306,65 +306,80 @@ def sparse_attention_last_status(stream=None) -> int:
 
 # ---------------------------------------------------------- latent attention --
 LATENT_DC, LATENT_DP, LATENT_DN, LATENT_DV = 512, 64, 128, 128
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _shaped(t: torch.Tensor, name: str, shape, dtype) -> torch.Tensor:
-    _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+def _full(t, name, shape, dtype):
+    """Address of a contiguous CUDA tensor of this shape and type."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous()):
+        _dev(t, name, dtype)
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-def _strided(t: torch.Tensor, name: str, dtype=torch.bfloat16) -> torch.Tensor:
-    """A CUDA tensor whose last axis is contiguous; the other strides are the caller's."""
+def _strided(t, name, dtype=_BF16):
+    """Strides of a CUDA tensor whose last axis is contiguous; the others are the caller's."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(-1) != 1:
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError(f"{name} must be contiguous in its last axis")
-    return t
+    return s
+
+
+def _latent_stream(stream):
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
+
+def _slot_stride(t, name, pages, d):
+    s = _strided(t, name)
+    if t.shape != (pages, 64, d):
+        raise ValueError(f"{name} must be [P,64,{d}] with one P for both caches, got {list(t.shape)}")
+    if pages > 1 and s[0] != 64 * s[1]:
+        raise ValueError(f"{name}: slots must be evenly spaced (page stride 64 times the slot stride)")
+    return s[1]
 
 
 def _latent_cache(ckv, kpe):
-    """(ckv, its slot stride, kpe, its slot stride, pages) of a cache [P,64,512] and [P,64,64]; either
+    """(ckv, its slot stride, kpe, its slot stride), pages of a cache [P,64,512] and [P,64,64]; either
     may be part of a wider array (slots evenly spaced)."""
-    strides = []
-    for t, name, d in ((ckv, "ckv_cache", LATENT_DC), (kpe, "kpe_cache", LATENT_DP)):
-        _strided(t, name)
-        if t.dim() != 3 or tuple(t.shape[1:]) != (64, d) or t.shape[0] != ckv.shape[0]:
-            raise ValueError(f"{name} must be [P,64,{d}] with one P for both caches, got {list(t.shape)}")
-        if t.shape[0] > 1 and t.stride(0) != 64 * t.stride(1):
-            raise ValueError(f"{name}: slots must be evenly spaced (page stride 64 times the slot stride)")
-        strides.append(t.stride(1))
-    return ckv, strides[0], kpe, strides[1], ckv.shape[0]
+    pages = ckv.shape[0] if isinstance(ckv, torch.Tensor) and ckv.dim() else 0
+    cs, ks = _slot_stride(ckv, "ckv_cache", pages, LATENT_DC), _slot_stride(kpe, "kpe_cache", pages, LATENT_DP)
+    return (ckv.data_ptr(), cs, kpe.data_ptr(), ks), pages
 
 
 def _latent_queries(q_nope, q_pe, out, lse):
-    _dev(q_nope, "q_nope", torch.bfloat16)
-    if q_nope.dim() != 4 or q_nope.shape[3] != LATENT_DC:
-        raise ValueError(f"q_nope must be [B,next_n,H,512], got {list(q_nope.shape)}")
-    rows = q_nope.shape[:3]
-    _shaped(q_pe, "q_pe", (*rows, LATENT_DP), torch.bfloat16)
+    rows = _dev(q_nope, "q_nope", _BF16).shape
+    if len(rows) != 4 or rows[3] != LATENT_DC:
+        raise ValueError(f"q_nope must be [B,next_n,H,512], got {list(rows)}")
+    rows = rows[:3]
+    queries = q_nope.data_ptr(), _full(q_pe, "q_pe", (*rows, LATENT_DP), _BF16)
     if out is None:
-        out = torch.empty((*rows, LATENT_DC), dtype=torch.bfloat16, device=q_nope.device)
+        out = torch.empty_like(q_nope)
+    else:
+        _full(out, "out", (*rows, LATENT_DC), _BF16)
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=q_nope.device)
-    return rows, _shaped(out, "out", (*rows, LATENT_DC), torch.bfloat16), _shaped(lse, "lse", rows, torch.float32)
+        lse = torch.empty(rows, dtype=_F32, device=q_nope.device)
+    else:
+        _full(lse, "lse", rows, _F32)
+    return rows, queries, out, lse
 
 
 def _tables(block_table, seq_lens, B):
-    _dev(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B},max_pages], got {list(block_table.shape)}")
-    return block_table, _shaped(seq_lens, "seq_lens", (B,), torch.int32)
+    shape = _dev(block_table, "block_table", _I32).shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must be [{B},max_pages], got {list(shape)}")
+    return (block_table.data_ptr(), _full(seq_lens, "seq_lens", (B,), _I32)), shape[1]
 
 
 def _key_weights(weights, B, max_pages):
-    _dev(weights, "weights", torch.float32)
-    if weights.dim() != 2 or weights.shape[0] != B or weights.shape[1] < 64 * max_pages:
-        raise ValueError(f"weights must be [{B}, at least {64 * max_pages}], got {list(weights.shape)}")
-    return weights
+    shape = _dev(weights, "weights", _F32).shape
+    if len(shape) != 2 or shape[0] != B or shape[1] < 64 * max_pages:
+        raise ValueError(f"weights must be [{B}, at least {64 * max_pages}], got {list(shape)}")
+    return weights.data_ptr(), shape[1]
 
 
 def latent_attention_paged(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_lens, sm_scale, out=None, lse=None,
@@ -374,16 +389,12 @@ def latent_attention_paged(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_
     token i of sequence b sees its first seq_lens[b] - next_n + i + 1 keys.  Returns (out
     [B,next_n,H,512] bf16, lse [B,next_n,H] fp32, base 2).  weights fp32 [B, >= 64 max_pages]: the
     softmax weight of every key, summed over the sequence's rows, is added to it."""
-    (B, nn, H), out, lse = _latent_queries(q_nope, q_pe, out, lse)
-    ckv, cs, kpe, ks, pages = _latent_cache(ckv_cache, kpe_cache)
-    block_table, seq_lens = _tables(block_table, seq_lens, B)
-    maxp = block_table.shape[1]
-    if weights is not None:
-        _key_weights(weights, B, maxp)
-    rc = lib().dsa_latent_attention_paged(_ptr(q_nope), _ptr(q_pe), _ptr(ckv), cs, _ptr(kpe), ks, _ptr(block_table),
-                                          _ptr(seq_lens), B, nn, H, maxp, pages, float(sm_scale), _ptr(out), _ptr(lse),
-                                          None if weights is None else _ptr(weights),
-                                          0 if weights is None else weights.shape[1], _stream_ptr(stream))
+    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse)
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
+    tables, maxp = _tables(block_table, seq_lens, rows[0])
+    w, ldw = (None, 0) if weights is None else _key_weights(weights, rows[0], maxp)
+    rc = lib().dsa_latent_attention_paged(*queries, *cache, *tables, *rows, maxp, pages, sm_scale, out.data_ptr(),
+                                          lse.data_ptr(), w, ldw, _latent_stream(stream))
     _check("dsa_latent_attention_paged", rc)
     return out, lse
 
@@ -393,15 +404,14 @@ def latent_attention_shared_prefix(q_nope, q_pe, ckv_cache, kpe_cache, prefix_ta
     """latent_attention_paged for a batch that shares a prefix: every row also sees the prefix_len[0]
     keys behind prefix_table (int32 [prefix_pages]), which are read once for the whole batch; seq_lens
     counts a sequence's own keys."""
-    (B, nn, H), out, lse = _latent_queries(q_nope, q_pe, out, lse)
-    ckv, cs, kpe, ks, pages = _latent_cache(ckv_cache, kpe_cache)
-    block_table, seq_lens = _tables(block_table, seq_lens, B)
-    prefix_table = _shaped(prefix_table, "prefix_table", (prefix_table.numel(),), torch.int32)
-    prefix_len = _shaped(prefix_len, "prefix_len", (1,), torch.int32)
-    rc = lib().dsa_latent_attention_shared_prefix(_ptr(q_nope), _ptr(q_pe), _ptr(ckv), cs, _ptr(kpe), ks,
-                                                  _ptr(prefix_table), _ptr(prefix_len), prefix_table.shape[0],
-                                                  _ptr(block_table), _ptr(seq_lens), B, nn, H, block_table.shape[1],
-                                                  pages, float(sm_scale), _ptr(out), _ptr(lse), _stream_ptr(stream))
+    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse)
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
+    tables, maxp = _tables(block_table, seq_lens, rows[0])
+    n = prefix_table.numel()
+    rc = lib().dsa_latent_attention_shared_prefix(*queries, *cache, _full(prefix_table, "prefix_table", (n,), _I32),
+                                                  _full(prefix_len, "prefix_len", (1,), _I32), n, *tables, *rows, maxp,
+                                                  pages, sm_scale, out.data_ptr(), lse.data_ptr(),
+                                                  _latent_stream(stream))
     _check("dsa_latent_attention_shared_prefix", rc)
     return out, lse
 
@@ -412,26 +422,24 @@ def latent_cache_evict(ckv_cache, kpe_cache, weights, block_table, seq_lens, bud
     largest weights (ties: the lowest index), in their old order, with their weights and, if given, the
     indexer's keys k_cache [P,64,128] and scales [P,64].  Returns (kept int32 [B,budget]: old indices,
     then -1; new_lens int32 [B], which may be seq_lens itself)."""
-    ckv, cs, kpe, ks, pages = _latent_cache(ckv_cache, kpe_cache)
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
     B = block_table.shape[0]
-    block_table, seq_lens = _tables(block_table, seq_lens, B)
-    maxp = block_table.shape[1]
-    _key_weights(weights, B, maxp)
+    tables, maxp = _tables(block_table, seq_lens, B)
+    w, ldw = _key_weights(weights, B, maxp)
     if (k_cache is None) != (k_cache_scale is None):
         raise ValueError("k_cache and k_cache_scale go together")
+    keys = (None, None)
     if k_cache is not None:
-        k_cache = _shaped(_u8(k_cache, "k_cache"), "k_cache", (pages, 64, HEAD_DIM), torch.uint8)
-        _shaped(k_cache_scale, "k_cache_scale", (pages, 64), torch.float32)
+        keys = (_full(_u8(k_cache, "k_cache"), "k_cache", (pages, 64, HEAD_DIM), torch.uint8),
+                _full(k_cache_scale, "k_cache_scale", (pages, 64), _F32))
+    budget, recent = int(budget), int(recent)
     if kept is None:
-        kept = torch.empty((B, max(0, budget)), dtype=torch.int32, device=ckv.device)
+        kept = torch.empty((B, max(0, budget)), dtype=_I32, device=ckv_cache.device)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=ckv.device)
-    _shaped(kept, "kept", (B, max(0, budget)), torch.int32)
-    _shaped(new_lens, "new_lens", (B,), torch.int32)
-    rc = lib().dsa_latent_cache_evict(_ptr(ckv), cs, _ptr(kpe), ks, None if k_cache is None else _ptr(k_cache),
-                                      None if k_cache is None else _ptr(k_cache_scale), _ptr(weights),
-                                      weights.shape[1], _ptr(block_table), _ptr(seq_lens), B, maxp, pages,
-                                      int(budget), int(recent), _ptr(kept), _ptr(new_lens), _stream_ptr(stream))
+        new_lens = torch.empty((B,), dtype=_I32, device=ckv_cache.device)
+    rc = lib().dsa_latent_cache_evict(*cache, *keys, w, ldw, *tables, B, maxp, pages, budget, recent,
+                                      _full(kept, "kept", (B, max(0, budget)), _I32),
+                                      _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
     _check("dsa_latent_cache_evict", rc)
     return kept, new_lens
 
@@ -441,29 +449,25 @@ def latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, sm_scale, causal=Tr
     token and head strides), k_pe [Tk,64] bf16; sequence z has queries cu_q[z]..cu_q[z+1] and keys
     cu_k[z]..cu_k[z+1] (int32), its last query sees all its keys.  Returns (out [Tq,H,128] bf16, lse
     [Tq,H] fp32, base 2)."""
-    for t, name in ((q, "q"), (k_nope, "k_nope"), (k_pe, "k_pe"), (v, "v")):
-        _strided(t, name)
+    sq, sk, sp, sv = _strided(q, "q"), _strided(k_nope, "k_nope"), _strided(k_pe, "k_pe"), _strided(v, "v")
     if q.dim() != 3 or q.shape[2] != LATENT_DN + LATENT_DP:
         raise ValueError(f"q must be [Tq,H,192], got {list(q.shape)}")
     Tq, H = q.shape[:2]
-    Tk = k_nope.shape[0]
-    if tuple(k_nope.shape) != (Tk, H, LATENT_DN) or tuple(v.shape) != (Tk, H, LATENT_DV):
+    Tk = v.shape[0]
+    if k_nope.shape != (Tk, H, LATENT_DN) or v.shape != (Tk, H, LATENT_DV):
         raise ValueError("k_nope and v must be [Tk,H,128]")
-    if tuple(k_pe.shape) != (Tk, LATENT_DP):
+    if k_pe.shape != (Tk, LATENT_DP):
         raise ValueError("k_pe must be [Tk,64]")
     S = cu_q.numel() - 1
-    _shaped(cu_q, "cu_q", (S + 1,), torch.int32)
-    _shaped(cu_k, "cu_k", (S + 1,), torch.int32)
+    cu = _full(cu_q, "cu_q", (S + 1,), _I32), _full(cu_k, "cu_k", (S + 1,), _I32)
     if out is None:
-        out = torch.empty((Tq, H, LATENT_DV), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((Tq, H, LATENT_DV), dtype=_BF16, device=q.device)
     if lse is None:
-        lse = torch.empty((Tq, H), dtype=torch.float32, device=q.device)
-    _shaped(out, "out", (Tq, H, LATENT_DV), torch.bfloat16)
-    _shaped(lse, "lse", (Tq, H), torch.float32)
-    rc = lib().dsa_latent_attention_prefill(_ptr(q), q.stride(0), q.stride(1), _ptr(k_nope), k_nope.stride(0),
-                                            k_nope.stride(1), _ptr(k_pe), k_pe.stride(0), _ptr(v), v.stride(0),
-                                            v.stride(1), _ptr(cu_q), _ptr(cu_k), S, Tq, Tk, H, int(bool(causal)),
-                                            float(sm_scale), _ptr(out), _ptr(lse), _stream_ptr(stream))
+        lse = torch.empty((Tq, H), dtype=_F32, device=q.device)
+    rc = lib().dsa_latent_attention_prefill(q.data_ptr(), sq[0], sq[1], k_nope.data_ptr(), sk[0], sk[1],
+                                            k_pe.data_ptr(), sp[0], v.data_ptr(), sv[0], sv[1], *cu, S, Tq, Tk, H,
+                                            1 if causal else 0, sm_scale, _full(out, "out", (Tq, H, LATENT_DV), _BF16),
+                                            _full(lse, "lse", (Tq, H), _F32), _latent_stream(stream))
     _check("dsa_latent_attention_prefill", rc)
     return out, lse
 

@@ -4,190 +4,310 @@
 // recent others with the largest weights (equal weights: the lowest index),
 // compacted in place into logical slots [0, budget) in their old order.
 //
-// evict_select_kernel: one CTA per sequence.  Four 8-bit radix passes over
-// the order-preserving image of the weights give the smallest kept image T
-// and how many keys equal to T are kept; a pass in index order then writes the
-// kept list by prefix sums.
-// evict_move_kernel: a kept key never moves up (list entry i is >= i), so
-// walking the list upwards in batches, each read before it is written, is safe
-// in place.  Keys depend on each other only through their own bytes, so a CTA
-// takes one 128-byte column of every key of a sequence.
+// evict_select_kernel: a cluster of CTAs per sequence, each with a contiguous
+// slice of its weights in shared memory as order-preserving 32-bit images.
+// Four 8-bit radix passes (histograms summed over the cluster) give the
+// smallest kept image T and how many keys equal to T are kept; a last pass
+// counts kept keys per warp segment, and the prefix sums over warps and CTAs
+// place the kept list in index order.
+//
+// evict_move_kernel: bound by the moved bytes, 2 x 1152 per kept key (2 x 132
+// more with the indexer's cache).  A CTA takes 64 entries of a kept list, reads
+// their keys into registers, says so in a flag, and writes them to slots [64
+// c, 64 c + 64) once the entries that live in those slots have been read.  A
+// kept key never moves up (entry i is >= i), so those belong to this chunk or
+// lower ones: their flags, found by two searches in the list.  Chunks are
+// handed out in order and each reads before it waits, so the wait ends.
 #include "latent.h"
 
 namespace dsa {
 
 namespace {
-constexpr int ES_THREADS = 1024;
+constexpr int ES_THREADS = 512;
+constexpr int ES_WARPS = ES_THREADS / 32;
+constexpr int ES_COPIES = 32;              // histogram copies, one per lane: most weights share a few exponents
 constexpr int EM_THREADS = 256;
-constexpr int EM_UNROLL = 8;
-constexpr int EM_BATCH = EM_THREADS / 8 * EM_UNROLL;  // keys per batch: 8 lanes x 16 bytes per key
+constexpr int EM_KEYS = EVICT_CHUNK;       // kept keys per CTA
 
 // Order-preserving image; every NaN counts as the largest weight.
-__device__ __forceinline__ uint32_t weight_key(float w) {
-  return w != w ? 0xffffffffu : ordered_key(w);
-}
+__device__ __forceinline__ uint32_t weight_key(float w) { return w != w ? 0xffffffffu : ordered_key(w); }
 
-// Exclusive prefix sum of x over the CTA and the total (tmp: 33 ints).
-__device__ __forceinline__ int block_scan(int x, int* tmp, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int v = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
-  }
-  __syncthreads();
-  if (lane == 31) tmp[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int s = tmp[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    tmp[lane] = s;
-  }
-  __syncthreads();
-  *total = tmp[31];
-  return v - x + (warp ? tmp[warp - 1] : 0);
+template <int CS>
+__device__ __forceinline__ void cluster_barrier() {
+  if constexpr (CS > 1) cluster_sync_all();
+  else __syncthreads();
+}
+template <int CS>
+__device__ __forceinline__ int cluster_read(const int* p, int rank) {
+  if constexpr (CS > 1) return ld_dsmem(p, rank);
+  else return *p;
 }
 }  // namespace
 
+template <int CS>
 __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictParams p) {
   pdl_enter();
-  __shared__ int hist[256], pick[3], tmp[32];
-  const int b = blockIdx.x, tid = threadIdx.x;
+  extern __shared__ uint32_t s_key[];      // [p.cached] images of the slice
+  __shared__ int s_copy[ES_COPIES][256 + 1], s_hist[2][256], s_all[256], pick[3];
+  __shared__ int s_gt[ES_WARPS], s_eq[ES_WARPS], s_tot[2];
+  const int b = blockIdx.x / CS, rank = CS > 1 ? (int)cluster_ctarank() : 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int L = p.seq_lens[b];
   if (L < 0 || L > (int64_t)p.max_pages * PAGE) {
     if (tid == 0) atomicOr(&p.status->now, ST_RANGE);
     L = 0;
   }
-  __syncthreads();  // every thread has its length: new_lens may be seq_lens
-  if (L > p.budget)  // the pages the move reads and writes
-    for (int i = tid; i < ceil_div(L, PAGE); i += ES_THREADS) {
-      const int page = p.block_table[(int64_t)b * p.max_pages + i];
-      if (page < 0 || page >= p.num_pages) atomicOr(&p.status->now, ST_RANGE);
-    }
-  const int n = min(L, p.budget);
+  cluster_barrier<CS>();  // every thread has its length: new_lens may be seq_lens
+  const int n = min(L, p.budget), all = CS * ES_THREADS, me = rank * ES_THREADS + tid;
   int32_t* kept = p.kept + (int64_t)b * p.budget;
-  for (int i = n + tid; i < p.budget; i += ES_THREADS) kept[i] = -1;
-  if (L <= p.budget) {
-    for (int i = tid; i < n; i += ES_THREADS) kept[i] = i;
-  } else {
-    const float* w = p.weights + (int64_t)b * p.ld_weights;
-    const int need = p.budget - p.recent, cand = L - p.recent;
-    for (int i = tid; i < p.recent; i += ES_THREADS) kept[need + i] = cand + i;
-    if (need > 0) {
-      uint32_t prefix = 0;
-      int rem = need;  // rank of the last kept key among those that share the prefix
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < cand; i += ES_THREADS) {
-          const uint32_t k = weight_key(w[i]);
-          if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (tid < 32) radix_pick_digit(hist, rem, pick);
-        __syncthreads();
-        prefix |= (uint32_t)pick[0] << shift;
-        rem = pick[1];
-        __syncthreads();
-      }
-      int base = 0, ties = 0;  // kept so far, equal keys so far
-      for (int i0 = 0; i0 < cand; i0 += ES_THREADS) {
-        const int i = i0 + tid;
-        const uint32_t k = i < cand ? weight_key(w[i]) : 0;
-        const bool eq = i < cand && k == prefix;
-        int n_eq, n_keep;
-        const int before = block_scan(eq, tmp, &n_eq);
-        const bool keep = i < cand && (k > prefix || (eq && ties + before < rem));
-        const int at = block_scan(keep, tmp, &n_keep);
-        if (keep) kept[base + at] = i;
-        base += n_keep;
-        ties += n_eq;
-      }
-    }
-  }
-  if (tid == 0) {
+  float* new_w = p.new_w + (int64_t)b * p.budget;
+  const float* w = p.weights + (int64_t)b * p.ld_weights;
+  for (int i = n + me; i < p.budget; i += all) kept[i] = -1;
+  for (int i = me; i < p.chunks; i += all) p.flags[(int64_t)b * p.chunks + i] = 0;
+  if (me == 0) {
     p.old_lens[b] = L;
     p.new_lens[b] = n;
+    if (b == 0) *p.ticket = 0;
   }
+  if (L <= p.budget) {  // (the same in the whole cluster)
+    for (int i = me; i < n; i += all) kept[i] = i;
+    return;
+  }
+  // the pages that the move reads and writes
+  for (int i = me; i < ceil_div(L, PAGE); i += all) {
+    const int page = p.block_table[(int64_t)b * p.max_pages + i];
+    if (page < 0 || page >= p.num_pages) atomicOr(&p.status->now, ST_RANGE);
+  }
+  const int need = p.budget - p.recent, cand = L - p.recent;
+  for (int i = me; i < p.recent; i += all) {
+    kept[need + i] = cand + i;
+    new_w[need + i] = w[cand + i];
+  }
+  if (need == 0) return;
+  // this CTA's slice [lo, hi); what exceeds the cached part is read again
+  const int per = ceil_div(ceil_div(cand, CS), 32) * 32;
+  const int lo = min(cand, rank * per), hi = min(cand, lo + per), cached = min(hi, lo + p.cached);
+  auto key = [&](int i) { return i < cached ? s_key[i - lo] : weight_key(w[i]); };
+  uint32_t prefix = 0;
+  int rem = need;  // rank of the last kept key among those that share the prefix
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = tid; i < ES_COPIES * 257; i += ES_THREADS) (&s_copy[0][0])[i] = 0;
+    __syncthreads();
+    for (int i = lo + tid; i < hi; i += ES_THREADS) {
+      uint32_t k;
+      if (pass == 0) {
+        k = weight_key(w[i]);
+        if (i < cached) s_key[i - lo] = k;
+      } else {
+        k = key(i);
+      }
+      if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&s_copy[lane][(k >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      int x = 0;
+#pragma unroll
+      for (int c = 0; c < ES_COPIES; ++c) x += s_copy[c][tid];
+      s_hist[pass & 1][tid] = x;
+    }
+    cluster_barrier<CS>();  // (two buffers: the pass after the next is behind another barrier)
+    if (tid < 256) {
+      int x = 0;
+#pragma unroll
+      for (int r = 0; r < CS; ++r) x += cluster_read<CS>(&s_hist[pass & 1][tid], r);
+      s_all[tid] = x;
+    }
+    __syncthreads();
+    if (warp == 0) radix_pick_digit(s_all, rem, pick);
+    __syncthreads();
+    prefix |= (uint32_t)pick[0] << shift;
+    rem = pick[1];
+  }
+  // keys above and equal to the threshold per warp segment, warp and CTA
+  const int seg = ceil_div(ceil_div(max(0, hi - lo), ES_WARPS), 32) * 32;
+  const int s0 = min(hi, lo + warp * seg), s1 = min(hi, s0 + seg);
+  int gt = 0, eq = 0;
+  for (int i0 = s0; i0 < s1; i0 += 32) {
+    const uint32_t k = i0 + lane < s1 ? key(i0 + lane) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < s1 && k == prefix));
+  }
+  if (lane == 0) {
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
+  }
+  __syncthreads();
+  int gt0 = 0, eq0 = 0, gt1 = 0, eq1 = 0;  // before this warp in the CTA, and in the CTA
+#pragma unroll
+  for (int i = 0; i < ES_WARPS; ++i) {
+    gt0 += i < warp ? s_gt[i] : 0;
+    eq0 += i < warp ? s_eq[i] : 0;
+    gt1 += s_gt[i];
+    eq1 += s_eq[i];
+  }
+  if (tid == 0) {
+    s_tot[0] = gt1;
+    s_tot[1] = eq1;
+  }
+  cluster_barrier<CS>();
+  for (int r = 0; r < rank; ++r) {
+    gt0 += cluster_read<CS>(&s_tot[0], r);
+    eq0 += cluster_read<CS>(&s_tot[1], r);
+  }
+  const uint32_t lt = lanemask_lt();
+  for (int i0 = s0; i0 < s1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < s1 ? key(i) : 0;
+    const bool is_gt = i < s1 && k > prefix, is_eq = i < s1 && k == prefix;
+    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
+    const int e = eq0 + __popc(me_ & lt);  // equal keys before this one
+    if (is_gt || (is_eq && e < rem)) {
+      const int at = gt0 + __popc(mg & lt) + min(e, rem);
+      kept[at] = i;
+      new_w[at] = w[i];
+    }
+    gt0 += __popc(mg);
+    eq0 += __popc(me_);
+  }
+  cluster_barrier<CS>();  // nobody leaves while its counts may be read
 }
 
-// blockIdx.x: column of 128 bytes: 0-7 ckv, 8 kpe, 9 weights (and key scales), 10 indexer keys.
 __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParams p) {
   pdl_enter();
-  const int b = blockIdx.y, col = blockIdx.x, tid = threadIdx.x;
-  if (b == 0 && col == 0 && tid == 0) {  // the call's last kernel
+  __shared__ int s_from[EM_KEYS], s_to[EM_KEYS], s_job[3];  // slots (-1: stays, or a page outside the cache)
+  const int tid = threadIdx.x;
+  if (tid == 0) s_job[0] = atomicAdd(p.ticket, 1);
+  __syncthreads();
+  const int b = s_job[0] / p.chunks, c = s_job[0] % p.chunks;
+  if (s_job[0] == 0 && tid == 0) {  // the call's last kernel; only the wait below still reports
     p.status->last = p.status->now;
     p.status->now = 0;
   }
-  const int L = p.old_lens[b], n = min(L, p.budget);
-  if (L <= p.budget) return;
+  const int L = p.old_lens[b], n = p.budget;
+  if (L <= n) return;
+  const int i0 = c * EM_KEYS, i1 = min(n, i0 + EM_KEYS);
   const int32_t* kept = p.kept + (int64_t)b * p.budget;
   const int32_t* table = p.block_table + (int64_t)b * p.max_pages;
-  auto slot = [&](int s) -> int64_t {
+  auto slot = [&](int s) {
     const int page = table[s / PAGE];
-    return page >= 0 && page < p.num_pages ? (int64_t)page * PAGE + s % PAGE : -1;  // (reported by the selection)
+    return page >= 0 && page < p.num_pages ? page * PAGE + s % PAGE : -1;
   };
-  if (col == 9) {
-    float* w = p.weights + (int64_t)b * p.ld_weights;
-    for (int i0 = 0; i0 < n; i0 += EM_THREADS) {
-      const int i = i0 + tid;
-      float x = 0.f, y = 0.f;
-      int64_t to = -1, from = -1;
-      if (i < n) {
-        const int k = kept[i];
-        x = w[k];
-        if (p.k_scale) {
-          to = slot(i);
-          from = slot(k);
-          if (to >= 0 && from >= 0) y = p.k_scale[from];
-        }
-      }
-      __syncthreads();
-      if (i < n) w[i] = x;
-      if (to >= 0 && from >= 0) p.k_scale[to] = y;
-    }
-    __syncthreads();
-    for (int i = n + tid; i < L; i += EM_THREADS) w[i] = 0.f;
-    return;
-  }
-  uint8_t* base = col < 8 ? p.ckv + 128 * col : col == 8 ? p.kpe : p.k_cache;
-  const int64_t stride = col < 8 ? p.ckv_stride : col == 8 ? p.kpe_stride : 128;
-  const int lane8 = tid & 7;
-  for (int i0 = 0; i0 < n; i0 += EM_BATCH) {
-    uint4 v[EM_UNROLL];
-    int64_t to[EM_UNROLL];
-#pragma unroll
-    for (int j = 0; j < EM_UNROLL; ++j) {
-      const int i = i0 + j * (EM_THREADS / 8) + (tid >> 3);
-      to[j] = -1;
-      if (i < n) {
-        const int k = kept[i];
-        if (k != i) {
-          const int64_t from = slot(k);
-          to[j] = slot(i);
-          if (from < 0) to[j] = -1;
-          if (to[j] >= 0) v[j] = *reinterpret_cast<const uint4*>(base + from * stride + 16 * lane8);
-        }
+  bool moves = false;
+  if (tid < EM_KEYS) {
+    int from = -1, to = -1;
+    if (i0 + tid < i1) {
+      const int k = kept[i0 + tid];
+      if (k != i0 + tid) {
+        from = slot(k);
+        to = slot(i0 + tid);
       }
     }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < EM_UNROLL; ++j)
-      if (to[j] >= 0) *reinterpret_cast<uint4*>(base + to[j] * stride + 16 * lane8) = v[j];
+    moves = from >= 0 && to >= 0;
+    s_from[tid] = moves ? from : -1;
+    s_to[tid] = to;
+  } else if (tid >= EM_THREADS - 2) {
+    // entries of the list that live in the slots written here: [s_job[1], s_job[2])
+    const int limit = tid == EM_THREADS - 2 ? i0 : i1;
+    int x = 0, y = i1;  // kept[i] >= i, so none of them lies past i1
+    while (x < y) {
+      const int mid = (x + y) >> 1;
+      if (kept[mid] < limit) x = mid + 1;
+      else y = mid;
+    }
+    s_job[1 + (tid - (EM_THREADS - 2))] = x;
   }
+  // the weights: compacted by the selection, the rest of the old length 0
+  float* w = p.weights + (int64_t)b * p.ld_weights;
+  const float* new_w = p.new_w + (int64_t)b * p.budget;
+  if (i0 + tid < i1) w[i0 + tid] = new_w[i0 + tid];
+  const int strip = ceil_div(L - n, p.chunks);
+  for (int i = n + c * strip + tid; i < min(L, n + (c + 1) * strip); i += EM_THREADS) w[i] = 0.f;
+  const bool any = __syncthreads_or(moves);
+  uint4 v[EM_KEYS * 64 / EM_THREADS], e[EM_KEYS * 8 / EM_THREADS], x[EM_KEYS * 8 / EM_THREADS];
+  float scale = 0.f;
+  if (any) {
+#pragma unroll
+    for (int j = 0; j < EM_KEYS * 64 / EM_THREADS; ++j) {
+      const int k = (j * EM_THREADS + tid) >> 6;
+      if (s_from[k] >= 0) v[j] = *reinterpret_cast<const uint4*>(p.ckv + (int64_t)s_from[k] * p.ckv_stride + 16 * (tid & 63));
+    }
+#pragma unroll
+    for (int j = 0; j < EM_KEYS * 8 / EM_THREADS; ++j) {
+      const int k = (j * EM_THREADS + tid) >> 3;
+      if (s_from[k] >= 0) {
+        e[j] = *reinterpret_cast<const uint4*>(p.kpe + (int64_t)s_from[k] * p.kpe_stride + 16 * (tid & 7));
+        if (p.k_cache) x[j] = *reinterpret_cast<const uint4*>(p.k_cache + (int64_t)s_from[k] * 128 + 16 * (tid & 7));
+      }
+    }
+    if (p.k_cache && tid < EM_KEYS && s_from[tid] >= 0) scale = p.k_scale[s_from[tid]];
+  }
+  // read: publish, then wait for the lower chunks whose keys live in the
+  // slots written here (this chunk's own are behind the barrier)
+  __syncthreads();
+  int* flags = p.flags + (int64_t)b * p.chunks;
+  if (tid == 0) {
+    __threadfence();
+    atomicExch(&flags[c], 1);
+  }
+  if (!any) return;
+  if (tid == 0) {
+    const uint64_t t0 = globaltimer_ns();
+    bool ok = true;
+    for (int d = s_job[1] / EM_KEYS; ok && d < c && d * EM_KEYS < s_job[2]; ++d)
+      for (uint32_t spin = 1; *(volatile int*)&flags[d] == 0; ++spin)
+        if ((spin & 255u) == 0u && globaltimer_ns() - t0 > p.wait_ns) {
+          ok = false;
+          break;
+        }
+    __threadfence();
+    if (!ok) atomicOr(&p.status->last, ST_TIMEOUT);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < EM_KEYS * 64 / EM_THREADS; ++j) {
+    const int k = (j * EM_THREADS + tid) >> 6;
+    if (s_from[k] >= 0) *reinterpret_cast<uint4*>(p.ckv + (int64_t)s_to[k] * p.ckv_stride + 16 * (tid & 63)) = v[j];
+  }
+#pragma unroll
+  for (int j = 0; j < EM_KEYS * 8 / EM_THREADS; ++j) {
+    const int k = (j * EM_THREADS + tid) >> 3;
+    if (s_from[k] >= 0) {
+      *reinterpret_cast<uint4*>(p.kpe + (int64_t)s_to[k] * p.kpe_stride + 16 * (tid & 7)) = e[j];
+      if (p.k_cache) *reinterpret_cast<uint4*>(p.k_cache + (int64_t)s_to[k] * 128 + 16 * (tid & 7)) = x[j];
+    }
+  }
+  if (p.k_cache && tid < EM_KEYS && s_from[tid] >= 0) p.k_scale[s_to[tid]] = scale;
+}
+
+template <int CS>
+static cudaError_t launch_select_cs(const EvictParams& p, cudaStream_t s) {
+  static DeviceFlags attr_set;
+  cudaError_t e = set_smem_attr_once(evict_select_kernel<CS>, EVICT_CACHED_MAX * 4, attr_set);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.B * CS);
+  cfg.blockDim = dim3(ES_THREADS);
+  cfg.dynamicSmemBytes = 4 * (size_t)p.cached;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, evict_select_kernel<CS>, p);
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
-  count_launch();
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(p.B), dim3(ES_THREADS), 0, s, p);
+  const cudaError_t e = p.cluster > 1 ? launch_select_cs<EVICT_CLUSTER>(p, s) : launch_select_cs<1>(p, s);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(evict_move_kernel, dim3(p.k_cache ? 11 : 10, p.B), dim3(EM_THREADS), 0, s, p);
+  return launch_pdl(evict_move_kernel, dim3((unsigned)((int64_t)p.B * p.chunks)), dim3(EM_THREADS), 0, s, p);
 }
 
 }  // namespace dsa

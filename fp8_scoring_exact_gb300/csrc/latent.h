@@ -71,6 +71,10 @@ struct LatentAttnParams {
   float* logits;                // [B, blocks, max_pages, 64, n] scaled logits (-inf: not seen), for the key weights
 };
 
+constexpr int EVICT_CLUSTER = 8;
+constexpr int EVICT_CACHED_MAX = 32768;  // weights a CTA of the selection holds at most (128 KB)
+constexpr int EVICT_CHUNK = 64;
+
 // Eviction in place: every sequence of more than `budget` keys keeps its last
 // `recent` keys and the budget - recent others with the largest weights.
 struct EvictParams {
@@ -86,7 +90,13 @@ struct EvictParams {
   int B, max_pages, num_pages, budget, recent;
   int32_t* kept;                // [B, budget]
   int32_t* new_lens;            // [B]
+  int cluster, cached;          // CTAs per sequence of the selection; weights each holds in shared memory
+  int chunks;                   // of EVICT_CHUNK kept keys, per sequence
+  uint64_t wait_ns;
   int32_t* old_lens;            // [B] scratch: the validated lengths (new_lens may be seq_lens itself)
+  float* new_w;                 // [B, budget] the kept keys' weights
+  int* flags;                   // [B, chunks] 1: the chunk's keys have been read
+  int* ticket;                  // [1] chunks handed out
   LatentStatus* status;
 };
 

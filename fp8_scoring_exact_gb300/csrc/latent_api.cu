@@ -253,9 +253,6 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535)
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, HEAD + (size_t)B * 4);
-  if (!base) return DSA_ERR_CUDA;
   EvictParams p{};
   p.ckv = reinterpret_cast<uint8_t*>(ckv);
   p.kpe = reinterpret_cast<uint8_t*>(kpe);
@@ -274,7 +271,28 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   p.recent = recent;
   p.kept = kept;
   p.new_lens = new_lens;
-  p.old_lens = reinterpret_cast<int32_t*>(base + HEAD);
+  // one CTA per sequence up to 16K keys; beyond, a cluster shares them
+  const int64_t keys = (int64_t)max_pages * PAGE;
+  p.cluster = keys > 16384 ? EVICT_CLUSTER : 1;
+  p.cached = (int)std::min<int64_t>(EVICT_CACHED_MAX, keys / p.cluster + 32);
+  p.chunks = ceil_div(budget, EVICT_CHUNK);
+  if ((int64_t)B * p.chunks >= (1ll << 31) - 1) return DSA_ERR_UNSUPPORTED;
+  p.wait_ns = option_wait_ns();
+  size_t off = HEAD;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  const size_t o_len = take(4 * (size_t)B), o_w = take(4 * (size_t)B * budget), o_fl = take(4 * (size_t)B * p.chunks),
+               o_ti = take(4);
+  std::lock_guard<std::mutex> lk(g_mu);
+  uint8_t* base = get_scratch(stream, off);
+  if (!base) return DSA_ERR_CUDA;
+  p.old_lens = reinterpret_cast<int32_t*>(base + o_len);
+  p.new_w = reinterpret_cast<float*>(base + o_w);
+  p.flags = reinterpret_cast<int*>(base + o_fl);
+  p.ticket = reinterpret_cast<int*>(base + o_ti);
   p.status = reinterpret_cast<LatentStatus*>(base);
   return launch_evict(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

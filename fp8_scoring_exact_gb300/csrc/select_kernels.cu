@@ -1249,11 +1249,6 @@ constexpr int WIDE_CLUSTER = 8;
 constexpr int WIDE_THREADS = 512;
 constexpr int WIDE_UNROLL = 4;  // float4 loads in flight per thread
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ uint32_t cluster_id_x() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
@@ -1264,21 +1259,6 @@ __device__ __forceinline__ uint32_t cluster_count_x() {
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
   return r;
 }
-// all threads of all CTAs of the cluster; orders shared and global memory
-// at cluster scope
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// 32-bit load from the shared memory of CTA `rank` of the cluster, at the
-// offset `p` has in this CTA
-__device__ __forceinline__ int ld_dsmem(const int* p, uint32_t rank) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
-  int v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 __global__ void __cluster_dims__(WIDE_CLUSTER, 1, 1) __launch_bounds__(WIDE_THREADS)
     wide_cluster_kernel(const WideParams p) {
   pdl_enter();

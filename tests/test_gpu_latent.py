@@ -276,7 +276,8 @@ def test_decode_leaves_its_inputs_alone(B):
     (64, 8, [0, 1, 64, 65, 300], "random"), (100, 0, [1000, 99, 101], "ties"), (1, 1, [500, 1, 0], "random"),
     (1, 0, [500, 2], "random"), (256, 256, [1000, 257], "random"), (2048, 100, [9000, 2049, 2047], "ties"),
     (300, 10, [1300, 777], "zero"), (300, 10, [1300, 777], "nan"), (5000, 37, [70000, 5001], "random"),
-    (40, 4, list(range(0, 400, 3)), "ties"), (20000, 1000, [33000], "signed")])
+    (40, 4, list(range(0, 400, 3)), "ties"), (20000, 1000, [33000], "signed"), (777, 70, [266666, 17000, 800], "random"),
+    (16000, 15999, [16500, 16001], "random"), (15000, 0, [16384], "ties")])
 @pytest.mark.parametrize("indexer,joint,alias", [(False, False, False), (True, True, True)])
 def test_evict_matches_oracle(B, budget, recent, lens, kind, indexer, joint, alias):
     c = Cache(lens, seed=budget + recent, joint=joint)
