@@ -39,9 +39,9 @@ constexpr float PF_RESCALE_AT = 8.f;
 constexpr uint32_t PF_OFF_Q = 0;       // per tile 3 chunks of 128 rows x 64 dims
 constexpr uint32_t PF_OFF_RING = PF_OFF_Q + 6 * PF_SLOT;
 constexpr uint32_t PF_OFF_MISC = PF_OFF_RING + PF_SLOTS * PF_SLOT;
-// barriers: slot full / empty, q full / empty, then per tile S full, P full, PV done, O empty, drain
+// barriers: slot full / empty, q full / empty, then per tile S full, P full (each half), PV done, O empty, turn, drain
 constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1, B_P = B_S + 2,
-              B_V = B_P + 2, B_O = B_V + 2, B_DRAIN = B_O + 2, PF_BARS = B_DRAIN + 2;
+              B_V = B_P + 4, B_O = B_V + 2, B_TURN = B_O + 2, B_DRAIN = B_TURN + 2, PF_BARS = B_DRAIN + 2;
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // 12 + 4 int64
@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(B_S + i), 1);
       mbar_init(bar(B_P + i), 4);
+      mbar_init(bar(B_P + 2 + i), 4);
+      mbar_init(bar(B_TURN + i), 1);
       mbar_init(bar(B_V + i), 1);
       mbar_init(bar(B_O + i), 4);
       mbar_init(bar(B_DRAIN + i), 1);
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     const uint32_t leader = elect_one();
     const uint32_t d_s = tmem + 128 * t, d_o = tmem + 256 + 128 * t;
     const uint32_t q_lo = desc_lo_kmajor(sbase + PF_OFF_Q + t * 3 * PF_SLOT);
-    uint32_t seg = 0, it = 0, slot = 0;  // pieces; this tile's key tiles; ring position of the piece's first key tile
+    uint32_t seg = 0, it = 0, slot = 0, turn = 0;  // pieces; this tile's key tiles; ring position of the piece; key tiles
     bool ok = true;
     // slots [s, s + n) without reading them (each only once it has been filled:
     // its barrier counts one arrival of either issuer per filling)
@@ -286,54 +288,59 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
       const int first = pc.blk * PF_ROWS + 128 * t;
       const int mine = first < pc.seq.n ? ceil_div(keys_seen(p, pc.seq, first + 128), PF_KEYS) : 0;
       if (!(ok = mbar_wait_warp(bar(B_QF), seg & 1, abort_flag, stats))) break;
-      for (int k = k0; ok && k < k1; ++k) {
-        {
-          // S of key tile k; P of the tile before it has been read (waited for below)
-          const uint32_t s0 = slot + 5 * (k - k0);
-          if (k < mine) {
-            for (uint32_t c = 0; c < 3; ++c) {
-              const uint32_t st = (s0 + c) % PF_SLOTS;
-              if (!(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + c) / PF_SLOTS) & 1, abort_flag, stats))) break;
-              tc_fence_after();
-              const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma_bf16_ss(leader, d_s, q_lo + c * (PF_SLOT >> 4) + 2 * j, k_lo + 2 * j, ID_S, c > 0 || j > 0);
-              mma_commit_warp(leader, bar(B_EMPTY + st));
-            }
-            if (!ok) break;
-            mma_commit_warp(leader, bar(B_S + t));
-          } else {
-            ok = pass_on(s0, 3);
-            if (!ok) break;
-          }
-          if (k == k1 - 1) mma_commit_warp(leader, bar(B_QE));
-        }
-        if (k >= mine) {  // its values are not read either
-          ok = pass_on(slot + 5 * (k - k0) + 3, 2);
-        } else {
-          // O += P V of key tile k
-          const uint32_t s0 = slot + 5 * (k - k0) + 3;
-          if (!(ok = mbar_wait_warp(bar(B_P + t), it & 1, abort_flag, stats))) break;
-          if (k == k0 && !(ok = mbar_wait_warp(bar(B_O + t), (seg & 1) ^ 1, abort_flag, stats))) break;
-          for (uint32_t c = 0; c < 2; ++c) {
+      for (int k = k0; k < k1; ++k, ++turn) {
+        const uint32_t s0 = slot + 5 * (k - k0);
+        // The tiles' S are issued in turn: interleaved they would both be
+        // ready late, and both softmaxes would run while the tensor cores idle.
+        if (t == 1 || turn > 0)
+          if (!(ok = mbar_wait_warp(bar(B_TURN + t), (t == 1 ? turn : turn - 1) & 1, abort_flag, stats))) break;
+        // S of key tile k (P of the tile before it has been read: waited for below)
+        if (k < mine) {
+          for (uint32_t c = 0; c < 3; ++c) {
             const uint32_t st = (s0 + c) % PF_SLOTS;
             if (!(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + c) / PF_SLOTS) & 1, abort_flag, stats))) break;
             tc_fence_after();
-            const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
+            const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)  // 16 keys: 8 columns of P, 2 KB of V
-              mma_bf16_ts(leader, d_o + 64 * c, d_s + 8 * j, v_lo + 128 * j, ID_O, k > k0 || j > 0);
+            for (int j = 0; j < 4; ++j)
+              mma_bf16_ss(leader, d_s, q_lo + c * (PF_SLOT >> 4) + 2 * j, k_lo + 2 * j, ID_S, c > 0 || j > 0);
             mma_commit_warp(leader, bar(B_EMPTY + st));
           }
           if (!ok) break;
-          mma_commit_warp(leader, bar(B_V + t));
-          if (!(ok = mbar_wait_warp(bar(B_V + t), it & 1, abort_flag, stats))) break;
-          ++it;
+          mma_commit_warp(leader, bar(B_S + t));
+        } else if (!(ok = pass_on(s0, 3))) {
+          break;
         }
+        if (lane == 0) mbar_arrive(bar(B_TURN + (t ^ 1)));
+        if (k == k1 - 1) mma_commit_warp(leader, bar(B_QE));
+        if (k >= mine) {  // its values are not read either
+          if (!(ok = pass_on(s0 + 3, 2))) break;
+          continue;
+        }
+        // O += P V of key tile k, in the halves the weights come in
+        if (k == k0 && !(ok = mbar_wait_warp(bar(B_O + t), (seg & 1) ^ 1, abort_flag, stats))) break;
+        for (uint32_t half = 0; half < 2; ++half) {
+          if (!(ok = mbar_wait_warp(bar(B_P + 2 * half + t), it & 1, abort_flag, stats))) break;
+          for (uint32_t c = 0; c < 2; ++c) {
+            const uint32_t st = (s0 + 3 + c) % PF_SLOTS;
+            if (half == 0 && !(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + 3 + c) / PF_SLOTS) & 1, abort_flag, stats)))
+              break;
+            tc_fence_after();
+            const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT) + 512 * half;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 16 keys: 8 columns of P, 2 KB of V
+              mma_bf16_ts(leader, d_o + 64 * c, d_s + 32 * half + 8 * j, v_lo + 128 * j, ID_O,
+                          k > k0 || half > 0 || j > 0);
+            if (half == 1) mma_commit_warp(leader, bar(B_EMPTY + st));
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        mma_commit_warp(leader, bar(B_V + t));
+        if (!(ok = mbar_wait_warp(bar(B_V + t), it & 1, abort_flag, stats))) break;
+        ++it;
       }
       slot += 5 * (k1 - k0);
-      // a tile without rows or keys here leaves its softmax warps nothing to read
       ++seg;
     }
   } else if (warp >= 4) {
@@ -356,14 +363,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         mbar_wait_warp(bar(B_S + t), it & 1, abort_flag, stats);
         tc_fence_after();
         uint32_t s[128];
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+        const bool masked = (k + 1) * PF_KEYS > lim0;
+        tmem_ld32(d_s, s);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(d_s + 32 * c, s + 32 * c);
-        tmem_wait_ld();
-        if ((k + 1) * PF_KEYS > lim0) {
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld32(s + 32 * c);
+          if (c < 3) tmem_ld32(d_s + 32 * (c + 1), s + 32 * (c + 1));
+          if (!masked) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mx[(j >> 1) & 3] = fmax3(mx[(j >> 1) & 3], __uint_as_float(s[32 * c + j]), __uint_as_float(s[32 * c + j + 1]));
+          }
+        }
+        if (masked) {
           const int left = lim - k * PF_KEYS;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 128; ++c) {
             if (c >= left) s[c] = 0xff800000u;  // -inf
+            mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+          }
           // the next sequence's values share the tile: they become 0 (a
           // weight of 0 does not silence a NaN)
           const int valid = pc.seq.m - k * PF_KEYS;
@@ -377,9 +396,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             fence_proxy_async_smem();
           }
         }
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-        for (int c = 0; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
         const float top = p.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
         if (__any_sync(0xffffffffu, moves)) {
@@ -416,11 +432,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
           tmem_st32(d_s + 32 * c, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_P + 2 * c + t));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P + t));
       }
       slot += 5 * (k1 > k0 ? k1 - k0 : 0);
       // ---- the piece's result
