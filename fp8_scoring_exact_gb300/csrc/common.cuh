@@ -177,6 +177,35 @@ __device__ __forceinline__ uint64_t wait_limit(const Stats* st) {
   return l ? l : WAIT_LIMIT_NS;
 }
 
+// The same for a phase that the other CTA of a cluster arrives on.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Address of this CTA's shared-memory location in CTA `rank` of the cluster,
+// and an arrival on a barrier there.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// (release: for shared-memory writes of this thread; it takes some 1500
+// cycles, so tcgen05 accesses alone, which tcgen05.fence orders, arrive relaxed)
+template <bool RELEASE>
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
+  if constexpr (RELEASE)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  else
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // Bounded wait: true when the phase with `parity` completed; false when the
 // CTA-wide abort flag is set or the time limit passed (then it sets both the
 // abort flag and the status bit).  The polling loop is out of line: the hot
@@ -247,6 +276,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return mbar_wait_warp_slow(bar, parity, abort_flag, st);
 }
 
+// The same for a phase that another CTA of the cluster arrives on.
+__device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                       Stats* st) {
+  return mbar_wait_warp(bar, parity, abort_flag, st) && __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity));
+}
+
 // Warp-uniform bounded wait for a warp whose wake-up latency has slack (the
 // TMA producer, which runs ahead of the MMA): between polls it sleeps, so it
 // takes no issue slots from the epilogue warps that share its SM
@@ -312,6 +347,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
           dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// Loads into this CTA's shared memory that report to a barrier of the pair's
+// even CTA (`bar`: its address in the cluster).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, int x, int y, int z,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, "
+      "%4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
@@ -438,6 +490,48 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t leader, uint32_t d_tmem, ui
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
       : "memory");
+}
+// The same two over a pair of CTAs (cta_group::2, issued in the pair's even
+// CTA): A's and D's rows are split between the CTAs, B's N rows as well, each
+// at the same shared-memory and TMEM addresses in both.
+__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t b,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
+      : "memory");
+}
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 db;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 db, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
+      : "memory");
+}
+// The pair's commit: the barrier at this offset arrives once in both CTAs.
+__device__ __forceinline__ void mma_commit_pair(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\tsetp.ne.b32 e, %1, 0;\n\tmov.b16 m, 3;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 // The leader's commit: the mbarrier arrives once when all it issued completes.
 __device__ __forceinline__ void mma_commit_warp(uint32_t leader, uint32_t bar) {

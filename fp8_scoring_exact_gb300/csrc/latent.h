@@ -108,10 +108,10 @@ struct PrefillParams {
   float scale_log2;
   __nv_bfloat16* out;           // [Tq, H, 128]
   float* lse;                   // [Tq, H]
-  int grid;
+  int grid;                     // pairs of CTAs
   uint64_t wait_ns;
-  int64_t* per;                 // [1] units per CTA
-  int64_t* start;               // [grid, S + 1] first unit of each sequence, worked out by every CTA for itself
+  int64_t* per;                 // [1] units per pair
+  int64_t* start;               // [2 grid, S + 1] first unit of each sequence, worked out by every CTA for itself
   float* part_o;                // [2 grid, 256, 128] unnormalised outputs of the pieces of cut blocks
   float2* part_ml;              // [2 grid, 256]: reference maximum (base-2 units) and sum
   LatentStatus* status;
@@ -125,7 +125,8 @@ struct LatentMaps {
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 // Tensor maps of the expanded form: q [Tq, H, 192], k_nope and v [Tk, H, 128],
-// boxes of 64 dims x 1 head x 128 tokens; k_pe [Tk, 64].
+// boxes of 64 dims x 1 head x 128 queries or 64
+// keys; k_pe [Tk, 64].
 struct PrefillMaps {
   CUtensorMap q, k_nope, k_pe, v;
 };

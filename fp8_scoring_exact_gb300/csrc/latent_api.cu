@@ -107,14 +107,14 @@ bool tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t stride, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 [tokens, heads, dims], boxes of 64 dims x 1 head x 128 tokens.
+// bf16 [tokens, heads, dims], boxes of 64 dims x 1 head x box_tokens.
 bool tmap_heads(CUtensorMap* m, const void* base, int64_t tokens, int heads, int dims_, int64_t token_stride,
-                int64_t head_stride) {
+                int64_t head_stride, int box_tokens) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)dims_, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
-  const cuuint32_t box[3] = {64, 1, 128}, one[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_tokens}, one[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -324,13 +324,13 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   p.scale_log2 = sm_scale * 1.4426950408889634f;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  p.grid = std::min(option_grid(), 1024);
+  p.grid = std::max(1, std::min(option_grid(), 1024) / 2);
   p.wait_ns = option_wait_ns();
   PrefillMaps m;
-  if (!tmap_heads(&m.q, q, Tq, H, LA_DN + LA_DP, q_token_stride, q_head_stride) ||
-      !tmap_heads(&m.k_nope, k_nope, Tk, H, LA_DN, kn_token_stride, kn_head_stride) ||
-      !tmap_heads(&m.v, v, Tk, H, LA_DV, v_token_stride, v_head_stride) ||
-      !tmap_rows(&m.k_pe, k_pe, Tk, kp_token_stride, 1, 128, 1))
+  if (!tmap_heads(&m.q, q, Tq, H, LA_DN + LA_DP, q_token_stride, q_head_stride, 128) ||
+      !tmap_heads(&m.k_nope, k_nope, Tk, H, LA_DN, kn_token_stride, kn_head_stride, 64) ||
+      !tmap_heads(&m.v, v, Tk, H, LA_DV, v_token_stride, v_head_stride, 64) ||
+      !tmap_rows(&m.k_pe, k_pe, Tk, kp_token_stride, 1, 64, 1))
     return DSA_ERR_CUDA;
   size_t off = HEAD;
   auto take = [&](size_t bytes) {
@@ -338,7 +338,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
     off = align_up(off + bytes, 256);
     return o;
   };
-  const size_t o_per = take(8), o_start = take(8 * ((size_t)S + 1) * p.grid), o_ml = take(8 * 512 * (size_t)p.grid),
+  const size_t o_per = take(8), o_start = take(8 * ((size_t)S + 1) * 2 * p.grid), o_ml = take(8 * 512 * (size_t)p.grid),
                o_po = take(4 * 512 * (size_t)p.grid * LA_DV);
   std::lock_guard<std::mutex> lk(g_mu);
   uint8_t* base = get_scratch(stream, off);

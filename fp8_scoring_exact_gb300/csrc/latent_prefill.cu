@@ -5,20 +5,22 @@
 // the causal mask); a key of head h is (k_nope[s, h] | k_pe[s]), 192 dims,
 // its value v[s, h], 128 dims.  Softmax in base 2 as in latent_attn.cu.
 //
-// 640 operations per (query, key, head): bound by the tensor cores.  A CTA
-// takes blocks of 256 queries of one head, two M = 128 tiles that share every
-// key tile (128 keys) in shared memory; S (128 x 128 fp32 each) and O (128 x
-// 128 each) fill the 512 TMEM columns, the weights go back to TMEM over their
-// logits as bf16 and are the second product's A operand there:
-//     S = Q [128 x 192] . K^T    12 steps, 64 cycles each
-//     O += P [128 x 128] . V      8 steps x 2 halves of the value dims
-// While one tile's softmax runs, the tensor cores work for the other.  Each
-// tile has an issuing warp of its own: its next S may only overwrite P once
-// the product that reads P is done, a wait that must not hold up the other
-// tile.  A softmax thread owns a row: no exchange between threads, and as in
-// latent_attn.cu the reference maximum moves only past 2^8.
+// 640 operations per (query, key, head): bound by the tensor cores.  A pair of
+// CTAs (cta_group::2) takes blocks of 256 queries of one head, 128 per CTA,
+// against tiles of 128 keys:
+//     S [256 x 128] = Q [256 x 192] . K^T    12 steps
+//     O [256 x 128] += P [256 x 128] . V      8 steps
+// The pair's MMA splits the B operand: each CTA holds 64 of a tile's keys and
+// 64 of the value dims, so a key tile costs 40 KB of shared memory and of copies
+// per CTA and four of them fit beside the queries.  S has three buffers of 128 columns
+// in TMEM, O the fourth; the weights go back over their logits as bf16 and are
+// the second product's A operand there: the logits of the next tiles are made
+// while this one's softmax runs.  The softmax has two threads per row;
+// as in latent_attn.cu the reference maximum moves only past 2^8.
+// (One CTA per block with two 128-query tiles and one S buffer each ran at 56%
+// tensor time: a tile's next S had to wait for its softmax and its product.)
 //
-// Every CTA takes an equal run of the call's units (a unit: a key tile of a
+// Every pair takes an equal run of the call's units (a unit: a key tile of a
 // block, and PF_BLOCK_UNITS more per block); a block cut by a run's border is
 // joined by the merge kernel in the order of its pieces.
 #include "latent.h"
@@ -27,26 +29,31 @@ namespace dsa {
 
 namespace {
 
-constexpr int PF_ROWS = 256;           // queries per block: two MMA tiles
+constexpr int PF_ROWS = 256;           // queries per block: 128 per CTA of a pair
 constexpr int PF_KEYS = 128;           // keys per tile
 constexpr int PF_BLOCK_UNITS = 2;      // what starting and ending a block costs, in key tiles
-constexpr uint32_t PF_SLOT = PF_KEYS * 128;  // 128 rows x 64 dims, bf16
-constexpr int PF_SLOTS = 8;            // ring: a key tile takes 3 (128 + 64 dims), its values 2
-constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue, 4-7 and 8-11 softmax
+constexpr uint32_t PF_QCHUNK = 128 * 128;  // 128 queries x 64 dims, bf16
+constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
+constexpr int PF_PER_TILE = 5;         // slots of a key tile: 3 of its 64 keys (192 dims), 2 of 64 value dims
+constexpr int PF_SLOTS = 21;
+constexpr int PF_BUFS = 3;             // S buffers: with O they fill the 512 TMEM columns
+constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue (even CTA), 4-11 softmax
 constexpr int PF_THREADS = 32 * PF_WARPS;
 constexpr float PF_RESCALE_AT = 8.f;
 
-constexpr uint32_t PF_OFF_Q = 0;       // per tile 3 chunks of 128 rows x 64 dims
-constexpr uint32_t PF_OFF_RING = PF_OFF_Q + 6 * PF_SLOT;
+constexpr uint32_t PF_OFF_Q = 0;
+constexpr uint32_t PF_OFF_RING = PF_OFF_Q + 3 * PF_QCHUNK;
 constexpr uint32_t PF_OFF_MISC = PF_OFF_RING + PF_SLOTS * PF_SLOT;
-// barriers: slot full / empty, q full / empty, then per tile S full, P full (each half), PV done, O empty, turn, drain
-constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1, B_P = B_S + 2,
-              B_V = B_P + 4, B_O = B_V + 2, B_TURN = B_O + 2, B_DRAIN = B_TURN + 2, PF_BARS = B_DRAIN + 2;
+// Barriers of the even CTA: slot full, q full, P full (per buffer and half), O empty; of both: slot empty, q empty, S
+// full, product done (per buffer), values of a sequence's last tile there; drain
+constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1,
+              B_P = B_S + PF_BUFS, B_V = B_P + 2 * PF_BUFS, B_O = B_V + PF_BUFS, B_Z = B_O + 1, B_DRAIN = B_Z + 1, PF_BARS = B_DRAIN + 2;
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
-constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // 12 + 4 int64
-constexpr uint32_t PF_SMEM = PF_OFF_SCAN + 128 + 1024;
-static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128, "shared memory per CTA");
+constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // PF_WARPS + 1 int64
+constexpr uint32_t PF_OFF_ROW = PF_OFF_SCAN + 112;   // [parity][half][row]: exchanged between a row's two threads
+constexpr uint32_t PF_SMEM = PF_OFF_ROW + 2 * 2 * 128 * 4 + 1024;  // + alignment
+static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128 && 8 * (PF_WARPS + 1) <= 112, "shared memory per CTA");
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 __device__ __forceinline__ float ex2(float x) {
@@ -72,7 +79,7 @@ __device__ __forceinline__ int block_tiles(const PrefillParams& p, const Seq& s,
   return ceil_div(keys_seen(p, s, (blk + 1) * PF_ROWS), PF_KEYS);
 }
 
-// One CTA's pieces: next() gives sequence, head, block and key tiles [k0, k1).
+// One pair's pieces: next() gives sequence, head, block and key tiles [k0, k1).
 struct Pieces {
   int64_t t, t1, s0;  // next unit, end, first unit of the current block
   int z, h, blk;
@@ -118,9 +125,9 @@ struct Pieces {
 };
 
 // Numbers the units of all sequences (start[], the same in every CTA); the
-// pieces of units [c per, (c + 1) per) for c = `cta`.
+// pieces of units [c per, (c + 1) per) for c = `pair`.
 template <int THREADS>
-__device__ __forceinline__ Pieces plan_pieces(const PrefillParams& p, int64_t* start, int cta, int64_t* tmp, int* status) {
+__device__ __forceinline__ Pieces plan_pieces(const PrefillParams& p, int64_t* start, int pair, int64_t* tmp, int* status) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t base = 0;
   for (int z0 = 0; z0 < p.S; z0 += THREADS) {
@@ -152,20 +159,20 @@ __device__ __forceinline__ Pieces plan_pieces(const PrefillParams& p, int64_t* s
     base += all;
   }
   const int64_t per = max((int64_t)(PF_BLOCK_UNITS + 1), (base + p.grid - 1) / p.grid);
-  const int64_t t = min(base, cta * per);
+  const int64_t t = min(base, pair * per);
   if (tid == 0) {
     start[p.S] = base;
-    tmp[12] = 0;
+    tmp[THREADS / 32] = 0;
     if (blockIdx.x == 0) *p.per = per;
   }
   __syncthreads();
   for (int z = tid; z < p.S; z += THREADS)
-    if (start[z] <= t && t < start[z + 1]) tmp[12] = z;
+    if (start[z] <= t && t < start[z + 1]) tmp[THREADS / 32] = z;
   __syncthreads();
   Pieces r;
   r.t = t;
   r.t1 = min(base, t + per);
-  r.z = (int)tmp[12];
+  r.z = (int)tmp[THREADS / 32];
   r.s0 = start[r.z];
   bool bad;
   r.seq = load_seq(p, r.z, bad);
@@ -181,7 +188,7 @@ __device__ __forceinline__ Pieces plan_pieces(const PrefillParams& p, int64_t* s
 
 }  // namespace
 
-__global__ void __launch_bounds__(PF_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -191,6 +198,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + PF_OFF_FLAG + 4);
   Stats* stats = reinterpret_cast<Stats*>(smem + PF_OFF_STAT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  auto lead_bar = [&](int i) { return cluster_addr(bar(i), 0); };  // in the even CTA
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -201,217 +210,218 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
     tma_prefetch_desc(&maps.k_nope);
     tma_prefetch_desc(&maps.k_pe);
     tma_prefetch_desc(&maps.v);
-    for (int i = 0; i < PF_SLOTS; ++i) {
-      mbar_init(bar(B_FULL + i), 1);
-      mbar_init(bar(B_EMPTY + i), 2);  // both tiles' issuers
-    }
-    mbar_init(bar(B_QF), 1);
-    mbar_init(bar(B_QE), 2);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * PF_SLOTS + 2; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < PF_BUFS; ++i) {
       mbar_init(bar(B_S + i), 1);
-      mbar_init(bar(B_P + i), 4);
-      mbar_init(bar(B_P + 2 + i), 4);
-      mbar_init(bar(B_TURN + i), 1);
+      mbar_init(bar(B_P + 2 * i), 8);  // four softmax warps of each CTA
+      mbar_init(bar(B_P + 2 * i + 1), 8);
       mbar_init(bar(B_V + i), 1);
-      mbar_init(bar(B_O + i), 4);
-      mbar_init(bar(B_DRAIN + i), 1);
     }
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN + 1), 1);
+    mbar_init(bar(B_O), 16);
+    mbar_init(bar(B_Z), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(s_tmem), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(s_tmem), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  Pieces pc = plan_pieces<PF_THREADS>(p, p.start + (int64_t)blockIdx.x * (p.S + 1), blockIdx.x,
+  Pieces pc = plan_pieces<PF_THREADS>(p, p.start + (int64_t)blockIdx.x * (p.S + 1), blockIdx.x >> 1,
                                       reinterpret_cast<int64_t*>(smem + PF_OFF_SCAN), &stats->status);
   uint32_t n_slot = 0, n_q = 0;  // producer: copies armed
   int k0, k1, tiles;
+  const uint32_t d_o = tmem + 128 * PF_BUFS;
 
   if (warp == 0) {
     // ------------------------------------------------------- TMA producer --
+    // Each CTA loads its part; both report to the even CTA's barriers, whose
+    // producer expects the bytes of both.
     bool ok = true;
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
       if (!(ok = mbar_wait_warp(bar(B_QE), (n_q & 1) ^ 1, abort_flag, stats))) break;
-      const int row = pc.seq.q0 + pc.blk * PF_ROWS;
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar(B_QF), 6 * PF_SLOT);
-        for (int c = 0; c < 6; ++c)
-          tma_load_3d(sbase + PF_OFF_Q + c * PF_SLOT, &maps.q, 64 * (c % 3), pc.h, row + 128 * (c / 3), bar(B_QF));
+        if (rank == 0) mbar_arrive_expect_tx(bar(B_QF), 2 * 3 * PF_QCHUNK);
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d_pair(sbase + PF_OFF_Q + c * PF_QCHUNK, &maps.q, 64 * c, pc.h,
+                           pc.seq.q0 + pc.blk * PF_ROWS + 128 * rank, lead_bar(B_QF));
       }
       ++n_q;
       for (int k = k0; ok && k < k1; ++k) {
         const int key = pc.seq.k0 + k * PF_KEYS;
-        for (int c = 0; c < 5; ++c, ++n_slot) {  // k_nope, k_nope, k_pe, v, v
+        for (int c = 0; c < PF_PER_TILE; ++c, ++n_slot) {
           const int st = n_slot % PF_SLOTS;
           if (!(ok = mbar_wait_warp(bar(B_EMPTY + st), ((n_slot / PF_SLOTS) & 1) ^ 1, abort_flag, stats))) break;
           if (lane == 0) {
-            const uint32_t dst = sbase + PF_OFF_RING + st * PF_SLOT;
-            mbar_arrive_expect_tx(bar(B_FULL + st), PF_SLOT);
+            const uint32_t dst = sbase + PF_OFF_RING + st * PF_SLOT, full = lead_bar(B_FULL + st);
+            if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2 * PF_SLOT);
             if (c < 2)
-              tma_load_3d(dst, &maps.k_nope, 64 * c, pc.h, key, bar(B_FULL + st));
+              tma_load_3d_pair(dst, &maps.k_nope, 64 * c, pc.h, key + 64 * rank, full);
             else if (c == 2)
-              tma_load_2d(dst, &maps.k_pe, 0, key, bar(B_FULL + st));
+              tma_load_2d_pair(dst, &maps.k_pe, 0, key + 64 * rank, full);
             else
-              tma_load_3d(dst, &maps.v, 64 * (c - 3), pc.h, key, bar(B_FULL + st));
+              tma_load_3d_pair(dst, &maps.v, 64 * rank, pc.h, key + 64 * (c - 3), full);
           }
         }
       }
     }
-  } else if (warp == 1 || warp == 2) {
-    // ---------------------------------------- the issuer of tile `t` (0, 1) --
-    const uint32_t t = warp - 1;
-    constexpr uint32_t ID_S = idesc_bf16_f32(128, PF_KEYS, false, false);
-    constexpr uint32_t ID_O = idesc_bf16_f32(128, 64, false, true);
+  } else if (warp == 1 && rank == 0) {
+    // ----------------------------------------------------------- S issuer --
+    constexpr uint32_t ID_S = idesc_bf16_f32(256, PF_KEYS, false, false);
     const uint32_t leader = elect_one();
-    const uint32_t d_s = tmem + 128 * t, d_o = tmem + 256 + 128 * t;
-    const uint32_t q_lo = desc_lo_kmajor(sbase + PF_OFF_Q + t * 3 * PF_SLOT);
-    uint32_t seg = 0, it = 0, slot = 0, turn = 0;  // pieces; this tile's key tiles; ring position of the piece; key tiles
+    const uint32_t q_lo = desc_lo_kmajor(sbase + PF_OFF_Q);
+    uint32_t seg = 0, it = 0;
     bool ok = true;
-    // slots [s, s + n) without reading them (each only once it has been filled:
-    // its barrier counts one arrival of either issuer per filling)
-    auto pass_on = [&](uint32_t s, uint32_t n) {
-      for (uint32_t e = s + n; s < e; ++s) {
-        if (!mbar_wait_warp(bar(B_FULL + s % PF_SLOTS), (s / PF_SLOTS) & 1, abort_flag, stats)) return false;
-        if (lane == 0) mbar_arrive(bar(B_EMPTY + s % PF_SLOTS));
-      }
-      return true;
-    };
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
-      // key tiles that this query tile sees (the other tile may see one more)
-      const int first = pc.blk * PF_ROWS + 128 * t;
-      const int mine = first < pc.seq.n ? ceil_div(keys_seen(p, pc.seq, first + 128), PF_KEYS) : 0;
-      if (!(ok = mbar_wait_warp(bar(B_QF), seg & 1, abort_flag, stats))) break;
-      for (int k = k0; k < k1; ++k, ++turn) {
-        const uint32_t s0 = slot + 5 * (k - k0);
-        // The tiles' S are issued in turn: interleaved they would both be
-        // ready late, and both softmaxes would run while the tensor cores idle.
-        if (t == 1 || turn > 0)
-          if (!(ok = mbar_wait_warp(bar(B_TURN + t), (t == 1 ? turn : turn - 1) & 1, abort_flag, stats))) break;
-        // S of key tile k (P of the tile before it has been read: waited for below)
-        if (k < mine) {
-          for (uint32_t c = 0; c < 3; ++c) {
-            const uint32_t st = (s0 + c) % PF_SLOTS;
-            if (!(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + c) / PF_SLOTS) & 1, abort_flag, stats))) break;
-            tc_fence_after();
-            const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
+      if (!(ok = mbar_wait_warp_cluster(bar(B_QF), seg & 1, abort_flag, stats))) break;
+      for (int k = k0; k < k1; ++k, ++it) {
+        const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
+        // the weights that were in the buffer have been multiplied
+        if (!(ok = mbar_wait_warp(bar(B_V + sb), sp ^ 1, abort_flag, stats))) break;
+        for (uint32_t c = 0; c < 3; ++c) {
+          const uint32_t n = PF_PER_TILE * it + c, st = n % PF_SLOTS;
+          if (!(ok = mbar_wait_warp_cluster(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          tc_fence_after();
+          const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_bf16_ss(leader, d_s, q_lo + c * (PF_SLOT >> 4) + 2 * j, k_lo + 2 * j, ID_S, c > 0 || j > 0);
-            mma_commit_warp(leader, bar(B_EMPTY + st));
-          }
-          if (!ok) break;
-          mma_commit_warp(leader, bar(B_S + t));
-        } else if (!(ok = pass_on(s0, 3))) {
-          break;
-        }
-        if (lane == 0) mbar_arrive(bar(B_TURN + (t ^ 1)));
-        if (k == k1 - 1) mma_commit_warp(leader, bar(B_QE));
-        if (k >= mine) {  // its values are not read either
-          if (!(ok = pass_on(s0 + 3, 2))) break;
-          continue;
-        }
-        // O += P V of key tile k, in the halves the weights come in
-        if (k == k0 && !(ok = mbar_wait_warp(bar(B_O + t), (seg & 1) ^ 1, abort_flag, stats))) break;
-        for (uint32_t half = 0; half < 2; ++half) {
-          if (!(ok = mbar_wait_warp(bar(B_P + 2 * half + t), it & 1, abort_flag, stats))) break;
-          for (uint32_t c = 0; c < 2; ++c) {
-            const uint32_t st = (s0 + 3 + c) % PF_SLOTS;
-            if (half == 0 && !(ok = mbar_wait_warp(bar(B_FULL + st), ((s0 + 3 + c) / PF_SLOTS) & 1, abort_flag, stats)))
-              break;
-            tc_fence_after();
-            const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT) + 512 * half;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // 16 keys: 8 columns of P, 2 KB of V
-              mma_bf16_ts(leader, d_o + 64 * c, d_s + 32 * half + 8 * j, v_lo + 128 * j, ID_O,
-                          k > k0 || half > 0 || j > 0);
-            if (half == 1) mma_commit_warp(leader, bar(B_EMPTY + st));
-          }
-          if (!ok) break;
+          for (int j = 0; j < 4; ++j)
+            mma_bf16_ss_pair(leader, tmem + 128 * sb, q_lo + c * (PF_QCHUNK >> 4) + 2 * j, k_lo + 2 * j, ID_S,
+                             c > 0 || j > 0);
+          mma_commit_pair(leader, bar(B_EMPTY + st));
         }
         if (!ok) break;
-        mma_commit_warp(leader, bar(B_V + t));
-        if (!(ok = mbar_wait_warp(bar(B_V + t), it & 1, abort_flag, stats))) break;
-        ++it;
+        mma_commit_pair(leader, bar(B_S + sb));
+        if (k == k1 - 1) mma_commit_pair(leader, bar(B_QE));
       }
-      slot += 5 * (k1 - k0);
+      ++seg;
+    }
+  } else if (warp == 2 && rank == 0) {
+    // ----------------------------------------------------------- O issuer --
+    constexpr uint32_t ID_O = idesc_bf16_f32(256, LA_DV, false, true);
+    const uint32_t leader = elect_one();
+    uint32_t seg = 0, it = 0;
+    bool ok = true;
+    for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
+      if (k1 <= k0) continue;
+      // the previous piece's O has been read out
+      if (!(ok = mbar_wait_warp_cluster(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
+      for (int k = k0; ok && k < k1; ++k, ++it) {
+        const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
+        if (pc.seq.m - k * PF_KEYS < PF_KEYS) {
+          // the sequence ends in this tile: its values are there, so both
+          // CTAs' softmax warps may clear what follows
+          for (uint32_t half = 0; ok && half < 2; ++half) {
+            const uint32_t n = PF_PER_TILE * it + 3 + half;
+            ok = mbar_wait_warp_cluster(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+          }
+          if (!ok) break;
+          mma_commit_pair(leader, bar(B_Z));
+        }
+        for (uint32_t half = 0; half < 2; ++half) {  // 64 keys: the weights' halves and the values' slots
+          const uint32_t n = PF_PER_TILE * it + 3 + half, st = n % PF_SLOTS;
+          if (!(ok = mbar_wait_warp_cluster(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_warp_cluster(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
+          tc_fence_after();
+          const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // 16 keys: 8 columns of P, 2 KB of V
+            mma_bf16_ts_pair(leader, d_o, tmem + 128 * sb + 32 * half + 8 * j, v_lo + 128 * j, ID_O,
+                             k > k0 || half > 0 || j > 0);
+          mma_commit_pair(leader, bar(B_EMPTY + st));
+        }
+        if (!ok) break;
+        mma_commit_pair(leader, bar(B_V + sb));
+      }
       ++seg;
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------- softmax warps --
-    // (a wait that gives up leaves the result undefined; the loops still end)
-    const uint32_t t = (warp - 4) >> 2;
+    // Two threads per row, 64 of the 128 keys each; they exchange their maxima
+    // through shared memory (one barrier per key tile, two buffers: a warp past
+    // the next tile's barrier knows that all have read this one's).  (A wait that gives up leaves the result undefined; the loops
+    // still end.)
+    const uint32_t half = (warp - 4) >> 2;
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    const uint32_t d_s = tmem + 128 * t + lanes, d_o = tmem + 256 + 128 * t + lanes;
-    uint32_t it = 0, slot = 0;
+    float* s_row = reinterpret_cast<float*>(smem + PF_OFF_ROW);
+    const uint32_t lead_p = lead_bar(B_P + half);
+    uint32_t it = 0, tails = 0;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
-      const int first = pc.blk * PF_ROWS + 128 * t, i = first + r;  // this row's query within its sequence
-      const int mine = first < pc.seq.n ? ceil_div(keys_seen(p, pc.seq, first + 128), PF_KEYS) : 0;
-      const int lim = i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0;
-      const int lim0 = keys_seen(p, pc.seq, first + 1);  // the tile's first row sees least
-      float ref = neg_inf(), l[4] = {0.f, 0.f, 0.f, 0.f};
-      const int end = min(k1, mine);
-      for (int k = k0; k < end; ++k, ++it) {
-        mbar_wait_warp(bar(B_S + t), it & 1, abort_flag, stats);
+      const int first = pc.blk * PF_ROWS + 128 * (int)rank, i = first + r;  // this row's query within its sequence
+      const int lim = (i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0) - 64 * (int)half;
+      const int lim0 = first < pc.seq.n ? keys_seen(p, pc.seq, first + 1) : 0;  // the CTA's first row sees least
+      float ref = neg_inf();
+      uint64_t l[2] = {0, 0};                // its sum so far, in four parts
+      for (int k = k0; k < k1; ++k, ++it) {
+        const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
+        const uint32_t d_s = tmem + 128 * sb + 64 * half + lanes;  // this thread's logits
+        const uint32_t d_p = tmem + 128 * sb + 32 * half + lanes;  // its weights, over the first half's logits
+        mbar_wait_warp(bar(B_S + sb), sp, abort_flag, stats);
         tc_fence_after();
-        uint32_t s[128];
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-        const bool masked = (k + 1) * PF_KEYS > lim0;
+        uint32_t s[64];
         tmem_ld32(d_s, s);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld32(s + 32 * c);
-          if (c < 3) tmem_ld32(d_s + 32 * (c + 1), s + 32 * (c + 1));
-          if (!masked) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2)
-              mx[(j >> 1) & 3] = fmax3(mx[(j >> 1) & 3], __uint_as_float(s[32 * c + j]), __uint_as_float(s[32 * c + j + 1]));
-          }
-        }
-        if (masked) {
+        tmem_ld32(d_s + 32, s + 32);
+        tmem_wait_ld32(s);
+        tmem_wait_ld32(s + 32);
+        bool cleared = false;
+        if ((k + 1) * PF_KEYS > lim0) {
           const int left = lim - k * PF_KEYS;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
+          for (int c = 0; c < 64; ++c)
             if (c >= left) s[c] = 0xff800000u;  // -inf
-            mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
-          }
           // the next sequence's values share the tile: they become 0 (a
-          // weight of 0 does not silence a NaN)
+          // weight of 0 does not silence a NaN); a CTA's slots hold its value
+          // dims of all 128 keys
           const int valid = pc.seq.m - k * PF_KEYS;
           if (valid < PF_KEYS) {
-            for (uint32_t c = 3; c < 5; ++c) {
-              const uint32_t n = slot + 5 * (k - k0) + c;
-              mbar_wait_warp(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
-              uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + (n % PF_SLOTS) * PF_SLOT);
-              for (int x = valid * 8 + r; x < PF_KEYS * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
+            cleared = true;
+            mbar_wait_warp(bar(B_Z), tails++ & 1, abort_flag, stats);
+            for (uint32_t c = 0; c < 2; ++c) {
+              uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
+              for (int x = max(0, valid - 64 * (int)c) * 8 + 128 * (int)half + r; x < 64 * 8; x += 256)
+                v[x] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
           }
         }
-        const float top = p.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // both threads have read their logits past this barrier, so weights may
+        // be written over either's
+        float* x = s_row + 256 * (it & 1);
+        x[128 * half + r] = top;
+        named_bar_sync(1, 256);
+        top = p.scale_log2 * fmaxf(top, x[128 * (half ^ 1) + r]);
         const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
         if (__any_sync(0xffffffffu, moves)) {
           const float a = moves ? ex2(ref - top) : 1.f;  // 0 from a reference of -inf
           if (moves) ref = top;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) l[j] *= a;
-          if (k > k0) {  // (S of this tile was issued after the product before it was done)
+          for (int j = 0; j < 2; ++j) l[j] = fmul2(l[j], pack2(a, a));
+          if (k > k0) {
+            mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
+            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[16];
-              tmem_ld16(d_o + 16 * c, o);
+              const uint32_t oa = d_o + lanes + 64 * half + 16 * c;
+              tmem_ld16(oa, o);
               tmem_wait_ld();
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
-              tmem_st16(d_o + 16 * c, o);
+              tmem_st16(oa, o);
             }
           }
         }
@@ -421,54 +431,65 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
         const uint64_t nr2 = pack2(nr, nr);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 x = unpack2(fma2(pack2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale2, nr2));
-            const float e0 = ex2(x.x), e1 = ex2(x.y);
-            l[2 * (j & 1)] += e0;
-            l[2 * (j & 1) + 1] += e1;
+          for (int j = 0; j < 16; ++j) {
+            const float2 x2 = unpack2(fma2(
+                pack2(__uint_as_float(s[32 * c + 2 * j]), __uint_as_float(s[32 * c + 2 * j + 1])), scale2, nr2));
+            const float e0 = ex2(x2.x), e1 = ex2(x2.y);
+            l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
             const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_st32(d_s + 32 * c, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_P + 2 * c + t));
+          tmem_st16(d_p + 16 * c, w);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t b = lead_p + 16 * sb;
+          if (cleared) mbar_arrive_cluster<true>(b);
+          else mbar_arrive_cluster<false>(b);
         }
       }
-      slot += 5 * (k1 > k0 ? k1 - k0 : 0);
-      // ---- the piece's result
-      const float sum = (l[0] + l[1]) + (l[2] + l[3]);
-      const bool cut = k0 > 0 || k1 < tiles;
-      const int64_t part = 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0);
-      const int64_t prow = part * PF_ROWS + 128 * t + r;
+      // ---- the piece's result: a row's two sums, then each thread its value dims
+      const float2 la = unpack2(l[0]), lb = unpack2(l[1]);
+      float sum = (la.x + la.y) + (lb.x + lb.y);
+      named_bar_sync(1, 256);  // the maxima have been read
+      s_row[128 * half + r] = sum;
+      named_bar_sync(1, 256);
+      sum = s_row[r] + s_row[128 + r];
+      named_bar_sync(1, 256);
+      const bool cut = k0 > 0 || k1 < tiles, any = k1 > k0;
+      const int64_t part = 2 * (int64_t)(blockIdx.x >> 1) + (k0 == 0 ? 1 : 0);
+      const int64_t prow = part * PF_ROWS + 128 * rank + r;
       const bool here = i < pc.seq.n;
       const int64_t row = (int64_t)(pc.seq.q0 + i) * p.H + pc.h;
-      if (cut) {
-        p.part_ml[prow] = make_float2(ref, sum);
-      } else if (here) {
-        p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
+      if (half == 0) {
+        if (cut) {
+          p.part_ml[prow] = make_float2(ref, sum);
+        } else if (here) {
+          p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
+        }
       }
       const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-      const bool any = end > k0;
       if (any) {
-        mbar_wait_warp(bar(B_V + t), (it - 1) & 1, abort_flag, stats);
+        mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
         tc_fence_after();
       }
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4; ++c) {
         uint32_t o[16];
+        const int dim = 64 * half + 16 * c;
         if (any) {
-          tmem_ld16(d_o + 16 * c, o);
+          tmem_ld16(d_o + lanes + dim, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = 0;
         }
         if (cut) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * LA_DV + 16 * c);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * LA_DV + dim);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
@@ -481,15 +502,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
                 __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * LA_DV + 16 * c);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * LA_DV + dim);
           dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
           dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (k1 > k0) {
+      if (any) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_O + t));
+        if (lane == 0) mbar_arrive_cluster<false>(lead_bar(B_O));
       }
     }
   }
@@ -498,21 +519,25 @@ __global__ void __launch_bounds__(PF_THREADS, 1)
   __syncthreads();
   if (*abort_flag) {
     // before shared memory and TMEM are released, the copies and MMAs
-    // already issued land: the last phase armed on each slot, a last commit
-    if (warp == 0 && lane == 0) {
-      for (uint32_t s = 0; s < PF_SLOTS; ++s)
-        if (n_slot > s) mbar_drain(bar(B_FULL + s), ((n_slot - 1 - s) / PF_SLOTS) & 1);
-      if (n_q) mbar_drain(bar(B_QF), (n_q - 1) & 1);
-    } else if (warp == 1 || warp == 2) {
-      mma_commit_warp(elect_one(), bar(B_DRAIN + warp - 1));
-      mbar_drain(bar(B_DRAIN + warp - 1), 0);
+    // already issued land: the last phase armed on each slot (the even CTA's
+    // barriers count both CTAs' bytes), a last commit
+    if (rank == 0) {
+      if (warp == 0 && lane == 0) {
+        for (uint32_t s = 0; s < PF_SLOTS; ++s)
+          if (n_slot > s) mbar_drain(bar(B_FULL + s), ((n_slot - 1 - s) / PF_SLOTS) & 1);
+        if (n_q) mbar_drain(bar(B_QF), (n_q - 1) & 1);
+      } else if (warp == 1 || warp == 2) {
+        mma_commit_pair(elect_one(), bar(B_DRAIN + warp - 1));
+        mbar_drain(bar(B_DRAIN + warp - 1), 0);
+      }
     }
     __syncthreads();
   }
   if (threadIdx.x == 0 && stats->status) atomicOr(&p.status->now, stats->status);
+  cluster_sync_all();  // nothing of the pair is in flight any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -584,7 +609,7 @@ cudaError_t launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStr
   cudaError_t e = set_smem_attr_once(prefill_kernel, PF_SMEM, attr_set);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(prefill_kernel, dim3(p.grid), dim3(PF_THREADS), PF_SMEM, s, m, p);
+  e = launch_pdl(prefill_kernel, dim3(2 * p.grid), dim3(PF_THREADS), PF_SMEM, s, m, p);
   if (e != cudaSuccess) return e;
   count_launch();
   return launch_pdl(prefill_merge_kernel, dim3(p.grid, PF_ROWS / 32), dim3(PM_THREADS), 0, s, p);
