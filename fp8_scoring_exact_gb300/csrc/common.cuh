@@ -134,6 +134,16 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The aligned forms, for converged warps and a barrier known at compile time.
+template <int ID, int THREADS>
+__device__ __forceinline__ void bar_sync_all() {
+  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+template <int ID, int THREADS>
+__device__ __forceinline__ void bar_arrive_all() {
+  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
+
 // ------------------------------------------------------------- mbarriers ----
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -177,18 +187,6 @@ __device__ __forceinline__ uint64_t wait_limit(const Stats* st) {
   return l ? l : WAIT_LIMIT_NS;
 }
 
-// The same for a phase that the other CTA of a cluster arrives on.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Address of this CTA's shared-memory location in CTA `rank` of the cluster,
 // and an arrival on a barrier there.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
@@ -276,10 +274,57 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return mbar_wait_warp_slow(bar, parity, abort_flag, st);
 }
 
-// The same for a phase that another CTA of the cluster arrives on.
-__device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+// Warp-uniform bounded wait in which one lane polls for the warp (a poll is an
+// access per lane to one shared-memory word) and the vote orders the others
+// behind it; CLUSTER: for a phase that another CTA of the cluster arrives on.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
+        "@e mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
+        "@e mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
+        : "memory");
+  return __any_sync(0xffffffffu, ok);
+}
+template <bool CLUSTER>
+static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                        Stats* st) {
-  return mbar_wait_warp(bar, parity, abort_flag, st) && __all_sync(0xffffffffu, mbar_try_wait_cluster(bar, parity));
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_poll_warp<CLUSTER>(bar, parity)) return true;
+    if ((it & 7u) == 7u) {
+      int give_up = 0;
+      if ((threadIdx.x & 31) == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (*abort_flag) {
+          give_up = 1;
+        } else if (now - t0 > wait_limit(st)) {
+          *abort_flag = 1;
+          atomicOr(&st->status, ST_TIMEOUT);
+          give_up = 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
+    }
+  }
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, Stats* st) {
+  if (mbar_poll_warp<CLUSTER>(bar, parity)) return true;
+  return mbar_wait_one_slow<CLUSTER>(bar, parity, abort_flag, st);
 }
 
 // Warp-uniform bounded wait for a warp whose wake-up latency has slack (the

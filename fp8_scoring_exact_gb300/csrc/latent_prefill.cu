@@ -37,7 +37,7 @@ constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
 constexpr int PF_PER_TILE = 5;         // slots of a key tile: 3 of its 64 keys (192 dims), 2 of 64 value dims
 constexpr int PF_SLOTS = 21;
 constexpr int PF_BUFS = 3;             // S buffers: with O they fill the 512 TMEM columns
-constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue (even CTA), 4-11 softmax
+constexpr int PF_WARPS = 8;           // 0 copies, 1 and 2 issue (even CTA), 4-11 softmax
 constexpr int PF_THREADS = 32 * PF_WARPS;
 constexpr float PF_RESCALE_AT = 8.f;
 
@@ -219,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     }
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_DRAIN + 1), 1);
-    mbar_init(bar(B_O), 16);
+    mbar_init(bar(B_O), 8);
     mbar_init(bar(B_Z), 1);
     fence_mbar_init();
   }
@@ -281,14 +281,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     bool ok = true;
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
-      if (!(ok = mbar_wait_warp_cluster(bar(B_QF), seg & 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one<true>(bar(B_QF), seg & 1, abort_flag, stats))) break;
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         // the weights that were in the buffer have been multiplied
         if (!(ok = mbar_wait_warp(bar(B_V + sb), sp ^ 1, abort_flag, stats))) break;
         for (uint32_t c = 0; c < 3; ++c) {
           const uint32_t n = PF_PER_TILE * it + c, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_warp_cluster(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one<true>(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
@@ -312,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
       // the previous piece's O has been read out
-      if (!(ok = mbar_wait_warp_cluster(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one<true>(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
       for (int k = k0; ok && k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         if (pc.seq.m - k * PF_KEYS < PF_KEYS) {
@@ -320,15 +320,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
           // CTAs' softmax warps may clear what follows
           for (uint32_t half = 0; ok && half < 2; ++half) {
             const uint32_t n = PF_PER_TILE * it + 3 + half;
-            ok = mbar_wait_warp_cluster(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+            ok = mbar_wait_one<true>(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
           }
           if (!ok) break;
           mma_commit_pair(leader, bar(B_Z));
         }
         for (uint32_t half = 0; half < 2; ++half) {  // 64 keys: the weights' halves and the values' slots
           const uint32_t n = PF_PER_TILE * it + 3 + half, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_warp_cluster(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
-          if (!(ok = mbar_wait_warp_cluster(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one<true>(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one<true>(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
 #pragma unroll
@@ -348,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     // through shared memory (one barrier per key tile, two buffers: a warp past
     // the next tile's barrier knows that all have read this one's).  (A wait that gives up leaves the result undefined; the loops
     // still end.)
-    const uint32_t half = (warp - 4) >> 2;
+    const uint32_t half = 0;
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     float* s_row = reinterpret_cast<float*>(smem + PF_OFF_ROW);
@@ -367,16 +367,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         const uint32_t d_p = tmem + 128 * sb + 32 * half + lanes;  // its weights, over the first half's logits
         mbar_wait_warp(bar(B_S + sb), sp, abort_flag, stats);
         tc_fence_after();
-        uint32_t s[64];
-        tmem_ld32(d_s, s);
-        tmem_ld32(d_s + 32, s + 32);
-        tmem_wait_ld32(s);
-        tmem_wait_ld32(s + 32);
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(d_s + 32 * c, s + 32 * c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
         bool cleared = false;
         if ((k + 1) * PF_KEYS > lim0) {
           const int left = lim - k * PF_KEYS;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < 128; ++c)
             if (c >= left) s[c] = 0xff800000u;  // -inf
           // the next sequence's values share the tile: they become 0 (a
           // weight of 0 does not silence a NaN); a CTA's slots hold its value
@@ -387,23 +387,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
             mbar_wait_warp(bar(B_Z), tails++ & 1, abort_flag, stats);
             for (uint32_t c = 0; c < 2; ++c) {
               uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
-              for (int x = max(0, valid - 64 * (int)c) * 8 + 128 * (int)half + r; x < 64 * 8; x += 256)
+              for (int x = max(0, valid - 64 * (int)c) * 8 + 128 * (int)half + r; x < 64 * 8; x += 128)
                 v[x] = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
           }
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int c = 0; c < 64; c += 2)
+        for (int c = 0; c < 128; c += 2)
           mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // both threads have read their logits past this barrier, so weights may
-        // be written over either's
-        float* x = s_row + 256 * (it & 1);
-        x[128 * half + r] = top;
-        named_bar_sync(1, 256);
-        top = p.scale_log2 * fmaxf(top, x[128 * (half ^ 1) + r]);
+        top *= p.scale_log2;
         const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
         if (__any_sync(0xffffffffu, moves)) {
           const float a = moves ? ex2(ref - top) : 1.f;  // 0 from a reference of -inf
@@ -414,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
             mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               uint32_t o[16];
               const uint32_t oa = d_o + lanes + 64 * half + 16 * c;
               tmem_ld16(oa, o);
@@ -431,35 +427,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         const uint64_t nr2 = pack2(nr, nr);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
+          uint32_t w[32];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < 32; ++j) {
             const float2 x2 = unpack2(fma2(
-                pack2(__uint_as_float(s[32 * c + 2 * j]), __uint_as_float(s[32 * c + 2 * j + 1])), scale2, nr2));
+                pack2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale2, nr2));
             const float e0 = ex2(x2.x), e1 = ex2(x2.y);
             l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
             const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_st16(d_p + 16 * c, w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t b = lead_p + 16 * sb;
-          if (cleared) mbar_arrive_cluster<true>(b);
-          else mbar_arrive_cluster<false>(b);
+          tmem_st32(d_p + 32 * c, w);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster<false>(lead_p + 16 * sb + 8 * c);
         }
       }
       // ---- the piece's result: a row's two sums, then each thread its value dims
       const float2 la = unpack2(l[0]), lb = unpack2(l[1]);
       float sum = (la.x + la.y) + (lb.x + lb.y);
-      named_bar_sync(1, 256);  // the maxima have been read
-      s_row[128 * half + r] = sum;
-      named_bar_sync(1, 256);
-      sum = s_row[r] + s_row[128 + r];
-      named_bar_sync(1, 256);
       const bool cut = k0 > 0 || k1 < tiles, any = k1 > k0;
       const int64_t part = 2 * (int64_t)(blockIdx.x >> 1) + (k0 == 0 ? 1 : 0);
       const int64_t prow = part * PF_ROWS + 128 * rank + r;
@@ -478,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         tc_fence_after();
       }
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
         const int dim = 64 * half + 16 * c;
         if (any) {
