@@ -112,7 +112,7 @@ struct PrefillParams {
   uint64_t wait_ns;
   int64_t* per;                 // [1] units per pair
   int64_t* start;               // [2 grid, S + 1] first unit of each sequence, worked out by every CTA for itself
-  float* part_o;                // [2 grid, 256, 128] unnormalised outputs of the pieces of cut blocks
+  float* part_o;                // [2 grid, 128 / 4, 256, 4] unnormalised outputs of the pieces of cut blocks
   float2* part_ml;              // [2 grid, 256]: reference maximum (base-2 units) and sum
   LatentStatus* status;
 };

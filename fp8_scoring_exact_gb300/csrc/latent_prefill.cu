@@ -12,11 +12,11 @@
 //     O [256 x 128] += P [256 x 128] . V      8 steps
 // The pair's MMA splits the B operand: each CTA holds 64 of a tile's keys and
 // 64 of the value dims, so a key tile costs 40 KB of shared memory and of copies
-// per CTA and four of them fit beside the queries.  S has three buffers of 128 columns
+// per CTA and three and a half of them fit beside the queries and the output.  S has three buffers of 128 columns
 // in TMEM, O the fourth; the weights go back over their logits as bf16 and are
 // the second product's A operand there: the logits of the next tiles are made
-// while this one's softmax runs.  The softmax has two threads per row;
-// as in latent_attn.cu the reference maximum moves only past 2^8.
+// while this one's softmax runs, a thread per row.  As in latent_attn.cu the
+// reference maximum moves only past 2^8.
 // (One CTA per block with two 128-query tiles and one S buffer each ran at 56%
 // tensor time: a tile's next S had to wait for its softmax and its product.)
 //
@@ -35,15 +35,16 @@ constexpr int PF_BLOCK_UNITS = 2;      // what starting and ending a block costs
 constexpr uint32_t PF_QCHUNK = 128 * 128;  // 128 queries x 64 dims, bf16
 constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
 constexpr int PF_PER_TILE = 5;         // slots of a key tile: 3 of its 64 keys (192 dims), 2 of 64 value dims
-constexpr int PF_SLOTS = 21;
+constexpr int PF_SLOTS = 18;
 constexpr int PF_BUFS = 3;             // S buffers: with O they fill the 512 TMEM columns
-constexpr int PF_WARPS = 8;           // 0 copies, 1 and 2 issue (even CTA), 4-11 softmax
+constexpr int PF_WARPS = 8;           // 0 copies, 1 and 2 issue (even CTA), 4-7 softmax
 constexpr int PF_THREADS = 32 * PF_WARPS;
 constexpr float PF_RESCALE_AT = 8.f;
 
 constexpr uint32_t PF_OFF_Q = 0;
 constexpr uint32_t PF_OFF_RING = PF_OFF_Q + 3 * PF_QCHUNK;
-constexpr uint32_t PF_OFF_MISC = PF_OFF_RING + PF_SLOTS * PF_SLOT;
+constexpr uint32_t PF_OFF_OUT = PF_OFF_RING + PF_SLOTS * PF_SLOT;  // 128 output rows of 256 bytes
+constexpr uint32_t PF_OFF_MISC = PF_OFF_OUT + 128 * 2 * LA_DV;
 // Barriers of the even CTA: slot full, q full, P full (per buffer and half), O empty; of both: slot empty, q empty, S
 // full, product done (per buffer), values of a sequence's last tile there; drain
 constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1,
@@ -51,9 +52,8 @@ constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF +
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // PF_WARPS + 1 int64
-constexpr uint32_t PF_OFF_ROW = PF_OFF_SCAN + 112;   // [parity][half][row]: exchanged between a row's two threads
-constexpr uint32_t PF_SMEM = PF_OFF_ROW + 2 * 2 * 128 * 4 + 1024;  // + alignment
-static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128 && 8 * (PF_WARPS + 1) <= 112, "shared memory per CTA");
+constexpr uint32_t PF_SMEM = PF_OFF_SCAN + 8 * (PF_WARPS + 2) + 1024;  // + alignment
+static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128, "shared memory per CTA");
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 __device__ __forceinline__ float ex2(float x) {
@@ -300,6 +300,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         if (!ok) break;
         mma_commit_pair(leader, bar(B_S + sb));
         if (k == k1 - 1) mma_commit_pair(leader, bar(B_QE));
+        if (pc.seq.m - k * PF_KEYS < PF_KEYS) {
+          // the sequence ends in this tile: once its values are there, both
+          // CTAs' softmax warps may clear what follows
+          for (uint32_t c = 3; ok && c < 5; ++c) {
+            const uint32_t n = PF_PER_TILE * it + c;
+            ok = mbar_wait_one<true>(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive(bar(B_Z));
+            mbar_arrive_cluster<true>(cluster_addr(bar(B_Z), 1));
+          }
+        }
       }
       ++seg;
     }
@@ -315,16 +328,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
       if (!(ok = mbar_wait_one<true>(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
       for (int k = k0; ok && k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
-        if (pc.seq.m - k * PF_KEYS < PF_KEYS) {
-          // the sequence ends in this tile: its values are there, so both
-          // CTAs' softmax warps may clear what follows
-          for (uint32_t half = 0; ok && half < 2; ++half) {
-            const uint32_t n = PF_PER_TILE * it + 3 + half;
-            ok = mbar_wait_one<true>(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
-          }
-          if (!ok) break;
-          mma_commit_pair(leader, bar(B_Z));
-        }
         for (uint32_t half = 0; half < 2; ++half) {  // 64 keys: the weights' halves and the values' slots
           const uint32_t n = PF_PER_TILE * it + 3 + half, st = n % PF_SLOTS;
           if (!(ok = mbar_wait_one<true>(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
@@ -344,27 +347,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------- softmax warps --
-    // Two threads per row, 64 of the 128 keys each; they exchange their maxima
-    // through shared memory (one barrier per key tile, two buffers: a warp past
-    // the next tile's barrier knows that all have read this one's).  (A wait that gives up leaves the result undefined; the loops
-    // still end.)
-    const uint32_t half = 0;
+    // A thread owns a row: no exchange.  (A wait that gives up leaves the result
+    // undefined; the loops still end.)
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    float* s_row = reinterpret_cast<float*>(smem + PF_OFF_ROW);
-    const uint32_t lead_p = lead_bar(B_P + half);
+    const uint32_t lead_p = lead_bar(B_P);
     uint32_t it = 0, tails = 0;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       const int first = pc.blk * PF_ROWS + 128 * (int)rank, i = first + r;  // this row's query within its sequence
-      const int lim = (i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0) - 64 * (int)half;
-      const int lim0 = first < pc.seq.n ? keys_seen(p, pc.seq, first + 1) : 0;  // the CTA's first row sees least
+      const int lim = i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0;
+      // what the CTA's first row sees, the least (without rows here nothing matters)
+      const int lim0 = first < pc.seq.n ? keys_seen(p, pc.seq, first + 1) : 0x7fffffff;
       float ref = neg_inf();
       uint64_t l[2] = {0, 0};                // its sum so far, in four parts
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
-        const uint32_t d_s = tmem + 128 * sb + 64 * half + lanes;  // this thread's logits
-        const uint32_t d_p = tmem + 128 * sb + 32 * half + lanes;  // its weights, over the first half's logits
+        const uint32_t d_s = tmem + 128 * sb + lanes;  // the row's logits, then its weights
         mbar_wait_warp(bar(B_S + sb), sp, abort_flag, stats);
         tc_fence_after();
         uint32_t s[128];
@@ -372,27 +371,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         for (int c = 0; c < 4; ++c) tmem_ld32(d_s + 32 * c, s + 32 * c);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-        bool cleared = false;
         if ((k + 1) * PF_KEYS > lim0) {
           const int left = lim - k * PF_KEYS;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c >= left) s[c] = 0xff800000u;  // -inf
-          // the next sequence's values share the tile: they become 0 (a
-          // weight of 0 does not silence a NaN); a CTA's slots hold its value
-          // dims of all 128 keys
-          const int valid = pc.seq.m - k * PF_KEYS;
-          if (valid < PF_KEYS) {
-            cleared = true;
-            mbar_wait_warp(bar(B_Z), tails++ & 1, abort_flag, stats);
-            for (uint32_t c = 0; c < 2; ++c) {
-              uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
-              for (int x = max(0, valid - 64 * (int)c) * 8 + 128 * (int)half + r; x < 64 * 8; x += 128)
-                v[x] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        }
+        // the next sequence's values share its last tile: they become 0 (a
+        // weight of 0 does not silence a NaN); a CTA's slots hold its value
+        // dims of all 128 keys
+        const int valid = pc.seq.m - k * PF_KEYS;
+        if (valid < PF_KEYS) {
+          mbar_wait_one<true>(bar(B_Z), tails++ & 1, abort_flag, stats);
+          for (uint32_t c = 0; c < 2; ++c) {
+            uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
+            for (int x = max(0, valid - 64 * (int)c) * 8 + r; x < 64 * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();
+          // for the issuer in the other CTA (the arrivals below are relaxed)
+          __syncwarp();
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -412,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t o[16];
-              const uint32_t oa = d_o + lanes + 64 * half + 16 * c;
+              const uint32_t oa = d_o + lanes + 16 * c;
               tmem_ld16(oa, o);
               tmem_wait_ld();
 #pragma unroll
@@ -437,67 +435,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
             const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
             w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_st32(d_p + 32 * c, w);
+          tmem_st32(d_s + 32 * c, w);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster<false>(lead_p + 16 * sb + 8 * c);
         }
       }
-      // ---- the piece's result: a row's two sums, then each thread its value dims
+      // ---- the piece's result
       const float2 la = unpack2(l[0]), lb = unpack2(l[1]);
       float sum = (la.x + la.y) + (lb.x + lb.y);
       const bool cut = k0 > 0 || k1 < tiles, any = k1 > k0;
-      const int64_t part = 2 * (int64_t)(blockIdx.x >> 1) + (k0 == 0 ? 1 : 0);
-      const int64_t prow = part * PF_ROWS + 128 * rank + r;
+      const int64_t piece = 2 * (int64_t)(blockIdx.x >> 1) + (k0 == 0 ? 1 : 0);
       const bool here = i < pc.seq.n;
       const int64_t row = (int64_t)(pc.seq.q0 + i) * p.H + pc.h;
-      if (half == 0) {
-        if (cut) {
-          p.part_ml[prow] = make_float2(ref, sum);
-        } else if (here) {
-          p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
-        }
+      if (cut) {
+        p.part_ml[piece * PF_ROWS + 128 * rank + r] = make_float2(ref, sum);
+      } else if (here) {
+        p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
       }
-      const float inv = cut ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      // O into registers in one go, so that the next piece's may begin
+      uint32_t o[128];
       if (any) {
         mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
         tc_fence_after();
-      }
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[16];
-        const int dim = 64 * half + 16 * c;
-        if (any) {
-          tmem_ld16(d_o + lanes + dim, o);
-          tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0;
-        }
-        if (cut) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * LA_DV + dim);
+        for (int c = 0; c < 4; ++c) tmem_ld32(d_o + lanes + 32 * c, o + 32 * c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
-                                 __uint_as_float(o[4 * j + 3]));
-        } else if (here) {
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 b =
-                __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * LA_DV + dim);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-      if (any) {
+        for (int c = 0; c < 4; ++c) tmem_wait_ld32(o + 32 * c);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster<false>(lead_bar(B_O));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) o[c] = 0;
+      }
+      if (cut) {
+        // [piece][dim / 4][row][4]: lanes are rows
+        float4* dst = reinterpret_cast<float4*>(p.part_o) + piece * 32 * PF_ROWS + 128 * rank + r;
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          dst[c * PF_ROWS] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                         __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+      } else {
+        // through shared memory, so that a warp writes whole rows (a thread
+        // writing its own: 32 lines per instruction, 3000 cycles a block)
+        uint4* out = reinterpret_cast<uint4*>(smem + PF_OFF_OUT) + 16 * 32 * q;  // this warp's 32 rows of 16 x 16 bytes
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * j]) * inv,
+                                                           __uint_as_float(o[8 * c + 2 * j + 1]) * inv);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          out[16 * lane + (c ^ (lane & 15))] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        const int left = pc.seq.n - (first + 32 * q);  // rows of this warp that exist
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)(pc.seq.q0 + first + 32 * q) * p.H + pc.h) * LA_DV);
+#pragma unroll 4
+        for (int x = lane >> 4; x < min(32, left); x += 2)
+          dst[(int64_t)x * p.H * 16 + (lane & 15)] = out[16 * x + ((lane & 15) ^ (x & 15))];
+        __syncwarp();
       }
     }
   }
@@ -564,16 +566,16 @@ __global__ void __launch_bounds__(PM_THREADS) prefill_merge_kernel(const Prefill
   for (int r = 32 * blockIdx.y + warp; r < 32 * (int)blockIdx.y + 32; r += PM_THREADS / 32) {
     const int i = blk * PF_ROWS + r;
     if (i >= seq.n) return;
-    auto at = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * PF_ROWS + r; };
+    auto at = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
     float m = neg_inf();
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[at(c)].x);
+    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[at(c) * PF_ROWS + r].x);
     const float mm = m == neg_inf() ? 0.f : m;
     float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int64_t c = c0; c <= c1; ++c) {
-      const float2 ml = p.part_ml[at(c)];
+      const float2 ml = p.part_ml[at(c) * PF_ROWS + r];
       const float x = ex2(ml.x - mm);
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(c) * LA_DV) + lane);
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (at(c) * 32 + lane) * PF_ROWS + r);
       sum += x * ml.y;
       if (x != 0.f) {
         o.x += x * v.x;
