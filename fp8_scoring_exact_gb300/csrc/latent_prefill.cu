@@ -35,9 +35,9 @@ constexpr int PF_BLOCK_UNITS = 2;      // what starting and ending a block costs
 constexpr uint32_t PF_QCHUNK = 128 * 128;  // 128 queries x 64 dims, bf16
 constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
 constexpr int PF_PER_TILE = 5;         // slots of a key tile: 3 of its 64 keys (192 dims), 2 of 64 value dims
-constexpr int PF_SLOTS = 18;
+constexpr int PF_SLOTS = 17;
 constexpr int PF_BUFS = 3;             // S buffers: with O they fill the 512 TMEM columns
-constexpr int PF_WARPS = 8;           // 0 copies, 1 and 2 issue (even CTA), 4-7 softmax
+constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue (even CTA), 4-7 softmax, 8-11 output
 constexpr int PF_THREADS = 32 * PF_WARPS;
 constexpr float PF_RESCALE_AT = 8.f;
 
@@ -52,7 +52,8 @@ constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF +
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // PF_WARPS + 1 int64
-constexpr uint32_t PF_SMEM = PF_OFF_SCAN + 8 * (PF_WARPS + 2) + 1024;  // + alignment
+constexpr uint32_t PF_OFF_ROW = PF_OFF_SCAN + 8 * (PF_WARPS + 2);  // [parity][row] reference and sum of a piece
+constexpr uint32_t PF_SMEM = PF_OFF_ROW + 2 * 128 * 8 + 1024;      // + alignment
 static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128, "shared memory per CTA");
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
@@ -345,14 +346,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
       }
       ++seg;
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // ----------------------------------------------------- softmax warps --
     // A thread owns a row: no exchange.  (A wait that gives up leaves the result
     // undefined; the loops still end.)
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t lead_p = lead_bar(B_P);
-    uint32_t it = 0, tails = 0;
+    float2* s_row = reinterpret_cast<float2*>(smem + PF_OFF_ROW) + r;
+    uint32_t it = 0, tails = 0, seg = 0;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       const int first = pc.blk * PF_ROWS + 128 * (int)rank, i = first + r;  // this row's query within its sequence
@@ -366,16 +368,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         const uint32_t d_s = tmem + 128 * sb + lanes;  // the row's logits, then its weights
         mbar_wait_warp(bar(B_S + sb), sp, abort_flag, stats);
         tc_fence_after();
-        uint32_t s[128];
+        // (64 logits at a time: the second half is read twice, which costs less
+        // than the registers of all 128)
+        const bool masked = (k + 1) * PF_KEYS > lim0;
+        const int left = lim - k * PF_KEYS;
+        uint32_t s[64];
+        auto load = [&](int half) {
+          tmem_ld32(d_s + 64 * half, s);
+          tmem_ld32(d_s + 64 * half + 32, s + 32);
+          tmem_wait_ld32(s);
+          tmem_wait_ld32(s + 32);
+          if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(d_s + 32 * c, s + 32 * c);
+            for (int c = 0; c < 64; ++c)
+              if (64 * half + c >= left) s[c] = 0xff800000u;  // -inf
+          }
+        };
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(s + 32 * c);
-        if ((k + 1) * PF_KEYS > lim0) {
-          const int left = lim - k * PF_KEYS;
+        for (int half = 1; half >= 0; --half) {
+          load(half);
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= left) s[c] = 0xff800000u;  // -inf
+          for (int c = 0; c < 64; c += 2)
+            mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         }
         // the next sequence's values share its last tile: they become 0 (a
         // weight of 0 does not silence a NaN); a CTA's slots hold its value
@@ -392,10 +407,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
           __syncwarp();
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         top *= p.scale_log2;
         const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
@@ -425,34 +436,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         const uint64_t nr2 = pack2(nr, nr);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[32];
+          if (c == 1) load(1);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float2 x2 = unpack2(fma2(
-                pack2(__uint_as_float(s[64 * c + 2 * j]), __uint_as_float(s[64 * c + 2 * j + 1])), scale2, nr2));
-            const float e0 = ex2(x2.x), e1 = ex2(x2.y);
-            l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
-            const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int e = 32 * h + 2 * j;
+              const float2 x =
+                  unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nr2));
+              const float e0 = ex2(x.x), e1 = ex2(x.y);
+              l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
+              const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+              w[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            tmem_st16(d_s + 32 * c + 16 * h, w);
           }
-          tmem_st32(d_s + 32 * c, w);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster<false>(lead_p + 16 * sb + 8 * c);
         }
       }
-      // ---- the piece's result
       const float2 la = unpack2(l[0]), lb = unpack2(l[1]);
-      float sum = (la.x + la.y) + (lb.x + lb.y);
+      s_row[128 * (seg++ & 1)] = make_float2(ref, (la.x + la.y) + (lb.x + lb.y));
+      __syncwarp();
+      bar_sync_all<1, 256>();  // (the output warps are done with the piece before)
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------ output warps --
+    // Each piece's result, while the softmax warps are at the next piece.
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const float2* s_row = reinterpret_cast<const float2*>(smem + PF_OFF_ROW) + r;
+    uint32_t it = 0, seg = 0;
+    for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       const bool cut = k0 > 0 || k1 < tiles, any = k1 > k0;
       const int64_t piece = 2 * (int64_t)(blockIdx.x >> 1) + (k0 == 0 ? 1 : 0);
-      const bool here = i < pc.seq.n;
-      const int64_t row = (int64_t)(pc.seq.q0 + i) * p.H + pc.h;
+      const int first = pc.blk * PF_ROWS + 128 * (int)rank;
+      if (any) it += k1 - k0;
+      __syncwarp();
+      bar_sync_all<1, 256>();
+      const float2 rs = s_row[128 * (seg++ & 1)];
+      const float ref = rs.x, sum = rs.y;
       if (cut) {
-        p.part_ml[piece * PF_ROWS + 128 * rank + r] = make_float2(ref, sum);
-      } else if (here) {
-        p.lse[row] = sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
+        p.part_ml[piece * PF_ROWS + 128 * rank + r] = rs;
+      } else if (first + r < pc.seq.n) {
+        p.lse[(int64_t)(pc.seq.q0 + first + r) * p.H + pc.h] =
+            sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       // O into registers in one go, so that the next piece's may begin
@@ -496,9 +527,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         __syncwarp();
         const int left = pc.seq.n - (first + 32 * q);  // rows of this warp that exist
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)(pc.seq.q0 + first + 32 * q) * p.H + pc.h) * LA_DV);
-#pragma unroll 4
-        for (int x = lane >> 4; x < min(32, left); x += 2)
-          dst[(int64_t)x * p.H * 16 + (lane & 15)] = out[16 * x + ((lane & 15) ^ (x & 15))];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const int x = 2 * c + (lane >> 4);
+          if (x < left) dst[(int64_t)x * p.H * 16 + (lane & 15)] = out[16 * x + ((lane & 15) ^ (x & 15))];
+        }
         __syncwarp();
       }
     }
