@@ -30,6 +30,7 @@ struct LatentStatus {
 // numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
 // tiles in one item are a piece, whose id is item + c.
 constexpr int LA_ITEM_UNITS = 2;  // what starting and ending a piece costs, in tiles
+constexpr int LA_MAX_WEIGHT_ROWS = 8192;  // rows of a sequence whose lse fit in shared memory
 constexpr int LA_MIN_UNITS = LA_ITEM_UNITS + 2;  // of a CTA
 
 // Process-wide options and the launch counter (api.cu).

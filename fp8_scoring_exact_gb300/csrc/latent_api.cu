@@ -73,6 +73,7 @@ int check_cached(const LatentAttnParams& p) {
   if (!aligned16(p.q_nope) || !aligned16(p.q_pe) || !aligned16(p.ckv) || !aligned16(p.kpe) || !aligned16(p.out))
     return DSA_ERR_ARG;
   if (p.weights && p.ld_weights < (int64_t)p.max_pages * PAGE) return DSA_ERR_ARG;
+  if (p.weights && (int64_t)p.next_n * p.H > LA_MAX_WEIGHT_ROWS) return DSA_ERR_UNSUPPORTED;
   if ((int64_t)p.B * p.next_n * p.H >= (1ll << 31) / 64 || p.next_n > 65535 || (int64_t)p.max_pages * PAGE >= (1ll << 30) ||
       (int64_t)p.prefix_pages * PAGE >= (1ll << 30) || (int64_t)p.num_pages * PAGE >= (1ll << 31) || p.B > 65535)
     return DSA_ERR_UNSUPPORTED;

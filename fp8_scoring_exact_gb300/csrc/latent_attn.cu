@@ -608,51 +608,110 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   }
 }
 
-// Joins the pieces of a row, in their order: one CTA per row.  Rows whose only
-// piece was written by its CTA are left alone.
-constexpr int MG_THREADS = 256;
-constexpr int MG_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
-__global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAttnParams p) {
+// The pieces of a row: two runs of ids (prefix, own keys) and its place in their blocks.
+struct RowPieces {
+  int id0[2], cnt[2], col[2], n;
+  __device__ __forceinline__ RowPieces(const LatentAttnParams& p, int64_t row) {
+    const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = *p.per;
+    n = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int w = k ? p.prefix_items + b * p.blocks + r / p.n : (int)(row / p.n);
+      cnt[k] = id0[k] = 0;
+      col[k] = k ? r % p.n : (int)(row % p.n);
+      if (k == 0 && !p.prefix_items) continue;
+      const int s0 = p.start[w], s1 = p.start[w + 1];
+      if (s0 == s1) continue;
+      id0[k] = w + (s0 + LA_ITEM_UNITS) / per;  // the CTA of its first tile
+      cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
+      n += cnt[k];
+    }
+  }
+  // the only piece of a row without a prefix wrote its result itself
+  __device__ __forceinline__ bool done(const LatentAttnParams& p) const { return n == 1 && !p.prefix_items; }
+  __device__ __forceinline__ int64_t at(const LatentAttnParams& p, int i) const {
+    return i < cnt[0] ? (int64_t)(id0[0] + i) * p.n + col[0] : (int64_t)(id0[1] + i - cnt[0]) * p.n + col[1];
+  }
+};
+
+// The call's last kernel.  CTAs [0, rows): one row each, its pieces joined in
+// their order.  The CTAs after them, if key weights are wanted: `spread` per
+// sequence, weights[b, s] += sum over the rows that see key s of 2^(u - lse) from
+// the logits that the main kernel left, N / 4 lanes per key and 4 rows per lane;
+// they work the rows' lse out of the pieces themselves rather than wait.
+constexpr int FIN_THREADS = 256;
+constexpr int FIN_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
+template <int N>
+__global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const LatentAttnParams p, int spread) {
   pdl_enter();
-  __shared__ float s_w[MG_MAX];
+  __shared__ float s_w[FIN_MAX];
   __shared__ float s_part[LA_DC];
-  __shared__ float s_tmp[MG_THREADS / 32];
-  const int64_t row = blockIdx.x;
-  if (row == 0 && threadIdx.x == 0 && !p.weights) {  // the call's last kernel
+  __shared__ float s_tmp[FIN_THREADS / 32];
+  extern __shared__ float s_lse[];  // [rows of a sequence]
+  const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.next_n * p.H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (row == 0 && tid == 0) {
     p.status->last = p.status->now;
     p.status->now = 0;
   }
-  const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = *p.per;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int id0[2], cnt[2], col[2], n = 0;  // runs of piece ids, the row's place in its block
+  if (row >= rows) {
+    const int R = p.next_n * p.H, b = (int)(row - rows) / spread;
+    for (int i = tid; i < R; i += FIN_THREADS) {
+      const RowPieces rp(p, (int64_t)b * R + i);
+      if (rp.done(p)) {
+        s_lse[i] = p.lse[(int64_t)b * R + i];
+        continue;
+      }
+      float m = neg_inf(), sum = 0.f;
+      for (int j = 0; j < rp.n; ++j) m = fmaxf(m, p.part_ml[rp.at(p, j)].x);
+      const float mm = m == neg_inf() ? 0.f : m;
+      for (int j = 0; j < rp.n; ++j) {
+        const float2 ml = p.part_ml[rp.at(p, j)];
+        sum += ex2(ml.x - mm) * ml.y;
+      }
+      s_lse[i] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+    }
+    __syncthreads();
+    constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK;  // lanes per key, keys per step
+    bool bad;
+    const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT);
+    const int sub = tid % LPK, kk = tid / LPK;
+    for (int t = (int)(row - rows) % spread; t < tiles; t += spread) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int w = k ? p.prefix_items + b * p.blocks + r / p.n : (int)(row / p.n);
-    cnt[k] = id0[k] = 0;
-    col[k] = k ? r % p.n : (int)(row % p.n);
-    if (k == 0 && !p.prefix_items) continue;
-    const int s0 = p.start[w], s1 = p.start[w + 1];
-    if (s0 == s1) continue;
-    id0[k] = w + (s0 + LA_ITEM_UNITS) / per;  // the CTA of its first tile
-    cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
-    n += cnt[k];
+      for (int k = kk; k < LT; k += KEYS) {
+        float sum = 0.f;
+        for (int j = 0; j < p.blocks; ++j) {
+          const int64_t tile = (int64_t)(b * p.blocks + j) * p.max_pages + t;
+          const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
+          const int r = j * N + 4 * sub;
+          if (r < R) sum += u.x == neg_inf() ? 0.f : ex2(u.x - s_lse[r]);
+          if (r + 1 < R) sum += u.y == neg_inf() ? 0.f : ex2(u.y - s_lse[r + 1]);
+          if (r + 2 < R) sum += u.z == neg_inf() ? 0.f : ex2(u.z - s_lse[r + 2]);
+          if (r + 3 < R) sum += u.w == neg_inf() ? 0.f : ex2(u.w - s_lse[r + 3]);
+        }
+#pragma unroll
+        for (int o = 1; o < LPK; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int s = t * LT + k;
+        if (sub == 0 && s < len) p.weights[b * p.ld_weights + s] += sum;
+      }
+    }
+    return;
   }
-  if (n == 1 && !p.prefix_items) return;
-  auto at = [&](int i) -> int64_t {
-    return i < cnt[0] ? (int64_t)(id0[0] + i) * p.n + col[0] : (int64_t)(id0[1] + i - cnt[0]) * p.n + col[1];
-  };
+  const RowPieces rp(p, row);
+  const int n = rp.n;
+  if (rp.done(p)) return;
   float m = neg_inf();
-  for (int i = tid; i < n; i += MG_THREADS) m = fmaxf(m, p.part_ml[at(i)].x);
+  for (int i = tid; i < n; i += FIN_THREADS) m = fmaxf(m, p.part_ml[rp.at(p, i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_tmp[warp] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MG_THREADS / 32; ++i) m = fmaxf(m, s_tmp[i]);
+  for (int i = 0; i < FIN_THREADS / 32; ++i) m = fmaxf(m, s_tmp[i]);
   const float mm = m == neg_inf() ? 0.f : m;
   float sum = 0.f;
-  for (int i = tid; i < n; i += MG_THREADS) {
-    const float2 ml = p.part_ml[at(i)];
+  for (int i = tid; i < n; i += FIN_THREADS) {
+    const float2 ml = p.part_ml[rp.at(p, i)];
     const float x = ex2(ml.x - mm);
     s_w[i] = x;
     sum += x * ml.y;
@@ -664,14 +723,14 @@ __global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAt
   __syncthreads();
   sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < MG_THREADS / 32; ++i) sum += s_tmp[i];
+  for (int i = 0; i < FIN_THREADS / 32; ++i) sum += s_tmp[i];
   // two halves of the CTA take every other piece, 4 dims per thread
   const int half = tid >> 7, d = 4 * (tid & 127);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = half; i < n; i += 2) {
     const float x = s_w[i];
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(i) * LA_DC + d));
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + rp.at(p, i) * LA_DC + d));
     if (x != 0.f) {  // a piece without a visible key adds nothing
       o.x += x * v.x;
       o.y += x * v.y;
@@ -691,42 +750,6 @@ __global__ void __launch_bounds__(MG_THREADS) latent_merge_kernel(const LatentAt
   if (tid == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
 }
 
-// weights[b, s] += sum over the rows that see key s of 2^(u - lse), from the
-// logits that the main kernel left: N / 4 lanes per key, 4 rows per lane.
-constexpr int WT_THREADS = 256;
-template <int N>
-__global__ void __launch_bounds__(WT_THREADS) latent_weights_kernel(const LatentAttnParams p) {
-  pdl_enter();
-  constexpr int LPK = N / 4, KEYS = WT_THREADS / LPK;  // lanes per key, keys per step
-  const int b = blockIdx.y, R = p.next_n * p.H;
-  if (b == 0 && blockIdx.x == 0 && threadIdx.x == 0) {  // the call's last kernel
-    p.status->last = p.status->now;
-    p.status->now = 0;
-  }
-  bool bad;
-  const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT), sub = threadIdx.x % LPK, kk = threadIdx.x / LPK;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-#pragma unroll 1
-    for (int k = kk; k < LT; k += KEYS) {
-      float sum = 0.f;
-      for (int j = 0; j < p.blocks; ++j) {
-        const int64_t tile = (int64_t)(b * p.blocks + j) * p.max_pages + t;
-        const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
-        const int r = j * N + 4 * sub;
-        const float* lse = p.lse + (int64_t)b * R + r;
-        if (r < R) sum += u.x == neg_inf() ? 0.f : ex2(u.x - lse[0]);
-        if (r + 1 < R) sum += u.y == neg_inf() ? 0.f : ex2(u.y - lse[1]);
-        if (r + 2 < R) sum += u.z == neg_inf() ? 0.f : ex2(u.z - lse[2]);
-        if (r + 3 < R) sum += u.w == neg_inf() ? 0.f : ex2(u.w - lse[3]);
-      }
-#pragma unroll
-      for (int o = 1; o < LPK; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const int s = t * LT + k;
-      if (sub == 0 && s < len) p.weights[b * p.ld_weights + s] += sum;
-    }
-  }
-}
-
 template <int N>
 static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
   static DeviceFlags attr_set;
@@ -736,11 +759,9 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
   e = launch_pdl(latent_attn_kernel<N>, dim3(p.grid), dim3(LA<N>::THREADS), LA<N>::SMEM, s, m, p);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(latent_merge_kernel, dim3((unsigned)(p.B * p.next_n * p.H)), dim3(MG_THREADS), 0, s, p);
-  if (e != cudaSuccess || !p.weights) return e;
-  count_launch();
-  return launch_pdl(latent_weights_kernel<N>, dim3(min(p.max_pages, ceil_div(16 * p.grid, p.B)), p.B), dim3(WT_THREADS),
-                    0, s, p);
+  const int R = p.next_n * p.H, spread = min(p.max_pages, ceil_div(8 * p.grid, p.B));
+  return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * R + (p.weights ? p.B * spread : 0))), dim3(FIN_THREADS),
+                    p.weights ? 4 * (size_t)R : 0, s, p, spread);
 }
 
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
