@@ -4,8 +4,11 @@
 // recent others with the largest weights (equal weights: the lowest index),
 // compacted in place into logical slots [0, budget) in their old order.
 //
-// evict_select_kernel: a cluster of CTAs per sequence, each with a contiguous
-// slice of its weights in shared memory as order-preserving 32-bit images.
+// evict_select_kernel: one to eight CTAs per sequence (a cluster), each with a
+// contiguous slice of its weights in shared memory as order-preserving 32-bit
+// images.  The CTAs double while each would have more than 16K keys: the
+// cluster's barriers cost more than they save below (eviction of 64 sequences of
+// up to 32K keys: 84 us with 1 CTA each, 77 with 2, 85 with 4, 121 with 8).
 // Four 8-bit radix passes (histograms summed over the cluster) give the
 // smallest kept image T and how many keys equal to T are kept; a last pass
 // counts kept keys per warp segment, and the prefix sums over warps and CTAs
@@ -23,7 +26,7 @@
 namespace dsa {
 
 namespace {
-constexpr int ES_THREADS = 512;
+constexpr int ES_THREADS = 1024;
 constexpr int ES_WARPS = ES_THREADS / 32;
 constexpr int ES_COPIES = 32;              // histogram copies, one per lane: most weights share a few exponents
 constexpr int EM_THREADS = 256;
@@ -57,7 +60,9 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
     if (tid == 0) atomicOr(&p.status->now, ST_RANGE);
     L = 0;
   }
-  cluster_barrier<CS>();  // every thread has its length: new_lens may be seq_lens
+  // (new_lens may be seq_lens: it is written where every thread has its length,
+  // or with the same length)
+  if constexpr (CS == 1) __syncthreads();
   const int n = min(L, p.budget), all = CS * ES_THREADS, me = rank * ES_THREADS + tid;
   int32_t* kept = p.kept + (int64_t)b * p.budget;
   float* new_w = p.new_w + (int64_t)b * p.budget;
@@ -66,11 +71,11 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
   for (int i = me; i < p.chunks; i += all) p.flags[(int64_t)b * p.chunks + i] = 0;
   if (me == 0) {
     p.old_lens[b] = L;
-    p.new_lens[b] = n;
     if (b == 0) *p.ticket = 0;
   }
   if (L <= p.budget) {  // (the same in the whole cluster)
     for (int i = me; i < n; i += all) kept[i] = i;
+    if (me == 0) p.new_lens[b] = n;
     return;
   }
   // the pages that the move reads and writes
@@ -83,7 +88,11 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
     kept[need + i] = cand + i;
     new_w[need + i] = w[cand + i];
   }
-  if (need == 0) return;
+  if (need == 0) {
+    cluster_barrier<CS>();
+    if (me == 0) p.new_lens[b] = n;
+    return;
+  }
   // this CTA's slice [lo, hi); what exceeds the cached part is read again
   const int per = ceil_div(ceil_div(cand, CS), 32) * 32;
   const int lo = min(cand, rank * per), hi = min(cand, lo + per), cached = min(hi, lo + p.cached);
@@ -172,6 +181,7 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
     eq0 += __popc(me_);
   }
   cluster_barrier<CS>();  // nobody leaves while its counts may be read
+  if (me == 0) p.new_lens[b] = n;
 }
 
 __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParams p) {
@@ -304,7 +314,10 @@ static cudaError_t launch_select_cs(const EvictParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s) {
-  const cudaError_t e = p.cluster > 1 ? launch_select_cs<EVICT_CLUSTER>(p, s) : launch_select_cs<1>(p, s);
+  const cudaError_t e = p.cluster == 8   ? launch_select_cs<8>(p, s)
+                        : p.cluster == 4 ? launch_select_cs<4>(p, s)
+                        : p.cluster == 2 ? launch_select_cs<2>(p, s)
+                                         : launch_select_cs<1>(p, s);
   if (e != cudaSuccess) return e;
   count_launch();
   return launch_pdl(evict_move_kernel, dim3((unsigned)((int64_t)p.B * p.chunks)), dim3(EM_THREADS), 0, s, p);

@@ -72,7 +72,8 @@ struct LatentAttnParams {
   float* logits;                // [B, blocks, max_pages, 64, n] scaled logits (-inf: not seen), for the key weights
 };
 
-constexpr int EVICT_CLUSTER = 8;
+constexpr int EVICT_CLUSTER = 8;           // CTAs per sequence of the selection at most
+constexpr int EVICT_KEYS_PER_CTA = 16384;  // a sequence's CTAs double while each has more than that
 constexpr int EVICT_CACHED_MAX = 32768;  // weights a CTA of the selection holds at most (128 KB)
 constexpr int EVICT_CHUNK = 64;
 

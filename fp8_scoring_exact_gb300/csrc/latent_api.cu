@@ -272,9 +272,10 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   p.recent = recent;
   p.kept = kept;
   p.new_lens = new_lens;
-  // one CTA per sequence up to 16K keys; beyond, a cluster shares them
+  // CTAs per sequence of the selection
   const int64_t keys = (int64_t)max_pages * PAGE;
-  p.cluster = keys > 16384 ? EVICT_CLUSTER : 1;
+  p.cluster = 1;
+  while (p.cluster < EVICT_CLUSTER && keys > (int64_t)EVICT_KEYS_PER_CTA * p.cluster) p.cluster *= 2;
   p.cached = (int)std::min<int64_t>(EVICT_CACHED_MAX, keys / p.cluster + 32);
   p.chunks = ceil_div(budget, EVICT_CHUNK);
   if ((int64_t)B * p.chunks >= (1ll << 31) - 1) return DSA_ERR_UNSUPPORTED;

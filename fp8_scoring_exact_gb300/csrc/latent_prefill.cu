@@ -564,8 +564,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
 }
 
 // Joins the pieces of cut blocks.  CTA (c, y): if the border between the runs
-// of c and c + 1 is the first inside some block, rows [32 y, + 32) of it; one
-// warp per row at a time, 4 dims per lane.
+// of c and c + 1 is the first inside some block, rows [32 y, + 32) of it; a
+// lane per row, 16 dims per warp.
 constexpr int PM_THREADS = 256;
 __global__ void __launch_bounds__(PM_THREADS) prefill_merge_kernel(const PrefillParams p) {
   pdl_enter();
@@ -596,34 +596,43 @@ __global__ void __launch_bounds__(PM_THREADS) prefill_merge_kernel(const Prefill
   const int64_t c0 = (s0 + PF_BLOCK_UNITS) / per, c1 = (s0 + PF_BLOCK_UNITS + tiles - 1) / per;
   if (tiles == 0 || c0 != blockIdx.x || c1 == c0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = 32 * blockIdx.y + warp; r < 32 * (int)blockIdx.y + 32; r += PM_THREADS / 32) {
-    const int i = blk * PF_ROWS + r;
-    if (i >= seq.n) return;
-    auto at = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
-    float m = neg_inf();
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[at(c) * PF_ROWS + r].x);
-    const float mm = m == neg_inf() ? 0.f : m;
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t c = c0; c <= c1; ++c) {
-      const float2 ml = p.part_ml[at(c) * PF_ROWS + r];
-      const float x = ex2(ml.x - mm);
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (at(c) * 32 + lane) * PF_ROWS + r);
-      sum += x * ml.y;
+  const int r = 32 * blockIdx.y + lane, i = blk * PF_ROWS + r;
+  if (blk * PF_ROWS + 32 * (int)blockIdx.y >= seq.n) return;
+  auto at = [&](int64_t c) { return 2 * c + (c == c0 ? 1 : 0); };
+  float m = neg_inf();
+  for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[at(c) * PF_ROWS + r].x);
+  const float mm = m == neg_inf() ? 0.f : m;
+  float sum = 0.f, o[16];
+#pragma unroll
+  for (int d = 0; d < 16; ++d) o[d] = 0.f;
+  for (int64_t c = c0; c <= c1; ++c) {
+    const float2 ml = p.part_ml[at(c) * PF_ROWS + r];
+    const float x = ex2(ml.x - mm);
+    sum += x * ml.y;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o) + (at(c) * 32 + 4 * warp + d) * PF_ROWS + r);
       if (x != 0.f) {
-        o.x += x * v.x;
-        o.y += x * v.y;
-        o.z += x * v.z;
-        o.w += x * v.w;
+        o[4 * d] += x * v.x;
+        o[4 * d + 1] += x * v.y;
+        o[4 * d + 2] += x * v.z;
+        o[4 * d + 3] += x * v.w;
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t row = (int64_t)(seq.q0 + i) * p.H + h;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DV + 4 * lane);
-    dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-    if (lane == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
   }
+  if (i >= seq.n) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = (int64_t)(seq.q0 + i) * p.H + h;
+  uint32_t w[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * d] * inv, o[2 * d + 1] * inv);
+    w[d] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + row * LA_DV + 16 * warp);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (warp == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
 }
 
 cudaError_t launch_prefill(const PrefillMaps& m, const PrefillParams& p, cudaStream_t s) {
