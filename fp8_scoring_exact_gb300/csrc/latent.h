@@ -30,7 +30,7 @@ struct LatentStatus {
 // numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
 // tiles in one item are a piece, whose id is item + c.
 constexpr int LA_ITEM_UNITS = 2;  // what starting and ending a piece costs, in tiles
-constexpr int LA_MAX_WEIGHT_ROWS = 8192;  // rows of a sequence whose lse fit in shared memory
+constexpr int LA_MAX_WEIGHT_ROWS = 4096;  // rows of a sequence with key weights (their sums lie in shared memory)
 constexpr int LA_MIN_UNITS = LA_ITEM_UNITS + 2;  // of a CTA
 
 // Process-wide options and the launch counter (api.cu).
@@ -69,7 +69,7 @@ struct LatentAttnParams {
   int32_t* start;               // [grid, items + 1] first unit of each item, worked out by every CTA for itself
   float* part_o;                // [items + grid, n, 512] unnormalised outputs of the pieces
   float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
-  float* logits;                // [B, blocks, max_pages, 64, n] scaled logits (-inf: not seen), for the key weights
+  float* logits;                // [B, blocks, max_pages, 64, n] unscaled logits (-inf: not seen), for the key weights
 };
 
 constexpr int EVICT_CLUSTER = 8;           // CTAs per sequence of the selection at most

@@ -73,8 +73,8 @@ struct LA {
   static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base, rescale, scan
   static constexpr uint32_t OFF_STAT = OFF_FLAG + 128;                           // Stats: this CTA's status and wait limit
   static constexpr uint32_t SMEM = OFF_STAT + 128 + 1024;                        // + alignment
-  static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer
-  static constexpr uint32_t TMEM_COLS = N == 64 ? 512 : N == 32 ? 256 : 128;     // 6 N, to a power of two
+  static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer (2 N each)
+  static constexpr uint32_t TMEM_COLS = N == 64 ? 512 : N == 32 ? 256 : 128;     // 8 N
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -341,6 +341,10 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
     constexpr uint32_t ID_S = idesc_bf16_f32(64, N, false, false);
     const uint32_t leader = elect_one();
     const uint32_t q_lo = desc_lo_kmajor(sbase + C::OFF_Q);
+    // Each step's addition to the accumulator truncates.  Where the logits
+    // themselves are wanted (key weights come back in fp32) their 36 steps are
+    // split over two accumulators, which halves that error.
+    const uint32_t split = p.logits ? 2 : 4;
     bool ok = true;
     while (ok && runs.next(w, k0, k1, whole)) {
       if (!(ok = mbar_wait_warp(bar(C::B_QF), seg & 1, abort_flag, stats))) break;
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         const uint32_t sb = it & 1;
         if (!(ok = mbar_wait_warp(bar(C::B_SE + sb), ((it >> 1) & 1) ^ 1, abort_flag, stats))) break;
         tc_fence_after();
-        const uint32_t d = tmem + C::TMEM_S + sb * N;
+        const uint32_t d = tmem + C::TMEM_S + sb * 2 * N;
         // the rope part first, so that its slot comes free first
         const uint32_t ks = it % C::KPES;
         if (!(ok = mbar_wait_warp(bar(C::B_KF + ks), (it / C::KPES) & 1, abort_flag, stats))) break;
@@ -363,8 +367,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
           const uint32_t k_lo = desc_lo_kmajor(sbase + C::OFF_PAIR + st * PAIR);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            mma_bf16_ss(leader, d, k_lo + (j >> 2) * (CHUNK >> 4) + 2 * (j & 3),
-                        q_lo + (2 * c + (j >> 2)) * (N * 128 >> 4) + 2 * (j & 3), ID_S, 1);
+            mma_bf16_ss(leader, d + (c >= split ? N : 0), k_lo + (j >> 2) * (CHUNK >> 4) + 2 * (j & 3),
+                        q_lo + (2 * c + (j >> 2)) * (N * 128 >> 4) + 2 * (j & 3), ID_S, c != split || j > 0);
         }
         if (!ok) break;
         mma_commit_warp(leader, bar(C::B_SF + sb));
@@ -423,10 +427,18 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         mbar_wait_warp(bar(C::B_SF + sb), (it >> 1) & 1, abort_flag, stats);
         tc_fence_after();
         uint32_t s[4 * M8];
-        const uint32_t sa = tmem + C::TMEM_S + sb * N + cb + ((uint32_t)(32 * q) << 16);
+        const uint32_t sa = tmem + C::TMEM_S + sb * 2 * N + cb + ((uint32_t)(32 * q) << 16);
         if constexpr (M8 == 4) tmem_ld16x256b_x4(sa, s);
         if constexpr (M8 == 2) tmem_ld16x256b_x2(sa, s);
         tmem_wait_ld();
+        if (p.logits) {
+          uint32_t s2[4 * M8];
+          if constexpr (M8 == 4) tmem_ld16x256b_x4(sa + N, s2);
+          if constexpr (M8 == 2) tmem_ld16x256b_x2(sa + N, s2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 4 * M8; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(s2[i]));
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_SE + sb));
@@ -461,8 +473,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
           float* dst = p.logits + (((int64_t)w * p.max_pages + k) * LT + 16 * q + g) * N + cc;
 #pragma unroll
           for (int m = 0; m < M8; ++m) {
-            *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(u[m][0] * p.scale_log2, u[m][1] * p.scale_log2);
-            *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2] * p.scale_log2, u[m][3] * p.scale_log2);
+            *reinterpret_cast<float2*>(dst + 8 * m) = make_float2(u[m][0], u[m][1]);
+            *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2], u[m][3]);
           }
         }
         float mx[2 * M8];
@@ -552,9 +564,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         if (direct) {
           s_alpha[st_id] = sum == 0.f ? 0.f : 1.f / sum;
           if (st_id < im.nrows) p.lse[im.row0 + st_id] = sum == 0.f ? neg_inf() : s_ref[st_id] + log2f(sum);
-        } else {
-          p.part_ml[piece * N + st_id] = make_float2(ref, sum);
         }
+        if (!direct || p.logits) p.part_ml[piece * N + st_id] = make_float2(ref, sum);
       }
       named_bar_sync(1, C::ST);
       mbar_wait_warp(bar(C::B_VD + ((it - 1) & 1)), ((it - 1) >> 1) & 1, abort_flag, stats);
@@ -636,9 +647,10 @@ struct RowPieces {
 
 // The call's last kernel.  CTAs [0, rows): one row each, its pieces joined in
 // their order.  The CTAs after them, if key weights are wanted: `spread` per
-// sequence, weights[b, s] += sum over the rows that see key s of 2^(u - lse) from
+// sequence, weights[b, s] += sum over the rows that see key s of 2^(u - m) / l from
 // the logits that the main kernel left, N / 4 lanes per key and 4 rows per lane;
-// they work the rows' lse out of the pieces themselves rather than wait.
+// they work the rows' maxima m and sums l out of the pieces themselves rather
+// than wait (and than use lse = m + log2 l, which as one number has lost bits).
 constexpr int FIN_THREADS = 256;
 constexpr int FIN_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
 template <int N>
@@ -647,7 +659,7 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
   __shared__ float s_w[FIN_MAX];
   __shared__ float s_part[LA_DC];
   __shared__ float s_tmp[FIN_THREADS / 32];
-  extern __shared__ float s_lse[];  // [rows of a sequence]
+  extern __shared__ float2 s_ml[];  // [rows of a sequence] (-m, 1 / l)
   const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.next_n * p.H;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (row == 0 && tid == 0) {
@@ -658,10 +670,6 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
     const int R = p.next_n * p.H, b = (int)(row - rows) / spread;
     for (int i = tid; i < R; i += FIN_THREADS) {
       const RowPieces rp(p, (int64_t)b * R + i);
-      if (rp.done(p)) {
-        s_lse[i] = p.lse[(int64_t)b * R + i];
-        continue;
-      }
       float m = neg_inf(), sum = 0.f;
       for (int j = 0; j < rp.n; ++j) m = fmaxf(m, p.part_ml[rp.at(p, j)].x);
       const float mm = m == neg_inf() ? 0.f : m;
@@ -669,7 +677,7 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
         const float2 ml = p.part_ml[rp.at(p, j)];
         sum += ex2(ml.x - mm) * ml.y;
       }
-      s_lse[i] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+      s_ml[i] = make_float2(-mm, sum == 0.f ? 0.f : 1.f / sum);
     }
     __syncthreads();
     constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK;  // lanes per key, keys per step
@@ -684,10 +692,10 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
           const int64_t tile = (int64_t)(b * p.blocks + j) * p.max_pages + t;
           const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
           const int r = j * N + 4 * sub;
-          if (r < R) sum += u.x == neg_inf() ? 0.f : ex2(u.x - s_lse[r]);
-          if (r + 1 < R) sum += u.y == neg_inf() ? 0.f : ex2(u.y - s_lse[r + 1]);
-          if (r + 2 < R) sum += u.z == neg_inf() ? 0.f : ex2(u.z - s_lse[r + 2]);
-          if (r + 3 < R) sum += u.w == neg_inf() ? 0.f : ex2(u.w - s_lse[r + 3]);
+          const float v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (r + e < R && v[e] != neg_inf()) sum += ex2(fmaf(v[e], p.scale_log2, s_ml[r + e].x)) * s_ml[r + e].y;
         }
 #pragma unroll
         for (int o = 1; o < LPK; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -761,7 +769,7 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
   count_launch();
   const int R = p.next_n * p.H, spread = min(p.max_pages, ceil_div(8 * p.grid, p.B));
   return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * R + (p.weights ? p.B * spread : 0))), dim3(FIN_THREADS),
-                    p.weights ? 4 * (size_t)R : 0, s, p, spread);
+                    p.weights ? 8 * (size_t)R : 0, s, p, spread);
 }
 
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {

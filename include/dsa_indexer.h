@@ -294,7 +294,7 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
  *   block_table [B, max_pages]        seq_lens [B] int32
  *   out [B, next_n, H, 512] bf16      lse [B, next_n, H] fp32
  *   weights [B, ld_weights] fp32 or null, ld_weights >= 64 * max_pages (with
- *           weights, next_n * H <= 8192)
+ *           weights, next_n * H <= 4096)
  */
 DSA_API int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe,
                                        const uint16_t* ckv, int64_t ckv_stride,

@@ -35,7 +35,7 @@ PREFILL = dict(q=OK, qs=16 * 192, qh=192, kn=OK, kns=2048, knh=128, kp=OK, kps=6
     ({"cs": 504}, ARG), ({"cs": 516}, ARG), ({"ks": 56}, ARG), ({"ks": 65}, ARG),
     ({"w": OK, "ldw": 255}, ARG),
     ({"B": 65536}, UNSUPPORTED), ({"np": 1 << 25}, UNSUPPORTED), ({"mp": 1 << 24}, UNSUPPORTED),
-    ({"H": 1 << 25}, UNSUPPORTED), ({"H": 8193, "w": OK, "ldw": 256}, UNSUPPORTED)])
+    ({"H": 1 << 25}, UNSUPPORTED), ({"H": 4097, "w": OK, "ldw": 256}, UNSUPPORTED)])
 def test_paged_refusals(change, code):
     assert _call("dsa_latent_attention_paged", PAGED, change) == code
 
