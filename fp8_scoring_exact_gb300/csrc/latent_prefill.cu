@@ -48,7 +48,7 @@ constexpr uint32_t PF_OFF_MISC = PF_OFF_OUT + 128 * 2 * LA_DV;
 // Barriers of the even CTA: slot full, q full, P full (per buffer and half), O empty; of both: slot empty, q empty, S
 // full, product done (per buffer), values of a sequence's last tile there; drain
 constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF + 1, B_S = B_QE + 1,
-              B_P = B_S + PF_BUFS, B_V = B_P + 2 * PF_BUFS, B_O = B_V + PF_BUFS, B_Z = B_O + 1, B_DRAIN = B_Z + 1, PF_BARS = B_DRAIN + 2;
+              B_P = B_S + PF_BUFS, B_V = B_P + 2 * PF_BUFS, B_O = B_V + PF_BUFS, B_Z = B_O + 1, B_DRAIN = B_Z + PF_BUFS, PF_BARS = B_DRAIN + 2;
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // PF_WARPS + 1 int64
@@ -221,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     mbar_init(bar(B_DRAIN), 1);
     mbar_init(bar(B_DRAIN + 1), 1);
     mbar_init(bar(B_O), 8);
-    mbar_init(bar(B_Z), 1);
+    for (int i = 0; i < PF_BUFS; ++i) mbar_init(bar(B_Z + i), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -303,15 +303,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         if (k == k1 - 1) mma_commit_pair(leader, bar(B_QE));
         if (pc.seq.m - k * PF_KEYS < PF_KEYS) {
           // the sequence ends in this tile: once its values are there, both
-          // CTAs' softmax warps may clear what follows
+          // CTAs' softmax warps may clear what follows (a barrier per S buffer:
+          // with blocks of one tile this warp is up to three ends ahead)
           for (uint32_t c = 3; ok && c < 5; ++c) {
             const uint32_t n = PF_PER_TILE * it + c;
             ok = mbar_wait_one<true>(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
           }
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive(bar(B_Z));
-            mbar_arrive_cluster<true>(cluster_addr(bar(B_Z), 1));
+            mbar_arrive(bar(B_Z + sb));
+            mbar_arrive_cluster<true>(cluster_addr(bar(B_Z + sb), 1));
           }
         }
       }
@@ -354,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t lead_p = lead_bar(B_P);
     float2* s_row = reinterpret_cast<float2*>(smem + PF_OFF_ROW) + r;
-    uint32_t it = 0, tails = 0, seg = 0;
+    uint32_t it = 0, tails = 0, seg = 0;  // tails: the phase of each buffer's B_Z
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       const int first = pc.blk * PF_ROWS + 128 * (int)rank, i = first + r;  // this row's query within its sequence
@@ -397,7 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         // dims of all 128 keys
         const int valid = pc.seq.m - k * PF_KEYS;
         if (valid < PF_KEYS) {
-          mbar_wait_one<true>(bar(B_Z), tails++ & 1, abort_flag, stats);
+          mbar_wait_one<true>(bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
+          tails ^= 1u << sb;
           for (uint32_t c = 0; c < 2; ++c) {
             uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
             for (int x = max(0, valid - 64 * (int)c) * 8 + r; x < 64 * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);

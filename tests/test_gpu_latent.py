@@ -389,6 +389,26 @@ def test_prefill_matches_oracle(B, H, qs, ks, joint, causal):
     _check_prefill(q, kv, kp, cu, out, lse, causal)
 
 
+@pytest.mark.parametrize("H,qs,ks", [(16, [90] * 40, [90] * 40), (16, [1, 130, 2] * 30, [128, 131, 200] * 30),
+                                     (31, [5] * 60, [300, 0, 256, 129] * 15), (64, [300, 40, 17] * 4, [300, 40, 17] * 4)])
+def test_prefill_of_many_short_sequences(B, H, qs, ks):
+    """Many blocks of one to three key tiles per CTA pair, most ending inside a tile."""
+    q, kv, kp, dev, cu = _prefill_inputs(qs, ks, H, seed=len(qs) + H, joint=True)
+    out, lse = B.latent_attention_prefill(*dev, SCALE)
+    assert B.latent_last_status() == 0
+    _check_prefill(q, kv, kp, cu, out, lse, True)
+
+
+@pytest.mark.parametrize("nn,H,lens", [(1, 16, [3, 64, 65, 1, 0, 130] * 120), (2, 64, [70, 1, 63] * 100)])
+def test_decode_of_many_short_sequences(B, nn, H, lens):
+    """Many pieces of one to three tiles per CTA."""
+    c = Cache(lens, seed=70 + H)
+    qn, qp = _queries(len(lens), nn, H, seed=71)
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == 0
+    _check_decode(c, qn, qp, out, lse)
+
+
 @pytest.mark.parametrize("scale,grow", [(12.0, False), (1.0, True), (1e-3, False)])
 def test_prefill_far_logits(B, scale, grow):
     q, kv, kp, dev, cu = _prefill_inputs([300], [700], 2, seed=31, joint=True, scale=scale)
