@@ -655,6 +655,7 @@ int host_stage_init(HostStage& hs, const HostLayout& L, cudaStream_t stream) {
 
 namespace dsa {
 uint64_t option_wait_ns() { return read_opts().wait_ns; }
+int option_withhold() { return read_opts().withhold; }
 int option_grid() { return read_opts().grid; }
 void count_launch() { g_launches.fetch_add(1); }
 }  // namespace dsa

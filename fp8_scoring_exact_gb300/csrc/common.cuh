@@ -239,6 +239,14 @@ static __device__ __noinline__ bool mbar_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// The same with one deadline (globaltimer) for several barriers, of which some
+// may never complete: 10 ms is far beyond any copy or MMA in flight.
+constexpr uint64_t DRAIN_ALL_NS = 10000000ull;
+static __device__ __noinline__ void mbar_drain_until(uint32_t bar, uint32_t parity, uint64_t deadline) {
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() > deadline) return;
+}
+
 // Warp-uniform bounded wait: every lane polls (so every lane acquires the
 // phase) and every lane returns the same value, so code after it that needs
 // a converged warp (tcgen05.ld .sync.aligned, shuffles) never diverges.

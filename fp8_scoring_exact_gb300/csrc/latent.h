@@ -35,6 +35,7 @@ constexpr int LA_MIN_UNITS = LA_ITEM_UNITS + 2;  // of a CTA
 
 // Process-wide options and the launch counter (api.cu).
 uint64_t option_wait_ns();
+int option_withhold();
 int option_grid();  // CTAs of the persistent kernels: the option, else the SM count
 void count_launch();
 // Frees the scratch of the latent operators (latent_api.cu); called by dsa_indexer_release.
@@ -65,6 +66,7 @@ struct LatentAttnParams {
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
   int items, grid;
   uint64_t wait_ns;
+  int withhold;                 // test option: the first keys are never loaded (a wait must run out)
   int32_t* per;                 // [1] units per CTA
   int32_t* start;               // [grid, items + 1] first unit of each item, worked out by every CTA for itself
   float* part_o;                // [items + grid, n, 512] unnormalised outputs of the pieces
@@ -112,6 +114,7 @@ struct PrefillParams {
   float* lse;                   // [Tq, H]
   int grid;                     // pairs of CTAs
   uint64_t wait_ns;
+  int withhold;                 // test option: the first keys are never loaded (a wait must run out)
   int64_t* per;                 // [1] units per pair
   int64_t* start;               // [2 grid, S + 1] first unit of each sequence, worked out by every CTA for itself
   float* part_o;                // [2 grid, 128 / 4, 256, 4] unnormalised outputs of the pieces of cut blocks

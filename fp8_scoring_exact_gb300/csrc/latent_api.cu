@@ -135,6 +135,7 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   p.grid = std::min(option_grid(), 1024);
   if ((int64_t)p.items * (std::max(p.max_pages, p.prefix_pages) + LA_ITEM_UNITS) >= (1ll << 31) - (1 << 20)) return DSA_ERR_UNSUPPORTED;
   p.wait_ns = option_wait_ns();
+  p.withhold = option_withhold();
   LatentMaps m;
   const int64_t slots = (int64_t)p.num_pages * PAGE;
   if (!tmap_rows(&m.q_nope, p.q_nope, rows, LA_DC, 8, p.n, 8) || !tmap_rows(&m.q_pe, p.q_pe, rows, LA_DP, 1, p.n, 1) ||
@@ -328,6 +329,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   p.lse = lse;
   p.grid = std::max(1, std::min(option_grid(), 1024) / 2);
   p.wait_ns = option_wait_ns();
+  p.withhold = option_withhold();
   PrefillMaps m;
   if (!tmap_heads(&m.q, q, Tq, H, LA_DN + LA_DP, q_token_stride, q_head_stride, 128) ||
       !tmap_heads(&m.k_nope, k_nope, Tk, H, LA_DN, kn_token_stride, kn_head_stride, 64) ||

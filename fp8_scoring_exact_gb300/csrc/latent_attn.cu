@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         const int slot = __shfl_sync(0xffffffffu, pages, k & 31) * PAGE;
         const int ks = n_kpe % C::KPES;
         if (!(ok = mbar_wait_warp(bar(C::B_KE + ks), ((n_kpe / C::KPES) & 1) ^ 1, abort_flag, stats))) break;
-        if (lane == 0) {
+        if (lane == 0 && !(p.withhold && n_kpe == 0)) {
           mbar_arrive_expect_tx(bar(C::B_KF + ks), CHUNK);
           tma_load_2d(sbase + C::OFF_KPE + ks * CHUNK, &maps.kpe, 0, slot, bar(C::B_KF + ks));
         }
@@ -599,16 +599,17 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   if (*abort_flag) {
     // before shared memory and TMEM are released, the copies and MMAs
     // already issued land: the last phase armed on each slot, a last commit
+    const uint64_t until = globaltimer_ns() + DRAIN_ALL_NS;
     if (warp == 0 && lane == 0) {
       for (uint32_t s = 0; s < C::PAIRS; ++s)
-        if (n_pair > s) mbar_drain(bar(C::B_PF + s), ((n_pair - 1 - s) / C::PAIRS) & 1);
+        if (n_pair > s) mbar_drain_until(bar(C::B_PF + s), ((n_pair - 1 - s) / C::PAIRS) & 1, until);
       for (uint32_t s = 0; s < C::KPES; ++s)
-        if (n_kpe > s) mbar_drain(bar(C::B_KF + s), ((n_kpe - 1 - s) / C::KPES) & 1);
-      if (n_q) mbar_drain(bar(C::B_QF), (n_q - 1) & 1);
+        if (n_kpe > s) mbar_drain_until(bar(C::B_KF + s), ((n_kpe - 1 - s) / C::KPES) & 1, until);
+      if (n_q) mbar_drain_until(bar(C::B_QF), (n_q - 1) & 1, until);
     } else if (warp == 1 || warp == C::W_PV) {
       const uint32_t db = bar(C::B_DRAIN + (warp == C::W_PV));
       mma_commit_warp(elect_one(), db);  // (elect.sync picks the lane that issued: it is deterministic)
-      mbar_drain(db, 0);
+      mbar_drain_until(db, 0, until);
     }
     __syncthreads();
   }

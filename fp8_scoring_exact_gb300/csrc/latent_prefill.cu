@@ -260,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         for (int c = 0; c < PF_PER_TILE; ++c, ++n_slot) {
           const int st = n_slot % PF_SLOTS;
           if (!(ok = mbar_wait_warp(bar(B_EMPTY + st), ((n_slot / PF_SLOTS) & 1) ^ 1, abort_flag, stats))) break;
-          if (lane == 0) {
+          if (lane == 0 && !(p.withhold && n_slot == 0)) {
             const uint32_t dst = sbase + PF_OFF_RING + st * PF_SLOT, full = lead_bar(B_FULL + st);
             if (rank == 0) mbar_arrive_expect_tx(bar(B_FULL + st), 2 * PF_SLOT);
             if (c < 2)
@@ -543,18 +543,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
   __syncthreads();
   if (*abort_flag) {
     // before shared memory and TMEM are released, the copies and MMAs
-    // already issued land: the last phase armed on each slot (the even CTA's
-    // barriers count both CTAs' bytes), a last commit
+    // already issued land: a last commit, and the last phase armed on each
+    // slot.  Those count both CTAs' bytes, and a phase of which the other CTA
+    // issued no copy never completes, nor can the odd CTA wait for its own:
+    // both give copies in flight a fixed time as well.
+    const uint64_t until = globaltimer_ns() + DRAIN_ALL_NS;
     if (rank == 0) {
       if (warp == 0 && lane == 0) {
         for (uint32_t s = 0; s < PF_SLOTS; ++s)
-          if (n_slot > s) mbar_drain(bar(B_FULL + s), ((n_slot - 1 - s) / PF_SLOTS) & 1);
-        if (n_q) mbar_drain(bar(B_QF), (n_q - 1) & 1);
+          if (n_slot > s) mbar_drain_until(bar(B_FULL + s), ((n_slot - 1 - s) / PF_SLOTS) & 1, until);
+        if (n_q) mbar_drain_until(bar(B_QF), (n_q - 1) & 1, until);
       } else if (warp == 1 || warp == 2) {
         mma_commit_pair(elect_one(), bar(B_DRAIN + warp - 1));
-        mbar_drain(bar(B_DRAIN + warp - 1), 0);
+        mbar_drain_until(bar(B_DRAIN + warp - 1), 0, until);
       }
     }
+    while (globaltimer_ns() < until) __nanosleep(1000);
     __syncthreads();
   }
   if (threadIdx.x == 0 && stats->status) atomicOr(&p.status->now, stats->status);

@@ -423,8 +423,8 @@ typedef enum {
                                   2000000, range 1..60000000): the kernel then lets the copies and MMAs it
                                   already issued land, returns early, and the call reports DSA_ERR_TIMEOUT */
   DSA_OPT_TEST_WITHHOLD = 9,   /* test option: 1 makes the fused operator's main scorer never signal its first
-                                  accumulator, so that its epilogue's wait runs out after DSA_OPT_WAIT_LIMIT_US
-                                  and the call reports DSA_ERR_TIMEOUT (its output is then undefined); default 0 */
+                                  accumulator, and the latent attention kernels never load their first keys,
+                                  so that a wait runs out after DSA_OPT_WAIT_LIMIT_US and the call reports DSA_ERR_TIMEOUT (its output is then undefined); default 0 */
   DSA_OPT_MATRIX_ROW_MIN = 10  /* dsa_indexer_topk_from_scores and the unfused operator's selection: rows from
                                   which CTAs take whole rows, or half rows when there are many long ones
                                   (threshold, one pass over the row, selection by the CTA that finishes the

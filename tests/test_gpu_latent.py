@@ -490,3 +490,75 @@ def test_calls_follow_one_another_on_a_stream(B):
         assert np.array_equal(kept[b, :len(rows)], rows)
         flat[slots[:len(rows)]] = old[slots[rows]]
     _check_decode(d, qn, qp, out2.double().cpu().numpy(), lse2.double().cpu().numpy())
+
+
+def test_evict_replays_from_a_graph(B):
+    """Captured once, replayed on other weights and lengths (short enough for one CTA and long enough
+    for a cluster per sequence)."""
+    for lens, budget in (([700, 300], 256), ([40000, 20000], 3000)):
+        a, g = Cache(lens, seed=50), torch.Generator().manual_seed(51)
+        W = a.table.shape[1] * 64
+        w1, w2 = torch.rand((2, W), generator=g), torch.rand((2, W), generator=g)
+        ck, kp = a.device()
+        dw, dl, table = w1.cuda(), _ints(lens), a.table.cuda()
+        kept, new = B.latent_cache_evict(ck, kp, dw, table, dl, budget, 7)  # sizes the scratch
+        torch.cuda.synchronize()
+        assert np.array_equal(kept[0].cpu().numpy(), la.kept_keys(w1[0].numpy(), lens[0], budget, 7))
+        gr, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            B.latent_cache_evict(ck, kp, dw, table, dl, budget, 7, kept=kept, new_lens=new)  # ... of this stream
+        torch.cuda.synchronize()
+        with torch.cuda.graph(gr, stream=s):
+            B.latent_cache_evict(ck, kp, dw, table, dl, budget, 7, kept=kept, new_lens=new)
+        ck.copy_(a.data[..., :512])
+        kp.copy_(a.data[..., 512:])
+        dw.copy_(w2)
+        dl.copy_(_ints([lens[0] - 5, lens[1]]))
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        old = a.data.view(torch.int16).reshape(-1, 576)
+        got = ck.cpu().view(torch.int16).reshape(-1, 512)
+        for b, L in enumerate((lens[0] - 5, lens[1])):
+            rows = la.kept_keys(w2[b].numpy(), L, budget, 7)
+            assert np.array_equal(kept[b, :len(rows)].cpu().numpy(), rows)
+            slots = la.slots_of(a.table[b].numpy(), L)
+            assert torch.equal(got[slots[:len(rows)]], old[slots[rows], :512])
+
+
+def test_wait_limit_ends_the_kernels(B):
+    """With a test option the kernels never load their first keys, so that the waits for them (limit 50 ms here)
+    run out: the calls come back, say so, and the next ones are right."""
+    c = Cache([3000, 500], seed=60)
+    qn, qp = _queries(2, 1, 64, seed=61)
+    q, kv, kp, dev, cu = _prefill_inputs([300, 20], [900, 20], 4, seed=62, joint=True)
+    B.set_option("wait_limit_us", 50000)
+    B.set_option("test_withhold", 1)
+    try:
+        _decode(B, c, qn, qp)
+        assert B.latent_last_status() == B.DSA_ERR_TIMEOUT
+        B.latent_attention_prefill(*dev, SCALE)
+        assert B.latent_last_status() == B.DSA_ERR_TIMEOUT
+    finally:
+        B.set_option("test_withhold", 0)
+        B.set_option("wait_limit_us", 2000000)
+    out, lse = _decode(B, c, qn, qp)
+    assert B.latent_last_status() == 0
+    _check_decode(c, qn, qp, out, lse)
+    out, lse = B.latent_attention_prefill(*dev, SCALE)
+    assert B.latent_last_status() == 0
+    _check_prefill(q, kv, kp, cu, out, lse, True)
+
+
+def test_example_runs(B):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "latent_decode.py")
+    spec = importlib.util.spec_from_file_location("latent_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    said = []
+    off, lens, status, latent, lse = m.main(say=said.append)
+    # absorbed and expanded forms round at different places: bf16 keys, values, weights and outputs
+    assert off < 8 * BF and status == 0 and lens == [512 + 3, 512 + 3, 90 + 8]
+    assert len(said) == 4 and bool(torch.isfinite(latent.float()).all()) and bool(torch.isfinite(lse).all())
