@@ -133,6 +133,15 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same; returns whether the predicate held in any of the threads.
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
+  int r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\tbarrier.red.or.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"(id), "r"(nthreads), "r"((int)pred)
+               : "memory");
+  return r != 0;
+}
 
 // The aligned forms, for converged warps and a barrier known at compile time.
 template <int ID, int THREADS>

@@ -40,6 +40,7 @@ namespace {
 constexpr int LT = PAGE;                       // keys per tile
 constexpr uint32_t CHUNK = LT * 128;           // 64 keys x 64 dims, bf16
 constexpr uint32_t PAIR = 2 * CHUNK;           // 64 keys x 128 dims
+constexpr float NO_REF = -1.7e38f;              // the reference of a row that has seen no key: any logit passes it
 constexpr float RESCALE_AT = 8.f;              // a row's reference moves when its maximum passes it by this
 
 template <int N>
@@ -70,7 +71,7 @@ struct LA {
   static constexpr uint32_t OFF_REF = OFF_RED + 4 * N * 4;                       // [N] reference maxima
   static constexpr uint32_t OFF_ALPHA = OFF_REF + N * 4;                         // [N] factors
   static constexpr uint32_t OFF_LIM = OFF_ALPHA + N * 4;                         // [N] visible keys per row
-  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base, rescale, scan
+  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base
   static constexpr uint32_t OFF_STAT = OFF_FLAG + 128;                           // Stats: this CTA's status and wait limit
   static constexpr uint32_t SMEM = OFF_STAT + 128 + 1024;                        // + alignment
   static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer (2 N each)
@@ -247,7 +248,6 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
   volatile int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_FLAG);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG + 4);
-  volatile int* s_resc = reinterpret_cast<int*>(smem + C::OFF_FLAG + 8);  // [2]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Stats* stats = reinterpret_cast<Stats*>(smem + C::OFF_STAT);
 
@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    s_resc[0] = s_resc[1] = 0;
     stats->status = 0;
     stats->wait_ns = p.wait_ns;
     tma_prefetch_desc(&maps.q_nope);
@@ -477,33 +476,43 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
             *reinterpret_cast<float2*>(dst + 8 * N + 8 * m) = make_float2(u[m][2], u[m][3]);
           }
         }
-        float mx[2 * M8];
+        // does a logit lie so far above its row's reference that the row's
+        // maximum has to be found?  (always in a piece's first tile)
+        bool rescale = true;
+        if (k > k0) {
+          float over = neg_inf();
 #pragma unroll
-        for (int i = 0; i < 2 * M8; ++i) mx[i] = fmaxf(u[i >> 1][i & 1], u[i >> 1][2 + (i & 1)]);
-        over_keys<2 * M8>(mx, lane, [](float a, float b) { return fmaxf(a, b); });
-        s_red[q * N + own_row<2 * M8>(lane) + cb] = mx[0];
-        named_bar_sync(1, C::ST);
-        if (st_id < N) {
-          const float top = p.scale_log2 * fmaxf(fmaxf(s_red[st_id], s_red[N + st_id]),
-                                                 fmaxf(s_red[2 * N + st_id], s_red[3 * N + st_id]));
-          float a = 1.f;
-          if (top > ref + RESCALE_AT || (ref == neg_inf() && top > ref)) {
-            a = ex2(ref - top);  // 0 from a reference of -inf
-            ref = top;
-            s_resc[sb] = 1;
+          for (int m = 0; m < M8; ++m) {
+            const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * m + cc]);
+            over = fmaxf(over, fmaf(fmaxf(u[m][0], u[m][2]), p.scale_log2, -f.x));
+            over = fmaxf(over, fmaf(fmaxf(u[m][1], u[m][3]), p.scale_log2, -f.y));
           }
-          s_alpha[st_id] = a;
-          s_ref[st_id] = ref == neg_inf() ? 0.f : ref;
+          rescale = named_bar_or(1, C::ST, over > RESCALE_AT);
         }
-        named_bar_sync(1, C::ST);
-        const bool rescale = s_resc[sb] != 0;
-        if (st_id == 0) s_resc[sb ^ 1] = 0;  // the next tile's flag: set after the next barrier at the earliest
-        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
-        // the MMA wants of both operands) for P
         if (rescale) {
+          float mx[2 * M8];
+#pragma unroll
+          for (int i = 0; i < 2 * M8; ++i) mx[i] = fmaxf(u[i >> 1][i & 1], u[i >> 1][2 + (i & 1)]);
+          over_keys<2 * M8>(mx, lane, [](float a, float b) { return fmaxf(a, b); });
+          s_red[q * N + own_row<2 * M8>(lane) + cb] = mx[0];
+          named_bar_sync(1, C::ST);
+          if (st_id < N) {
+            const float top = p.scale_log2 * fmaxf(fmaxf(s_red[st_id], s_red[N + st_id]),
+                                                   fmaxf(s_red[2 * N + st_id], s_red[3 * N + st_id]));
+            float a = 1.f;
+            if (top > ref + RESCALE_AT || (ref == neg_inf() && top > ref)) {
+              a = ex2(ref - top);  // 0 from a reference of -inf
+              ref = top;
+            }
+            s_alpha[st_id] = a;
+            s_ref[st_id] = fmaxf(ref, NO_REF);
+          }
+          named_bar_sync(1, C::ST);
 #pragma unroll
           for (int i = 0; i < 2 * M8; ++i) l[i] *= s_alpha[8 * (i >> 1) + cc + (i & 1)];
         }
+        // weights: fp32 into the sums, rounded to bf16 (the type of V, which
+        // the MMA wants of both operands) for P
         uint32_t r[M8][2];
 #pragma unroll
         for (int m = 0; m < M8; ++m) {
