@@ -662,6 +662,7 @@ struct RowPieces {
 // they work the rows' maxima m and sums l out of the pieces themselves rather
 // than wait (and than use lse = m + log2 l, which as one number has lost bits).
 constexpr int FIN_THREADS = 256;
+constexpr int FIN_BATCH = 4;
 constexpr int FIN_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
 template <int N>
 __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const LatentAttnParams p, int spread) {
@@ -689,28 +690,46 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
       }
       s_ml[i] = make_float2(-mm, sum == 0.f ? 0.f : 1.f / sum);
     }
-    __syncthreads();
-    constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK;  // lanes per key, keys per step
+    constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK, STEPS = LT / KEYS;  // lanes per key, keys per step, steps per tile
     bool bad;
     const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT);
     const int sub = tid % LPK, kk = tid / LPK;
-    for (int t = (int)(row - rows) % spread; t < tiles; t += spread) {
+    // FIN_BATCH steps at a time, their loads together: one after the other
+    // they were the kernel's time
+    const int t0 = (int)(row - rows) % spread, steps = tiles > t0 ? ceil_div(tiles - t0, spread) * STEPS : 0;
+    for (int i0 = 0; i0 < steps; i0 += FIN_BATCH) {
+      float old[FIN_BATCH], sum[FIN_BATCH];
+      int key[FIN_BATCH];
 #pragma unroll
-      for (int k = kk; k < LT; k += KEYS) {
-        float sum = 0.f;
-        for (int j = 0; j < p.blocks; ++j) {
-          const int64_t tile = (int64_t)(b * p.blocks + j) * p.max_pages + t;
-          const float4 u = __ldcs(reinterpret_cast<const float4*>(p.logits + (tile * LT + k) * N + 4 * sub));
+      for (int x = 0; x < FIN_BATCH; ++x) {
+        const int i = i0 + x;
+        key[x] = (t0 + i / STEPS * spread) * LT + i % STEPS * KEYS + kk;
+        if (i >= steps || key[x] >= len) key[x] = -1;
+        old[x] = sub == 0 && key[x] >= 0 ? p.weights[b * p.ld_weights + key[x]] : 0.f;
+        sum[x] = 0.f;
+      }
+      for (int j = 0; j < p.blocks; ++j) {
+        const float* base = p.logits + (int64_t)(b * p.blocks + j) * p.max_pages * LT * N + 4 * sub;
+        float4 u[FIN_BATCH];
+#pragma unroll
+        for (int x = 0; x < FIN_BATCH; ++x)
+          u[x] = key[x] >= 0 ? __ldcs(reinterpret_cast<const float4*>(base + (int64_t)key[x] * N))
+                             : make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
+        if (i0 == 0 && j == 0) __syncthreads();  // s_ml, behind the first loads
+#pragma unroll
+        for (int x = 0; x < FIN_BATCH; ++x) {
           const int r = j * N + 4 * sub;
-          const float v[4] = {u.x, u.y, u.z, u.w};
+          const float v[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (r + e < R && v[e] != neg_inf()) sum += ex2(fmaf(v[e], p.scale_log2, s_ml[r + e].x)) * s_ml[r + e].y;
+            if (r + e < R && v[e] != neg_inf()) sum[x] += ex2(fmaf(v[e], p.scale_log2, s_ml[r + e].x)) * s_ml[r + e].y;
         }
+      }
 #pragma unroll
-        for (int o = 1; o < LPK; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int s = t * LT + k;
-        if (sub == 0 && s < len) p.weights[b * p.ld_weights + s] += sum;
+      for (int x = 0; x < FIN_BATCH; ++x) {
+#pragma unroll
+        for (int o = 1; o < LPK; o <<= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+        if (sub == 0 && key[x] >= 0) p.weights[b * p.ld_weights + key[x]] = old[x] + sum[x];
       }
     }
     return;
@@ -742,7 +761,8 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < FIN_THREADS / 32; ++i) sum += s_tmp[i];
-  // two halves of the CTA take every other piece, 4 dims per thread
+  // two halves of the CTA take every other piece, 4 dims per thread (loading
+  // the first pieces ahead of the factors gained nothing)
   const int half = tid >> 7, d = 4 * (tid & 127);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
