@@ -40,7 +40,7 @@ namespace {
 constexpr int LT = PAGE;                       // keys per tile
 constexpr uint32_t CHUNK = LT * 128;           // 64 keys x 64 dims, bf16
 constexpr uint32_t PAIR = 2 * CHUNK;           // 64 keys x 128 dims
-constexpr float NO_REF = -1.7e38f;              // the reference of a row that has seen no key: any logit passes it
+constexpr float NO_REF = -3.402823466e38f;     // the reference of a row that has seen no key: any logit passes it
 constexpr float RESCALE_AT = 8.f;              // a row's reference moves when its maximum passes it by this
 
 template <int N>

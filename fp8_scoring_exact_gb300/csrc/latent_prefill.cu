@@ -37,8 +37,10 @@ constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
 constexpr int PF_PER_TILE = 5;         // slots of a key tile: 3 of its 64 keys (192 dims), 2 of 64 value dims
 constexpr int PF_SLOTS = 17;
 constexpr int PF_BUFS = 3;             // S buffers: with O they fill the 512 TMEM columns
-constexpr int PF_WARPS = 12;           // 0 copies, 1 and 2 issue (even CTA), 4-7 softmax, 8-11 output
+constexpr int PF_WARPS = 16;           // 0 copies, 1 and 2 issue (even CTA), 4-11 softmax, 12-15 output
 constexpr int PF_THREADS = 32 * PF_WARPS;
+constexpr int PF_ROW_THREADS = 384;    // of the softmax and output warps
+constexpr float PF_NO_REF = -3.402823466e38f;  // the reference of a row that has seen no key: any logit passes it
 constexpr float PF_RESCALE_AT = 8.f;
 
 constexpr uint32_t PF_OFF_Q = 0;
@@ -52,8 +54,9 @@ constexpr int B_FULL = 0, B_EMPTY = PF_SLOTS, B_QF = 2 * PF_SLOTS, B_QE = B_QF +
 constexpr uint32_t PF_OFF_STAT = PF_OFF_MISC + PF_BARS * 8;
 constexpr uint32_t PF_OFF_FLAG = PF_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t PF_OFF_SCAN = PF_OFF_FLAG + 16;   // PF_WARPS + 1 int64
-constexpr uint32_t PF_OFF_ROW = PF_OFF_SCAN + 8 * (PF_WARPS + 2);  // [parity][row] reference and sum of a piece
-constexpr uint32_t PF_SMEM = PF_OFF_ROW + 2 * 128 * 8 + 1024;      // + alignment
+constexpr uint32_t PF_OFF_ROW = PF_OFF_SCAN + 8 * (PF_WARPS + 2);  // [parity][half][row] reference and sum of a piece
+constexpr uint32_t PF_OFF_MAX = PF_OFF_ROW + 4 * 128 * 8;          // [half][row] a tile's maximum
+constexpr uint32_t PF_SMEM = PF_OFF_MAX + 2 * 128 * 4 + 1024;      // + alignment
 static_assert(PF_SMEM <= 227 * 1024 && sizeof(Stats) <= 128, "shared memory per CTA");
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
@@ -347,14 +350,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
       }
       ++seg;
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 12) {
     // ----------------------------------------------------- softmax warps --
-    // A thread owns a row: no exchange.  (A wait that gives up leaves the result
+    // Two threads per row, 64 keys of a tile each, in two warps that meet at
+    // a barrier of their own.  (A wait that gives up leaves the result
     // undefined; the loops still end.)
-    const int q = warp & 3, r = 32 * q + lane;
+    const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    const uint32_t lead_p = lead_bar(B_P);
-    float2* s_row = reinterpret_cast<float2*>(smem + PF_OFF_ROW) + r;
+    const uint32_t lead_p = lead_bar(B_P) + 8 * half;
+    float2* s_row = reinterpret_cast<float2*>(smem + PF_OFF_ROW) + 128 * half + r;
+    float* s_max = reinterpret_cast<float*>(smem + PF_OFF_MAX) + r;
     uint32_t it = 0, tails = 0, seg = 0;  // tails: the phase of each buffer's B_Z
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     for (; pc.next(p, k0, k1, tiles); pc.step(tiles)) {
@@ -362,66 +367,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
       const int lim = i < pc.seq.n ? keys_seen(p, pc.seq, i + 1) : 0;
       // what the CTA's first row sees, the least (without rows here nothing matters)
       const int lim0 = first < pc.seq.n ? keys_seen(p, pc.seq, first + 1) : 0x7fffffff;
-      float ref = neg_inf();
-      uint64_t l[2] = {0, 0};                // its sum so far, in four parts
+      float ref = PF_NO_REF;
+      uint64_t l[2] = {0, 0};                // this half's sum so far, in four parts
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         const uint32_t d_s = tmem + 128 * sb + lanes;  // the row's logits, then its weights
         mbar_wait_warp(bar(B_S + sb), sp, abort_flag, stats);
         tc_fence_after();
-        // (64 logits at a time: the second half is read twice, which costs less
-        // than the registers of all 128)
-        const bool masked = (k + 1) * PF_KEYS > lim0;
-        const int left = lim - k * PF_KEYS;
         uint32_t s[64];
-        auto load = [&](int half) {
-          tmem_ld32(d_s + 64 * half, s);
-          tmem_ld32(d_s + 64 * half + 32, s + 32);
-          tmem_wait_ld32(s);
-          tmem_wait_ld32(s + 32);
-          if (masked) {
+        tmem_ld32(d_s + 64 * half, s);
+        tmem_ld32(d_s + 64 * half + 32, s + 32);
+        tmem_wait_ld32(s);
+        tmem_wait_ld32(s + 32);
+        if ((k + 1) * PF_KEYS > lim0) {
+          const int left = lim - k * PF_KEYS - 64 * half;
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (64 * half + c >= left) s[c] = 0xff800000u;  // -inf
-          }
-        };
+          for (int c = 0; c < 64; ++c)
+            if (c >= left) s[c] = 0xff800000u;  // -inf
+        }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-          load(half);
-#pragma unroll
-          for (int c = 0; c < 64; c += 2)
-            mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        }
+        for (int c = 0; c < 64; c += 2)
+          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float top = p.scale_log2 * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         // the next sequence's values share its last tile: they become 0 (a
-        // weight of 0 does not silence a NaN); a CTA's slots hold its value
-        // dims of all 128 keys
+        // weight of 0 does not silence a NaN), in the 64 keys that this half's
+        // arrival releases; a CTA's slots hold its value dims of all 128 keys
         const int valid = pc.seq.m - k * PF_KEYS;
         if (valid < PF_KEYS) {
           mbar_wait_one<true>(bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
           tails ^= 1u << sb;
-          for (uint32_t c = 0; c < 2; ++c) {
-            uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + c) % PF_SLOTS) * PF_SLOT);
-            for (int x = max(0, valid - 64 * (int)c) * 8 + r; x < 64 * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
-          }
+          uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + half) % PF_SLOTS) * PF_SLOT);
+          for (int x = max(0, valid - 64 * half) * 8 + r; x < 64 * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           // for the issuer in the other CTA (the arrivals below are relaxed)
           __syncwarp();
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
         }
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        top *= p.scale_log2;
-        const bool moves = top > ref + PF_RESCALE_AT || (ref == neg_inf() && top > ref);
-        if (__any_sync(0xffffffffu, moves)) {
-          const float a = moves ? ex2(ref - top) : 1.f;  // 0 from a reference of -inf
+        // A vote of the two warps: only where a logit passes some row's reference
+        // (always in a piece's first tile) are the maxima exchanged.  It also
+        // comes between the other half's last read of its logits and the weights
+        // that go over them.
+        tc_fence_before();
+        if (named_bar_or(2 + q, 64, k == k0 || top > ref + PF_RESCALE_AT)) {
+          s_max[128 * half] = top;
+          named_bar_sync(2 + q, 64);
+          top = fmaxf(top, s_max[128 * (half ^ 1)]);
+          const bool moves = top > ref + PF_RESCALE_AT;
+          const float a = moves ? ex2(ref - top) : 1.f;  // 0 from no reference
           if (moves) ref = top;
 #pragma unroll
           for (int j = 0; j < 2; ++j) l[j] = fmul2(l[j], pack2(a, a));
-          if (k > k0) {
+          if (k > k0 && __any_sync(0xffffffffu, moves)) {
             mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 4 * half; c < 4 * half + 4; ++c) {
               uint32_t o[16];
               const uint32_t oa = d_o + lanes + 16 * c;
               tmem_ld16(oa, o);
@@ -430,42 +431,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * a);
               tmem_st16(oa, o);
             }
+            tmem_wait_st();
+            tc_fence_before();
           }
+          // (either half's arrival may start the product: all of O is ready by
+          // then, and s_max has been read)
+          named_bar_sync(2 + q, 64);
         }
+        tc_fence_after();
         // weights: fp32 into the sums, rounded to bf16 (the type of V, which
         // the MMA wants of both operands) over the logits in TMEM
-        const float nr = ref == neg_inf() ? 0.f : -ref;
-        const uint64_t nr2 = pack2(nr, nr);
+        const uint64_t nr2 = pack2(-ref, -ref);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c == 1) load(1);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int e = 32 * h + 2 * j;
-              const float2 x =
-                  unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nr2));
-              const float e0 = ex2(x.x), e1 = ex2(x.y);
-              l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
-              const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
-              w[j] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-            tmem_st16(d_s + 32 * c + 16 * h, w);
+          for (int j = 0; j < 16; ++j) {
+            const int e = 32 * h + 2 * j;
+            const float2 x =
+                unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, nr2));
+            const float e0 = ex2(x.x), e1 = ex2(x.y);
+            l[j & 1] = fadd2(l[j & 1], pack2(e0, e1));
+            const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster<false>(lead_p + 16 * sb + 8 * c);
+          tmem_st16(d_s + 32 * half + 16 * h, w);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster<false>(lead_p + 16 * sb);
       }
       const float2 la = unpack2(l[0]), lb = unpack2(l[1]);
-      s_row[128 * (seg++ & 1)] = make_float2(ref, (la.x + la.y) + (lb.x + lb.y));
+      s_row[256 * (seg++ & 1)] = make_float2(ref == PF_NO_REF ? neg_inf() : ref, (la.x + la.y) + (lb.x + lb.y));
       __syncwarp();
-      bar_sync_all<1, 256>();  // (the output warps are done with the piece before)
+      bar_sync_all<1, PF_ROW_THREADS>();  // (the output warps are done with the piece before)
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------ output warps --
     // Each piece's result, while the softmax warps are at the next piece.
     const int q = warp & 3, r = 32 * q + lane;
@@ -478,54 +480,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
       const int first = pc.blk * PF_ROWS + 128 * (int)rank;
       if (any) it += k1 - k0;
       __syncwarp();
-      bar_sync_all<1, 256>();
-      const float2 rs = s_row[128 * (seg++ & 1)];
-      const float ref = rs.x, sum = rs.y;
+      bar_sync_all<1, PF_ROW_THREADS>();
+      const float2 rs = s_row[256 * (seg & 1)];
+      const float ref = rs.x, sum = rs.y + s_row[256 * (seg & 1) + 128].y;
+      ++seg;
       if (cut) {
-        p.part_ml[piece * PF_ROWS + 128 * rank + r] = rs;
+        p.part_ml[piece * PF_ROWS + 128 * rank + r] = make_float2(ref, sum);
       } else if (first + r < pc.seq.n) {
         p.lse[(int64_t)(pc.seq.q0 + first + r) * p.H + pc.h] =
             sum == 0.f ? neg_inf() : (ref == neg_inf() ? 0.f : ref) + log2f(sum);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      // O into registers in one go, so that the next piece's may begin
-      uint32_t o[128];
       if (any) {
         mbar_wait_warp(bar(B_V + (it - 1) % PF_BUFS), (it - 1) / PF_BUFS & 1, abort_flag, stats);
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(d_o + lanes + 32 * c, o + 32 * c);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld32(o + 32 * c);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster<false>(lead_bar(B_O));
-      } else {
-#pragma unroll
-        for (int c = 0; c < 128; ++c) o[c] = 0;
       }
-      if (cut) {
-        // [piece][dim / 4][row][4]: lanes are rows
-        float4* dst = reinterpret_cast<float4*>(p.part_o) + piece * 32 * PF_ROWS + 128 * rank + r;
+      // O out of TMEM, 64 dims at a time; the next piece's may begin once the
+      // last are in registers.  Whole blocks go through shared memory, so that a
+      // warp writes whole rows (a thread writing its own: 32 lines per
+      // instruction, 3000 cycles a block).
+      uint4* out = reinterpret_cast<uint4*>(smem + PF_OFF_OUT) + 16 * 32 * q;  // this warp's 32 rows of 16 x 16 bytes
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          dst[c * PF_ROWS] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
-                                         __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
-      } else {
-        // through shared memory, so that a warp writes whole rows (a thread
-        // writing its own: 32 lines per instruction, 3000 cycles a block)
-        uint4* out = reinterpret_cast<uint4*>(smem + PF_OFF_OUT) + 16 * 32 * q;  // this warp's 32 rows of 16 x 16 bytes
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * j]) * inv,
-                                                           __uint_as_float(o[8 * c + 2 * j + 1]) * inv);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[64];
+        if (any) {
+          tmem_ld32(d_o + lanes + 64 * h, o);
+          tmem_ld32(d_o + lanes + 64 * h + 32, o + 32);
+          tmem_wait_ld32(o);
+          tmem_wait_ld32(o + 32);
+          if (h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster<false>(lead_bar(B_O));
           }
-          out[16 * lane + (c ^ (lane & 15))] = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) o[c] = 0;
         }
+        if (cut) {
+          // [piece][dim / 4][row][4]: lanes are rows
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + (piece * 32 + 16 * h) * PF_ROWS + 128 * rank + r;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            dst[c * PF_ROWS] = make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                           __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * c + 2 * j]) * inv,
+                                                             __uint_as_float(o[8 * c + 2 * j + 1]) * inv);
+              w[j] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            out[16 * lane + ((8 * h + c) ^ (lane & 15))] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (!cut) {
         __syncwarp();
         const int left = pc.seq.n - (first + 32 * q);  // rows of this warp that exist
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)(pc.seq.q0 + first + 32 * q) * p.H + pc.h) * LA_DV);
