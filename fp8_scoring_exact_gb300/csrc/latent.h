@@ -26,12 +26,14 @@ struct LatentStatus {
 
 // Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
 // 64) with the keys its rows see, cut into tiles of one page.  An item with
-// tiles counts LA_ITEM_UNITS units and one per tile; the items' units are
+// tiles counts item_units units and one per tile; the items' units are
 // numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
 // tiles in one item are a piece, whose id is item + c.
-constexpr int LA_ITEM_UNITS = 2;  // what starting and ending a piece costs, in tiles
+// What starting and ending a piece costs, in tiles: 2 without a prefix (128 rows of seven sequences: 72 us; 74 with 4);
+// 4 with one, where most of a sequence's own items are short and their pages cold (64 sequences behind 32768 shared
+// keys: 180 us with 2, 172 with 3, 168 with 4, 171 with 8; with a single page of their own 51.5 -> 53).
+constexpr int LA_ITEM_UNITS = 2, LA_PREFIX_ITEM_UNITS = 4;
 constexpr int LA_MAX_WEIGHT_ROWS = 4096;  // rows of a sequence with key weights (their sums lie in shared memory)
-constexpr int LA_MIN_UNITS = LA_ITEM_UNITS + 2;  // of a CTA
 
 // Process-wide options and the launch counter (api.cu).
 uint64_t option_wait_ns();
@@ -64,7 +66,7 @@ struct LatentAttnParams {
   // the call's row blocks and scratch
   int n;                        // rows per block
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
-  int items, grid;
+  int items, grid, item_units;
   uint64_t wait_ns;
   int withhold;                 // test option: the first keys are never loaded (a wait must run out)
   int32_t* per;                 // [1] units per CTA

@@ -133,7 +133,9 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   p.prefix_items = p.prefix_table ? (int)((rows + p.n - 1) / p.n) : 0;
   p.items = p.prefix_items + p.B * p.blocks;
   p.grid = std::min(option_grid(), 1024);
-  if ((int64_t)p.items * (std::max(p.max_pages, p.prefix_pages) + LA_ITEM_UNITS) >= (1ll << 31) - (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  p.item_units = p.prefix_table ? LA_PREFIX_ITEM_UNITS : LA_ITEM_UNITS;
+  if ((int64_t)p.items * (std::max(p.max_pages, p.prefix_pages) + p.item_units) >= (1ll << 31) - (1 << 20))
+    return DSA_ERR_UNSUPPORTED;
   p.wait_ns = option_wait_ns();
   p.withhold = option_withhold();
   LatentMaps m;

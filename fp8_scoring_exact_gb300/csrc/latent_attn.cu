@@ -157,7 +157,7 @@ __device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
 // The pieces of one CTA: next() gives item w and its tiles [k0, k1).
 struct Runs {
   const int32_t* start;
-  int t, t1, w;
+  int t, t1, w, extra;
   __device__ __forceinline__ bool next(int& item, int& k0, int& k1, bool& whole) {
     for (;;) {
       if (t >= t1) return false;
@@ -169,8 +169,8 @@ struct Runs {
       }
       const int u1 = min(t1, s1) - s0;
       item = w;
-      k0 = max(0, t - s0 - LA_ITEM_UNITS);
-      k1 = max(0, u1 - LA_ITEM_UNITS);
+      k0 = max(0, t - s0 - extra);
+      k1 = max(0, u1 - extra);
       whole = k0 == 0 && u1 == s1 - s0;
       t = s0 + u1;
       if (k1 > k0) return true;  // (a run may end before an item's first tile)
@@ -197,7 +197,7 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
         len = valid_len(p.seq_lens[(w - p.prefix_items) / p.blocks], p.max_pages, bad);
         if (bad) atomicOr(status, ST_RANGE);
       }
-      units = len ? ceil_div(len, LT) + LA_ITEM_UNITS : 0;
+      units = len ? ceil_div(len, LT) + p.item_units : 0;
     }
     int x = units;
 #pragma unroll
@@ -218,7 +218,7 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
     if (w < p.items) start[w] = base + before + x - units;
     base += all;
   }
-  const int per = max(LA_MIN_UNITS, ceil_div(base, p.grid));
+  const int per = max(p.item_units + 2, ceil_div(base, p.grid));
   const int t = min((int64_t)base, (int64_t)blockIdx.x * per);
   if (tid == 0) {
     start[p.items] = base;
@@ -229,7 +229,7 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
   for (int w = tid; w < p.items; w += THREADS)
     if (start[w] <= t && t < start[w + 1]) tmp[33] = w;  // one item at most
   __syncthreads();
-  return Runs{start, t, min(base, t + per), tmp[33]};
+  return Runs{start, t, (int)min((int64_t)base, (int64_t)t + per), tmp[33], p.item_units};
 }
 
 }  // namespace
@@ -643,7 +643,7 @@ struct RowPieces {
       if (k == 0 && !p.prefix_items) continue;
       const int s0 = p.start[w], s1 = p.start[w + 1];
       if (s0 == s1) continue;
-      id0[k] = w + (s0 + LA_ITEM_UNITS) / per;  // the CTA of its first tile
+      id0[k] = w + (s0 + p.item_units) / per;  // the CTA of its first tile
       cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
       n += cnt[k];
     }
