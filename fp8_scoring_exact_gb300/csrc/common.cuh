@@ -148,10 +148,6 @@ template <int ID, int THREADS>
 __device__ __forceinline__ void bar_sync_all() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
-template <int ID, int THREADS>
-__device__ __forceinline__ void bar_arrive_all() {
-  asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
-}
 
 // ------------------------------------------------------------- mbarriers ----
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -291,36 +287,26 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
   return mbar_wait_warp_slow(bar, parity, abort_flag, st);
 }
 
-// Warp-uniform bounded wait in which one lane polls for the warp (a poll is an
-// access per lane to one shared-memory word) and the vote orders the others
-// behind it; CLUSTER: for a phase that another CTA of the cluster arrives on.
-template <bool CLUSTER>
+// Warp-uniform bounded wait for a phase that another CTA of the cluster may
+// arrive on, in which one lane polls for the warp (a poll is an access per lane
+// to one shared-memory word): code in which other lanes than the elected one
+// touch what the phase guards needs a __syncwarp after it.
 __device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (CLUSTER)
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
-        "@e mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
-        "@e mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
+      "@e mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
+      : "memory");
   return __any_sync(0xffffffffu, ok);
 }
-template <bool CLUSTER>
 static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                        Stats* st) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
-    if (mbar_poll_warp<CLUSTER>(bar, parity)) return true;
+    if (mbar_poll_warp(bar, parity)) return true;
     if ((it & 7u) == 7u) {
       int give_up = 0;
       if ((threadIdx.x & 31) == 0) {
@@ -338,10 +324,9 @@ static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t bar, uint32_t pa
     }
   }
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, Stats* st) {
-  if (mbar_poll_warp<CLUSTER>(bar, parity)) return true;
-  return mbar_wait_one_slow<CLUSTER>(bar, parity, abort_flag, st);
+  if (mbar_poll_warp(bar, parity)) return true;
+  return mbar_wait_one_slow(bar, parity, abort_flag, st);
 }
 
 // Warp-uniform bounded wait for a warp whose wake-up latency has slack (the
@@ -542,20 +527,10 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t leader, uint32_t d_tmem, ui
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
       : "memory");
 }
-// The same with A in tensor memory: lane = row, two bf16 of K per column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
-                                            uint32_t idesc, uint32_t accumulate) {
-  constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
-  asm volatile(
-      "{\n\t.reg .pred e, p;\n\t.reg .b64 db;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 db, {%2, %6};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(HI)
-      : "memory");
-}
-// The same two over a pair of CTAs (cta_group::2, issued in the pair's even
-// CTA): A's and D's rows are split between the CTAs, B's N rows as well, each
-// at the same shared-memory and TMEM addresses in both.
+// The same over a pair of CTAs (cta_group::2, issued in the pair's even CTA):
+// A's and D's rows are split between the CTAs, B's N rows as well, each at the
+// same shared-memory and TMEM addresses in both; _ts: A in tensor memory (lane
+// = row, two bf16 of K per column).
 __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t leader, uint32_t d_tmem, uint32_t a, uint32_t b,
                                                  uint32_t idesc, uint32_t accumulate) {
   constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -650,23 +625,11 @@ __device__ __forceinline__ void tmem_ld16x256b_x4(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-// The same layout, 16 and 64 columns.
+// The same layout, 16 columns.
 __device__ __forceinline__ void tmem_ld16x256b_x2(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld16x256b_x8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
@@ -686,17 +649,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

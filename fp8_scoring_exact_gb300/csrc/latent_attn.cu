@@ -20,17 +20,35 @@
 // in TMEM; nothing but the result leaves the SM.
 //
 // Warps: 0 copies (a ring of 16 KB slots of 128 dims of a page, and 8 KB
-// slots of the rope dims), 1 issues the MMAs (S^T of the next tile before O^T
-// of this one, so the softmax is hidden), 2-5 do the softmax: the 16 x 256b
-// TMEM load leaves a thread two keys and N / 4 rows; the maximum over the 64
-// keys is three shuffle steps and one exchange through shared memory; the
-// weights go to shared memory as bf16 by stmatrix.  The reference maximum of
-// a row only moves when a tile exceeds it by 2^8 (fp32 sums and bf16 weights
-// have the range for that), so O^T is rarely rescaled.
+// slots of the rope dims), 1 issues S^T, the last O^T (a warp of its own: a
+// tile's weights are ready while the next tile's data are on their way, and
+// its slots should come free then), those between do the softmax: the 16 x
+// 256b TMEM load leaves a thread two keys and some rows; the weights go to
+// shared memory as bf16 by stmatrix.  The reference maximum of a row only
+// moves when a logit passes it by 8 (a factor of 2^8: fp32 sums and bf16
+// weights have the range for that), which a vote over the warps finds out; only
+// then are maxima exchanged and O^T is rescaled (finding the maximum of every
+// tile instead: 187 us against 175 for 64 sequences behind 32768 shared keys).
 //
 // Every CTA takes an equal run of the call's tiles, whatever item they
-// belong to; an item cut by a run's border is joined by the merge kernel in
+// belong to; an item cut by a run's border is joined by the finish kernel in
 // the order of its pieces, so results do not depend on timing.
+//
+// Rows per block: the least that holds a sequence's rows, as every block reads
+// the keys anew.  16 sequences of 32768 keys, in us, against the copy rate's 89:
+//     rows      N = 16   N = 32   N = 64
+//     16          102      106      109
+//     32          187      106      110
+//     64          356        -      114
+// 64 sequences of up to 131072 keys with two tokens of 16 heads (4.6 GB): 662 to
+// 682 us, 6.8 to 7.0 TB/s, the measured copy rate.  N = 64 is bound by its chain:
+// the query block leaves room for two tiles, a tile's copy, S^T, softmax and
+// O^T take about 5400 cycles one after the other, and 1620 of the 2700 per tile
+// are the tensor cores' (the M = 64 steps of S^T run at half their rate): 64
+// sequences of two tokens of 16 heads behind 32768 shared keys 168 us, 0.90
+// PFLOP/s; seven sequences of 128 heads 72 us, which read 193 MB twice.
+// (Prefetching the pages of tiles 2, 3, 5 or 8 ahead into L2 made all of these
+// slower: 16 sequences of 64 rows 122, 129, 164, 173 us.)
 #include "latent.h"
 
 namespace dsa {
@@ -661,8 +679,12 @@ struct RowPieces {
 // the logits that the main kernel left, N / 4 lanes per key and 4 rows per lane;
 // they work the rows' maxima m and sums l out of the pieces themselves rather
 // than wait (and than use lse = m + log2 l, which as one number has lost bits).
+// Bound by latency, a handful of dependent loads: 10 us for 896 rows of 11 pieces,
+// 13 for 2048 rows of 7, 15 with the weights of 32 sequences of up to 16384 keys
+// (17 MB of logits).  Summing them in the main kernel would need the final
+// maximum and sum of every row before its last tile.
 constexpr int FIN_THREADS = 256;
-constexpr int FIN_BATCH = 4;
+constexpr int FIN_BATCH = 4;    // loads in flight per thread of the weights' sums (one: 17 us instead of 15)
 constexpr int FIN_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
 template <int N>
 __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const LatentAttnParams p, int spread) {

@@ -12,13 +12,23 @@
 //     O [256 x 128] += P [256 x 128] . V      8 steps
 // The pair's MMA splits the B operand: each CTA holds 64 of a tile's keys and
 // 64 of the value dims, so a key tile costs 40 KB of shared memory and of copies
-// per CTA and three and a half of them fit beside the queries and the output.  S has three buffers of 128 columns
-// in TMEM, O the fourth; the weights go back over their logits as bf16 and are
-// the second product's A operand there: the logits of the next tiles are made
-// while this one's softmax runs, a thread per row.  As in latent_attn.cu the
-// reference maximum moves only past 2^8.
+// per CTA and three of them fit beside the queries and the output.  S has three
+// buffers of 128 columns in TMEM, O the fourth; the weights go back over their
+// logits as bf16 and are the second product's A operand there: the logits of the
+// next tiles are made while this one's softmax runs, two threads per row.  As in
+// latent_attn.cu a row's reference moves only when a logit passes it by 8.
 // (One CTA per block with two 128-query tiles and one S buffer each ran at 56%
-// tensor time: a tile's next S had to wait for its softmax and its product.)
+// tensor time: a tile's next S had to wait for its softmax and its product.  One
+// thread per row: 211 us where two take 206, for the first case below.  Loading
+// the next tile's logits while this one's become weights: 215.)
+//
+// 2048 queries on 16384 keys of 16 heads: 206 us, 1.56 PFLOP/s of the 1.94 that
+// a library product reaches.  A tile takes some 1620 cycles, 1280 of them the
+// tensor cores'; the softmax, which sets the pace, spends 360 on loading the
+// logits and their maximum, 920 on the weights and 320 on waits.  Nine prompts
+// of up to 2500 tokens: 91 us, 0.83 PFLOP/s of unmasked work; 38% more is done
+// than that in the tiles that the diagonal and the prompts' ends cut, and a
+// block's start and end and its two masked tiles cost about three tiles' time.
 //
 // Every pair takes an equal run of the call's units (a unit: a key tile of a
 // block, and PF_BLOCK_UNITS more per block); a block cut by a run's border is
@@ -287,14 +297,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     bool ok = true;
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
-      if (!(ok = mbar_wait_one<true>(bar(B_QF), seg & 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one(bar(B_QF), seg & 1, abort_flag, stats))) break;
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         // the weights that were in the buffer have been multiplied
         if (!(ok = mbar_wait_warp(bar(B_V + sb), sp ^ 1, abort_flag, stats))) break;
         for (uint32_t c = 0; c < 3; ++c) {
           const uint32_t n = PF_PER_TILE * it + c, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_one<true>(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
@@ -312,7 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
           // with blocks of one tile this warp is up to three ends ahead)
           for (uint32_t c = 3; ok && c < 5; ++c) {
             const uint32_t n = PF_PER_TILE * it + c;
-            ok = mbar_wait_one<true>(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+            ok = mbar_wait_one(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
           }
           if (!ok) break;
           if (lane == 0) {
@@ -332,13 +342,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
       // the previous piece's O has been read out
-      if (!(ok = mbar_wait_one<true>(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
       for (int k = k0; ok && k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         for (uint32_t half = 0; half < 2; ++half) {  // 64 keys: the weights' halves and the values' slots
           const uint32_t n = PF_PER_TILE * it + 3 + half, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_one<true>(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
-          if (!(ok = mbar_wait_one<true>(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
 #pragma unroll
@@ -397,7 +407,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         // arrival releases; a CTA's slots hold its value dims of all 128 keys
         const int valid = pc.seq.m - k * PF_KEYS;
         if (valid < PF_KEYS) {
-          mbar_wait_one<true>(bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
+          mbar_wait_one(bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
+          __syncwarp();
           tails ^= 1u << sb;
           uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + half) % PF_SLOTS) * PF_SLOT);
           for (int x = max(0, valid - 64 * half) * 8 + r; x < 64 * 8; x += 128) v[x] = make_uint4(0, 0, 0, 0);
