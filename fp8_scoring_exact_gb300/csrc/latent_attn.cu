@@ -673,103 +673,30 @@ struct RowPieces {
   }
 };
 
-// The call's last kernel.  CTAs [0, rows): one row each, its pieces joined in
-// their order.  The CTAs after them, if key weights are wanted: `spread` per
-// sequence, weights[b, s] += sum over the rows that see key s of 2^(u - m) / l from
-// the logits that the main kernel left, N / 4 lanes per key and 4 rows per lane;
-// they work the rows' maxima m and sums l out of the pieces themselves rather
-// than wait (and than use lse = m + log2 l, which as one number has lost bits).
-// Bound by latency, a handful of dependent loads: 10 us for 896 rows of 11 pieces,
-// 13 for 2048 rows of 7, 15 with the weights of 32 sequences of up to 16384 keys
-// (17 MB of logits).  Summing them in the main kernel would need the final
-// maximum and sum of every row before its last tile.
-constexpr int FIN_THREADS = 256;
-constexpr int FIN_BATCH = 4;    // loads in flight per thread of the weights' sums (one: 17 us instead of 15)
+// A row's pieces joined in their order, dims [d0, d0 + DIMS) of it: THREADS / (DIMS / 4)
+// parts take every so manieth piece, 4 dims per thread.
 constexpr int FIN_MAX = 2 * 1024;  // pieces of a row at most: the grid's CTAs, twice with a prefix
-template <int N>
-__global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const LatentAttnParams p, int spread) {
-  pdl_enter();
+template <int THREADS, int DIMS>
+__device__ __forceinline__ void join_row(const LatentAttnParams& p, int64_t row, int d0) {
+  constexpr int PER = DIMS / 4, PARTS = THREADS / PER, WARPS = THREADS / 32;
   __shared__ float s_w[FIN_MAX];
-  __shared__ float s_part[LA_DC];
-  __shared__ float s_tmp[FIN_THREADS / 32];
-  extern __shared__ float2 s_ml[];  // [rows of a sequence] (-m, 1 / l)
-  const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.next_n * p.H;
+  __shared__ float s_part[PARTS > 1 ? PARTS - 1 : 1][DIMS];
+  __shared__ float s_tmp[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (row == 0 && tid == 0) {
-    p.status->last = p.status->now;
-    p.status->now = 0;
-  }
-  if (row >= rows) {
-    const int R = p.next_n * p.H, b = (int)(row - rows) / spread;
-    for (int i = tid; i < R; i += FIN_THREADS) {
-      const RowPieces rp(p, (int64_t)b * R + i);
-      float m = neg_inf(), sum = 0.f;
-      for (int j = 0; j < rp.n; ++j) m = fmaxf(m, p.part_ml[rp.at(p, j)].x);
-      const float mm = m == neg_inf() ? 0.f : m;
-      for (int j = 0; j < rp.n; ++j) {
-        const float2 ml = p.part_ml[rp.at(p, j)];
-        sum += ex2(ml.x - mm) * ml.y;
-      }
-      s_ml[i] = make_float2(-mm, sum == 0.f ? 0.f : 1.f / sum);
-    }
-    constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK, STEPS = LT / KEYS;  // lanes per key, keys per step, steps per tile
-    bool bad;
-    const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT);
-    const int sub = tid % LPK, kk = tid / LPK;
-    // FIN_BATCH steps at a time, their loads together: one after the other
-    // they were the kernel's time
-    const int t0 = (int)(row - rows) % spread, steps = tiles > t0 ? ceil_div(tiles - t0, spread) * STEPS : 0;
-    for (int i0 = 0; i0 < steps; i0 += FIN_BATCH) {
-      float old[FIN_BATCH], sum[FIN_BATCH];
-      int key[FIN_BATCH];
-#pragma unroll
-      for (int x = 0; x < FIN_BATCH; ++x) {
-        const int i = i0 + x;
-        key[x] = (t0 + i / STEPS * spread) * LT + i % STEPS * KEYS + kk;
-        if (i >= steps || key[x] >= len) key[x] = -1;
-        old[x] = sub == 0 && key[x] >= 0 ? p.weights[b * p.ld_weights + key[x]] : 0.f;
-        sum[x] = 0.f;
-      }
-      for (int j = 0; j < p.blocks; ++j) {
-        const float* base = p.logits + (int64_t)(b * p.blocks + j) * p.max_pages * LT * N + 4 * sub;
-        float4 u[FIN_BATCH];
-#pragma unroll
-        for (int x = 0; x < FIN_BATCH; ++x)
-          u[x] = key[x] >= 0 ? __ldcs(reinterpret_cast<const float4*>(base + (int64_t)key[x] * N))
-                             : make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
-        if (i0 == 0 && j == 0) __syncthreads();  // s_ml, behind the first loads
-#pragma unroll
-        for (int x = 0; x < FIN_BATCH; ++x) {
-          const int r = j * N + 4 * sub;
-          const float v[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (r + e < R && v[e] != neg_inf()) sum[x] += ex2(fmaf(v[e], p.scale_log2, s_ml[r + e].x)) * s_ml[r + e].y;
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < FIN_BATCH; ++x) {
-#pragma unroll
-        for (int o = 1; o < LPK; o <<= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
-        if (sub == 0 && key[x] >= 0) p.weights[b * p.ld_weights + key[x]] = old[x] + sum[x];
-      }
-    }
-    return;
-  }
   const RowPieces rp(p, row);
   const int n = rp.n;
   if (rp.done(p)) return;
   float m = neg_inf();
-  for (int i = tid; i < n; i += FIN_THREADS) m = fmaxf(m, p.part_ml[rp.at(p, i)].x);
+  for (int i = tid; i < n; i += THREADS) m = fmaxf(m, p.part_ml[rp.at(p, i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_tmp[warp] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < FIN_THREADS / 32; ++i) m = fmaxf(m, s_tmp[i]);
+  for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_tmp[i]);
   const float mm = m == neg_inf() ? 0.f : m;
   float sum = 0.f;
-  for (int i = tid; i < n; i += FIN_THREADS) {
+  for (int i = tid; i < n; i += THREADS) {
     const float2 ml = p.part_ml[rp.at(p, i)];
     const float x = ex2(ml.x - mm);
     s_w[i] = x;
@@ -782,15 +709,13 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
   __syncthreads();
   sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < FIN_THREADS / 32; ++i) sum += s_tmp[i];
-  // two halves of the CTA take every other piece, 4 dims per thread (loading
-  // the first pieces ahead of the factors gained nothing)
-  const int half = tid >> 7, d = 4 * (tid & 127);
+  for (int i = 0; i < WARPS; ++i) sum += s_tmp[i];
+  const int part = tid / PER, d = 4 * (tid % PER);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = half; i < n; i += 2) {
+  for (int i = part; i < n; i += PARTS) {
     const float x = s_w[i];
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + rp.at(p, i) * LA_DC + d));
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + rp.at(p, i) * LA_DC + d0 + d));
     if (x != 0.f) {  // a piece without a visible key adds nothing
       o.x += x * v.x;
       o.y += x * v.y;
@@ -798,16 +723,115 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
       o.w += x * v.w;
     }
   }
-  if (half) *reinterpret_cast<float4*>(&s_part[d]) = o;
-  __syncthreads();
-  if (half == 0) {
-    const float4 v = *reinterpret_cast<const float4*>(&s_part[d]);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DC + d);
-    dst[0] = __floats2bfloat162_rn((o.x + v.x) * inv, (o.y + v.y) * inv);
-    dst[1] = __floats2bfloat162_rn((o.z + v.z) * inv, (o.w + v.w) * inv);
+  if (PARTS > 1) {
+    if (part) *reinterpret_cast<float4*>(&s_part[part - 1][d]) = o;
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int i = 0; i < PARTS - 1; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(&s_part[i][d]);
+      o.x += v.x;
+      o.y += v.y;
+      o.z += v.z;
+      o.w += v.w;
+    }
   }
-  if (tid == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + row * LA_DC + d0 + d);
+  dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  if (tid == 0 && d0 == 0) p.lse[row] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+}
+
+// The call's last kernel: CTA (row, chunk of dims).
+template <int THREADS, int DIMS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) latent_join_kernel(const LatentAttnParams p) {
+  pdl_enter();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  join_row<THREADS, DIMS>(p, blockIdx.x, DIMS * blockIdx.y);
+}
+
+// The same with key weights.  CTAs [0, rows) join a row each; of those after
+// them `spread` per sequence add to weights[b, s] the sum over the rows that see key s
+// of 2^(u - m) / l, from the logits that the main kernel left, N / 4 lanes per key
+// and 4 rows per lane; they work the rows' maxima m and sums l out of the pieces
+// themselves rather than wait (and than use lse = m + log2 l, which as one
+// number has lost bits).  Bound by latency, a handful of dependent loads: 15 us for
+// 32 sequences of up to 16384 keys and 16 rows (17 MB of logits).  Summing in
+// the main kernel would need every row's final maximum and sum before its last tile.
+constexpr int FIN_THREADS = 256;
+constexpr int FIN_BATCH = 4;    // loads in flight per thread (one: 17 us instead of 15)
+template <int N>
+__global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const LatentAttnParams p, int spread) {
+  pdl_enter();
+  extern __shared__ float2 s_ml[];  // [rows of a sequence] (-m, 1 / l)
+  const int64_t row = blockIdx.x, rows = (int64_t)p.B * p.next_n * p.H;
+  const int tid = threadIdx.x;
+  if (row == 0 && tid == 0) {
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  if (row < rows) {
+    join_row<FIN_THREADS, LA_DC>(p, row, 0);
+    return;
+  }
+  const int R = p.next_n * p.H, b = (int)(row - rows) / spread;
+  for (int i = tid; i < R; i += FIN_THREADS) {
+    const RowPieces rp(p, (int64_t)b * R + i);
+    float m = neg_inf(), sum = 0.f;
+    for (int j = 0; j < rp.n; ++j) m = fmaxf(m, p.part_ml[rp.at(p, j)].x);
+    const float mm = m == neg_inf() ? 0.f : m;
+    for (int j = 0; j < rp.n; ++j) {
+      const float2 ml = p.part_ml[rp.at(p, j)];
+      sum += ex2(ml.x - mm) * ml.y;
+    }
+    s_ml[i] = make_float2(-mm, sum == 0.f ? 0.f : 1.f / sum);
+  }
+  constexpr int LPK = N / 4, KEYS = FIN_THREADS / LPK, STEPS = LT / KEYS;  // lanes per key, keys per step, steps per tile
+  bool bad;
+  const int len = valid_len(p.seq_lens[b], p.max_pages, bad), tiles = ceil_div(len, LT);
+  const int sub = tid % LPK, kk = tid / LPK;
+  // FIN_BATCH steps at a time, their loads together: one after the other
+  // they were the kernel's time
+  const int t0 = (int)(row - rows) % spread, steps = tiles > t0 ? ceil_div(tiles - t0, spread) * STEPS : 0;
+  for (int i0 = 0; i0 < steps; i0 += FIN_BATCH) {
+    float old[FIN_BATCH], sum[FIN_BATCH];
+    int key[FIN_BATCH];
+#pragma unroll
+    for (int x = 0; x < FIN_BATCH; ++x) {
+      const int i = i0 + x;
+      key[x] = (t0 + i / STEPS * spread) * LT + i % STEPS * KEYS + kk;
+      if (i >= steps || key[x] >= len) key[x] = -1;
+      old[x] = sub == 0 && key[x] >= 0 ? p.weights[b * p.ld_weights + key[x]] : 0.f;
+      sum[x] = 0.f;
+    }
+    for (int j = 0; j < p.blocks; ++j) {
+      const float* base = p.logits + (int64_t)(b * p.blocks + j) * p.max_pages * LT * N + 4 * sub;
+      float4 u[FIN_BATCH];
+#pragma unroll
+      for (int x = 0; x < FIN_BATCH; ++x)
+        u[x] = key[x] >= 0 ? __ldcs(reinterpret_cast<const float4*>(base + (int64_t)key[x] * N))
+                           : make_float4(neg_inf(), neg_inf(), neg_inf(), neg_inf());
+      if (i0 == 0 && j == 0) __syncthreads();  // s_ml, behind the first loads
+#pragma unroll
+      for (int x = 0; x < FIN_BATCH; ++x) {
+        const int r = j * N + 4 * sub;
+        const float v[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r + e < R && v[e] != neg_inf()) sum[x] += ex2(fmaf(v[e], p.scale_log2, s_ml[r + e].x)) * s_ml[r + e].y;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < FIN_BATCH; ++x) {
+#pragma unroll
+      for (int o = 1; o < LPK; o <<= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+      if (sub == 0 && key[x] >= 0) p.weights[b * p.ld_weights + key[x]] = old[x] + sum[x];
+    }
+  }
 }
 
 template <int N>
@@ -820,8 +844,17 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
   if (e != cudaSuccess) return e;
   count_launch();
   const int R = p.next_n * p.H, spread = min(p.max_pages, ceil_div(8 * p.grid, p.B));
-  return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * R + (p.weights ? p.B * spread : 0))), dim3(FIN_THREADS),
-                    p.weights ? 8 * (size_t)R : 0, s, p, spread);
+  if (p.weights)
+    return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * (R + spread))), dim3(FIN_THREADS), 8 * (size_t)R, s,
+                      p, spread);
+  // few items, so rows of many pieces: more threads take fewer dims (a sequence of 131072 keys and 16 rows:
+  // 41 us, 43 the other way; two of 64 rows 68 and 75).  Else two parts of 256 dims (seven sequences of 128
+  // rows, 11 pieces each, 71 us and 78 the first way; 64 sequences behind 32768 shared keys 166 and 185).  128
+  // threads for all 512 dims are the best for even lengths (163), but a long sequence among short ones has
+  // as many pieces as one alone (30 us for the join instead of 17).
+  if (p.grid > 32 * (p.prefix_items ? p.prefix_items : p.items))
+    return launch_pdl(latent_join_kernel<256, 128, 4>, dim3(p.B * R, LA_DC / 128), dim3(256), 0, s, p);
+  return launch_pdl(latent_join_kernel<128, 256, 8>, dim3(p.B * R, LA_DC / 256), dim3(128), 0, s, p);
 }
 
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
