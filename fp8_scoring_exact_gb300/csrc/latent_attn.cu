@@ -43,10 +43,12 @@
 // 64 sequences of up to 131072 keys with two tokens of 16 heads (4.6 GB): 662 to
 // 682 us, 6.8 to 7.0 TB/s, the measured copy rate.  N = 64 is bound by its chain:
 // the query block leaves room for two tiles, a tile's copy, S^T, softmax and
-// O^T take about 5400 cycles one after the other, and 1620 of the 2700 per tile
+// O^T take some 4200 cycles one after the other, and 1650 of the 2100 per tile
 // are the tensor cores' (the M = 64 steps of S^T run at half their rate): 64
-// sequences of two tokens of 16 heads behind 32768 shared keys 168 us, 0.90
-// PFLOP/s; seven sequences of 128 heads 72 us, which read 193 MB twice.
+// sequences of two tokens of 16 heads behind 32768 shared keys 161 us, 0.94
+// PFLOP/s; seven sequences of 128 heads 70 us, which read 193 MB twice.  The MMAs
+// take shared memory's whole bandwidth, so the softmax keeps what it can in
+// registers (references read from shared memory for every tile: 167 us).
 // (Prefetching the pages of tiles 2, 3, 5 or 8 ahead into L2 made all of these
 // slower: 16 sequences of 64 rows 122, 129, 164, 173 us.)
 #include "latent.h"
@@ -435,7 +437,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
       const Item im = load_item(p, w);
       for (int c = st_id; c < N; c += C::ST)
         s_lim[c] = c >= im.nrows ? 0 : im.r0 < 0 ? im.len : max(0, im.len - p.next_n + 1 + (im.r0 + c) / p.H);
-      float l[2 * M8];                       // this thread's part of each row's sum
+      float2 f[M8];                          // the references of this thread's rows
+      float l[2 * M8];                       // its part of each row's sum
 #pragma unroll
       for (int i = 0; i < 2 * M8; ++i) l[i] = 0.f;
       ref = neg_inf();
@@ -501,9 +504,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
           float over = neg_inf();
 #pragma unroll
           for (int m = 0; m < M8; ++m) {
-            const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * m + cc]);
-            over = fmaxf(over, fmaf(fmaxf(u[m][0], u[m][2]), p.scale_log2, -f.x));
-            over = fmaxf(over, fmaf(fmaxf(u[m][1], u[m][3]), p.scale_log2, -f.y));
+            over = fmaxf(over, fmaf(fmaxf(u[m][0], u[m][2]), p.scale_log2, -f[m].x));
+            over = fmaxf(over, fmaf(fmaxf(u[m][1], u[m][3]), p.scale_log2, -f[m].y));
           }
           rescale = named_bar_or(1, C::ST, over > RESCALE_AT);
         }
@@ -528,15 +530,16 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
           named_bar_sync(1, C::ST);
 #pragma unroll
           for (int i = 0; i < 2 * M8; ++i) l[i] *= s_alpha[8 * (i >> 1) + cc + (i & 1)];
+#pragma unroll
+          for (int m = 0; m < M8; ++m) f[m] = *reinterpret_cast<const float2*>(&s_ref[8 * m + cc]);
         }
         // weights: fp32 into the sums, rounded to bf16 (the type of V, which
         // the MMA wants of both operands) for P
         uint32_t r[M8][2];
 #pragma unroll
         for (int m = 0; m < M8; ++m) {
-          const float2 f = *reinterpret_cast<const float2*>(&s_ref[8 * m + cc]);
-          const float a0 = ex2(fmaf(u[m][0], p.scale_log2, -f.x)), a1 = ex2(fmaf(u[m][1], p.scale_log2, -f.y));
-          const float b0 = ex2(fmaf(u[m][2], p.scale_log2, -f.x)), b1 = ex2(fmaf(u[m][3], p.scale_log2, -f.y));
+          const float a0 = ex2(fmaf(u[m][0], p.scale_log2, -f[m].x)), a1 = ex2(fmaf(u[m][1], p.scale_log2, -f[m].y));
+          const float b0 = ex2(fmaf(u[m][2], p.scale_log2, -f[m].x)), b1 = ex2(fmaf(u[m][3], p.scale_log2, -f[m].y));
           l[2 * m] += a0 + b0;
           l[2 * m + 1] += a1 + b1;
           const __nv_bfloat162 pa = __floats2bfloat162_rn(a0, a1), pc = __floats2bfloat162_rn(b0, b1);
