@@ -184,13 +184,14 @@ void release_latent_scratch() {
 }
 }  // namespace dsa
 
+// (an entry lets no C++ exception out: the table of scratch buffers may fail to grow)
 extern "C" {
 
 int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* ckv, int64_t ckv_stride,
                                const uint16_t* kpe, int64_t kpe_stride, const int32_t* block_table,
                                const int32_t* seq_lens, int B, int next_n, int H, int max_pages, int num_pages,
                                float sm_scale, uint16_t* out, float* lse, float* weights, int64_t ld_weights,
-                               dsa_stream_t stream) {
+                               dsa_stream_t stream) try {
   LatentAttnParams p{};
   p.q_nope = bf(q_nope);
   p.q_pe = bf(q_pe);
@@ -211,6 +212,8 @@ int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe, con
   p.weights = weights;
   p.ld_weights = ld_weights;
   return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return DSA_ERR_CUDA;
 }
 
 int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* ckv,
@@ -218,7 +221,7 @@ int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q
                                        const int32_t* prefix_table, const int32_t* prefix_len, int prefix_pages,
                                        const int32_t* block_table, const int32_t* seq_lens, int B, int next_n, int H,
                                        int max_pages, int num_pages, float sm_scale, uint16_t* out, float* lse,
-                                       dsa_stream_t stream) {
+                                       dsa_stream_t stream) try {
   if (!prefix_table || !prefix_len || prefix_pages <= 0) return DSA_ERR_ARG;
   LatentAttnParams p{};
   p.q_nope = bf(q_nope);
@@ -241,12 +244,14 @@ int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return DSA_ERR_CUDA;
 }
 
 int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride, uint8_t* k_cache,
                            float* k_cache_scale, float* weights, int64_t ld_weights, const int32_t* block_table,
                            const int32_t* seq_lens, int B, int max_pages, int num_pages, int budget, int recent,
-                           int32_t* kept, int32_t* new_lens, dsa_stream_t stream_) {
+                           int32_t* kept, int32_t* new_lens, dsa_stream_t stream_) try {
   if (!ckv || !kpe || !weights || !block_table || !seq_lens || !kept || !new_lens || !k_cache != !k_cache_scale)
     return DSA_ERR_ARG;
   if (B <= 0 || max_pages <= 0 || num_pages <= 0 || budget <= 0 || recent < 0 || recent > budget) return DSA_ERR_ARG;
@@ -300,6 +305,8 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   p.ticket = reinterpret_cast<int*>(base + o_ti);
   p.status = reinterpret_cast<LatentStatus*>(base);
   return launch_evict(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+} catch (...) {
+  return DSA_ERR_CUDA;
 }
 
 int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -307,7 +314,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
                                  const uint16_t* k_pe, int64_t kp_token_stride, const uint16_t* v,
                                  int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
                                  const int32_t* cu_k, int S, int Tq, int Tk, int H, int causal, float sm_scale,
-                                 uint16_t* out, float* lse, dsa_stream_t stream_) {
+                                 uint16_t* out, float* lse, dsa_stream_t stream_) try {
   if (!q || !k_nope || !k_pe || !v || !cu_q || !cu_k || !out || !lse) return DSA_ERR_ARG;
   if (S <= 0 || Tq <= 0 || Tk <= 0 || H <= 0 || !usable_scale(sm_scale * 1.4426950408889634f)) return DSA_ERR_ARG;
   const int64_t strides[] = {q_token_stride, q_head_stride, kn_token_stride, kn_head_stride,
@@ -355,9 +362,11 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   p.part_ml = reinterpret_cast<float2*>(base + o_ml);
   p.part_o = reinterpret_cast<float*>(base + o_po);
   return launch_prefill(m, p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+} catch (...) {
+  return DSA_ERR_CUDA;
 }
 
-int dsa_latent_last_status(dsa_stream_t stream_) {
+int dsa_latent_last_status(dsa_stream_t stream_) try {
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSA_ERR_CUDA;
   int dev = 0;
@@ -370,6 +379,8 @@ int dsa_latent_last_status(dsa_stream_t stream_) {
   const int st = s.last;
   if (st & ST_TIMEOUT) return DSA_ERR_TIMEOUT;
   return (st & ST_RANGE) ? DSA_ERR_RANGE : DSA_OK;
+} catch (...) {
+  return DSA_ERR_CUDA;
 }
 
 }  // extern "C"
