@@ -288,28 +288,30 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
 }
 
 // Warp-uniform bounded wait for a phase that another CTA of the cluster may
-// arrive on, in which one lane polls for the warp (a poll is an access per lane
-// to one shared-memory word): code in which other lanes than the elected one
-// touch what the phase guards needs a __syncwarp after it.
-__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
+// arrive on, in which the lane with `poller` set polls for the warp (a poll is
+// an access per lane to one shared-memory word).  That lane alone acquires the
+// phase, and elect.sync need not pick lane 0: a warp that issues copies or MMAs
+// on what the phase guards polls in the lane that issues them.  Where other
+// lanes touch what it guards, a __syncwarp has to follow.
+__device__ __forceinline__ bool mbar_poll_warp(uint32_t poller, uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.eq.u32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %3, 0;\n\tsetp.ne.u32 p, %3, %3;\n\t"
       "@e mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(threadIdx.x & 31)
+      : "r"(bar), "r"(parity), "r"(poller)
       : "memory");
   return __any_sync(0xffffffffu, ok);
 }
-static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                       Stats* st) {
+static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t poller, uint32_t bar, uint32_t parity,
+                                                       volatile int* abort_flag, Stats* st) {
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
-    if (mbar_poll_warp(bar, parity)) return true;
+    if (mbar_poll_warp(poller, bar, parity)) return true;
     if ((it & 7u) == 7u) {
       int give_up = 0;
-      if ((threadIdx.x & 31) == 0) {
+      if (poller) {
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         if (*abort_flag) {
@@ -320,13 +322,14 @@ static __device__ __noinline__ bool mbar_wait_one_slow(uint32_t bar, uint32_t pa
           give_up = 1;
         }
       }
-      if (__shfl_sync(0xffffffffu, give_up, 0)) return false;
+      if (__any_sync(0xffffffffu, give_up)) return false;
     }
   }
 }
-__device__ __forceinline__ bool mbar_wait_one(uint32_t bar, uint32_t parity, volatile int* abort_flag, Stats* st) {
-  if (mbar_poll_warp(bar, parity)) return true;
-  return mbar_wait_one_slow(bar, parity, abort_flag, st);
+__device__ __forceinline__ bool mbar_wait_one(uint32_t poller, uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                              Stats* st) {
+  if (mbar_poll_warp(poller, bar, parity)) return true;
+  return mbar_wait_one_slow(poller, bar, parity, abort_flag, st);
 }
 
 // Warp-uniform bounded wait for a warp whose wake-up latency has slack (the

@@ -299,14 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     bool ok = true;
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
-      if (!(ok = mbar_wait_one(bar(B_QF), seg & 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one(leader, bar(B_QF), seg & 1, abort_flag, stats))) break;
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         // the weights that were in the buffer have been multiplied
         if (!(ok = mbar_wait_warp(bar(B_V + sb), sp ^ 1, abort_flag, stats))) break;
         for (uint32_t c = 0; c < 3; ++c) {
           const uint32_t n = PF_PER_TILE * it + c, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_one(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(leader, bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t k_lo = desc_lo_kmajor(sbase + PF_OFF_RING + st * PF_SLOT);
 #pragma unroll
@@ -324,10 +324,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
           // with blocks of one tile this warp is up to three ends ahead)
           for (uint32_t c = 3; ok && c < 5; ++c) {
             const uint32_t n = PF_PER_TILE * it + c;
-            ok = mbar_wait_one(bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
+            ok = mbar_wait_one(leader, bar(B_FULL + n % PF_SLOTS), (n / PF_SLOTS) & 1, abort_flag, stats);
           }
           if (!ok) break;
-          if (lane == 0) {
+          if (leader) {  // (the lane that acquired them)
             mbar_arrive(bar(B_Z + sb));
             mbar_arrive_cluster<true>(cluster_addr(bar(B_Z + sb), 1));
           }
@@ -344,13 +344,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
     for (; ok && pc.next(p, k0, k1, tiles); pc.step(tiles)) {
       if (k1 <= k0) continue;
       // the previous piece's O has been read out
-      if (!(ok = mbar_wait_one(bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
+      if (!(ok = mbar_wait_one(leader, bar(B_O), (seg & 1) ^ 1, abort_flag, stats))) break;
       for (int k = k0; ok && k < k1; ++k, ++it) {
         const uint32_t sb = it % PF_BUFS, sp = it / PF_BUFS & 1;
         for (uint32_t half = 0; half < 2; ++half) {  // 64 keys: the weights' halves and the values' slots
           const uint32_t n = PF_PER_TILE * it + 3 + half, st = n % PF_SLOTS;
-          if (!(ok = mbar_wait_one(bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
-          if (!(ok = mbar_wait_one(bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(leader, bar(B_FULL + st), (n / PF_SLOTS) & 1, abort_flag, stats))) break;
+          if (!(ok = mbar_wait_one(leader, bar(B_P + 2 * sb + half), sp, abort_flag, stats))) break;
           tc_fence_after();
           const uint32_t v_lo = desc_lo_mnmajor(sbase + PF_OFF_RING + st * PF_SLOT, PF_SLOT);
 #pragma unroll
@@ -409,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PF_THREADS, 1)
         // arrival releases; a CTA's slots hold its value dims of all 128 keys
         const int valid = pc.seq.m - k * PF_KEYS;
         if (valid < PF_KEYS) {
-          mbar_wait_one(bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
+          mbar_wait_one(lane == 0, bar(B_Z + sb), tails >> sb & 1, abort_flag, stats);
           __syncwarp();
           tails ^= 1u << sb;
           uint4* v = reinterpret_cast<uint4*>(smem + PF_OFF_RING + ((PF_PER_TILE * it + 3 + half) % PF_SLOTS) * PF_SLOT);
