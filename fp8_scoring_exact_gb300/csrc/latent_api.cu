@@ -259,7 +259,9 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
       ld_weights < (int64_t)max_pages * PAGE)
     return DSA_ERR_ARG;
   if (!aligned16(ckv) || !aligned16(kpe) || !aligned16(k_cache)) return DSA_ERR_ARG;
-  if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535)
+  // (lengths and the kept list's entries are stepped through with 32-bit indices)
+  if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535 ||
+      budget >= (1 << 30))
     return DSA_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   EvictParams p{};

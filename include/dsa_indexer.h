@@ -332,7 +332,7 @@ DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uin
  *   k_cache, k_cache_scale: the indexer's keys [P, 64, 128] and scales [P, 64]
  *                           of the same pages, moved along, or both null
  *   kept [B, budget] int32: the old logical index of each kept key, ascending,
- *                           then -1
+ *                           then -1 (budget < 2^30)
  *   new_lens [B] int32:     min(seq_lens[b], budget) (may be seq_lens itself)
  */
 DSA_API int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride,
