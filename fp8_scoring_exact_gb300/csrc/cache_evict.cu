@@ -20,7 +20,8 @@
 // c, 64 c + 64) once the entries that live in those slots have been read.  A
 // kept key never moves up (entry i is >= i), so those belong to this chunk or
 // lower ones: their flags, found by two searches in the list.  Chunks are
-// handed out in order and each reads before it waits, so the wait ends.
+// handed out in order and each reads before it waits, so the wait ends.  One that
+// runs out all the same leaves its slots alone and is reported.
 //
 // 64 sequences of up to 32768 keys to 4096, the indexer's keys along: 77 us for
 // 650 MB, over the copy rate as part of it stays in L2.  Five of up to 131072 to
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParam
   // slots written here (this chunk's own are behind the barrier)
   __syncthreads();
   int* flags = p.flags + (int64_t)b * p.chunks;
-  if (tid == 0) {
+  if (tid == 0 && !(p.withhold && c == 0)) {
     __threadfence();
     atomicExch(&flags[c], 1);
   }
@@ -279,8 +280,10 @@ __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParam
         }
     __threadfence();
     if (!ok) atomicOr(&p.status->last, ST_TIMEOUT);
+    s_job[0] = ok;
   }
   __syncthreads();
+  if (!s_job[0]) return;  // these slots hold keys that may not have been read: they stay
 #pragma unroll
   for (int j = 0; j < EM_KEYS * 64 / EM_THREADS; ++j) {
     const int k = (j * EM_THREADS + tid) >> 6;

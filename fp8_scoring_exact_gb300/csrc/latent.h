@@ -99,6 +99,7 @@ struct EvictParams {
   int cluster, cached;          // CTAs per sequence of the selection; weights each holds in shared memory
   int chunks;                   // of EVICT_CHUNK kept keys, per sequence
   uint64_t wait_ns;
+  int withhold;                 // test option: a sequence's first chunk never says that it has been read
   int32_t* old_lens;            // [B] scratch: the validated lengths (new_lens may be seq_lens itself)
   float* new_w;                 // [B, budget] the kept keys' weights
   int* flags;                   // [B, chunks] 1: the chunk's keys have been read

@@ -290,6 +290,7 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   p.chunks = ceil_div(budget, EVICT_CHUNK);
   if ((int64_t)B * p.chunks >= (1ll << 31) - 1) return DSA_ERR_UNSUPPORTED;
   p.wait_ns = option_wait_ns();
+  p.withhold = option_withhold();
   size_t off = HEAD;
   auto take = [&](size_t bytes) {
     const size_t o = off;

@@ -334,6 +334,12 @@ DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uin
  *   kept [B, budget] int32: the old logical index of each kept key, ascending,
  *                           then -1 (budget < 2^30)
  *   new_lens [B] int32:     min(seq_lens[b], budget) (may be seq_lens itself)
+ *
+ * After DSA_ERR_TIMEOUT weights, kept and new_lens are those of the complete
+ * eviction, but groups of 64 slots in [0, budget) of a cut sequence may still
+ * hold what they held before, and the keys meant for them may be gone: such a
+ * sequence's cache has to be filled anew.  No slot is written while a key that
+ * is to be kept may be unread in it, and sequences that are not cut are whole.
  */
 DSA_API int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride,
                                    uint8_t* k_cache, float* k_cache_scale,
@@ -424,8 +430,10 @@ typedef enum {
                                   2000000, range 1..60000000): the kernel then lets the copies and MMAs it
                                   already issued land, returns early, and the call reports DSA_ERR_TIMEOUT */
   DSA_OPT_TEST_WITHHOLD = 9,   /* test option: 1 makes the fused operator's main scorer never signal its first
-                                  accumulator, and the latent attention kernels never load their first keys,
-                                  so that a wait runs out after DSA_OPT_WAIT_LIMIT_US and the call reports DSA_ERR_TIMEOUT (its output is then undefined); default 0 */
+                                  accumulator, the latent attention kernels never load their first keys, and the
+                                  eviction's first 64 kept keys of a sequence never count as read, so that a wait
+                                  runs out after DSA_OPT_WAIT_LIMIT_US and the call reports DSA_ERR_TIMEOUT (its
+                                  output is then undefined, an eviction's as its comment says); default 0 */
   DSA_OPT_MATRIX_ROW_MIN = 10  /* dsa_indexer_topk_from_scores and the unfused operator's selection: rows from
                                   which CTAs take whole rows, or half rows when there are many long ones
                                   (threshold, one pass over the row, selection by the CTA that finishes the

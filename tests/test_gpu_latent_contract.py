@@ -22,3 +22,53 @@ def test_prefill_repeats_bit_for_bit(B, H, qs, ks):  # noqa: F811
         assert torch.equal(lse.view(torch.int32), lse1.view(torch.int32))
     if sum(ks) < 2000:
         _check_prefill(q, kv, kp, cu, first, lse1, True)
+
+
+@pytest.mark.parametrize("indexer,joint", [(False, False), (True, True)])
+def test_eviction_whose_wait_ran_out_leaves_the_slots_alone(B, indexer, joint):  # noqa: F811
+    """With a test option the first 64 kept keys of a sequence never count as read, so that what waits for them
+    (limit 50 ms here) runs out: it is reported, and those slots keep their keys."""
+    lens, budget, recent = [400, 250, 330], 256, 20
+    c = Cache(lens, seed=82, joint=joint)
+    g = torch.Generator().manual_seed(83)
+    w = torch.rand((3, c.table.shape[1] * 64), generator=g)
+    w[:, :64] = 0.0  # the first 64 keys go, so that chunk 0 keeps keys that live in chunk 1's slots
+    kc = torch.randint(0, 256, (c.P, 64, 128), generator=g, dtype=torch.uint8)
+    ks = torch.rand((c.P, 64), generator=g)
+    ck, kp = c.device()
+    dw, dk, ds = w.cuda(), kc.cuda() if indexer else None, ks.cuda() if indexer else None
+    B.set_option("wait_limit_us", 50000)
+    B.set_option("test_withhold", 1)
+    try:
+        kept, new = B.latent_cache_evict(ck, kp, dw, c.table.cuda(), _ints(lens), budget, recent, k_cache=dk,
+                                         k_cache_scale=ds)
+        assert B.latent_last_status() == B.DSA_ERR_TIMEOUT
+    finally:
+        B.set_option("test_withhold", 0)
+        B.set_option("wait_limit_us", 2000000)
+    assert new.tolist() == [256, 250, 256]
+    want = c.data.clone().view(torch.int16).reshape(-1, 576)
+    old, wk, ws = want.clone(), kc.clone().reshape(-1, 128), ks.clone().reshape(-1)
+    for b, L in enumerate(lens):
+        rows = la.kept_keys(w[b].numpy(), L, budget, recent)
+        assert np.array_equal(kept[b, :len(rows)].cpu().numpy(), rows)
+        if L <= budget:
+            continue
+        assert rows[0] >= 64  # (or nothing here would have to wait)
+        # the chunks that hold some of the first 64 kept keys in their own slots
+        waits = {int(r) // 64 for r in rows[:64]} - {0}
+        assert waits and max(waits) < budget // 64
+        slots = torch.from_numpy(la.slots_of(c.table[b].numpy(), L))
+        for i, r in enumerate(rows):
+            if i // 64 in waits:
+                continue
+            want[slots[i]] = old[slots[r]]
+            wk[slots[i]] = kc.reshape(-1, 128)[slots[r]]
+            ws[slots[i]] = ks.reshape(-1)[slots[r]]
+    assert torch.equal(ck.cpu().contiguous().view(torch.int16).reshape(-1, 512), want[:, :512])
+    assert torch.equal(kp.cpu().contiguous().view(torch.int16).reshape(-1, 64), want[:, 512:])
+    if indexer:
+        assert torch.equal(dk.cpu().reshape(-1, 128), wk) and torch.equal(ds.cpu().reshape(-1), ws)
+    # the next call is a whole one again
+    kept, new = B.latent_cache_evict(ck, kp, dw, c.table.cuda(), _ints([256, 250, 256]), 100, 7)
+    assert B.latent_last_status() == 0 and new.tolist() == [100, 100, 100]
