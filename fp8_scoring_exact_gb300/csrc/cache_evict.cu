@@ -78,7 +78,10 @@ __global__ void __launch_bounds__(ES_THREADS) evict_select_kernel(const EvictPar
   for (int i = me; i < p.chunks; i += all) p.flags[(int64_t)b * p.chunks + i] = 0;
   if (me == 0) {
     p.old_lens[b] = L;
-    if (b == 0) *p.ticket = 0;
+    if (b == 0) {
+      *p.ticket = 0;
+      p.status->last = 0;  // the move kernel's CTAs add to it in any order
+    }
   }
   if (L <= p.budget) {  // (the same in the whole cluster)
     for (int i = me; i < n; i += all) kept[i] = i;
@@ -198,10 +201,8 @@ __global__ void __launch_bounds__(EM_THREADS) evict_move_kernel(const EvictParam
   if (tid == 0) s_job[0] = atomicAdd(p.ticket, 1);
   __syncthreads();
   const int b = s_job[0] / p.chunks, c = s_job[0] % p.chunks;
-  if (s_job[0] == 0 && tid == 0) {  // the call's last kernel; only the wait below still reports
-    p.status->last = p.status->now;
-    p.status->now = 0;
-  }
+  // the call's last kernel: what the selection found, beside what the waits below report
+  if (s_job[0] == 0 && tid == 0) atomicOr(&p.status->last, atomicExch(&p.status->now, 0));
   const int L = p.old_lens[b], n = p.budget;
   if (L <= n) return;
   const int i0 = c * EM_KEYS, i1 = min(n, i0 + EM_KEYS);

@@ -72,3 +72,29 @@ def test_eviction_whose_wait_ran_out_leaves_the_slots_alone(B, indexer, joint): 
     # the next call is a whole one again
     kept, new = B.latent_cache_evict(ck, kp, dw, c.table.cuda(), _ints([256, 250, 256]), 100, 7)
     assert B.latent_last_status() == 0 and new.tolist() == [100, 100, 100]
+
+
+def test_an_evictions_time_out_is_never_lost(B):  # noqa: F811
+    """Waits that run out at once report beside the chunk that collects the call's status, in any order; a bad page is
+    reported as well, and the next call starts from no status."""
+    lens, budget = [400] * 24, 256
+    c = Cache(lens, seed=84)
+    table, dl = c.table.cuda(), _ints(lens)
+    w = torch.ones((24, c.table.shape[1] * 64))
+    w[:, :64] = 0.0
+    ck, kp = c.device()
+    B.set_option("wait_limit_us", 1)
+    B.set_option("test_withhold", 1)
+    try:
+        for _ in range(200):
+            B.latent_cache_evict(ck, kp, w.cuda(), table, dl, budget, 20)
+            assert B.latent_last_status() == B.DSA_ERR_TIMEOUT
+    finally:
+        B.set_option("test_withhold", 0)
+        B.set_option("wait_limit_us", 2000000)
+    bad = c.table.clone()
+    bad[3, 1] = c.P
+    B.latent_cache_evict(ck, kp, w.cuda(), bad.cuda(), dl, budget, 20)
+    assert B.latent_last_status() == B.DSA_ERR_RANGE
+    B.latent_cache_evict(ck, kp, w.cuda(), table, dl, budget, 20)
+    assert B.latent_last_status() == 0
