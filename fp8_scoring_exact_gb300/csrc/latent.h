@@ -19,7 +19,8 @@ constexpr int LA_DN = 128, LA_DV = 128;  // expanded form: no-rope key dims and 
 
 // Status of a latent operator's call: its kernels OR into `now`; the last one
 // moves it to `last` and leaves `now` zero for the next call (also when the
-// call is replayed from a graph).
+// call is replayed from a graph).  An eviction's last kernel can itself give up
+// waiting: its CTAs OR into `last`, which the selection has cleared.
 struct LatentStatus {
   int now, last;
 };

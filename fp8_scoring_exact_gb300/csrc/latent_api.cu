@@ -16,11 +16,13 @@ using namespace dsa;
 
 namespace {
 
-// Scratch of one (device, stream): the status in its first 256 bytes, then
-// what the call lays out.  A buffer that has become too small is kept
+// Scratch of one (device, stream), and the status of the calls on it.  A buffer that has become too small is kept
 // until dsa_indexer_release: a captured graph may still hold its address, and
-// growing by half at least bounds what is kept to twice the last size.
+// growing by half at least bounds what is kept to twice the last size.  The
+// status has an allocation of its own that never moves, so that a graph
+// captured before the scratch grew reports where the others do.
 struct Scratch {
+  LatentStatus* status = nullptr;
   uint8_t* base = nullptr;
   size_t cap = 0;
   std::vector<uint8_t*> outgrown;
@@ -28,15 +30,25 @@ struct Scratch {
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
-constexpr size_t HEAD = 256;
-static_assert(sizeof(LatentStatus) <= HEAD, "the status is the head");
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Scratch with room for `need` bytes, the status first.  Null on an error.
-uint8_t* get_scratch(cudaStream_t stream, size_t need) {
+// Scratch with room for `need` bytes.  Null on an error.
+const Scratch* get_scratch(cudaStream_t stream, size_t need) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   Scratch& a = g_scratch[{dev, stream}];
+  if (!a.status) {
+    LatentStatus* p = nullptr;
+    if (cudaMalloc(&p, sizeof(*p)) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    if (cudaMemsetAsync(p, 0, sizeof(*p), stream) != cudaSuccess) {
+      cudaFree(p);
+      return nullptr;
+    }
+    a.status = p;
+  }
   if (a.cap < need) {
     const size_t want = align_up(std::max(need, a.cap + a.cap / 2), 1 << 20);
     uint8_t* p = nullptr;
@@ -44,15 +56,11 @@ uint8_t* get_scratch(cudaStream_t stream, size_t need) {
       cudaGetLastError();
       return nullptr;
     }
-    if (cudaMemsetAsync(p, 0, HEAD, stream) != cudaSuccess) {
-      cudaFree(p);
-      return nullptr;
-    }
     if (a.base) a.outgrown.push_back(a.base);
     a.base = p;
     a.cap = want;
   }
-  return a.base;
+  return &a;
 }
 
 // sm_scale * log2(e) has to be a positive finite number
@@ -144,7 +152,7 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
       !tmap_rows(&m.ckv, p.ckv, slots, p.ckv_stride, 8, PAGE, 2) ||
       !tmap_rows(&m.kpe, p.kpe, slots, p.kpe_stride, 1, PAGE, 1))
     return DSA_ERR_CUDA;
-  size_t off = HEAD;
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
@@ -155,9 +163,10 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
                o_po = take(4 * pieces * p.n * LA_DC),
                o_log = p.weights ? take(4 * (size_t)p.B * p.blocks * p.max_pages * PAGE * p.n) : 0;
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, off);
-  if (!base) return DSA_ERR_CUDA;
-  p.status = reinterpret_cast<LatentStatus*>(base);
+  const Scratch* scratch = get_scratch(stream, off);
+  if (!scratch) return DSA_ERR_CUDA;
+  uint8_t* base = scratch->base;
+  p.status = scratch->status;
   p.per = reinterpret_cast<int32_t*>(base + o_per);
   p.start = reinterpret_cast<int32_t*>(base + o_start);
   p.part_ml = reinterpret_cast<float2*>(base + o_ml);
@@ -177,6 +186,7 @@ void release_latent_scratch() {
     cudaGetDevice(&cur);
     cudaSetDevice(kv.first.first);
     if (kv.second.base) cudaFree(kv.second.base);
+    if (kv.second.status) cudaFree(kv.second.status);
     for (uint8_t* q : kv.second.outgrown) cudaFree(q);
     cudaSetDevice(cur);
   }
@@ -291,7 +301,7 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   if ((int64_t)B * p.chunks >= (1ll << 31) - 1) return DSA_ERR_UNSUPPORTED;
   p.wait_ns = option_wait_ns();
   p.withhold = option_withhold();
-  size_t off = HEAD;
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
@@ -300,13 +310,14 @@ int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int
   const size_t o_len = take(4 * (size_t)B), o_w = take(4 * (size_t)B * budget), o_fl = take(4 * (size_t)B * p.chunks),
                o_ti = take(4);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, off);
-  if (!base) return DSA_ERR_CUDA;
+  const Scratch* scratch = get_scratch(stream, off);
+  if (!scratch) return DSA_ERR_CUDA;
+  uint8_t* base = scratch->base;
   p.old_lens = reinterpret_cast<int32_t*>(base + o_len);
   p.new_w = reinterpret_cast<float*>(base + o_w);
   p.flags = reinterpret_cast<int*>(base + o_fl);
   p.ticket = reinterpret_cast<int*>(base + o_ti);
-  p.status = reinterpret_cast<LatentStatus*>(base);
+  p.status = scratch->status;
   return launch_evict(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 } catch (...) {
   return DSA_ERR_CUDA;
@@ -348,7 +359,7 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
       !tmap_heads(&m.v, v, Tk, H, LA_DV, v_token_stride, v_head_stride, 64) ||
       !tmap_rows(&m.k_pe, k_pe, Tk, kp_token_stride, 1, 64, 1))
     return DSA_ERR_CUDA;
-  size_t off = HEAD;
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, 256);
@@ -357,9 +368,10 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
   const size_t o_per = take(8), o_start = take(8 * ((size_t)S + 1) * 2 * p.grid), o_ml = take(8 * 512 * (size_t)p.grid),
                o_po = take(4 * 512 * (size_t)p.grid * LA_DV);
   std::lock_guard<std::mutex> lk(g_mu);
-  uint8_t* base = get_scratch(stream, off);
-  if (!base) return DSA_ERR_CUDA;
-  p.status = reinterpret_cast<LatentStatus*>(base);
+  const Scratch* scratch = get_scratch(stream, off);
+  if (!scratch) return DSA_ERR_CUDA;
+  uint8_t* base = scratch->base;
+  p.status = scratch->status;
   p.per = reinterpret_cast<int64_t*>(base + o_per);
   p.start = reinterpret_cast<int64_t*>(base + o_start);
   p.part_ml = reinterpret_cast<float2*>(base + o_ml);
@@ -376,9 +388,9 @@ int dsa_latent_last_status(dsa_stream_t stream_) try {
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
   auto it = g_scratch.find({dev, stream});
-  if (it == g_scratch.end() || !it->second.base) return DSA_OK;
+  if (it == g_scratch.end() || !it->second.status) return DSA_OK;
   LatentStatus s;
-  if (cudaMemcpy(&s, it->second.base, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaMemcpy(&s, it->second.status, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
   const int st = s.last;
   if (st & ST_TIMEOUT) return DSA_ERR_TIMEOUT;
   return (st & ST_RANGE) ? DSA_ERR_RANGE : DSA_OK;

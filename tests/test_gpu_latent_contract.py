@@ -98,3 +98,41 @@ def test_an_evictions_time_out_is_never_lost(B):  # noqa: F811
     assert B.latent_last_status() == B.DSA_ERR_RANGE
     B.latent_cache_evict(ck, kp, w.cuda(), table, dl, budget, 20)
     assert B.latent_last_status() == 0
+
+
+def _capture(stream, call):
+    """call() once on the stream, which sizes its scratch, then into a graph."""
+    with torch.cuda.stream(stream):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        call()
+    return g
+
+
+def test_a_graphs_status_outlives_the_scratch_it_was_captured_with(B):  # noqa: F811
+    c, big = Cache([300, 64], seed=85), Cache([4000] * 8, seed=86)
+    qn, qp = (x.cuda() for x in _queries(2, 1, 16, seed=87))
+    qbn, qbp = (x.cuda() for x in _queries(8, 2, 64, seed=88))
+    (ck, kp), table, lens = c.device(), c.table.cuda(), _ints(c.lens)
+    (bck, bkp), btable, blens = big.device(), big.table.cuda(), _ints(big.lens)
+    w = torch.zeros((8, big.table.shape[1] * 64), device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = torch.empty_like(qn), torch.empty((2, 1, 16), device="cuda")
+    g = _capture(s, lambda: B.latent_attention_paged(qn, qp, ck, kp, table, lens, SCALE, out=out, lse=lse))
+    with torch.cuda.stream(s):  # a larger call replaces the scratch
+        B.latent_attention_paged(qbn, qbp, bck, bkp, btable, blens, SCALE, weights=w)
+    assert B.latent_last_status(s) == 0
+    lens.copy_(_ints([300, 10 ** 6]))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g.replay()
+    assert B.latent_last_status(s) == B.DSA_ERR_RANGE
+    lens.copy_(_ints(c.lens))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        g.replay()
+    assert B.latent_last_status(s) == 0
+    _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
