@@ -393,8 +393,8 @@ def latent_attention_paged(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_
     cache, pages = _latent_cache(ckv_cache, kpe_cache)
     tables, maxp = _tables(block_table, seq_lens, rows[0])
     w, ldw = (None, 0) if weights is None else _key_weights(weights, rows[0], maxp)
-    rc = lib().dsa_latent_attention_paged(*queries, *cache, *tables, *rows, maxp, pages, sm_scale, out.data_ptr(),
-                                          lse.data_ptr(), w, ldw, _latent_stream(stream))
+    rc = lib().dsa_latent_attention_paged(*queries, *cache, *tables, *rows, maxp, pages, float(sm_scale),
+                                          out.data_ptr(), lse.data_ptr(), w, ldw, _latent_stream(stream))
     _check("dsa_latent_attention_paged", rc)
     return out, lse
 
@@ -410,7 +410,7 @@ def latent_attention_shared_prefix(q_nope, q_pe, ckv_cache, kpe_cache, prefix_ta
     n = prefix_table.numel()
     rc = lib().dsa_latent_attention_shared_prefix(*queries, *cache, _full(prefix_table, "prefix_table", (n,), _I32),
                                                   _full(prefix_len, "prefix_len", (1,), _I32), n, *tables, *rows, maxp,
-                                                  pages, sm_scale, out.data_ptr(), lse.data_ptr(),
+                                                  pages, float(sm_scale), out.data_ptr(), lse.data_ptr(),
                                                   _latent_stream(stream))
     _check("dsa_latent_attention_shared_prefix", rc)
     return out, lse
@@ -466,7 +466,8 @@ def latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, sm_scale, causal=Tr
         lse = torch.empty((Tq, H), dtype=_F32, device=q.device)
     rc = lib().dsa_latent_attention_prefill(q.data_ptr(), sq[0], sq[1], k_nope.data_ptr(), sk[0], sk[1],
                                             k_pe.data_ptr(), sp[0], v.data_ptr(), sv[0], sv[1], *cu, S, Tq, Tk, H,
-                                            1 if causal else 0, sm_scale, _full(out, "out", (Tq, H, LATENT_DV), _BF16),
+                                            1 if causal else 0, float(sm_scale),
+                                            _full(out, "out", (Tq, H, LATENT_DV), _BF16),
                                             _full(lse, "lse", (Tq, H), _F32), _latent_stream(stream))
     _check("dsa_latent_attention_prefill", rc)
     return out, lse

@@ -5,14 +5,16 @@ import pytest
 import torch
 
 from oracle import latent_attention as la
-from test_gpu_latent import B, SCALE, Cache, _check_decode, _check_prefill, _ints, _prefill_inputs, _queries  # noqa: F401
+from test_gpu_latent import (B, SCALE, Cache, _check_decode, _check_prefill, _ints, _prefill_inputs,  # noqa: F401
+                             _queries)
 
 pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("H,qs,ks", [(16, [300, 1, 90, 700], [300, 129, 90, 1400]), (4, [2048], [4096])])
 def test_prefill_repeats_bit_for_bit(B, H, qs, ks):  # noqa: F811
-    """Copies, products and the softmax meet at barriers of both CTAs of a pair: no result may depend on who came first."""
+    """Copies, products and the softmax meet at barriers of both CTAs of a pair: no result may depend on who came
+    first."""
     q, kv, kp, dev, cu = _prefill_inputs(qs, ks, H, seed=81, joint=True)
     first, lse1 = B.latent_attention_prefill(*dev, SCALE)
     runs = [B.latent_attention_prefill(*dev, SCALE) for _ in range(40)]
@@ -136,3 +138,18 @@ def test_a_graphs_status_outlives_the_scratch_it_was_captured_with(B):  # noqa: 
         g.replay()
     assert B.latent_last_status(s) == 0
     _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
+
+
+@pytest.mark.parametrize("scale", [np.float32(SCALE), np.float64(SCALE), torch.tensor(SCALE), 1])
+def test_scales_of_other_number_types(B, scale):  # noqa: F811
+    c = Cache([70, 3], seed=89)
+    qn, qp = (x.cuda() for x in _queries(2, 1, 16, seed=90))
+    (ck, kp), table, lens = c.device(), c.table.cuda(), _ints(c.lens)
+    _, _, _, dev, _ = _prefill_inputs([20], [30], 2, seed=91, joint=True)
+    calls = [lambda s: B.latent_attention_paged(qn, qp, ck, kp, table, lens, s),
+             lambda s: B.latent_attention_shared_prefix(qn, qp, ck, kp, table[0, :1].contiguous(), _ints([5]), table,
+                                                        lens, s),
+             lambda s: B.latent_attention_prefill(*dev, s)]
+    for call in calls:
+        for x, y in zip(call(scale), call(float(scale))):
+            assert torch.equal(x, y)
