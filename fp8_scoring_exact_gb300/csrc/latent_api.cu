@@ -32,11 +32,22 @@ std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Scratch with room for `need` bytes.  Null on an error.
+// Scratch with room for `need` bytes.  Null on an error, and where it would have
+// to grow in a capture: an allocation there ends the capture with an error,
+// or, where the capture's mode allows it, the clearing of the status would only
+// be recorded.
 const Scratch* get_scratch(cudaStream_t stream, size_t need) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   Scratch& a = g_scratch[{dev, stream}];
+  if (!a.status || a.cap < need) {
+    cudaStreamCaptureStatus capturing;
+    if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    if (capturing != cudaStreamCaptureStatusNone) return nullptr;
+  }
   if (!a.status) {
     LatentStatus* p = nullptr;
     if (cudaMalloc(&p, sizeof(*p)) != cudaSuccess) {

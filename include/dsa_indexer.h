@@ -275,8 +275,8 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
  * skipped), all DSA_ERR_RANGE; a pipeline wait that gave up: DSA_ERR_TIMEOUT.
  * Scratch is owned by the library per (device, stream) and grown on demand;
  * an outgrown buffer lives until dsa_indexer_release, so a captured graph
- * stays valid.  A call that has to grow it cannot be captured: run one of the
- * same sizes on the stream first.
+ * stays valid.  A call that has to grow it cannot be captured (DSA_ERR_CUDA; the
+ * capture goes on without it): run one of the same sizes on the stream first.
  */
 
 /*

@@ -153,3 +153,32 @@ def test_scales_of_other_number_types(B, scale):  # noqa: F811
     for call in calls:
         for x, y in zip(call(scale), call(float(scale))):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("mode", ["global", "relaxed"])
+def test_a_call_that_has_to_grow_the_scratch_leaves_a_capture_whole(B, mode):  # noqa: F811
+    c = Cache([70, 3], seed=92)
+    qn, qp = (x.cuda() for x in _queries(2, 1, 16, seed=93))
+    (ck, kp), table, lens = c.device(), c.table.cuda(), _ints(c.lens)
+    out, lse, x = torch.empty_like(qn), torch.empty((2, 1, 16), device="cuda"), torch.zeros(5, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def call():
+        B.latent_attention_paged(qn, qp, ck, kp, table, lens, SCALE, out=out, lse=lse)
+
+    B.release()  # no stream has scratch now
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s, capture_error_mode=mode):
+        with pytest.raises(B.IndexerError) as e:
+            call()
+        x.add_(1.0)
+    assert e.value.code == B.DSA_ERR_CUDA
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.all(x == 1.0) and B.latent_last_status(s) == 0
+    g = _capture(s, call)
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
