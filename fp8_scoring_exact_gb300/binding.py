@@ -334,6 +334,14 @@ def _latent_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
+def _new(shape, dtype, device, stream):
+    """An output, in memory of the stream that writes it: memory of another one may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _slot_stride(t, name, pages, d):
     s = _strided(t, name)
     if t.shape != (pages, 64, d):
@@ -351,18 +359,18 @@ def _latent_cache(ckv, kpe):
     return (ckv.data_ptr(), cs, kpe.data_ptr(), ks), pages
 
 
-def _latent_queries(q_nope, q_pe, out, lse):
+def _latent_queries(q_nope, q_pe, out, lse, stream):
     rows = _dev(q_nope, "q_nope", _BF16).shape
     if len(rows) != 4 or rows[3] != LATENT_DC:
         raise ValueError(f"q_nope must be [B,next_n,H,512], got {list(rows)}")
     rows = rows[:3]
     queries = q_nope.data_ptr(), _full(q_pe, "q_pe", (*rows, LATENT_DP), _BF16)
     if out is None:
-        out = torch.empty_like(q_nope)
+        out = _new((*rows, LATENT_DC), _BF16, q_nope.device, stream)
     else:
         _full(out, "out", (*rows, LATENT_DC), _BF16)
     if lse is None:
-        lse = torch.empty(rows, dtype=_F32, device=q_nope.device)
+        lse = _new(rows, _F32, q_nope.device, stream)
     else:
         _full(lse, "lse", rows, _F32)
     return rows, queries, out, lse
@@ -389,7 +397,7 @@ def latent_attention_paged(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_
     token i of sequence b sees its first seq_lens[b] - next_n + i + 1 keys.  Returns (out
     [B,next_n,H,512] bf16, lse [B,next_n,H] fp32, base 2).  weights fp32 [B, >= 64 max_pages]: the
     softmax weight of every key, summed over the sequence's rows, is added to it."""
-    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse)
+    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse, stream)
     cache, pages = _latent_cache(ckv_cache, kpe_cache)
     tables, maxp = _tables(block_table, seq_lens, rows[0])
     w, ldw = (None, 0) if weights is None else _key_weights(weights, rows[0], maxp)
@@ -404,7 +412,7 @@ def latent_attention_shared_prefix(q_nope, q_pe, ckv_cache, kpe_cache, prefix_ta
     """latent_attention_paged for a batch that shares a prefix: every row also sees the prefix_len[0]
     keys behind prefix_table (int32 [prefix_pages]), which are read once for the whole batch; seq_lens
     counts a sequence's own keys."""
-    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse)
+    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse, stream)
     cache, pages = _latent_cache(ckv_cache, kpe_cache)
     tables, maxp = _tables(block_table, seq_lens, rows[0])
     n = prefix_table.numel()
@@ -434,9 +442,9 @@ def latent_cache_evict(ckv_cache, kpe_cache, weights, block_table, seq_lens, bud
                 _full(k_cache_scale, "k_cache_scale", (pages, 64), _F32))
     budget, recent = int(budget), int(recent)
     if kept is None:
-        kept = torch.empty((B, max(0, budget)), dtype=_I32, device=ckv_cache.device)
+        kept = _new((B, max(0, budget)), _I32, ckv_cache.device, stream)
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=_I32, device=ckv_cache.device)
+        new_lens = _new((B,), _I32, ckv_cache.device, stream)
     rc = lib().dsa_latent_cache_evict(*cache, *keys, w, ldw, *tables, B, maxp, pages, budget, recent,
                                       _full(kept, "kept", (B, max(0, budget)), _I32),
                                       _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
@@ -461,9 +469,9 @@ def latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, sm_scale, causal=Tr
     S = cu_q.numel() - 1
     cu = _full(cu_q, "cu_q", (S + 1,), _I32), _full(cu_k, "cu_k", (S + 1,), _I32)
     if out is None:
-        out = torch.empty((Tq, H, LATENT_DV), dtype=_BF16, device=q.device)
+        out = _new((Tq, H, LATENT_DV), _BF16, q.device, stream)
     if lse is None:
-        lse = torch.empty((Tq, H), dtype=_F32, device=q.device)
+        lse = _new((Tq, H), _F32, q.device, stream)
     rc = lib().dsa_latent_attention_prefill(q.data_ptr(), sq[0], sq[1], k_nope.data_ptr(), sk[0], sk[1],
                                             k_pe.data_ptr(), sp[0], v.data_ptr(), sv[0], sv[1], *cu, S, Tq, Tk, H,
                                             1 if causal else 0, float(sm_scale),

@@ -182,3 +182,38 @@ def test_a_call_that_has_to_grow_the_scratch_leaves_a_capture_whole(B, mode):  #
     g.replay()
     torch.cuda.synchronize()
     _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
+
+
+def _freed_while_in_use(shape, dtype, fill):
+    """Gives a tensor's memory back while the current stream has yet to write it."""
+    x = torch.empty(shape, dtype=dtype, device="cuda")
+    torch.cuda._sleep(40_000_000)  # some 20 ms
+    x.fill_(fill)
+
+
+def test_outputs_of_a_call_on_a_given_stream_lie_in_its_memory(B):  # noqa: F811
+    """An output taken from the current stream's memory would be written by another stream while that memory's last
+    user, here a slow fill, still runs."""
+    lens = [70] * 40
+    c = Cache(lens, seed=94)
+    qn, qp = (x.cuda() for x in _queries(40, 1, 16, seed=95))
+    (ck, kp), table, dl = c.device(), c.table.cuda(), _ints(lens)
+    q, kv, kpe, dev, cu = _prefill_inputs([90], [90], 16, seed=96, joint=True)
+    w = torch.rand((40, c.table.shape[1] * 64), generator=torch.Generator().manual_seed(97))
+    dw, s = w.cuda(), torch.cuda.Stream()
+    B.latent_attention_paged(qn, qp, ck, kp, table, dl, SCALE, stream=s)  # (scratch, and this stream's memory)
+    B.latent_attention_prefill(*dev, SCALE, stream=s)
+    torch.cuda.synchronize()
+    _freed_while_in_use(tuple(qn.shape), torch.bfloat16, 7.0)
+    out, lse = B.latent_attention_paged(qn, qp, ck, kp, table, dl, SCALE, stream=s)
+    torch.cuda.synchronize()
+    _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
+    _freed_while_in_use((90, 16, 128), torch.bfloat16, 7.0)
+    out, lse = B.latent_attention_prefill(*dev, SCALE, stream=s)
+    torch.cuda.synchronize()
+    _check_prefill(q, kv, kpe, cu, out, lse, True)
+    _freed_while_in_use((40, 65), torch.int32, 7)
+    kept, new = B.latent_cache_evict(ck, kp, dw, table, dl, 65, 3, stream=s)
+    torch.cuda.synchronize()
+    for b in range(40):
+        assert np.array_equal(kept[b].cpu().numpy(), la.kept_keys(w[b].numpy(), 70, 65, 3))
