@@ -453,9 +453,9 @@ def latent_cache_evict(ckv_cache, kpe_cache, weights, block_table, seq_lens, bud
 
 
 def latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, sm_scale, causal=True, out=None, lse=None, stream=None):
-    """Latent attention of a ragged batch, expanded form: q [Tq,H,192], k_nope and v [Tk,H,128] (any
-    token and head strides), k_pe [Tk,64] bf16; sequence z has queries cu_q[z]..cu_q[z+1] and keys
-    cu_k[z]..cu_k[z+1] (int32), its last query sees all its keys.  Returns (out [Tq,H,128] bf16, lse
+    """Latent attention of a ragged batch, expanded form: q [Tq,H,192], k_nope and v [Tk,H,128] (token and
+    head strides positive multiples of 8), k_pe [Tk,64] bf16; sequence z has queries cu_q[z]..cu_q[z+1] and
+    keys cu_k[z]..cu_k[z+1] (int32), its last query sees all its keys.  Returns (out [Tq,H,128] bf16, lse
     [Tq,H] fp32, base 2)."""
     sq, sk, sp, sv = _strided(q, "q"), _strided(k_nope, "k_nope"), _strided(k_pe, "k_pe"), _strided(v, "v")
     if q.dim() != 3 or q.shape[2] != LATENT_DN + LATENT_DP:

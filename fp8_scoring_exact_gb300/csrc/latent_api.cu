@@ -342,6 +342,10 @@ int dsa_latent_attention_prefill(const uint16_t* q, int64_t q_token_stride, int6
                                  uint16_t* out, float* lse, dsa_stream_t stream_) try {
   if (!q || !k_nope || !k_pe || !v || !cu_q || !cu_k || !out || !lse) return DSA_ERR_ARG;
   if (S <= 0 || Tq <= 0 || Tk <= 0 || H <= 0 || !usable_scale(sm_scale * 1.4426950408889634f)) return DSA_ERR_ARG;
+  // the stride of an axis of one element is never taken, and may be anything
+  if (H == 1) q_head_stride = kn_head_stride = v_head_stride = LA_DN + LA_DP;
+  if (Tq == 1) q_token_stride = LA_DN + LA_DP;
+  if (Tk == 1) kn_token_stride = kp_token_stride = v_token_stride = LA_DN + LA_DP;
   const int64_t strides[] = {q_token_stride, q_head_stride, kn_token_stride, kn_head_stride,
                              kp_token_stride, v_token_stride, v_head_stride};
   for (int64_t x : strides)

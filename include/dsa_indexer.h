@@ -356,8 +356,9 @@ DSA_API int dsa_latent_cache_evict(uint16_t* ckv, int64_t ckv_stride, uint16_t* 
  * without it, all.  Softmax and lse in base 2 as above.
  *
  *   q [Tq, H, 192] (128 no-rope dims, then 64 rope dims)   k_nope, v [Tk, H, 128]   k_pe [Tk, 64]
- *   strides in elements, per token and per head, multiples of 8 (k_nope and v
- *   may be halves of one [Tk, H, 256] array)
+ *   strides in elements, per token and per head, positive multiples of 8, of an
+ *   axis of one element anything (k_nope and v may be halves of one [Tk, H, 256]
+ *   array); the arrays 16-byte aligned
  *   cu_q, cu_k [S + 1] int32, ascending, within [0, Tq] and [0, Tk]
  *   out [Tq, H, 128] bf16     lse [Tq, H] fp32 (rows outside every sequence are not written)
  */

@@ -217,3 +217,20 @@ def test_outputs_of_a_call_on_a_given_stream_lie_in_its_memory(B):  # noqa: F811
     torch.cuda.synchronize()
     for b in range(40):
         assert np.array_equal(kept[b].cpu().numpy(), la.kept_keys(w[b].numpy(), 70, 65, 3))
+
+
+def _odd(t):
+    """The same elements with strides of 1, 3 or 5 on the axes of one element."""
+    return t.as_strided(t.shape, [s if n > 1 else 1 + 2 * i for i, (n, s) in enumerate(zip(t.shape, t.stride()))])
+
+
+@pytest.mark.parametrize("H,qs,ks", [(1, [1], [1]), (1, [40], [70]), (3, [1], [70]), (2, [1], [1])])
+def test_prefill_takes_any_stride_of_an_axis_of_one(B, H, qs, ks):  # noqa: F811
+    q, kv, kpe, dev, cu = _prefill_inputs(qs, ks, H, seed=98, joint=True)
+    odd = [_odd(t) for t in dev[:4]]
+    odd[2] = dev[2].as_strided((ks[0], 64), (64 if ks[0] > 1 else 3, 1))
+    out, lse = B.latent_attention_prefill(*odd, *dev[4:], SCALE)
+    _check_prefill(q, kv, kpe, cu, out, lse, True)
+    with pytest.raises(B.IndexerError):  # where an axis is stepped along, its stride has to be a multiple of 8
+        wide = torch.zeros(1000, dtype=torch.bfloat16, device="cuda")
+        B.latent_attention_prefill(wide.as_strided((2, H, 192), (4, 192, 1)), *dev[1:], SCALE)
