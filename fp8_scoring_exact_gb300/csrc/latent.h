@@ -72,7 +72,9 @@ struct LatentAttnParams {
   int withhold;                 // test option: the first keys are never loaded (a wait must run out)
   int32_t* per;                 // [1] units per CTA
   int32_t* start;               // [grid, items + 1] first unit of each item, worked out by every CTA for itself
-  float* part_o;                // [items + grid, n, 512] unnormalised outputs of the pieces
+  // unnormalised outputs of the pieces: with a prefix all of them, [items + grid, n, 512]; without one those of cut
+  // items, of which a CTA has two at most, [2 grid, n, 512] (1: the one that starts with its item's first tile)
+  float* part_o;
   float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
   float* logits;                // [B, blocks, max_pages, 64, n] unscaled logits (-inf: not seen), for the key weights
 };

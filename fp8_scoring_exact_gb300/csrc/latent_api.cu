@@ -171,7 +171,7 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   };
   const size_t pieces = (size_t)p.items + p.grid;
   const size_t o_per = take(4), o_start = take(4 * ((size_t)p.items + 1) * p.grid), o_ml = take(8 * pieces * p.n),
-               o_po = take(4 * pieces * p.n * LA_DC),
+               o_po = take(4 * (p.prefix_items ? pieces : 2 * (size_t)p.grid) * p.n * LA_DC),
                o_log = p.weights ? take(4 * (size_t)p.B * p.blocks * p.max_pages * PAGE * p.n) : 0;
   std::lock_guard<std::mutex> lk(g_mu);
   const Scratch* scratch = get_scratch(stream, off);

@@ -589,6 +589,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
       named_bar_sync(1, C::ST);
       const bool direct = whole && !p.prefix_items;
       const int64_t piece = (int64_t)w + blockIdx.x;
+      const int64_t part = p.prefix_items ? piece : 2 * (int64_t)blockIdx.x + (k0 == 0 ? 1 : 0);
       if (st_id < N) {
         const float sum = (s_red[st_id] + s_red[N + st_id]) + (s_red[2 * N + st_id] + s_red[3 * N + st_id]);
         if (direct) {
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (c0 + i < im.nrows) p.part_o[(piece * N + c0 + i) * LA_DC + dim] = __uint_as_float(o[i]);
+            if (c0 + i < im.nrows) p.part_o[(part * N + c0 + i) * LA_DC + dim] = __uint_as_float(o[i]);
         }
       }
       tc_fence_before();
@@ -652,10 +653,10 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
 
 // The pieces of a row: two runs of ids (prefix, own keys) and its place in their blocks.
 struct RowPieces {
-  int id0[2], cnt[2], col[2], n;
+  int id0[2], cnt[2], col[2], n, cta0;
   __device__ __forceinline__ RowPieces(const LatentAttnParams& p, int64_t row) {
     const int R = p.next_n * p.H, b = (int)(row / R), r = (int)(row % R), per = *p.per;
-    n = 0;
+    n = cta0 = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int w = k ? p.prefix_items + b * p.blocks + r / p.n : (int)(row / p.n);
@@ -664,7 +665,8 @@ struct RowPieces {
       if (k == 0 && !p.prefix_items) continue;
       const int s0 = p.start[w], s1 = p.start[w + 1];
       if (s0 == s1) continue;
-      id0[k] = w + (s0 + p.item_units) / per;  // the CTA of its first tile
+      cta0 = (s0 + p.item_units) / per;  // the CTA of its first tile
+      id0[k] = w + cta0;
       cnt[k] = w + (s1 - 1) / per - id0[k] + 1;
       n += cnt[k];
     }
@@ -713,12 +715,18 @@ __device__ __forceinline__ void join_row(const LatentAttnParams& p, int64_t row,
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < WARPS; ++i) sum += s_tmp[i];
+  // rows of part_o: two runs with a prefix; without one the first piece's, then every second from there
+  const bool own = !p.prefix_items;
+  const int split = own ? 1 : rp.cnt[0], step = own ? 2 * p.n : p.n;
+  const int64_t row_a = own ? (int64_t)(2 * rp.cta0 + 1) * p.n + rp.col[1] : (int64_t)rp.id0[0] * p.n + rp.col[0];
+  const int64_t row_b = own ? (int64_t)(2 * rp.cta0) * p.n + rp.col[1] : (int64_t)(rp.id0[1] - split) * p.n + rp.col[1];
   const int part = tid / PER, d = 4 * (tid % PER);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = part; i < n; i += PARTS) {
     const float x = s_w[i];
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + rp.at(p, i) * LA_DC + d0 + d));
+    const int64_t at = (i < split ? row_a : row_b) + (int64_t)i * step;
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part_o + at * LA_DC + d0 + d));
     if (x != 0.f) {  // a piece without a visible key adds nothing
       o.x += x * v.x;
       o.y += x * v.y;

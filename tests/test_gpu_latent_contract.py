@@ -234,3 +234,23 @@ def test_prefill_takes_any_stride_of_an_axis_of_one(B, H, qs, ks):  # noqa: F811
     with pytest.raises(B.IndexerError):  # where an axis is stepped along, its stride has to be a multiple of 8
         wide = torch.zeros(1000, dtype=torch.bfloat16, device="cuda")
         B.latent_attention_prefill(wide.as_strided((2, H, 192), (4, 192, 1)), *dev[1:], SCALE)
+
+
+def test_scratch_of_many_sequences_is_that_of_the_cut_ones(B):  # noqa: F811
+    """600 sequences of 128 heads: 1200 row blocks, of which the 152 CTAs' runs cut two per CTA at most, 128 KB each.
+    (Slots for all of them would be 177 MB.)"""
+    lens = [1 + (37 * i) % 150 for i in range(600)]
+    c = Cache(lens, seed=99)
+    qn, qp = _queries(600, 1, 128, seed=100)
+    dq, dp = qn.cuda(), qp.cuda()
+    (ck, kp), table, dl = c.device(), c.table.cuda(), _ints(lens)
+    out, lse = torch.empty_like(dq), torch.empty((600, 1, 128), device="cuda")
+    B.latent_attention_paged(dq[:1], dp[:1], ck, kp, table[:1], dl[:1], SCALE)  # the kernels are loaded
+    torch.cuda.synchronize()
+    B.release()
+    before = torch.cuda.mem_get_info()[0]
+    B.latent_attention_paged(dq, dp, ck, kp, table, dl, SCALE, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert before - torch.cuda.mem_get_info()[0] <= 64 << 20
+    assert B.latent_last_status() == 0
+    _check_decode(c, qn, qp, out.double().cpu().numpy(), lse.double().cpu().numpy(), only=range(0, 600, 7))
