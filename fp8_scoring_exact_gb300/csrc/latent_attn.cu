@@ -685,7 +685,7 @@ template <int THREADS, int DIMS>
 __device__ __forceinline__ void join_row(const LatentAttnParams& p, int64_t row, int d0) {
   constexpr int PER = DIMS / 4, PARTS = THREADS / PER, WARPS = THREADS / 32;
   __shared__ float s_w[FIN_MAX];
-  __shared__ float s_part[PARTS > 1 ? PARTS - 1 : 1][DIMS];
+  __shared__ __align__(16) float s_part[PARTS > 1 ? PARTS - 1 : 1][DIMS];
   __shared__ float s_tmp[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const RowPieces rp(p, row);
