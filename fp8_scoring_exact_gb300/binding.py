@@ -305,6 +305,8 @@ def sparse_attention_last_status(stream=None) -> int:
 
 
 # ---------------------------------------------------------- latent attention --
+# Scratch belongs to the stream of the call or of the capture: calls and replays that share one have to run one
+# after the other (a graph that is to run beside others is captured on a stream of its own).
 LATENT_DC, LATENT_DP, LATENT_DN, LATENT_DV = 512, 64, 128, 128
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -396,7 +398,8 @@ def latent_attention_paged(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_
     ckv_cache [P,64,512], kpe_cache [P,64,64] bf16, block_table int32 [B,max_pages], seq_lens int32 [B];
     token i of sequence b sees its first seq_lens[b] - next_n + i + 1 keys.  Returns (out
     [B,next_n,H,512] bf16, lse [B,next_n,H] fp32, base 2).  weights fp32 [B, >= 64 max_pages]: the
-    softmax weight of every key, summed over the sequence's rows, is added to it."""
+    softmax weight of every key, summed over the sequence's rows, is added to it (at the cost of scratch
+    that grows with the table's width: 256 B max_pages bytes per row of a sequence)."""
     rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse, stream)
     cache, pages = _latent_cache(ckv_cache, kpe_cache)
     tables, maxp = _tables(block_table, seq_lens, rows[0])

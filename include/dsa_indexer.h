@@ -277,6 +277,11 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
  * an outgrown buffer lives until dsa_indexer_release, so a captured graph
  * stays valid.  A call that has to grow it cannot be captured (DSA_ERR_CUDA; the
  * capture goes on without it): run one of the same sizes on the stream first.
+ * Calls on one stream, graphs captured on it, and their replays on whatever
+ * stream, share that stream's scratch and status: they have to run one after
+ * the other.  Two at a time overwrite each other's partial results, and
+ * nothing reports it.  Graphs that are to run side by side are captured on a
+ * stream each.
  */
 
 /*
@@ -295,7 +300,11 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
  *   block_table [B, max_pages]        seq_lens [B] int32
  *   out [B, next_n, H, 512] bf16      lse [B, next_n, H] fp32
  *   weights [B, ld_weights] fp32 or null, ld_weights >= 64 * max_pages (with
- *           weights, next_n * H <= 4096)
+ *           weights, next_n * H <= 4096).  They take scratch for the logits of
+ *           every slot of the table, whatever the lengths, which the host does
+ *           not know: 256 * B * max_pages * r bytes, r = next_n * H rounded up to
+ *           16, 32 or a multiple of 64.  A table as wide as its longest sequence
+ *           keeps that small.
  */
 DSA_API int dsa_latent_attention_paged(const uint16_t* q_nope, const uint16_t* q_pe,
                                        const uint16_t* ckv, int64_t ckv_stride,

@@ -254,3 +254,39 @@ def test_scratch_of_many_sequences_is_that_of_the_cut_ones(B):  # noqa: F811
     assert before - torch.cuda.mem_get_info()[0] <= 64 << 20
     assert B.latent_last_status() == 0
     _check_decode(c, qn, qp, out.double().cpu().numpy(), lse.double().cpu().numpy(), only=range(0, 600, 7))
+
+
+def test_graphs_captured_on_streams_of_their_own_run_side_by_side(B):  # noqa: F811
+    """Both cut into pieces that meet in scratch; each has its own, so replays may overlap."""
+    ins = []
+    for i, (lens, H) in enumerate((([3000, 2500], 16), ([2000, 70, 900], 64))):
+        c = Cache(lens, seed=101 + i)
+        qn, qp = (x.cuda() for x in _queries(len(lens), 1, H, seed=103 + i))
+        (ck, kp), table, dl = c.device(), c.table.cuda(), _ints(lens)
+        out, lse = torch.empty_like(qn), torch.empty((len(lens), 1, H), device="cuda")
+        w = torch.zeros((len(lens), c.table.shape[1] * 64), device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+
+        def call(a=(qn, qp, ck, kp, table, dl, SCALE), o=out, z=lse, w=w):
+            w.zero_()
+            B.latent_attention_paged(*a, out=o, lse=z, weights=w)
+
+        ins.append((_capture(s, call), (out, lse, w), torch.cuda.Stream()))
+    alone = []
+    for g, res, s in ins:
+        g.replay()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in res])
+    for _ in range(30):
+        for _, res, _ in ins:
+            for t in res:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, _, s in ins:
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for (_, res, _), want in zip(ins, alone):
+            assert all(torch.equal(x, y) for x, y in zip(res, want))
