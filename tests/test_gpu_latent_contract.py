@@ -7,6 +7,7 @@ import torch
 from oracle import latent_attention as la
 from test_gpu_latent import (B, SCALE, Cache, _check_decode, _check_prefill, _ints, _prefill_inputs,  # noqa: F401
                              _queries)
+from test_latent_contract import check_lse, check_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -290,3 +291,34 @@ def test_graphs_captured_on_streams_of_their_own_run_side_by_side(B):  # noqa: F
         torch.cuda.synchronize()
         for (_, res, _), want in zip(ins, alone):
             assert all(torch.equal(x, y) for x, y in zip(res, want))
+
+
+@pytest.mark.parametrize("nn,H,lens", [(1, 16, [200]), (1, 128, [2100, 64]), (1, 16, [30000]), (2, 24, [640, 700]),
+                                       (4, 5, [4000, 130])])
+def test_key_weights_and_lse_have_the_bits_of_fp32(B, nn, H, lens):  # noqa: F811
+    c = Cache(lens, seed=110 + H)
+    qn, qp = _queries(len(lens), nn, H, seed=111 + nn)
+    (ck, kp), table, dl = c.device(), c.table.cuda(), _ints(lens)
+    w = torch.zeros((len(lens), c.table.shape[1] * 64), device="cuda")
+    _, lse = B.latent_attention_paged(qn.cuda(), qp.cuda(), ck, kp, table, dl, SCALE, weights=w)
+    _, lse1 = B.latent_attention_paged(qn.cuda(), qp.cuda(), ck, kp, table, dl, SCALE)
+    ckv, kpe = c.flat()
+    ref = la.decode(qn.double().numpy(), qp.double().numpy(), ckv, kpe, c.table.numpy(), lens, SCALE)
+    for b, L in enumerate(lens):
+        check_weights(w[b, :L].double().cpu().numpy(), ref[b][2])
+        for x in (lse, lse1):
+            check_lse(x[b].double().cpu().numpy().reshape(-1), ref[b][1])
+
+
+@pytest.mark.parametrize("H,qs,ks", [(4, [300, 70], [300, 700]), (2, [1000], [1500])])
+def test_prefill_lse_has_the_bits_of_fp32(B, H, qs, ks):  # noqa: F811
+    q, kv, kpe, dev, cu = _prefill_inputs(qs, ks, H, seed=112, joint=True)
+    _, lse = B.latent_attention_prefill(*dev, SCALE)
+    lse = lse.double().cpu().numpy()
+    for z in range(len(qs)):
+        (a, b), (m, n) = cu[0][z:z + 2], cu[1][z:z + 2]
+        sees = (n - m) - (b - a) + 1 + np.arange(b - a)
+        for h in range(H):
+            k = np.concatenate([kv[m:n, h, :128].double().numpy(), kpe[m:n].double().numpy()], 1)
+            ref = la.rows_over_keys(q[a:b, h].double().numpy(), k, k[:, :1], sees, SCALE)
+            check_lse(lse[a:b, h], ref[1])
