@@ -8,7 +8,8 @@
 // contiguous slice of its weights in shared memory as order-preserving 32-bit
 // images.  The CTAs double while each would have more than 16K keys: the
 // cluster's barriers cost more than they save below (eviction of 64 sequences of
-// up to 32K keys: 84 us with 1 CTA each, 77 with 2, 85 with 4, 121 with 8).
+// up to 32K keys: 154 us with 1 CTA each, 148 with 2, 156 with 4, 193 with 8; of
+// five of up to 128K: 195, 122, 80, 70).
 // Four 8-bit radix passes (histograms summed over the cluster) give the
 // smallest kept image T and how many keys equal to T are kept; a last pass
 // counts kept keys per warp segment, and the prefix sums over warps and CTAs
@@ -23,11 +24,15 @@
 // handed out in order and each reads before it waits, so the wait ends.  One that
 // runs out all the same leaves its slots alone and is reported.
 //
-// 64 sequences of up to 32768 keys to 4096, the indexer's keys along: 77 us for
-// 650 MB, over the copy rate as part of it stays in L2.  Five of up to 131072 to
-// 16384 (196 MB): 45 us, 30 of them the selection on 40 SMs: four passes over 16K
-// images per CTA, and the cluster's barriers between them.  One of 3000 keys to
-// 2048: 12 + 8 us, all latency.
+// With every kept key moving: 64 sequences of up to 32768 keys to 4096, the
+// indexer's keys along (656 MB): 148 us, 25 of them the selection; the move's 122
+// are 5.3 TB/s, 332 MB read from DRAM and 279 written.  Five of up to 131072 to
+// 16384 (191 MB): 70 us, 28 of them the selection on 40 SMs: four passes over 16K
+// images per CTA, and the cluster's barriers between them; 42 the move.  One of
+// 3000 keys to 2048: 12 + 8 us, all latency.  Where hardly a key changes its place
+// (the same weights and lengths again: some 13% and 6% of them) 77 and 45 us: the move
+// then takes 57 and 24, for the most part the dependent loads that a chunk
+// starts with (its number, the old length, two searches in the list).
 #include "latent.h"
 
 namespace dsa {

@@ -46,7 +46,8 @@
 // O^T take some 4200 cycles one after the other, and 1650 of the 2100 per tile
 // are the tensor cores' (the M = 64 steps of S^T run at half their rate): 64
 // sequences of two tokens of 16 heads behind 32768 shared keys 161 us, 0.94
-// PFLOP/s; seven sequences of 128 heads 70 us, which read 193 MB twice.  The MMAs
+// PFLOP/s; seven sequences of 128 heads 70 us, which read 282 MB from DRAM for their
+// 193, as a sequence's two blocks come to its keys at different times.  The MMAs
 // take shared memory's whole bandwidth, so the softmax keeps what it can in
 // registers (references read from shared memory for every tile: 167 us).
 // (Prefetching the pages of tiles 2, 3, 5 or 8 ahead into L2 made all of these

@@ -23,11 +23,12 @@
 // Loading the next tile's logits while this one's become weights: 215.  Two
 // buffers of logits and two of weights instead of three shared ones: 218.)
 //
-// 2048 queries on 16384 keys of 16 heads: 206 us, 1.56 PFLOP/s of the 1.94 that
-// a library product reaches.  A tile takes some 1620 cycles, 1280 of them the
+// 2048 queries on 16384 keys of 16 heads: 236 us in long runs, which meet the power
+// limit, 1.37 PFLOP/s of the 1.71 that a library product sustains; 206 us in short
+// ones, 1.56 of 1.94.  A tile takes some 1620 cycles, 1280 of them the
 // tensor cores'; the softmax spends 360 on loading the logits and their maximum,
 // 920 on the weights (without the exponentials the call took as long) and 320 on
-// waits.  Long runs meet the power limit: 230 us.  Nine prompts
+// waits.  Nine prompts
 // of up to 2500 tokens: 91 us, 0.83 PFLOP/s of unmasked work; 38% more is done
 // than that in the tiles that the diagonal and the prompts' ends cut, and a
 // block's start and end and its two masked tiles cost about three tiles' time.
