@@ -30,9 +30,9 @@ struct LatentStatus {
 // tiles counts item_units units and one per tile; the items' units are
 // numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
 // tiles in one item are a piece, whose id is item + c.
-// What starting and ending a piece costs, in tiles: 2 without a prefix (128 rows of seven sequences: 72 us; 74 with 4);
-// 4 with one, where most of a sequence's own items are short and their pages cold (64 sequences behind 32768 shared
-// keys: 180 us with 2, 172 with 3, 168 with 4, 171 with 8; with a single page of their own 51.5 -> 53).
+// What starting and ending a piece costs, in tiles: 2 without a prefix (128 rows of seven sequences: 70.2 us; 70.7 with
+// 4); 4 with one, where most of a sequence's own items are short and their pages cold (64 sequences behind 32768 shared
+// keys: 171 us with 2, 163 with 3, 159 with 4, 163 with 8).
 constexpr int LA_ITEM_UNITS = 2, LA_PREFIX_ITEM_UNITS = 4;
 constexpr int LA_MAX_WEIGHT_ROWS = 4096;  // rows of a sequence with key weights (their sums lie in shared memory)
 
@@ -136,8 +136,7 @@ struct LatentMaps {
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 // Tensor maps of the expanded form: q [Tq, H, 192], k_nope and v [Tk, H, 128],
-// boxes of 64 dims x 1 head x 128 queries or 64
-// keys; k_pe [Tk, 64].
+// boxes of 64 dims x 1 head x 128 queries or 64 keys; k_pe [Tk, 64].
 struct PrefillMaps {
   CUtensorMap q, k_nope, k_pe, v;
 };

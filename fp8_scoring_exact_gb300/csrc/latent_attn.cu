@@ -28,7 +28,7 @@
 // moves when a logit passes it by 8 (a factor of 2^8: fp32 sums and bf16
 // weights have the range for that), which a vote over the warps finds out; only
 // then are maxima exchanged and O^T is rescaled (finding the maximum of every
-// tile instead: 187 us against 175 for 64 sequences behind 32768 shared keys).
+// tile instead took 7% longer for 64 sequences behind 32768 shared keys).
 //
 // Every CTA takes an equal run of the call's tiles, whatever item they
 // belong to; an item cut by a run's border is joined by the finish kernel in
@@ -45,11 +45,11 @@
 // the query block leaves room for two tiles, a tile's copy, S^T, softmax and
 // O^T take some 4200 cycles one after the other, and 1650 of the 2100 per tile
 // are the tensor cores' (the M = 64 steps of S^T run at half their rate): 64
-// sequences of two tokens of 16 heads behind 32768 shared keys 161 us, 0.94
+// sequences of two tokens of 16 heads behind 32768 shared keys 160 us, 0.94
 // PFLOP/s; seven sequences of 128 heads 70 us, which read 282 MB from DRAM for their
 // 193, as a sequence's two blocks come to its keys at different times.  The MMAs
 // take shared memory's whole bandwidth, so the softmax keeps what it can in
-// registers (references read from shared memory for every tile: 167 us).
+// registers (references read from shared memory for every tile: 5 us more).
 // (Prefetching the pages of tiles 2, 3, 5 or 8 ahead into L2 made all of these
 // slower: 16 sequences of 64 rows 122, 129, 164, 173 us.)
 #include "latent.h"
@@ -860,10 +860,10 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
     return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * (R + spread))), dim3(FIN_THREADS), 8 * (size_t)R, s,
                       p, spread);
   // few items, so rows of many pieces: more threads take fewer dims (a sequence of 131072 keys and 16 rows:
-  // 41 us, 43 the other way; two of 64 rows 68 and 75).  Else two parts of 256 dims (seven sequences of 128
-  // rows, 11 pieces each, 71 us and 78 the first way; 64 sequences behind 32768 shared keys 166 and 185).  128
-  // threads for all 512 dims are the best for even lengths (163), but a long sequence among short ones has
-  // as many pieces as one alone (30 us for the join instead of 17).
+  // 37 us, 41 the other way; two of 64 rows 63 and 70).  Else two parts of 256 dims (seven sequences of 128
+  // rows, 11 pieces each, 70 us and 79 the first way; 64 sequences behind 32768 shared keys 159 and 183).  128
+  // threads for all 512 dims are the best for even lengths (156), but a long sequence among short ones has
+  // as many pieces as one alone (the sequence of 131072 keys: 48 us).
   if (p.grid > 32 * (p.prefix_items ? p.prefix_items : p.items))
     return launch_pdl(latent_join_kernel<256, 128, 4>, dim3(p.B * R, LA_DC / 128), dim3(256), 0, s, p);
   return launch_pdl(latent_join_kernel<128, 256, 8>, dim3(p.B * R, LA_DC / 256), dim3(128), 0, s, p);

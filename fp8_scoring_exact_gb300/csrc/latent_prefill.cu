@@ -19,7 +19,7 @@
 // latent_attn.cu a row's reference moves only when a logit passes it by 8.
 // (One CTA per block with two 128-query tiles and one S buffer each ran at 56%
 // tensor time: a tile's next S had to wait for its softmax and its product.  One
-// thread per row: 211 us where two take 206, for the first case below; four 216.
+// thread per row: 211 us where two take 206, in short runs of the first case below; four 216.
 // Loading the next tile's logits while this one's become weights: 215.  Two
 // buffers of logits and two of weights instead of three shared ones: 218.)
 //
@@ -45,7 +45,7 @@ namespace {
 constexpr int PF_ROWS = 256;           // queries per block: 128 per CTA of a pair
 constexpr int PF_KEYS = 128;           // keys per tile
 // What starting and ending a block costs, in key tiles: nine prompts of up to
-// 2500 tokens took 101.7, 93.7, 91.0 and 93.5 us with 1, 2, 3 and 4.
+// 2500 tokens took 101, 93.1, 90.7 and 92.8 us with 1, 2, 3 and 4.
 constexpr int PF_BLOCK_UNITS = 3;
 constexpr uint32_t PF_QCHUNK = 128 * 128;  // 128 queries x 64 dims, bf16
 constexpr uint32_t PF_SLOT = 64 * 128;     // 64 keys x 64 dims, bf16
