@@ -273,23 +273,27 @@ def test_graphs_captured_on_streams_of_their_own_run_side_by_side(B):  # noqa: F
             w.zero_()
             B.latent_attention_paged(*a, out=o, lse=z, weights=w)
 
-        ins.append((_capture(s, call), (out, lse, w), torch.cuda.Stream()))
+        # (the call's arguments live as long as its graph)
+        ins.append((_capture(s, call), (out, lse, w), torch.cuda.Stream(), call, (c, qn.cpu(), qp.cpu()), s))
     alone = []
-    for g, res, s in ins:
+    for g, res, _, _, (c, qn, qp), s in ins:
         g.replay()
         torch.cuda.synchronize()
+        assert B.latent_last_status(s) == 0
+        out, lse, w = (t.double().cpu().numpy() for t in res)
+        _check_decode(c, qn, qp, out, lse, weights=w)
         alone.append([t.clone() for t in res])
     for _ in range(30):
-        for _, res, _ in ins:
+        for _, res, *_ in ins:
             for t in res:
                 t.zero_()
         torch.cuda.synchronize()
         for _ in range(4):
-            for g, _, s in ins:
+            for g, _, s, *_ in ins:
                 with torch.cuda.stream(s):
                     g.replay()
         torch.cuda.synchronize()
-        for (_, res, _), want in zip(ins, alone):
+        for (_, res, *_), want in zip(ins, alone):
             assert all(torch.equal(x, y) for x, y in zip(res, want))
 
 
