@@ -340,6 +340,8 @@ def _new(shape, dtype, device, stream):
     """An output, in memory of the stream that writes it: memory of another one may still be in use there."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # any object that names a stream will do
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

@@ -326,3 +326,19 @@ def test_prefill_lse_has_the_bits_of_fp32(B, H, qs, ks):  # noqa: F811
             k = np.concatenate([kv[m:n, h, :128].double().numpy(), kpe[m:n].double().numpy()], 1)
             ref = la.rows_over_keys(q[a:b, h].double().numpy(), k, k[:, :1], sees, SCALE)
             check_lse(lse[a:b, h], ref[1])
+
+
+def test_any_object_that_names_a_stream(B):  # noqa: F811
+    class Raw:
+        def __init__(self, handle):
+            self.cuda_stream = handle
+
+    c = Cache([70, 3], seed=113)
+    qn, qp = (x.cuda() for x in _queries(2, 1, 16, seed=114))
+    (ck, kp), table, dl = c.device(), c.table.cuda(), _ints(c.lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (Raw(s.cuda_stream), Raw(0), s):
+        out, lse = B.latent_attention_paged(qn, qp, ck, kp, table, dl, SCALE, stream=stream)
+        torch.cuda.synchronize()
+        _check_decode(c, qn.cpu(), qp.cpu(), out.double().cpu().numpy(), lse.double().cpu().numpy())
