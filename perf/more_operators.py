@@ -351,7 +351,7 @@ def run(s):
                  torch.empty_like(s["k_pe"], memory_format=torch.contiguous_format)) if s["dense"] else (None, None)
         new_lens = binding.latent_cache_append(s["c"], s["k_pe"], s["cos_sin"], s["cu_new"], s["block_table"],
                                                s["seq_lens"], s["ckv"], s["kpe"], c_norm=s["c_norm"],
-                                               interleaved=s["interleaved"], index_k=s.get("index_k"),
+                                               pe_interleaved=s["interleaved"], index_k=s.get("index_k"),
                                                index_norm=s.get("index_norm"), hadamard=True,
                                                k_cache=s.get("k_cache"), k_cache_scale=s.get("k_scale"),
                                                c_out=dense[0], k_pe_out=dense[1])
