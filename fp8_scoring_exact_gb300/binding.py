@@ -47,6 +47,14 @@ SIGNATURES = {
                                         _P, _I64, _P]),
     "dsa_latent_attention_shared_prefix": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I,
                                                 ctypes.c_float, _P, _P, _P]),
+    "dsa_latent_attention_tree": (_I, [_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float,
+                                       _P, _P, _P]),
+    "dsa_indexer_encode": (_I, [_P, _I64, _I64, _I, _P, _P, ctypes.c_float, _P, _I64, _I64, _I, _P, _I, _P, _I, _I, _P,
+                                _P, _P, _I64, _I64, _P]),
+    "dsa_latent_cache_append": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, ctypes.c_float, _P, _P, ctypes.c_float, _P, _I,
+                                     _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64,
+                                     _P, _P]),
+    "dsa_latent_cache_accept": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "dsa_latent_cache_evict": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     "dsa_latent_attention_prefill": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _I, _I, _I,
                                           _I, _I, ctypes.c_float, _P, _P, _P]),
@@ -427,6 +435,161 @@ def latent_attention_shared_prefix(q_nope, q_pe, ckv_cache, kpe_cache, prefix_ta
                                                   _latent_stream(stream))
     _check("dsa_latent_attention_shared_prefix", rc)
     return out, lse
+
+
+def latent_attention_tree(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_lens, tree_mask, sm_scale,
+                          draft_lens=None, out=None, lse=None, stream=None):
+    """latent_attention_paged for drafted tokens that form a tree: the last draft_lens[b] (int32 [B]; without it
+    next_n) of a sequence's keys are its nodes; query i sees the keys before them and node j where bit j % 64 of
+    tree_mask[b, i, j // 64] is set (int64 [B, next_n, ceil(next_n / 64)]).  Queries past draft_lens[b] are padding:
+    zeros and lse -inf."""
+    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse, stream)
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
+    tables, maxp = _tables(block_table, seq_lens, rows[0])
+    mask = _full(tree_mask, "tree_mask", (rows[0], rows[1], (rows[1] + 63) // 64), torch.int64)
+    drafts = None if draft_lens is None else _full(draft_lens, "draft_lens", (rows[0],), _I32)
+    rc = lib().dsa_latent_attention_tree(*queries, *cache, *tables, mask, drafts, *rows, maxp, pages, float(sm_scale),
+                                         out.data_ptr(), lse.data_ptr(), _latent_stream(stream))
+    _check("dsa_latent_attention_tree", rc)
+    return out, lse
+
+
+def latent_cache_accept(ckv_cache, kpe_cache, block_table, seq_lens, draft_lens, path, path_lens, k_cache=None,
+                        k_cache_scale=None, new_lens=None, stream=None):
+    """Keeps the accepted path of every sequence's drafted nodes (its last draft_lens[b] keys): node path[b, j] (int32
+    [B, max_path], ascending), j < path_lens[b], moves to the j-th place behind the keys before the nodes, with the
+    indexer's keys and scales if given.  Returns new_lens int32 [B], which may be seq_lens itself."""
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
+    B = block_table.shape[0]
+    tables, maxp = _tables(block_table, seq_lens, B)
+    keys = _index_cache(k_cache, k_cache_scale, pages)
+    shape = _dev(path, "path", _I32).shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"path must be [{B},max_path], got {list(shape)}")
+    if new_lens is None:
+        new_lens = _new((B,), _I32, ckv_cache.device, stream)
+    rc = lib().dsa_latent_cache_accept(*cache, *keys, *tables, _full(draft_lens, "draft_lens", (B,), _I32),
+                                       path.data_ptr(), _full(path_lens, "path_lens", (B,), _I32), B, maxp, pages,
+                                       shape[1], _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
+    _check("dsa_latent_cache_accept", rc)
+    return new_lens
+
+
+def _index_cache(k_cache, k_cache_scale, pages):
+    if (k_cache is None) != (k_cache_scale is None):
+        raise ValueError("k_cache and k_cache_scale go together")
+    if k_cache is None:
+        return None, None
+    return (_full(_u8(k_cache, "k_cache"), "k_cache", (pages, 64, HEAD_DIM), torch.uint8),
+            _full(k_cache_scale, "k_cache_scale", (pages, 64), _F32))
+
+
+_ENCODE_PAIRS, _ENCODE_HADAMARD, _ENCODE_PE_HALVES = 1, 2, 4
+
+
+def _encode_flags(interleaved, hadamard, pe_interleaved):
+    return ((_ENCODE_PAIRS if interleaved else 0) | (_ENCODE_HADAMARD if hadamard else 0) |
+            (0 if pe_interleaved else _ENCODE_PE_HALVES))
+
+
+def _layer_norm(norm, name):
+    if norm is None:
+        return None, None, 0.0
+    weight, bias, eps = norm
+    return (_full(weight, f"{name} weight", (HEAD_DIM,), _F32), _full(bias, f"{name} bias", (HEAD_DIM,), _F32),
+            float(eps))
+
+
+def _rotation_table(cos_sin):
+    shape = _dev(cos_sin, "cos_sin", _F32).shape
+    if len(shape) != 2 or shape[1] != LATENT_DP:
+        raise ValueError(f"cos_sin must be [max_positions,64], got {list(shape)}")
+    return cos_sin.data_ptr(), shape[0]
+
+
+def _rows_of(t, name, shape):
+    """(address, strides of all axes but the last) of a bf16 tensor of this shape, contiguous in its last axis."""
+    s = _strided(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr(), *s[:-1]
+
+
+def indexer_encode(x, cos_sin, positions, norm=None, interleaved=False, hadamard=False, pe=None, pe_interleaved=True,
+                   codes=None, scale=None, pe_out=None, stream=None):
+    """Rows for the indexer from a projection's output x [T,64,128] (queries) or [T,1,128] (keys) bf16: LayerNorm with
+    norm = (weight [128], bias [128], eps), the first 64 dims rotated by the angles of cos_sin [max_positions,64] fp32
+    (32 cosines, 32 sines) at positions int32 [T] (negative: padding, left as it was), the Hadamard transform, e4m3
+    codes with one scale a token.  pe [T,H,64] bf16 are rope parts of the same tokens, rotated to pe_out (which may be
+    pe).  interleaved: pairs (2 i, 2 i + 1), else (i, i + 32).  Token and head strides are the caller's.  Returns (codes
+    float8_e4m3fn [T,G,128], scale fp32 [T], pe_out or None); x may be None, and codes and scale are then too."""
+    T = _dev(positions, "positions", _I32).numel()
+    table, n = _rotation_table(cos_sin)
+    G = H = 1
+    rows, parts, out = (None, 0, 0), (None, 0, 0), (None, 0, 0)
+    if x is not None:
+        if x.dim() != 3 or x.shape[1] not in (1, HEADS):
+            raise ValueError(f"x must be [T,64,128] or [T,1,128], got {list(x.shape)}")
+        G = x.shape[1]
+        rows = _rows_of(x, "x", (T, G, HEAD_DIM))
+        if codes is None:
+            codes = _new((T, G, HEAD_DIM), torch.float8_e4m3fn, x.device, stream)
+        if scale is None:
+            scale = _new((T,), _F32, x.device, stream)
+    elif norm is not None or codes is not None or scale is not None:
+        raise ValueError("norm, codes and scale go with x")
+    if pe is not None:
+        if pe.dim() != 3:
+            raise ValueError(f"pe must be [T,H,64], got {list(pe.shape)}")
+        H = pe.shape[1]
+        parts = _rows_of(pe, "pe", (T, H, LATENT_DP))
+        if pe_out is None:
+            pe_out = _new((T, H, LATENT_DP), _BF16, pe.device, stream)
+        out = _rows_of(pe_out, "pe_out", (T, H, LATENT_DP))
+    elif pe_out is not None:
+        raise ValueError("pe_out goes with pe")
+    rc = lib().dsa_indexer_encode(*rows, G, *_layer_norm(norm, "norm"), *parts, H, table, n, positions.data_ptr(), T,
+                                  _encode_flags(interleaved, hadamard, pe_interleaved),
+                                  None if x is None else _full(_u8(codes, "codes"), "codes", (T, G, HEAD_DIM), torch.uint8),
+                                  None if x is None else _full(scale, "scale", (T,), _F32), *out, _latent_stream(stream))
+    _check("dsa_indexer_encode", rc)
+    return codes, scale, pe_out
+
+
+def latent_cache_append(c, k_pe, cos_sin, cu_new, block_table, seq_lens, ckv_cache, kpe_cache, c_norm=None,
+                        pe_interleaved=True, index_k=None, index_norm=None, interleaved=False, hadamard=False,
+                        k_cache=None, k_cache_scale=None, positions=None, c_out=None, k_pe_out=None, new_lens=None,
+                        stream=None):
+    """New tokens into the paged cache: tokens cu_new[b]..cu_new[b+1] (int32) of c [T,512] and k_pe [T,64] bf16 behind
+    the seq_lens[b] keys of sequence b: c normalised with c_norm = (weight [512] fp32, eps), k_pe rotated, index_k
+    [T,128] encoded as indexer_encode does (index_norm, interleaved, hadamard) into k_cache [P,64,128] and k_cache_scale
+    [P,64].  positions int32 [T]: of the angles, by default a token's place in its sequence.  c_out and k_pe_out get
+    what the cache gets.  Returns new_lens int32 [B], which may be seq_lens itself."""
+    T = c.shape[0]
+    rows, parts = _rows_of(c, "c", (T, LATENT_DC)), _rows_of(k_pe, "k_pe", (T, LATENT_DP))
+    cache, pages = _latent_cache(ckv_cache, kpe_cache)
+    B = block_table.shape[0]
+    tables, maxp = _tables(block_table, seq_lens, B)
+    keys = _index_cache(k_cache, k_cache_scale, pages)
+    if (index_k is None) != (k_cache is None):
+        raise ValueError("index_k and k_cache go together")
+    if index_k is None and index_norm is not None:
+        raise ValueError("index_norm goes with index_k")
+    index = (None, 0) if index_k is None else _rows_of(index_k, "index_k", (T, HEAD_DIM))
+    weight, eps = (None, 0.0) if c_norm is None else (_full(c_norm[0], "c_norm weight", (LATENT_DC,), _F32),
+                                                      float(c_norm[1]))
+    table, n = _rotation_table(cos_sin)
+    if new_lens is None:
+        new_lens = _new((B,), _I32, ckv_cache.device, stream)
+    rc = lib().dsa_latent_cache_append(*rows, *parts, *index, weight, eps, *_layer_norm(index_norm, "index_norm"), table,
+                                       n, None if positions is None else _full(positions, "positions", (T,), _I32),
+                                       _full(cu_new, "cu_new", (B + 1,), _I32), *tables, B, T, maxp, pages,
+                                       _encode_flags(interleaved, hadamard, pe_interleaved), *cache, *keys,
+                                       *((None, 0) if c_out is None else _rows_of(c_out, "c_out", (T, LATENT_DC))),
+                                       *((None, 0) if k_pe_out is None else _rows_of(k_pe_out, "k_pe_out", (T, LATENT_DP))),
+                                       _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
+    _check("dsa_latent_cache_append", rc)
+    return new_lens
 
 
 def latent_cache_evict(ckv_cache, kpe_cache, weights, block_table, seq_lens, budget, recent, k_cache=None,

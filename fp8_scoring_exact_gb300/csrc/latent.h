@@ -1,7 +1,8 @@
 // latent.h -- parameters and host launchers of the latent-attention operators:
 // dense attention over the paged latent cache (latent_attn.cu), eviction from
-// that cache (cache_evict.cu) and prefill in the expanded form
-// (latent_prefill.cu).  Their entry points are in latent_api.cu.
+// that cache (cache_evict.cu), prefill in the expanded form (latent_prefill.cu),
+// new tokens encoded and appended (token_encode.cu) and the accepted path of
+// drafted ones (cache_accept.cu).  Their entry points are in latent_api.cu.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,9 +22,30 @@ constexpr int LA_DN = 128, LA_DV = 128;  // expanded form: no-rope key dims and 
 // moves it to `last` and leaves `now` zero for the next call (also when the
 // call is replayed from a graph).  An eviction's last kernel can itself give up
 // waiting: its CTAs OR into `last`, which the selection has cleared.
+// A call of one kernel collects its status in the CTA that ends last, which `ticket` finds out.
 struct LatentStatus {
   int now, last;
+  unsigned ticket;  // CTAs of a call of one kernel that have ended; 0 between calls
 };
+#ifdef __CUDACC__
+// Ends a call of one kernel: the CTA that is the last to come here collects the call's status, and gets true; what
+// every CTA read and wrote before is behind it.
+__device__ __forceinline__ bool last_cta(LatentStatus* st, bool bad) {
+  __shared__ int s_last;
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    if (any) atomicOr(&st->now, ST_RANGE);
+    __threadfence();
+    s_last = gridDim.x == 1 || atomicInc(&st->ticket, gridDim.x - 1) == gridDim.x - 1;
+    if (s_last) {
+      __threadfence();
+      st->last = atomicExch(&st->now, 0);
+    }
+  }
+  __syncthreads();
+  return s_last;
+}
+#endif
 
 // Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
 // 64) with the keys its rows see, cut into tiles of one page.  An item with
@@ -65,6 +87,10 @@ struct LatentAttnParams {
   int64_t ld_weights;
   LatentStatus* status;
   // the call's row blocks and scratch
+  // a tree of drafted tokens: the sequence's last keys (null tree_mask: next_n tokens in a row)
+  const uint64_t* tree_mask;    // [B, next_n, mask_words]: node i sees node j where bit j % 64 of word j / 64 is set
+  const int32_t* draft_lens;    // [B] nodes of a sequence, or null: next_n, or all its keys if it has fewer
+  int mask_words;
   int n;                        // rows per block
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
   int items, grid, item_units;
@@ -128,6 +154,73 @@ struct PrefillParams {
   LatentStatus* status;
 };
 
+// How rows of 128 dims are encoded for the indexer.
+struct RowEncoding {
+  const float *norm_w, *norm_b;  // [128] LayerNorm, or null
+  float eps;
+  bool pairs, hadamard;          // rotated pairs (2 i, 2 i + 1), else (i, i + 32); Hadamard transform behind
+};
+
+// Rows of T tokens encoded for the indexer, and rope parts of the same tokens rotated.
+struct EncodeParams {
+  const __nv_bfloat16* x;        // [T, G, 128] or null
+  int64_t x_token, x_head;       // strides in elements
+  int G;                         // 64 or 1
+  RowEncoding enc;
+  const __nv_bfloat16* pe;       // [T, H, 64] or null
+  int64_t pe_token, pe_head;
+  int H;
+  bool pe_pairs;
+  const float* cos_sin;          // [max_positions, 64]: 32 cosines, 32 sines
+  int max_positions;
+  const int32_t* positions;      // [T]; negative: padding
+  int T;
+  uint8_t* codes;                // [T, G, 128]
+  float* scale;                  // [T]
+  __nv_bfloat16* pe_out;         // [T, H, 64], may be pe
+  int64_t po_token, po_head;
+  int index_ctas;                // CTAs that encode; the rest rotate
+  LatentStatus* status;
+};
+
+// New tokens into the paged cache: sequence b's tokens [cu_new[b], cu_new[b + 1]) behind its seq_lens[b] keys.
+struct AppendParams {
+  const __nv_bfloat16 *c, *k_pe, *index_k;  // [T, 512], [T, 64], [T, 128] or null
+  int64_t c_stride, kp_stride, ik_stride;
+  const float* c_norm;           // [512] RMSNorm, or null
+  float c_eps;
+  RowEncoding enc;
+  bool pe_pairs;
+  const float* cos_sin;
+  int max_positions;
+  const int32_t* positions;      // [T], or null: a token's logical slot
+  const int32_t *cu_new, *block_table, *seq_lens;
+  int B, T, max_pages, num_pages;
+  __nv_bfloat16 *ckv, *kpe;
+  int64_t ckv_stride, kpe_stride;
+  uint8_t* k_cache;              // [P, 64, 128] or null
+  float* k_scale;
+  __nv_bfloat16 *c_out, *k_pe_out;  // [T, 512], [T, 64]: what the cache gets, or null
+  int64_t c_out_stride, kp_out_stride;
+  int32_t* new_lens;             // [B], may be seq_lens
+  int latent_ctas;               // CTAs that normalise latents; the rest rotate and encode
+  LatentStatus* status;
+};
+
+// The accepted path of every sequence's drafted nodes, moved together behind its settled keys.
+struct AcceptParams {
+  uint8_t *ckv, *kpe;            // rows of 1024 and 128 bytes
+  int64_t ckv_stride, kpe_stride;  // bytes
+  uint8_t* k_cache;              // [P, 64, 128] or null
+  float* k_scale;
+  const int32_t *block_table, *seq_lens, *draft_lens;
+  const int32_t* path;           // [B, max_path] nodes, ascending
+  const int32_t* path_lens;      // [B]
+  int B, max_pages, num_pages, max_path;
+  int32_t* new_lens;             // [B], may be seq_lens
+  LatentStatus* status;
+};
+
 // Tensor maps of cached attention: queries [rows, 512] and [rows, 64], caches
 // [slots, 512] and [slots, 64], all bf16 in 128-byte swizzled boxes of 64 dims.
 struct LatentMaps {
@@ -135,6 +228,9 @@ struct LatentMaps {
 };
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
+cudaError_t launch_encode(EncodeParams p, cudaStream_t s);
+cudaError_t launch_append(AppendParams p, cudaStream_t s);
+cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
 // Tensor maps of the expanded form: q [Tq, H, 192], k_nope and v [Tk, H, 128],
 // boxes of 64 dims x 1 head x 128 queries or 64 keys; k_pe [Tk, 64].
 struct PrefillMaps {

@@ -83,7 +83,32 @@ const __nv_bfloat16* bf(const T* p) {
   return reinterpret_cast<const __nv_bfloat16*>(p);
 }
 
-// Arguments shared by the two forms of cached attention.
+// A stride in elements: a positive multiple of 8 (16 bytes), of an axis of one element anything.
+bool usable_stride(int64_t& stride, int64_t extent, int64_t instead) {
+  if (extent == 1) stride = instead;
+  return stride > 0 && !(stride & 7) && stride < (1ll << 38);
+}
+
+// Index rows' LayerNorm and order of pairs.
+bool usable_encoding(RowEncoding& e, const float* w, const float* b, float eps, int flags) {
+  if (!w != !b || !aligned16(w) || !aligned16(b) || (w && !(eps >= 0.f && eps <= 3.4e38f))) return false;
+  e.norm_w = w;
+  e.norm_b = b;
+  e.eps = eps;
+  e.pairs = flags & DSA_ENCODE_PAIRS;
+  e.hadamard = flags & DSA_ENCODE_HADAMARD;
+  return true;
+}
+constexpr int ENCODE_FLAGS = DSA_ENCODE_PAIRS | DSA_ENCODE_HADAMARD | DSA_ENCODE_PE_HALVES;
+
+// Status of the calls on a stream, for operators that need no other scratch; null on an error.
+LatentStatus* get_status(cudaStream_t stream) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const Scratch* s = get_scratch(stream, 0);
+  return s ? s->status : nullptr;
+}
+
+// Arguments shared by the forms of cached attention.
 int check_cached(const LatentAttnParams& p) {
   if (!p.q_nope || !p.q_pe || !p.ckv || !p.kpe || !p.block_table || !p.seq_lens || !p.out || !p.lse) return DSA_ERR_ARG;
   if (p.B <= 0 || p.next_n <= 0 || p.H <= 0 || p.max_pages <= 0 || p.num_pages <= 0) return DSA_ERR_ARG;
@@ -265,6 +290,184 @@ int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uint16_t* q
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return DSA_ERR_CUDA;
+}
+
+int dsa_latent_attention_tree(const uint16_t* q_nope, const uint16_t* q_pe, const uint16_t* ckv, int64_t ckv_stride,
+                              const uint16_t* kpe, int64_t kpe_stride, const int32_t* block_table,
+                              const int32_t* seq_lens, const uint64_t* tree_mask, const int32_t* draft_lens, int B,
+                              int next_n, int H, int max_pages, int num_pages, float sm_scale, uint16_t* out,
+                              float* lse, dsa_stream_t stream) try {
+  if (!tree_mask || (reinterpret_cast<uintptr_t>(tree_mask) & 7u)) return DSA_ERR_ARG;
+  LatentAttnParams p{};
+  p.q_nope = bf(q_nope);
+  p.q_pe = bf(q_pe);
+  p.ckv = bf(ckv);
+  p.kpe = bf(kpe);
+  p.ckv_stride = ckv_stride;
+  p.kpe_stride = kpe_stride;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.tree_mask = tree_mask;
+  p.draft_lens = draft_lens;
+  p.B = B;
+  p.next_n = next_n;
+  p.H = H;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.mask_words = next_n > 0 ? ceil_div(next_n, 64) : 0;
+  p.scale_log2 = sm_scale * 1.4426950408889634f;
+  p.out = reinterpret_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  return run_cached(p, reinterpret_cast<cudaStream_t>(stream));
+} catch (...) {
+  return DSA_ERR_CUDA;
+}
+
+int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride, int G,
+                       const float* norm_weight, const float* norm_bias, float norm_eps, const uint16_t* pe,
+                       int64_t pe_token_stride, int64_t pe_head_stride, int H, const float* cos_sin, int max_positions,
+                       const int32_t* positions, int T, int flags, uint8_t* codes, float* scale, uint16_t* pe_out,
+                       int64_t po_token_stride, int64_t po_head_stride, dsa_stream_t stream_) try {
+  if ((!x && !pe) || !cos_sin || !positions || T <= 0 || max_positions <= 0 || (flags & ~ENCODE_FLAGS)) return DSA_ERR_ARG;
+  if (!x != !codes || !x != !scale || !pe != !pe_out) return DSA_ERR_ARG;
+  EncodeParams p{};
+  if (!usable_encoding(p.enc, norm_weight, norm_bias, norm_eps, flags) || (!x && norm_weight)) return DSA_ERR_ARG;
+  if (!aligned16(x) || !aligned16(pe) || !aligned16(cos_sin) || !aligned16(codes) || !aligned16(pe_out)) return DSA_ERR_ARG;
+  if (x && ((G != 1 && G != DSA_HEADS) || !usable_stride(x_token_stride, T, DSA_HEADS * DSA_HEAD_DIM) ||
+            !usable_stride(x_head_stride, G, DSA_HEAD_DIM)))
+    return DSA_ERR_ARG;
+  if (pe && (H <= 0 || !usable_stride(pe_token_stride, T, LA_DP) || !usable_stride(pe_head_stride, H, LA_DP) ||
+             !usable_stride(po_token_stride, T, LA_DP) || !usable_stride(po_head_stride, H, LA_DP)))
+    return DSA_ERR_ARG;
+  // in place only element by element
+  if (pe && pe == pe_out && (pe_token_stride != po_token_stride || pe_head_stride != po_head_stride)) return DSA_ERR_ARG;
+  if (T >= (1 << 30) || (pe && (int64_t)T * H >= (1ll << 36))) return DSA_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  p.x = bf(x);
+  p.x_token = x_token_stride;
+  p.x_head = x_head_stride;
+  p.G = x ? G : 1;
+  p.pe = bf(pe);
+  p.pe_token = pe_token_stride;
+  p.pe_head = pe_head_stride;
+  p.H = H;
+  p.pe_pairs = !(flags & DSA_ENCODE_PE_HALVES);
+  p.cos_sin = cos_sin;
+  p.max_positions = max_positions;
+  p.positions = positions;
+  p.T = T;
+  p.codes = codes;
+  p.scale = scale;
+  p.pe_out = reinterpret_cast<__nv_bfloat16*>(pe_out);
+  p.po_token = po_token_stride;
+  p.po_head = po_head_stride;
+  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  return launch_encode(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+} catch (...) {
+  return DSA_ERR_CUDA;
+}
+
+int dsa_latent_cache_append(const uint16_t* c, int64_t c_stride, const uint16_t* k_pe, int64_t k_pe_stride,
+                            const uint16_t* index_k, int64_t index_k_stride, const float* c_norm, float c_eps,
+                            const float* index_norm_weight, const float* index_norm_bias, float index_norm_eps,
+                            const float* cos_sin, int max_positions, const int32_t* positions, const int32_t* cu_new,
+                            const int32_t* block_table, const int32_t* seq_lens, int B, int T, int max_pages,
+                            int num_pages, int flags, uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe,
+                            int64_t kpe_stride, uint8_t* k_cache, float* k_cache_scale, uint16_t* c_out,
+                            int64_t c_out_stride, uint16_t* k_pe_out, int64_t k_pe_out_stride, int32_t* new_lens,
+                            dsa_stream_t stream_) try {
+  if (!c || !k_pe || !cos_sin || !cu_new || !block_table || !seq_lens || !ckv || !kpe || !new_lens) return DSA_ERR_ARG;
+  if (!index_k != !k_cache || !k_cache != !k_cache_scale || (flags & ~ENCODE_FLAGS)) return DSA_ERR_ARG;
+  if (B <= 0 || T <= 0 || max_pages <= 0 || num_pages <= 0 || max_positions <= 0) return DSA_ERR_ARG;
+  if (c_norm && !(c_eps >= 0.f && c_eps <= 3.4e38f)) return DSA_ERR_ARG;
+  if (!usable_stride(c_stride, T, LA_DC) || !usable_stride(k_pe_stride, T, LA_DP) ||
+      (index_k && !usable_stride(index_k_stride, T, DSA_HEAD_DIM)) || (c_out && !usable_stride(c_out_stride, T, LA_DC)) ||
+      (k_pe_out && !usable_stride(k_pe_out_stride, T, LA_DP)))
+    return DSA_ERR_ARG;
+  if (ckv_stride < LA_DC || kpe_stride < LA_DP || (ckv_stride & 7) || (kpe_stride & 7)) return DSA_ERR_ARG;
+  for (const void* q : {(const void*)c, (const void*)k_pe, (const void*)index_k, (const void*)c_norm,
+                        (const void*)cos_sin, (const void*)ckv, (const void*)kpe, (const void*)k_cache,
+                        (const void*)c_out, (const void*)k_pe_out})
+    if (!aligned16(q)) return DSA_ERR_ARG;
+  // in place only row by row
+  if ((c_out == c && c_out_stride != c_stride) || (k_pe_out == k_pe && k_pe_out_stride != k_pe_stride)) return DSA_ERR_ARG;
+  AppendParams p{};
+  if (!usable_encoding(p.enc, index_norm_weight, index_norm_bias, index_norm_eps, flags) || (!index_k && index_norm_weight))
+    return DSA_ERR_ARG;
+  if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535 || T >= (1 << 30))
+    return DSA_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  p.c = bf(c);
+  p.k_pe = bf(k_pe);
+  p.index_k = bf(index_k);
+  p.c_stride = c_stride;
+  p.kp_stride = k_pe_stride;
+  p.ik_stride = index_k_stride;
+  p.c_norm = c_norm;
+  p.c_eps = c_eps;
+  p.pe_pairs = !(flags & DSA_ENCODE_PE_HALVES);
+  p.cos_sin = cos_sin;
+  p.max_positions = max_positions;
+  p.positions = positions;
+  p.cu_new = cu_new;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.B = B;
+  p.T = T;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.ckv = reinterpret_cast<__nv_bfloat16*>(ckv);
+  p.kpe = reinterpret_cast<__nv_bfloat16*>(kpe);
+  p.ckv_stride = ckv_stride;
+  p.kpe_stride = kpe_stride;
+  p.k_cache = k_cache;
+  p.k_scale = k_cache_scale;
+  p.c_out = reinterpret_cast<__nv_bfloat16*>(c_out);
+  p.k_pe_out = reinterpret_cast<__nv_bfloat16*>(k_pe_out);
+  p.c_out_stride = c_out_stride;
+  p.kp_out_stride = k_pe_out_stride;
+  p.new_lens = new_lens;
+  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  return launch_append(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+} catch (...) {
+  return DSA_ERR_CUDA;
+}
+
+int dsa_latent_cache_accept(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride, uint8_t* k_cache,
+                            float* k_cache_scale, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* draft_lens, const int32_t* path, const int32_t* path_lens, int B,
+                            int max_pages, int num_pages, int max_path, int32_t* new_lens, dsa_stream_t stream_) try {
+  if (!ckv || !kpe || !block_table || !seq_lens || !draft_lens || !path || !path_lens || !new_lens ||
+      !k_cache != !k_cache_scale)
+    return DSA_ERR_ARG;
+  if (B <= 0 || max_pages <= 0 || num_pages <= 0 || max_path <= 0) return DSA_ERR_ARG;
+  if (ckv_stride < LA_DC || kpe_stride < LA_DP || (ckv_stride & 7) || (kpe_stride & 7)) return DSA_ERR_ARG;
+  if (!aligned16(ckv) || !aligned16(kpe) || !aligned16(k_cache)) return DSA_ERR_ARG;
+  if ((int64_t)max_pages * PAGE >= (1ll << 30) || (int64_t)num_pages * PAGE >= (1ll << 31) || B > 65535 ||
+      max_path >= (1 << 30))
+    return DSA_ERR_UNSUPPORTED;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  AcceptParams p{};
+  p.ckv = reinterpret_cast<uint8_t*>(ckv);
+  p.kpe = reinterpret_cast<uint8_t*>(kpe);
+  p.ckv_stride = 2 * ckv_stride;
+  p.kpe_stride = 2 * kpe_stride;
+  p.k_cache = k_cache;
+  p.k_scale = k_cache_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.draft_lens = draft_lens;
+  p.path = path;
+  p.path_lens = path_lens;
+  p.B = B;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.max_path = max_path;
+  p.new_lens = new_lens;
+  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  return launch_accept(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 } catch (...) {
   return DSA_ERR_CUDA;
 }

@@ -4,7 +4,8 @@
 // prefix keys (if any) and then the logical keys [0, seq_lens[b] - next_n + i
 // + 1) of its sequence; with u_s = scale_log2 * (q_nope . ckv[s] + q_pe .
 // kpe[s]) its output is sum_s 2^(u_s - lse) ckv[s], lse = log2(sum_s 2^u_s).
-// A row that sees no key gets zeros and lse = -inf.
+// A row that sees no key gets zeros and lse = -inf.  Of a tree of drafted tokens
+// node i sees the keys before the nodes, and the nodes that its bits name.
 //
 // A key is 1152 bytes and costs a row 2176 operations, so up to about 128
 // rows a sequence the cache's bandwidth bounds the call, beyond that (a
@@ -92,7 +93,8 @@ struct LA {
   static constexpr uint32_t OFF_REF = OFF_RED + 4 * N * 4;                       // [N] reference maxima
   static constexpr uint32_t OFF_ALPHA = OFF_REF + N * 4;                         // [N] factors
   static constexpr uint32_t OFF_LIM = OFF_ALPHA + N * 4;                         // [N] visible keys per row
-  static constexpr uint32_t OFF_FLAG = OFF_LIM + N * 4;                          // abort, tmem base
+  static constexpr uint32_t OFF_BITS = OFF_LIM + N * 4;                          // [N] a tree's visible keys per row
+  static constexpr uint32_t OFF_FLAG = OFF_BITS + N * 8;                         // abort, tmem base
   static constexpr uint32_t OFF_STAT = OFF_FLAG + 128;                           // Stats: this CTA's status and wait limit
   static constexpr uint32_t SMEM = OFF_STAT + 128 + 1024;                        // + alignment
   static constexpr uint32_t TMEM_S = 4 * N;                                      // column of the first S^T buffer (2 N each)
@@ -146,6 +148,15 @@ __device__ __forceinline__ int own_row(int lane) {
   return 8 * (i >> 1) + 2 * (lane & 3) + (i & 1);
 }
 
+// Drafted nodes of sequence b, its last keys; a sequence of an invalid number of them counts as empty.
+__device__ __forceinline__ int tree_nodes(const LatentAttnParams& p, int b, int& len, bool& bad) {
+  if (!p.draft_lens) return min(p.next_n, len);
+  const int n = p.draft_lens[b];
+  if (n >= 0 && n <= p.next_n && n <= len) return n;
+  bad = true;
+  return len = 0;
+}
+
 // One item: a block of rows and the keys they see.
 struct Item {
   int row0, nrows;         // flat query rows
@@ -153,7 +164,10 @@ struct Item {
   int lim0;                // keys that the block's first row sees; later tokens see one more each
   int r0;                  // first row within its sequence (-1: a prefix, every row sees all)
   const int32_t* table;
+  // a tree: the sequence, its nodes, and the keys before them, which every row of a node sees
+  int b, nodes, ctx;
 };
+template <bool TREE>
 __device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
   Item it;
   bool bad;
@@ -172,7 +186,31 @@ __device__ __forceinline__ Item load_item(const LatentAttnParams& p, int w) {
   it.len = valid_len(p.seq_lens[b], p.max_pages, bad);
   it.lim0 = max(0, it.len - p.next_n + 1 + it.r0 / p.H);
   it.table = p.block_table + (int64_t)b * p.max_pages;
+  if constexpr (TREE) {
+    it.b = b;
+    it.nodes = tree_nodes(p, b, it.len, bad);
+    it.ctx = it.len - it.nodes;
+    it.lim0 = it.r0 + p.n > it.nodes * p.H ? 0 : it.ctx;  // (rows that see nothing are masked in every tile)
+  }
   return it;
+}
+
+// Which keys of tile k a tree's row sees, one bit per key.
+__device__ __forceinline__ uint64_t tree_bits(const LatentAttnParams& p, const Item& it, int row, int k) {
+  const int node = row / p.H, d0 = k * LT - it.ctx;  // place of the tile's first key among the drafted
+  if (row >= p.next_n * p.H || node >= it.nodes) return 0;
+  const uint64_t* mask = p.tree_mask + ((int64_t)it.b * p.next_n + node) * p.mask_words;
+  auto word = [&](int w) {
+    const int left = it.nodes - 64 * w;
+    if (left <= 0) return (uint64_t)0;
+    return left >= 64 ? mask[w] : mask[w] & (((uint64_t)1 << left) - 1);
+  };
+  if (d0 >= 0) {
+    const int w = d0 >> 6, s = d0 & 63;
+    return s ? word(w) >> s | word(w + 1) << (64 - s) : word(w);
+  }
+  if (d0 <= -LT) return ~(uint64_t)0;
+  return word(0) << -d0 | (((uint64_t)1 << -d0) - 1);
 }
 
 // The pieces of one CTA: next() gives item w and its tiles [k0, k1).
@@ -201,7 +239,7 @@ struct Runs {
 
 // Numbers the items' units (start[]), the same in every CTA; returns this
 // CTA's units and first item.  tmp: 34 ints of shared memory.
-template <int THREADS>
+template <int THREADS, bool TREE>
 __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, int* status) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* start = p.start + (int64_t)blockIdx.x * (p.items + 1);
@@ -216,6 +254,8 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
       int len = pre;
       if (w >= p.prefix_items) {
         len = valid_len(p.seq_lens[(w - p.prefix_items) / p.blocks], p.max_pages, bad);
+        // (a block without a node has nothing to do)
+        if (TREE && w % p.blocks * p.n >= tree_nodes(p, w / p.blocks, len, bad) * p.H) len = 0;
         if (bad) atomicOr(status, ST_RANGE);
       }
       units = len ? ceil_div(len, LT) + p.item_units : 0;
@@ -255,7 +295,7 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
 
 }  // namespace
 
-template <int N>
+template <int N, bool TREE>
 __global__ void __launch_bounds__(LA<N>::THREADS, 1)
     latent_attn_kernel(const __grid_constant__ LatentMaps maps, const LatentAttnParams p) {
   using C = LA<N>;
@@ -267,6 +307,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   float* s_ref = reinterpret_cast<float*>(smem + C::OFF_REF);
   float* s_alpha = reinterpret_cast<float*>(smem + C::OFF_ALPHA);
   int* s_lim = reinterpret_cast<int*>(smem + C::OFF_LIM);
+  uint64_t* s_bits = reinterpret_cast<uint64_t*>(smem + C::OFF_BITS);
   volatile int* abort_flag = reinterpret_cast<int*>(smem + C::OFF_FLAG);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -305,7 +346,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   // (the scan's scratch lies in the exchange buffer of the softmax)
-  Runs runs = plan_runs<C::THREADS>(p, reinterpret_cast<int*>(smem + C::OFF_RED), &stats->status);
+  Runs runs = plan_runs<C::THREADS, TREE>(p, reinterpret_cast<int*>(smem + C::OFF_RED), &stats->status);
   __syncthreads();
   uint32_t it = 0;       // this CTA's tiles so far
   uint32_t seg = 0;      // and its pieces
@@ -317,7 +358,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
     // ------------------------------------------------------- TMA producer --
     bool ok = true;
     while (ok && runs.next(w, k0, k1, whole)) {
-      const Item im = load_item(p, w);
+      const Item im = load_item<TREE>(p, w);
       if (!(ok = mbar_wait_warp(bar(C::B_QE), (seg & 1) ^ 1, abort_flag, stats))) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar(C::B_QF), 9 * N * 128);
@@ -435,8 +476,8 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
     constexpr int HALVES = C::SW / 4;
     float ref = neg_inf();                   // threads st_id < N: the reference maximum of row st_id
     while (runs.next(w, k0, k1, whole)) {
-      const Item im = load_item(p, w);
-      for (int c = st_id; c < N; c += C::ST)
+      const Item im = load_item<TREE>(p, w);
+      for (int c = st_id; !TREE && c < N; c += C::ST)
         s_lim[c] = c >= im.nrows ? 0 : im.r0 < 0 ? im.len : max(0, im.len - p.next_n + 1 + (im.r0 + c) / p.H);
       float2 f[M8];                          // the references of this thread's rows
       float l[2 * M8];                       // its part of each row's sum
@@ -466,7 +507,7 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
         // slots past the sequence may hold anything: their values become 0
         // in the tile itself (a weight of 0 does not silence a NaN)
         const int valid = im.len - k * LT;
-        if (valid < LT) {
+        if (!TREE && valid < LT) {
           for (int i = st_id; i < (LT - valid) * 64; i += C::ST) {
             const int row = valid + (i >> 6), ch = (i >> 3) & 7, x = i & 7;  // row, chunk of 64 dims, 16 bytes
             const uint32_t ps = (4 * it + (ch >> 1)) % C::PAIRS;
@@ -479,7 +520,35 @@ __global__ void __launch_bounds__(LA<N>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4 * M8; ++i) u[i >> 2][i & 3] = __uint_as_float(s[i]);
         const int key = k * LT + 16 * q + g;
-        if ((k + 1) * LT > im.lim0 || im.nrows < N) {
+        if (TREE && (k + 1) * LT > im.lim0) {
+          // (every thread has read the bits of earlier tiles: it has met the others since, in the vote below)
+          if (st_id < N) s_bits[st_id] = tree_bits(p, im, im.r0 + st_id, k);
+          named_bar_sync(1, C::ST);
+          // keys that no row of the block sees may hold anything, as those past the end
+          uint32_t lo = 0, hi = 0;
+          for (int c = lane; c < N; c += 32) {
+            lo |= (uint32_t)s_bits[c];
+            hi |= (uint32_t)(s_bits[c] >> 32);
+          }
+          const uint64_t seen = (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 | __reduce_or_sync(0xffffffffu, lo);
+          if (~seen) {
+            for (int i = st_id; i < LT * 64; i += C::ST) {
+              const int row = i >> 6, ch = (i >> 3) & 7, x = i & 7;  // row, chunk of 64 dims, 16 bytes
+              const uint32_t ps = (4 * it + (ch >> 1)) % C::PAIRS;
+              if (!(seen >> row & 1))
+                *reinterpret_cast<uint4*>(smem + C::OFF_PAIR + ps * PAIR + (ch & 1) * CHUNK + row * 128 + 16 * x) =
+                    make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < M8; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t bits = s_bits[8 * m + cc + e] >> (16 * q + g);
+              if (!(bits & 1)) u[m][e] = neg_inf();
+              if (!(bits >> 8 & 1)) u[m][2 + e] = neg_inf();
+            }
+        } else if (!TREE && ((k + 1) * LT > im.lim0 || im.nrows < N)) {
           named_bar_sync(1, C::ST);  // s_lim
 #pragma unroll
           for (int m = 0; m < M8; ++m)
@@ -846,13 +915,13 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
   }
 }
 
-template <int N>
+template <int N, bool TREE>
 static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
   static DeviceFlags attr_set;
-  cudaError_t e = set_smem_attr_once(latent_attn_kernel<N>, LA<N>::SMEM, attr_set);
+  cudaError_t e = set_smem_attr_once(latent_attn_kernel<N, TREE>, LA<N>::SMEM, attr_set);
   if (e != cudaSuccess) return e;
   count_launch();
-  e = launch_pdl(latent_attn_kernel<N>, dim3(p.grid), dim3(LA<N>::THREADS), LA<N>::SMEM, s, m, p);
+  e = launch_pdl(latent_attn_kernel<N, TREE>, dim3(p.grid), dim3(LA<N>::THREADS), LA<N>::SMEM, s, m, p);
   if (e != cudaSuccess) return e;
   count_launch();
   const int R = p.next_n * p.H, spread = min(p.max_pages, ceil_div(8 * p.grid, p.B));
@@ -870,7 +939,8 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
 }
 
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
-  return p.n == 16 ? launch_n<16>(m, p, s) : p.n == 32 ? launch_n<32>(m, p, s) : launch_n<64>(m, p, s);
+  if (p.tree_mask) return p.n == 16 ? launch_n<16, true>(m, p, s) : p.n == 32 ? launch_n<32, true>(m, p, s) : launch_n<64, true>(m, p, s);
+  return p.n == 16 ? launch_n<16, false>(m, p, s) : p.n == 32 ? launch_n<32, false>(m, p, s) : launch_n<64, false>(m, p, s);
 }
 
 }  // namespace dsa

@@ -254,7 +254,7 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
 /*
  * Latent attention (keys and values from one shared latent vector a token).
  *
- * The four operators below share one cache: per slot a 512-dim compressed
+ * The operators below share one cache: per slot a 512-dim compressed
  * vector ckv (the key's no-rope part and the value) and a 64-dim rope part
  * kpe, bf16, in pages of 64 slots; logical key s of sequence b lives in slot
  * block_table[b][s / 64] * 64 + s % 64, as in dsa_indexer_topk_paged.
@@ -329,6 +329,120 @@ DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uin
                                                const int32_t* block_table, const int32_t* seq_lens,
                                                int B, int next_n, int H, int max_pages, int num_pages,
                                                float sm_scale, uint16_t* out, float* lse, dsa_stream_t stream);
+
+/*
+ * Decode of drafted tokens that form a tree: the last draft_lens[b] of the
+ * seq_lens[b] keys of sequence b are its nodes (without draft_lens next_n of
+ * them, or all its keys if it has fewer).  Query i, for every head, sees the
+ * keys before the nodes and node j where bit j % 64 of tree_mask[b, i, j / 64] is
+ * set (its ancestors and itself, or whatever is wanted); otherwise as
+ * dsa_latent_attention_paged.  A node that no query sees may hold anything.
+ * Queries i >= draft_lens[b] are padding: their rows get zeros and lse = -inf.  A number of nodes below 0, above next_n or above
+ * seq_lens[b] is DSA_ERR_RANGE, and the sequence counts as empty.
+ *
+ *   tree_mask [B, next_n, ceil(next_n / 64)] uint64, 8-byte aligned   draft_lens [B] int32 or null
+ */
+DSA_API int dsa_latent_attention_tree(const uint16_t* q_nope, const uint16_t* q_pe,
+                                      const uint16_t* ckv, int64_t ckv_stride,
+                                      const uint16_t* kpe, int64_t kpe_stride,
+                                      const int32_t* block_table, const int32_t* seq_lens,
+                                      const uint64_t* tree_mask, const int32_t* draft_lens,
+                                      int B, int next_n, int H, int max_pages, int num_pages, float sm_scale,
+                                      uint16_t* out, float* lse, dsa_stream_t stream);
+
+/*
+ * Keeps the accepted path of every sequence's drafted nodes: node path[b, j],
+ * j < path_lens[b], moves to logical slot seq_lens[b] - draft_lens[b] + j, and
+ * new_lens[b] = seq_lens[b] - draft_lens[b] + path_lens[b].  The path ascends and
+ * names nodes in [0, draft_lens[b]); one that does not, or lengths that do not
+ * fit, is DSA_ERR_RANGE and leaves the sequence as it is (new_lens[b] =
+ * seq_lens[b]).  A node whose page or target page is outside the cache is not
+ * moved.  No two sequences may share the pages of their nodes.
+ *
+ *   path [B, max_path] int32   path_lens, draft_lens [B] int32
+ *   k_cache, k_cache_scale: the indexer's keys and scales, moved along, or both null
+ *   new_lens [B] int32 (may be seq_lens itself)
+ */
+DSA_API int dsa_latent_cache_accept(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride,
+                                    uint8_t* k_cache, float* k_cache_scale,
+                                    const int32_t* block_table, const int32_t* seq_lens,
+                                    const int32_t* draft_lens, const int32_t* path, const int32_t* path_lens,
+                                    int B, int max_pages, int num_pages, int max_path,
+                                    int32_t* new_lens, dsa_stream_t stream);
+
+/* Flags of dsa_indexer_encode and dsa_latent_cache_append. */
+typedef enum {
+  DSA_ENCODE_PAIRS = 1,     /* index rows rotate dims (2 i, 2 i + 1) together; without it dims (i, i + 32) */
+  DSA_ENCODE_HADAMARD = 2,  /* index rows go through the Hadamard transform */
+  DSA_ENCODE_PE_HALVES = 4  /* rope parts rotate dims (i, i + 32) together; without it dims (2 i, 2 i + 1) */
+} dsa_encode_flag;
+
+/*
+ * Rows ready for the indexer: what dsa_indexer_topk takes as q (G = 64) or as k
+ * (G = 1), from a projection's output x, and the rope parts of the same tokens'
+ * attention queries or keys, rotated.  For token t with position positions[t]:
+ *
+ *     y[g] = (x[t, g] - mean) / sqrt(var + norm_eps) * norm_weight + norm_bias   over its 128 dims (null: y = x)
+ *     pair i of dims [0, 64): (a, b) -> (a cos_i - b sin_i, a sin_i + b cos_i)
+ *     y[g] = H y[g] / sqrt(128), H[d, e] = (-1)^popcount(d & e)   (with DSA_ENCODE_HADAMARD)
+ *     scale[t] = max over g, d of |y| / 448, or 1 where all are 0;   codes[t, g] = e4m3(y / scale[t])
+ *
+ * in fp32 with one rounding, to nearest even.  The rope parts pe[t, h] (64 dims)
+ * turn by the same angles and are rounded to bf16.  A token whose position is
+ * negative is padding, and one at or past max_positions is DSA_ERR_RANGE
+ * (dsa_latent_last_status): their outputs stay as they were.  x must be finite; a
+ * token with an infinity or NaN has undefined codes and scale.
+ *
+ *   x [T, G, 128] bf16, G = 64 or 1, or null        codes [T, G, 128] e4m3   scale [T] fp32
+ *   pe [T, H, 64] bf16, or null                     pe_out [T, H, 64] bf16 (may be pe, with its strides)
+ *   norm_weight, norm_bias [128] fp32, or both null
+ *   cos_sin [max_positions, 64] fp32: 32 cosines, then 32 sines, of each position's angles
+ *   positions [T] int32
+ *   token and head strides in elements, positive multiples of 8, of an axis of one element anything;
+ *   all arrays but scale and positions 16-byte aligned
+ */
+DSA_API int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride, int G,
+                               const float* norm_weight, const float* norm_bias, float norm_eps,
+                               const uint16_t* pe, int64_t pe_token_stride, int64_t pe_head_stride, int H,
+                               const float* cos_sin, int max_positions, const int32_t* positions, int T, int flags,
+                               uint8_t* codes, float* scale,
+                               uint16_t* pe_out, int64_t po_token_stride, int64_t po_head_stride,
+                               dsa_stream_t stream);
+
+/*
+ * New tokens into the cache: tokens [cu_new[b], cu_new[b + 1]) of the T given
+ * go to the logical slots of sequence b from seq_lens[b] on, and new_lens[b]
+ * becomes seq_lens[b] + cu_new[b + 1] - cu_new[b].  Per token: its latent c,
+ * RMS-normalised (c / sqrt(mean c^2 + c_eps) * c_norm; null: as it is), its rope part k_pe
+ * rotated, and, if given, its index key encoded as dsa_indexer_encode does, with
+ * a scale of its own.  c_out and k_pe_out, where not null, get the same values as
+ * the cache, for a prefill in the expanded form.  The angles are those of
+ * positions[t], or, without positions, of the token's logical slot (which is not
+ * its position where keys have been evicted or where drafted tokens form a tree).
+ *
+ *   c [T, 512], k_pe [T, 64] bf16    index_k [T, 128] bf16 or null, with k_cache and k_cache_scale
+ *   c_norm [512] fp32 or null        index_norm_weight, index_norm_bias [128] fp32, or both null
+ *   cu_new [B + 1] int32, ascending, within [0, T]; tokens outside every sequence are padding
+ *   positions [T] int32 or null      c_out [T, 512], k_pe_out [T, 64] bf16 or null (may be c and k_pe)
+ *   strides in elements, as in dsa_indexer_encode    new_lens [B] int32 (may be seq_lens itself)
+ *
+ * A sequence whose border, length or new length does not fit the arrays or its
+ * table is skipped (new_lens[b] = seq_lens[b]); a token whose position is outside
+ * [0, max_positions), or whose page is outside the cache, is not written.  Both
+ * are DSA_ERR_RANGE.  No two sequences may write one page.
+ */
+DSA_API int dsa_latent_cache_append(const uint16_t* c, int64_t c_stride, const uint16_t* k_pe, int64_t k_pe_stride,
+                                    const uint16_t* index_k, int64_t index_k_stride,
+                                    const float* c_norm, float c_eps,
+                                    const float* index_norm_weight, const float* index_norm_bias,
+                                    float index_norm_eps,
+                                    const float* cos_sin, int max_positions, const int32_t* positions,
+                                    const int32_t* cu_new, const int32_t* block_table, const int32_t* seq_lens,
+                                    int B, int T, int max_pages, int num_pages, int flags,
+                                    uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, int64_t kpe_stride,
+                                    uint8_t* k_cache, float* k_cache_scale,
+                                    uint16_t* c_out, int64_t c_out_stride, uint16_t* k_pe_out, int64_t k_pe_out_stride,
+                                    int32_t* new_lens, dsa_stream_t stream);
 
 /*
  * Eviction in place: a sequence with more than `budget` keys keeps its last

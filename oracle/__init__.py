@@ -31,6 +31,9 @@ Python for unit tests of that logic.  `checks.py` holds the parity criteria.
 over the KV entries its top-K indices name, base-2 softmax, 512-dim output
 and log-sum-exp, in float64.
 
+`token_encode.py` is the oracle of the rows that the indexer and the latent
+cache are given: norms, rotation by position, Hadamard transform, e4m3 codes.
+
 Pins: tests/test_oracle_*.py check every function here against the format
 definition, torch's independent float8 decoder, Python-integer brute force,
 hand-computed worked examples, closed-form special cases, subset enumeration

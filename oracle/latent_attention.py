@@ -7,6 +7,8 @@ Definitions:
                   lse = log2(sum_s 2^u_s); out = sum_s 2^(u_s - lse) ckv[s];
                   token i of next_n sees the first len - next_n + i + 1 keys
   shared prefix   every row sees the prefix keys, then its own sequence's
+  tree            node i of a sequence's last n keys sees the keys before them
+                  and the nodes named for it
   key weights     sum over the rows that see key s of 2^(u_s - lse)
   expanded form   the same softmax over keys (k_nope[s, h] | k_pe[s]) and
                   values v[s, h]; query i of n sees the first m - n + i + 1 of
@@ -30,13 +32,14 @@ PAGE = 64
 
 
 def rows_over_keys(q, k, v, visible, sm_scale):
-    """q [R, D], k [N, D], v [N, E] float64, visible [R]: (out [R, E], lse [R],
-    p [R, N], magnitude [R, E], spread [R])."""
+    """q [R, D], k [N, D], v [N, E] float64, visible [R] keys from the first on, or [R, N]
+    truth values: (out [R, E], lse [R], p [R, N], magnitude [R, E], spread [R])."""
     R, N = q.shape[0], k.shape[0]
     if N == 0:
         e = np.zeros((R, v.shape[1]))
         return e, np.full(R, -np.inf), np.zeros((R, 0)), e, np.zeros(R)
-    see = np.arange(N)[None, :] < np.asarray(visible)[:, None]
+    visible = np.asarray(visible)
+    see = visible if visible.ndim == 2 else np.arange(N)[None, :] < visible[:, None]
     u = np.where(see, (q @ k.T) * (sm_scale * LOG2E), -np.inf)
     m = np.where(see.any(1), u.max(1), 0.0)
     e = np.exp2(u - m[:, None])
@@ -68,6 +71,27 @@ def decode(q_nope, q_pe, ckv, kpe, block_table, seq_lens, sm_scale, prefix_table
         q = np.concatenate([q_nope[b], q_pe[b]], -1).reshape(nn * H, -1)
         sees = prefix_len + np.repeat(np.maximum(0, L - nn + 1 + np.arange(nn)), H)
         res.append(rows_over_keys(q, k, v, sees, sm_scale))
+    return res
+
+
+def tree(q_nope, q_pe, ckv, kpe, block_table, seq_lens, seen, sm_scale):
+    """decode() for drafted nodes: seen[b] is the list of sets of nodes that each node of sequence b sees
+    (its last len(seen[b]) keys); queries behind them see nothing."""
+    B, nn, H, _ = q_nope.shape
+    res = []
+    for b in range(B):
+        L, n = int(seq_lens[b]), len(seen[b])
+        slots = slots_of(block_table[b], L)
+        v = ckv[slots]
+        k = np.concatenate([v, kpe[slots]], 1)
+        q = np.concatenate([q_nope[b], q_pe[b]], -1).reshape(nn * H, -1)
+        sees = np.zeros((nn, L), bool)
+        for i, s in enumerate(seen[b]):
+            sees[i, :L - n] = True
+            sees[i, [L - n + j for j in s]] = True
+        hidden = ~sees.any(0)  # what nobody sees may hold anything
+        v[hidden], k[hidden] = 0.0, 0.0
+        res.append(rows_over_keys(q, k, v, np.repeat(sees, H, 0), sm_scale))
     return res
 
 
