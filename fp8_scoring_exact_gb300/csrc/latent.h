@@ -91,13 +91,14 @@ struct LatentAttnParams {
   const uint64_t* tree_mask;    // [B, next_n, mask_words]: node i sees node j where bit j % 64 of word j / 64 is set
   const int32_t* draft_lens;    // [B] nodes of a sequence, or null: next_n, or all its keys if it has fewer
   int mask_words;
-  int n;                        // rows per block
+  int n;                        // rows per block (128: of a pair of CTAs; grid then counts pairs)
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
   int items, grid, item_units;
   uint64_t wait_ns;
   int withhold;                 // test option: the first keys are never loaded (a wait must run out)
   int32_t* per;                 // [1] units per CTA
-  int32_t* start;               // [grid, items + 1] first unit of each item, worked out by every CTA for itself
+  // [grid, items + 1] ([2 grid, items + 1] for pairs of CTAs) first unit of each item, worked out by every CTA for itself
+  int32_t* start;
   // unnormalised outputs of the pieces: with a prefix all of them, [items + grid, n, 512]; without one those of cut
   // items, of which a CTA has two at most, [2 grid, n, 512] (1: the one that starts with its item's first tile)
   float* part_o;
@@ -227,6 +228,8 @@ struct LatentMaps {
   CUtensorMap q_nope, q_pe, ckv, kpe;
 };
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
+// Trees of more than 64 rows a sequence (p.n = 128): runs of pairs of CTAs, the main kernel alone.
+cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_encode(EncodeParams p, cudaStream_t s);
 cudaError_t launch_append(AppendParams p, cudaStream_t s);

@@ -172,11 +172,13 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.B * R;
   // the rows of a block: a prefix gathers the rows of the whole batch, so its
   // blocks are full; else the smallest block that holds a sequence's rows
-  p.n = p.prefix_table || R > 32 ? 64 : R > 16 ? 32 : 16;
+  const bool pairs = p.tree_mask && R > 64;
+  p.n = pairs ? 128 : p.prefix_table || R > 32 ? 64 : R > 16 ? 32 : 16;
   p.blocks = ceil_div(R, p.n);
   p.prefix_items = p.prefix_table ? (int)((rows + p.n - 1) / p.n) : 0;
   p.items = p.prefix_items + p.B * p.blocks;
   p.grid = std::min(option_grid(), 1024);
+  const int ctas = pairs ? (p.grid = std::max(1, p.grid / 2), 2 * p.grid) : p.grid;
   p.item_units = p.prefix_table ? LA_PREFIX_ITEM_UNITS : LA_ITEM_UNITS;
   if ((int64_t)p.items * (std::max(p.max_pages, p.prefix_pages) + p.item_units) >= (1ll << 31) - (1 << 20))
     return DSA_ERR_UNSUPPORTED;
@@ -184,7 +186,8 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   p.withhold = option_withhold();
   LatentMaps m;
   const int64_t slots = (int64_t)p.num_pages * PAGE;
-  if (!tmap_rows(&m.q_nope, p.q_nope, rows, LA_DC, 8, p.n, 8) || !tmap_rows(&m.q_pe, p.q_pe, rows, LA_DP, 1, p.n, 1) ||
+  if (!tmap_rows(&m.q_nope, p.q_nope, rows, LA_DC, 8, std::min(p.n, 64), 8) ||
+      !tmap_rows(&m.q_pe, p.q_pe, rows, LA_DP, 1, std::min(p.n, 64), 1) ||
       !tmap_rows(&m.ckv, p.ckv, slots, p.ckv_stride, 8, PAGE, 2) ||
       !tmap_rows(&m.kpe, p.kpe, slots, p.kpe_stride, 1, PAGE, 1))
     return DSA_ERR_CUDA;
@@ -195,7 +198,7 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
     return o;
   };
   const size_t pieces = (size_t)p.items + p.grid;
-  const size_t o_per = take(4), o_start = take(4 * ((size_t)p.items + 1) * p.grid), o_ml = take(8 * pieces * p.n),
+  const size_t o_per = take(4), o_start = take(4 * ((size_t)p.items + 1) * ctas), o_ml = take(8 * pieces * p.n),
                o_po = take(4 * (p.prefix_items ? pieces : 2 * (size_t)p.grid) * p.n * LA_DC),
                o_log = p.weights ? take(4 * (size_t)p.B * p.blocks * p.max_pages * PAGE * p.n) : 0;
   std::lock_guard<std::mutex> lk(g_mu);

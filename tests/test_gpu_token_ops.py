@@ -544,6 +544,26 @@ def test_tree_reports_bad_arguments(B):  # noqa: F811
     assert B.latent_last_status() == 0
 
 
+@pytest.mark.parametrize("nn,H", [(3, 16), (8, 16), (16, 128)])
+def test_tree_wait_limit_ends_the_kernels(B, nn, H):  # noqa: F811
+    """With a test option the first keys are never loaded, so that the waits for them (limit 50 ms here) run out: the
+    call comes back, says so, and the next one is right."""
+    c = Cache([3000, 500], seed=37)
+    seen = [_seen_of(_random_tree(np.random.default_rng(b), nn)) for b in range(2)]
+    qn, qp = _queries(2, nn, H, seed=38)
+    B.set_option("wait_limit_us", 50000)
+    B.set_option("test_withhold", 1)
+    try:
+        _tree(B, c, qn, qp, _mask(seen, nn), None)
+        assert B.latent_last_status() == B.DSA_ERR_TIMEOUT
+    finally:
+        B.set_option("test_withhold", 0)
+        B.set_option("wait_limit_us", 2000000)
+    out, lse = _tree(B, c, qn, qp, _mask(seen, nn), None)
+    assert B.latent_last_status() == 0
+    _check_tree(c, qn, qp, out, lse, seen)
+
+
 # ------------------------------------------------------------------ accept --
 @pytest.mark.parametrize("seqs", [
     # (length, nodes, path) of each sequence
