@@ -99,7 +99,7 @@ struct LatentAttnParams {
   int32_t* per;                 // [1] units per CTA
   // [grid, items + 1] ([2 grid, items + 1] for pairs of CTAs) first unit of each item, worked out by every CTA for itself
   int32_t* start;
-  // unnormalised outputs of the pieces: with a prefix all of them, [items + grid, n, 512]; without one those of cut
+  // unnormalised outputs of the pieces ([128 / 4 dims, 128 rows, 4] each where they are a pair's): with a prefix all of them, [items + grid, n, 512]; without one those of cut
   // items, of which a CTA has two at most, [2 grid, n, 512] (1: the one that starts with its item's first tile)
   float* part_o;
   float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
@@ -228,7 +228,7 @@ struct LatentMaps {
   CUtensorMap q_nope, q_pe, ckv, kpe;
 };
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
-// Trees of more than 64 rows a sequence (p.n = 128): runs of pairs of CTAs, the main kernel alone.
+// Trees of more than 64 rows a sequence (p.n = 128): runs of pairs of CTAs.
 cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
 cudaError_t launch_encode(EncodeParams p, cudaStream_t s);

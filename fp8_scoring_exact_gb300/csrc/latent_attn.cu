@@ -758,19 +758,6 @@ __global__ void __launch_bounds__(FIN_THREADS) latent_finish_kernel(const Latent
   }
 }
 
-// The call's last kernel, without key weights.
-static cudaError_t launch_join(const LatentAttnParams& p, cudaStream_t s) {
-  const int R = p.next_n * p.H;
-  // few items, so rows of many pieces: more threads take fewer dims (a sequence of 131072 keys and 16 rows:
-  // 37 us, 41 the other way; two of 64 rows 63 and 70).  Else two parts of 256 dims (seven sequences of 128
-  // rows, 11 pieces each, 70 us and 79 the first way; 64 sequences behind 32768 shared keys 159 and 183).  128
-  // threads for all 512 dims are the best for even lengths (156), but a long sequence among short ones has
-  // as many pieces as one alone (the sequence of 131072 keys: 48 us).
-  if (p.grid > 32 * (p.prefix_items ? p.prefix_items : p.items))
-    return launch_pdl(latent_join_kernel<256, 128, 4>, dim3(p.B * R, LA_DC / 128), dim3(256), 0, s, p);
-  return launch_pdl(latent_join_kernel<128, 256, 8>, dim3(p.B * R, LA_DC / 256), dim3(128), 0, s, p);
-}
-
 template <int N, bool TREE>
 static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
   static DeviceFlags attr_set;
@@ -784,16 +771,18 @@ static cudaError_t launch_n(const LatentMaps& m, const LatentAttnParams& p, cuda
   if (p.weights)
     return launch_pdl(latent_finish_kernel<N>, dim3((unsigned)(p.B * (R + spread))), dim3(FIN_THREADS), 8 * (size_t)R, s,
                       p, spread);
-  return launch_join(p, s);
+  // few items, so rows of many pieces: more threads take fewer dims (a sequence of 131072 keys and 16 rows:
+  // 37 us, 41 the other way; two of 64 rows 63 and 70).  Else two parts of 256 dims (seven sequences of 128
+  // rows, 11 pieces each, 70 us and 79 the first way; 64 sequences behind 32768 shared keys 159 and 183).  128
+  // threads for all 512 dims are the best for even lengths (156), but a long sequence among short ones has
+  // as many pieces as one alone (the sequence of 131072 keys: 48 us).
+  if (p.grid > 32 * (p.prefix_items ? p.prefix_items : p.items))
+    return launch_pdl(latent_join_kernel<256, 128, 4>, dim3(p.B * R, LA_DC / 128), dim3(256), 0, s, p);
+  return launch_pdl(latent_join_kernel<128, 256, 8>, dim3(p.B * R, LA_DC / 256), dim3(128), 0, s, p);
 }
 
 cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
-  if (p.n == 128) {
-    const cudaError_t e = launch_tree_pair(m, p, s);
-    if (e != cudaSuccess) return e;
-    count_launch();
-    return launch_join(p, s);
-  }
+  if (p.n == 128) return launch_tree_pair(m, p, s);
   if (p.tree_mask)
     return p.n == 16 ? launch_n<16, true>(m, p, s) : p.n == 32 ? launch_n<32, true>(m, p, s) : launch_n<64, true>(m, p, s);
   return p.n == 16 ? launch_n<16, false>(m, p, s) : p.n == 32 ? launch_n<32, false>(m, p, s) : launch_n<64, false>(m, p, s);

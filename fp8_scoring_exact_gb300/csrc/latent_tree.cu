@@ -45,14 +45,15 @@ constexpr uint32_t TP_OFF_K = TP_OFF_P + 2 * TP_CHUNK;
 constexpr uint32_t TP_OFF_R = TP_OFF_K + TP_SLOTS * TP_SLOT;  // the page's rope parts
 constexpr uint32_t TP_OFF_V = TP_OFF_R + TP_CHUNK;
 constexpr uint32_t TP_OFF_MISC = TP_OFF_V + TP_SLOTS * TP_SLOT;
-// Barriers of the even CTA: K, rope, V and Q full, S empty (per buffer), P full, O read out; of both: K, rope, V and Q
-// empty, S full (per buffer), product done, a masked tile's values there; drain
-constexpr int T_KF = 0, T_KE = T_KF + TP_SLOTS, T_VF = T_KE + TP_SLOTS, T_VE = T_VF + TP_SLOTS, T_RF = T_VE + TP_SLOTS,
-              T_RE = T_RF + 1, T_QF = T_RE + 1, T_QE = T_QF + 1, T_SF = T_QE + 1, T_SE = T_SF + 2, T_PF = T_SE + 2,
-              T_PD = T_PF + 1, T_OE = T_PD + 1, T_Z = T_OE + 1, T_DRAIN = T_Z + 1, T_BARS = T_DRAIN + 2;
+// Barriers of the even CTA: K, rope, V and Q full, S empty (per buffer), P full (per 32 keys), O read out; of both: K,
+// rope and Q empty, S full (per buffer), product of 32 keys done, a masked tile's values there; drain
+constexpr int T_KF = 0, T_KE = T_KF + TP_SLOTS, T_VF = T_KE + TP_SLOTS, T_RF = T_VF + TP_SLOTS, T_RE = T_RF + 1,
+              T_QF = T_RE + 1, T_QE = T_QF + 1, T_SF = T_QE + 1, T_SE = T_SF + 2, T_PF = T_SE + 2, T_PD = T_PF + 4,
+              T_OE = T_PD + 4, T_Z = T_OE + 1, T_DRAIN = T_Z + 1, T_BARS = T_DRAIN + 2;
 constexpr uint32_t TP_OFF_STAT = TP_OFF_MISC + (T_BARS * 8 + 127) / 128 * 128;
 constexpr uint32_t TP_OFF_FLAG = TP_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t TP_OFF_SEEN = TP_OFF_FLAG + 16;   // [parity][warp] keys that some row of the block sees
+constexpr uint32_t TP_OFF_NOTE = TP_OFF_SEEN + 2 * 8 * 8;  // 16 bytes that the odd CTA's copies read and write
 // per group of 32 rows: a masked tile's bits [row][page], then [part][row] maxima or sums
 constexpr uint32_t TP_OFF_ROW = TP_OFF_SEEN + 2 * 8 * 8 + 112;
 constexpr uint32_t TP_SMEM = TP_OFF_ROW + 2 * 512 + 1024;  // + alignment
@@ -73,6 +74,18 @@ __device__ __forceinline__ int load_pages(const LatentAttnParams& p, const Item&
     }
   }
   return page;
+}
+
+// Tells a barrier of another CTA that this warp's weights are in this CTA's
+// shared memory: a copy of 16 bytes that counts on the barrier there.  It comes
+// behind the warp's fences from generic to async proxy, and its completion releases what precedes it to
+// the cluster; an arrival with release at cluster scope does so by a fence that
+// waits on all of the SM's traffic (1500 to 4000 cycles beside the copies of
+// keys).
+__device__ __forceinline__ void note_cluster(uint32_t dst, uint32_t src, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+               "r"(src), "r"(bar)
+               : "memory");
 }
 
 }  // namespace
@@ -99,7 +112,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
     tma_prefetch_desc(&maps.q_pe);
     tma_prefetch_desc(&maps.ckv);
     tma_prefetch_desc(&maps.kpe);
-    for (int i = 0; i < T_BARS; ++i) mbar_init(bar(i), i == T_SE || i == T_SE + 1 || i == T_PF || i == T_OE ? 16 : 1);
+    for (int i = 0; i < T_BARS; ++i) mbar_init(bar(i), i == T_SE || i == T_SE + 1 || i == T_OE ? 16 : i >= T_PF && i < T_PD ? 2 : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -166,7 +179,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         if (k == k0 || (k & 15) == 0) pages = load_pages(p, im, k & ~15, lane, bad);
         for (int c = 0; c < TP_SLOTS; ++c) {
           const int slot = __shfl_sync(0xffffffffu, pages, 2 * (k & 15) + (c >> 1)) * PAGE;
-          if (!(ok = mbar_wait_warp(bar(T_VE + c), (it & 1) ^ 1, abort_flag, stats))) break;
+          // the products of page h's second half end the use of its slots
+          if (!(ok = mbar_wait_warp(bar(T_PD + (c | 1)), (it & 1) ^ 1, abort_flag, stats))) break;
           if (lane == 0) {
             if (rank == 0) mbar_arrive_expect_tx(bar(T_VF + c), 2 * TP_SLOT);
             tma_load_3d_pair(sbase + TP_OFF_V + c * TP_SLOT, &maps.ckv, 0, slot, 4 * (c & 1) + 2 * rank, lead_bar(T_VF + c));
@@ -232,19 +246,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
           }
           __syncwarp();
         }
-        if (!(ok = mbar_wait_one(leader, bar(T_PF), it & 1, abort_flag, stats))) break;
-        for (uint32_t c = 0; c < TP_SLOTS; ++c) {
-          if (!(ok = mbar_wait_one(leader, bar(T_VF + c), it & 1, abort_flag, stats))) break;
+        // 32 keys at a time: their weights' arrival from the other CTA takes some 1500 cycles, in which the buffer of
+        // the others is used
+        for (uint32_t c = 0; c < 4; ++c) {
+          if (!(ok = mbar_wait_one(leader, bar(T_PF + c), it & 1, abort_flag, stats))) break;
+          const uint32_t h = c >> 1;
+          if (!(c & 1)) {
+            ok = mbar_wait_one(leader, bar(T_VF + c), it & 1, abort_flag, stats) &&
+                 mbar_wait_one(leader, bar(T_VF + c + 1), it & 1, abort_flag, stats);
+            if (!ok) break;
+          }
           tc_fence_after();
-          const uint32_t h = c >> 1, v_lo = desc_lo_mnmajor(sbase + TP_OFF_V + c * TP_SLOT, TP_CHUNK);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)  // 16 keys: 32 bytes of a P row, 2 KB of V
-            mma_bf16_ss_pair(leader, tmem + 128 * (c & 1), p_lo + h * (TP_CHUNK >> 4) + 2 * j, v_lo + 128 * j, ID_O,
-                             k > k0 || h > 0 || j > 0);
-          mma_commit_pair(leader, bar(T_VE + c));
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t v_lo = desc_lo_mnmajor(sbase + TP_OFF_V + (2 * h + n) * TP_SLOT, TP_CHUNK);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // 16 keys: 32 bytes of a P row, 2 KB of V
+              const uint32_t j = 2 * (c & 1) + i;
+              mma_bf16_ss_pair(leader, tmem + 128 * n, p_lo + h * (TP_CHUNK >> 4) + 2 * j, v_lo + 128 * j, ID_O,
+                               k > k0 || c > 0 || i > 0);
+            }
+          }
+          mma_commit_pair(leader, bar(T_PD + c));
         }
         if (!ok) break;
-        mma_commit_pair(leader, bar(T_PD));
       }
       ++seg;
     }
@@ -252,23 +277,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
     // ----------------------------------------------------- softmax warps --
     // Row r = 32 (q & 1) + lane of the CTA in four warps: page q >> 1 of the
     // tile and keys [32 ch, + 32) of it, which meet at a barrier of their group of 32 rows.
-    // (A wait that gives up leaves the result undefined; the loops still end.)
+    // A wait that gives up leaves the result undefined; the loops still end.
+    // From then on the warp's weights are not announced any more (`ok`): the
+    // announcement counts on a barrier whose phases end only with the other CTA's
+    // bytes, and a second arrival in one phase is an error.
     const int q = warp & 3, ch = (warp - 4) >> 2, g = q & 1, h = q >> 1, r = 32 * g + lane, part = 2 * h + ch;
     const int tid = threadIdx.x - 128, sw = warp - 4;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     uint64_t* s_seen = reinterpret_cast<uint64_t*>(smem + TP_OFF_SEEN);
     uint64_t* s_bits = reinterpret_cast<uint64_t*>(smem + TP_OFF_ROW + 512 * g);  // [lane][page]
     float* s_red = reinterpret_cast<float*>(smem + TP_OFF_ROW + 512 * g);         // [part][lane]
-    const uint32_t lead_s = lead_bar(T_SE), lead_p = lead_bar(T_PF), lead_o = lead_bar(T_OE);
+    const uint32_t lead_s = lead_bar(T_SE), lead_p = lead_bar(T_PF + part), lead_o = lead_bar(T_OE);
+    const uint32_t lead_note = cluster_addr(sbase + TP_OFF_NOTE, 0);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     uint32_t masked = 0;  // masked tiles so far
+    bool ok = true;
     while (runs.next(w, k0, k1, whole)) {
       const Item im = load_item<true>(p, w);
       float ref = TP_NO_REF;
       uint64_t l[2] = {0, 0};  // this thread's part of the row's sum, in four parts
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it & 1;
-        mbar_wait_warp(bar(T_SF + sb), (it >> 1) & 1, abort_flag, stats);
+        ok &= mbar_wait_warp(bar(T_SF + sb), (it >> 1) & 1, abort_flag, stats);
         tc_fence_after();
         uint32_t s[32];
         tmem_ld32(tmem + TP_D_S + 64 * sb + 32 * ch + lanes, s);
@@ -294,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
             if (!(mine >> c & 1)) s[c] = 0xff800000u;  // -inf
           // keys that no row of the block sees may hold anything, as those past the end: their values become 0 (a
           // weight of 0 does not silence a NaN)
-          mbar_wait_one(lane == 0, bar(T_Z), masked & 1, abort_flag, stats);
+          ok &= mbar_wait_one(lane == 0, bar(T_Z), masked & 1, abort_flag, stats);
           __syncwarp();
           ++masked;
 #pragma unroll
@@ -321,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 2; ++j) l[j] = fmul2(l[j], pack2(a, a));
           if (k > k0 && __any_sync(0xffffffffu, moves)) {
-            mbar_wait_warp(bar(T_PD), (it - 1) & 1, abort_flag, stats);
+            ok &= mbar_wait_warp(bar(T_PD + 3), (it - 1) & 1, abort_flag, stats);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -334,8 +364,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
               tmem_st16(oa, o);
             }
             tmem_wait_st();
+            tc_fence_before();
           }
-          named_bar_sync(2 + g, 128);  // s_red has been read
+          // s_red has been read, and all of the rows' O is ready: any quarter's arrival may start its product
+          named_bar_sync(2 + g, 128);
+          tc_fence_after();
         }
         // weights: fp32 into the sums, rounded to bf16 (the type of V, which
         // the MMA wants of both operands) for P
@@ -349,8 +382,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
           const __nv_bfloat162 b = __floats2bfloat162_rn(e0, e1);
           x[j] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        // the weight buffer is free once the product that read it last is done
-        if (it > 0) mbar_wait_warp(bar(T_PD), (it - 1) & 1, abort_flag, stats);
+        // this part of the weight buffer is free once the product that read it last is done
+        if (it > 0) ok &= mbar_wait_warp(bar(T_PD + part), (it - 1) & 1, abort_flag, stats);
         uint8_t* row = smem + TP_OFF_P + h * TP_CHUNK + r * 128;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -359,9 +392,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (rank == 0) mbar_arrive(bar(T_PF));
-          else mbar_arrive_cluster<true>(lead_p);
+        if (lane == 0 && ok) {
+          if (rank == 0) mbar_arrive_expect_tx(bar(T_PF + part), 16);
+          else note_cluster(lead_note, sbase + TP_OFF_NOTE, lead_p);
         }
       }
       // ---- the piece's result: the row's sum, then O out of TMEM
@@ -378,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         else if (row) p.lse[im.row0 + i] = sum == 0.f ? neg_inf() : ref + log2f(sum);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      mbar_wait_warp(bar(T_PD), (it - 1) & 1, abort_flag, stats);
+      ok &= mbar_wait_warp(bar(T_PD + 3), (it - 1) & 1, abort_flag, stats);
       tc_fence_after();
       const int dim = 256 * ch + 128 * h;
 #pragma unroll 1
@@ -404,10 +437,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
             }
           }
         } else if (row) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (cut * TP_ROWS + i) * LA_DC + dim + 32 * c);
+          // [piece][dim / 4][row][4]: lanes are rows
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + (cut * (LA_DC / 4) + (dim + 32 * c) / 4) * TP_ROWS + i;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            dst[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+            dst[j * TP_ROWS] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
                                  __uint_as_float(o[4 * j + 3]));
         }
       }
@@ -441,12 +475,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
   }
 }
 
+// The call's last kernel: joins the pieces of cut items, in their order, and
+// gives the rows of items without a key their zeros.  CTA (item, 32 rows, 8 /
+// PARTS strips of 16 dims): a lane per row, a strip per warp, or, with PARTS = 8, one
+// strip of which each warp takes every eighth piece.
+constexpr int TJ_THREADS = 256;
+template <int PARTS>
+__global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnParams p) {
+  pdl_enter();
+  __shared__ float s_o[PARTS > 1 ? PARTS - 1 : 1][16][32];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
+    p.status->last = p.status->now;
+    p.status->now = 0;
+  }
+  const int w = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s0 = p.start[w], s1 = p.start[w + 1], per = *p.per;
+  const int b = w / p.blocks, R = p.next_n * p.H, r0 = w % p.blocks * TP_ROWS;
+  const int i = 32 * blockIdx.y + lane, d0 = 16 * (PARTS > 1 ? blockIdx.z : 8 * blockIdx.z + warp), part = PARTS > 1 ? warp : 0;
+  const bool row = r0 + i < R;
+  // the runs of its first and its last tile
+  const int c0 = s1 > s0 ? (s0 + p.item_units) / per : 0, n = s1 > s0 ? (s1 - 1) / per - c0 + 1 : 0;
+  if (n == 1) return;  // (its only piece wrote the result)
+  float m = neg_inf();
+  for (int j = 0; j < n; ++j) m = fmaxf(m, row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i].x : 0.f);
+  const float mm = m == neg_inf() ? 0.f : m;
+  float sum = 0.f, o[16];
+#pragma unroll
+  for (int d = 0; d < 16; ++d) o[d] = 0.f;
+#pragma unroll 2
+  for (int j = 0; j < n; ++j) {
+    const float2 ml = row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i] : make_float2(0.f, 0.f);
+    const float x = ex2(ml.x - mm);
+    sum += x * ml.y;
+    if (PARTS > 1 && j % PARTS != part) continue;
+    const int64_t piece = 2 * (int64_t)(c0 + j) + (j == 0 ? 1 : 0);
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (piece * (LA_DC / 4) + d0 / 4) * TP_ROWS + i;
+    float4 v[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = row ? __ldcs(src + d * TP_ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (ml.y != 0.f) {  // a piece without a visible key adds nothing
+        o[4 * d] += x * v[d].x;
+        o[4 * d + 1] += x * v[d].y;
+        o[4 * d + 2] += x * v[d].z;
+        o[4 * d + 3] += x * v[d].w;
+      }
+  }
+  if constexpr (PARTS > 1) {
+    if (part) {
+#pragma unroll
+      for (int d = 0; d < 16; ++d) s_o[part - 1][d][lane] = o[d];
+    }
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int j = 0; j < PARTS - 1; ++j)
+#pragma unroll
+      for (int d = 0; d < 16; ++d) o[d] += s_o[j][d][lane];
+  }
+  if (!row) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t at = (int64_t)b * R + r0 + i;
+  uint32_t y[8];
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * d] * inv, o[2 * d + 1] * inv);
+    y[d] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + at * LA_DC + d0);
+  dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (d0 == 0) p.lse[at] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+}
+
 cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {
   static DeviceFlags attr_set;
-  const cudaError_t e = set_smem_attr_once(tree_pair_kernel, TP_SMEM, attr_set);
+  cudaError_t e = set_smem_attr_once(tree_pair_kernel, TP_SMEM, attr_set);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(tree_pair_kernel, dim3(2 * p.grid), dim3(TP_THREADS), TP_SMEM, s, m, p);
+  e = launch_pdl(tree_pair_kernel, dim3(2 * p.grid), dim3(TP_THREADS), TP_SMEM, s, m, p);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  if (p.grid > 8 * p.items)  // rows of many pieces
+    return launch_pdl(tree_join_kernel<8>, dim3(p.items, 4, 32), dim3(TJ_THREADS), 0, s, p);
+  return launch_pdl(tree_join_kernel<1>, dim3(p.items, 4, 4), dim3(TJ_THREADS), 0, s, p);
 }
 
 }  // namespace dsa
