@@ -367,6 +367,11 @@ def _latent_cache(ckv, kpe):
     """(ckv, its slot stride, kpe, its slot stride), pages of a cache [P,64,512] and [P,64,64]; either
     may be part of a wider array (slots evenly spaced)."""
     pages = ckv.shape[0] if isinstance(ckv, torch.Tensor) and ckv.dim() else 0
+    if (isinstance(kpe, torch.Tensor) and ckv.is_cuda and kpe.is_cuda and ckv.dtype is kpe.dtype is _BF16 and
+            ckv.shape == (pages, 64, LATENT_DC) and kpe.shape == (pages, 64, LATENT_DP)):  # (nothing to refuse, in short)
+        (a0, a1, a2), (b0, b1, b2) = ckv.stride(), kpe.stride()
+        if a2 == b2 == 1 and a0 == 64 * a1 and b0 == 64 * b1:
+            return (ckv.data_ptr(), a1, kpe.data_ptr(), b1), pages
     cs, ks = _slot_stride(ckv, "ckv_cache", pages, LATENT_DC), _slot_stride(kpe, "kpe_cache", pages, LATENT_DP)
     return (ckv.data_ptr(), cs, kpe.data_ptr(), ks), pages
 
@@ -437,17 +442,91 @@ def latent_attention_shared_prefix(q_nope, q_pe, ckv_cache, kpe_cache, prefix_ta
     return out, lse
 
 
+def _here(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor of this shape and type on the current device."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape and
+            t.is_contiguous()):
+        return t.data_ptr()
+    raise _refusal(t, name, shape, dtype, dev)
+
+
+def _refusal(t, name, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        return ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
+    if t.dtype is not dtype:
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        return ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return ValueError(f"{name} must be contiguous")
+
+
+def _rows_here(t, name, shape, dev):
+    """The same for bf16 rows contiguous in their last axis, with the strides of the other axes."""
+    if isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is _BF16 and t.shape == shape:
+        *s, last = t.stride()
+        if last == 1:
+            return t.data_ptr(), *s
+        raise ValueError(f"{name} must be contiguous in its last axis")
+    raise _refusal(t, name, shape, _BF16, dev)
+
+
+def _current_device(t):
+    """Index of the current device; `t`: some tensor of the call (without a CUDA tensor CUDA is not asked)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("tensors must be CUDA tensors")
+    return torch._C._cuda_getDevice()
+
+
+def _pages_here(ckv, kpe, block_table, seq_lens, dev):
+    """((ckv, its slot stride, kpe, its slot stride), (block_table, seq_lens), (B, max_pages, pages))."""
+    cache, pages = _latent_cache(ckv, kpe)
+    if not ckv.get_device() == kpe.get_device() == dev:
+        raise ValueError(f"the caches must be on the current device, {dev}")
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"block_table must be [B,max_pages], got {list(shape)}")
+    return (cache, (_here(block_table, "block_table", shape, _I32, dev),
+                    _here(seq_lens, "seq_lens", shape[:1], _I32, dev)), (*shape, pages))
+
+
+def _index_cache(k_cache, k_cache_scale, pages, dev):
+    if k_cache is None and k_cache_scale is None:
+        return None, None
+    if k_cache is None or k_cache_scale is None:
+        raise ValueError("k_cache and k_cache_scale go together")
+    return (_codes_here(k_cache, "k_cache", (pages, 64, HEAD_DIM), dev),
+            _here(k_cache_scale, "k_cache_scale", (pages, 64), _F32, dev))
+
+
+def _codes_here(t, name, shape, dev):
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float8_e4m3fn:
+        return _here(t, name, shape, torch.float8_e4m3fn, dev)
+    return _here(t, name, shape, torch.uint8, dev)
+
+
 def latent_attention_tree(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_lens, tree_mask, sm_scale,
                           draft_lens=None, out=None, lse=None, stream=None):
     """latent_attention_paged for drafted tokens that form a tree: the last draft_lens[b] (int32 [B]; without it
-    next_n) of a sequence's keys are its nodes; query i sees the keys before them and node j where bit j % 64 of
-    tree_mask[b, i, j // 64] is set (int64 [B, next_n, ceil(next_n / 64)]).  Queries past draft_lens[b] are padding:
-    zeros and lse -inf."""
-    rows, queries, out, lse = _latent_queries(q_nope, q_pe, out, lse, stream)
-    cache, pages = _latent_cache(ckv_cache, kpe_cache)
-    tables, maxp = _tables(block_table, seq_lens, rows[0])
-    mask = _full(tree_mask, "tree_mask", (rows[0], rows[1], (rows[1] + 63) // 64), torch.int64)
-    drafts = None if draft_lens is None else _full(draft_lens, "draft_lens", (rows[0],), _I32)
+    next_n, or all keys if there are fewer) of a sequence's keys are its nodes; query i sees the keys before them and
+    node j where bit j % 64 of tree_mask[b, i, j // 64] is set (int64 [B, next_n, ceil(next_n / 64)]).  Queries past
+    draft_lens[b] are padding: zeros and lse -inf."""
+    dev = _current_device(q_nope)
+    cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
+    nn, H = q_nope.shape[1:3] if q_nope.dim() == 4 else (0, 0)
+    shape, rows = (B, nn, H, LATENT_DC), (B, nn, H)
+    queries = _here(q_nope, "q_nope", shape, _BF16, dev), _here(q_pe, "q_pe", (B, nn, H, LATENT_DP), _BF16, dev)
+    mask = _here(tree_mask, "tree_mask", (B, nn, (nn + 63) // 64), torch.int64, dev)
+    drafts = None if draft_lens is None else _here(draft_lens, "draft_lens", (B,), _I32, dev)
+    if out is None:
+        out = _new(shape, _BF16, q_nope.device, stream)
+    else:
+        _here(out, "out", shape, _BF16, dev)
+    if lse is None:
+        lse = _new(rows, _F32, q_nope.device, stream)
+    else:
+        _here(lse, "lse", rows, _F32, dev)
     rc = lib().dsa_latent_attention_tree(*queries, *cache, *tables, mask, drafts, *rows, maxp, pages, float(sm_scale),
                                          out.data_ptr(), lse.data_ptr(), _latent_stream(stream))
     _check("dsa_latent_attention_tree", rc)
@@ -459,29 +538,20 @@ def latent_cache_accept(ckv_cache, kpe_cache, block_table, seq_lens, draft_lens,
     """Keeps the accepted path of every sequence's drafted nodes (its last draft_lens[b] keys): node path[b, j] (int32
     [B, max_path], ascending), j < path_lens[b], moves to the j-th place behind the keys before the nodes, with the
     indexer's keys and scales if given.  Returns new_lens int32 [B], which may be seq_lens itself."""
-    cache, pages = _latent_cache(ckv_cache, kpe_cache)
-    B = block_table.shape[0]
-    tables, maxp = _tables(block_table, seq_lens, B)
-    keys = _index_cache(k_cache, k_cache_scale, pages)
-    shape = _dev(path, "path", _I32).shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError(f"path must be [{B},max_path], got {list(shape)}")
+    dev = _current_device(ckv_cache)
+    cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
+    keys = _index_cache(k_cache, k_cache_scale, pages, dev)
+    width = path.shape[-1] if path.dim() else 0
+    nodes = _here(path, "path", (B, width), _I32, dev)
     if new_lens is None:
         new_lens = _new((B,), _I32, ckv_cache.device, stream)
-    rc = lib().dsa_latent_cache_accept(*cache, *keys, *tables, _full(draft_lens, "draft_lens", (B,), _I32),
-                                       path.data_ptr(), _full(path_lens, "path_lens", (B,), _I32), B, maxp, pages,
-                                       shape[1], _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
+    else:
+        _here(new_lens, "new_lens", (B,), _I32, dev)
+    rc = lib().dsa_latent_cache_accept(*cache, *keys, *tables, _here(draft_lens, "draft_lens", (B,), _I32, dev), nodes,
+                                       _here(path_lens, "path_lens", (B,), _I32, dev), B, maxp, pages, width,
+                                       new_lens.data_ptr(), _latent_stream(stream))
     _check("dsa_latent_cache_accept", rc)
     return new_lens
-
-
-def _index_cache(k_cache, k_cache_scale, pages):
-    if (k_cache is None) != (k_cache_scale is None):
-        raise ValueError("k_cache and k_cache_scale go together")
-    if k_cache is None:
-        return None, None
-    return (_full(_u8(k_cache, "k_cache"), "k_cache", (pages, 64, HEAD_DIM), torch.uint8),
-            _full(k_cache_scale, "k_cache_scale", (pages, 64), _F32))
 
 
 _ENCODE_PAIRS, _ENCODE_HADAMARD, _ENCODE_PE_HALVES = 1, 2, 4
@@ -492,27 +562,17 @@ def _encode_flags(interleaved, hadamard, pe_interleaved):
             (0 if pe_interleaved else _ENCODE_PE_HALVES))
 
 
-def _layer_norm(norm, name):
+def _layer_norm(norm, name, dev):
     if norm is None:
         return None, None, 0.0
     weight, bias, eps = norm
-    return (_full(weight, f"{name} weight", (HEAD_DIM,), _F32), _full(bias, f"{name} bias", (HEAD_DIM,), _F32),
+    return (_here(weight, f"{name} weight", (HEAD_DIM,), _F32, dev), _here(bias, f"{name} bias", (HEAD_DIM,), _F32, dev),
             float(eps))
 
 
-def _rotation_table(cos_sin):
-    shape = _dev(cos_sin, "cos_sin", _F32).shape
-    if len(shape) != 2 or shape[1] != LATENT_DP:
-        raise ValueError(f"cos_sin must be [max_positions,64], got {list(shape)}")
-    return cos_sin.data_ptr(), shape[0]
-
-
-def _rows_of(t, name, shape):
-    """(address, strides of all axes but the last) of a bf16 tensor of this shape, contiguous in its last axis."""
-    s = _strided(t, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr(), *s[:-1]
+def _rotation_table(cos_sin, dev):
+    n = cos_sin.shape[0] if cos_sin.dim() else 0
+    return _here(cos_sin, "cos_sin", (n, LATENT_DP), _F32, dev), n
 
 
 def indexer_encode(x, cos_sin, positions, norm=None, interleaved=False, hadamard=False, pe=None, pe_interleaved=True,
@@ -523,35 +583,44 @@ def indexer_encode(x, cos_sin, positions, norm=None, interleaved=False, hadamard
     codes with one scale a token.  pe [T,H,64] bf16 are rope parts of the same tokens, rotated to pe_out (which may be
     pe).  interleaved: pairs (2 i, 2 i + 1), else (i, i + 32).  Token and head strides are the caller's.  Returns (codes
     float8_e4m3fn [T,G,128], scale fp32 [T], pe_out or None); x may be None, and codes and scale are then too."""
-    T = _dev(positions, "positions", _I32).numel()
-    table, n = _rotation_table(cos_sin)
+    dev = _current_device(positions)
+    T = positions.numel()
+    at = _here(positions, "positions", (T,), _I32, dev)
+    table, n = _rotation_table(cos_sin, dev)
     G = H = 1
-    rows, parts, out = (None, 0, 0), (None, 0, 0), (None, 0, 0)
+    rows = parts = out = (None, 0, 0)
+    to = (None, None)
     if x is not None:
-        if x.dim() != 3 or x.shape[1] not in (1, HEADS):
+        G = x.shape[1] if x.dim() == 3 else 0
+        if G != HEADS and G != 1:
             raise ValueError(f"x must be [T,64,128] or [T,1,128], got {list(x.shape)}")
-        G = x.shape[1]
-        rows = _rows_of(x, "x", (T, G, HEAD_DIM))
+        shape = (T, G, HEAD_DIM)
+        rows = _rows_here(x, "x", shape, dev)
         if codes is None:
-            codes = _new((T, G, HEAD_DIM), torch.float8_e4m3fn, x.device, stream)
+            codes = _new(shape, torch.float8_e4m3fn, x.device, stream)
+        else:
+            _codes_here(codes, "codes", shape, dev)
         if scale is None:
             scale = _new((T,), _F32, x.device, stream)
+        else:
+            _here(scale, "scale", (T,), _F32, dev)
+        to = codes.data_ptr(), scale.data_ptr()
     elif norm is not None or codes is not None or scale is not None:
         raise ValueError("norm, codes and scale go with x")
     if pe is not None:
-        if pe.dim() != 3:
-            raise ValueError(f"pe must be [T,H,64], got {list(pe.shape)}")
-        H = pe.shape[1]
-        parts = _rows_of(pe, "pe", (T, H, LATENT_DP))
+        H = pe.shape[1] if pe.dim() == 3 else 0
+        shape = (T, H, LATENT_DP)
+        parts = _rows_here(pe, "pe", shape, dev)
         if pe_out is None:
-            pe_out = _new((T, H, LATENT_DP), _BF16, pe.device, stream)
-        out = _rows_of(pe_out, "pe_out", (T, H, LATENT_DP))
+            pe_out = _new(shape, _BF16, pe.device, stream)
+            out = pe_out.data_ptr(), H * LATENT_DP, LATENT_DP
+        else:
+            out = _rows_here(pe_out, "pe_out", shape, dev)
     elif pe_out is not None:
         raise ValueError("pe_out goes with pe")
-    rc = lib().dsa_indexer_encode(*rows, G, *_layer_norm(norm, "norm"), *parts, H, table, n, positions.data_ptr(), T,
-                                  _encode_flags(interleaved, hadamard, pe_interleaved),
-                                  None if x is None else _full(_u8(codes, "codes"), "codes", (T, G, HEAD_DIM), torch.uint8),
-                                  None if x is None else _full(scale, "scale", (T,), _F32), *out, _latent_stream(stream))
+    rc = lib().dsa_indexer_encode(*rows, G, *_layer_norm(norm, "norm", dev), *parts, H, table, n, at, T,
+                                  _encode_flags(interleaved, hadamard, pe_interleaved), *to, *out,
+                                  _latent_stream(stream))
     _check("dsa_indexer_encode", rc)
     return codes, scale, pe_out
 
@@ -565,29 +634,31 @@ def latent_cache_append(c, k_pe, cos_sin, cu_new, block_table, seq_lens, ckv_cac
     [T,128] encoded as indexer_encode does (index_norm, interleaved, hadamard) into k_cache [P,64,128] and k_cache_scale
     [P,64].  positions int32 [T]: of the angles, by default a token's place in its sequence.  c_out and k_pe_out get
     what the cache gets.  Returns new_lens int32 [B], which may be seq_lens itself."""
+    dev = _current_device(c)
     T = c.shape[0]
-    rows, parts = _rows_of(c, "c", (T, LATENT_DC)), _rows_of(k_pe, "k_pe", (T, LATENT_DP))
-    cache, pages = _latent_cache(ckv_cache, kpe_cache)
-    B = block_table.shape[0]
-    tables, maxp = _tables(block_table, seq_lens, B)
-    keys = _index_cache(k_cache, k_cache_scale, pages)
+    rows, parts = _rows_here(c, "c", (T, LATENT_DC), dev), _rows_here(k_pe, "k_pe", (T, LATENT_DP), dev)
+    cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
+    keys = _index_cache(k_cache, k_cache_scale, pages, dev)
     if (index_k is None) != (k_cache is None):
         raise ValueError("index_k and k_cache go together")
     if index_k is None and index_norm is not None:
         raise ValueError("index_norm goes with index_k")
-    index = (None, 0) if index_k is None else _rows_of(index_k, "index_k", (T, HEAD_DIM))
-    weight, eps = (None, 0.0) if c_norm is None else (_full(c_norm[0], "c_norm weight", (LATENT_DC,), _F32),
+    index = (None, 0) if index_k is None else _rows_here(index_k, "index_k", (T, HEAD_DIM), dev)
+    weight, eps = (None, 0.0) if c_norm is None else (_here(c_norm[0], "c_norm weight", (LATENT_DC,), _F32, dev),
                                                       float(c_norm[1]))
-    table, n = _rotation_table(cos_sin)
+    table, n = _rotation_table(cos_sin, dev)
     if new_lens is None:
         new_lens = _new((B,), _I32, ckv_cache.device, stream)
-    rc = lib().dsa_latent_cache_append(*rows, *parts, *index, weight, eps, *_layer_norm(index_norm, "index_norm"), table,
-                                       n, None if positions is None else _full(positions, "positions", (T,), _I32),
-                                       _full(cu_new, "cu_new", (B + 1,), _I32), *tables, B, T, maxp, pages,
-                                       _encode_flags(interleaved, hadamard, pe_interleaved), *cache, *keys,
-                                       *((None, 0) if c_out is None else _rows_of(c_out, "c_out", (T, LATENT_DC))),
-                                       *((None, 0) if k_pe_out is None else _rows_of(k_pe_out, "k_pe_out", (T, LATENT_DP))),
-                                       _full(new_lens, "new_lens", (B,), _I32), _latent_stream(stream))
+    else:
+        _here(new_lens, "new_lens", (B,), _I32, dev)
+    rc = lib().dsa_latent_cache_append(
+        *rows, *parts, *index, weight, eps, *_layer_norm(index_norm, "index_norm", dev), table, n,
+        None if positions is None else _here(positions, "positions", (T,), _I32, dev),
+        _here(cu_new, "cu_new", (B + 1,), _I32, dev), *tables, B, T, maxp, pages,
+        _encode_flags(interleaved, hadamard, pe_interleaved), *cache, *keys,
+        *((None, 0) if c_out is None else _rows_here(c_out, "c_out", (T, LATENT_DC), dev)),
+        *((None, 0) if k_pe_out is None else _rows_here(k_pe_out, "k_pe_out", (T, LATENT_DP), dev)),
+        new_lens.data_ptr(), _latent_stream(stream))
     _check("dsa_latent_cache_append", rc)
     return new_lens
 

@@ -204,7 +204,7 @@ struct AppendParams {
   __nv_bfloat16 *c_out, *k_pe_out;  // [T, 512], [T, 64]: what the cache gets, or null
   int64_t c_out_stride, kp_out_stride;
   int32_t* new_lens;             // [B], may be seq_lens
-  int latent_ctas;               // CTAs that normalise latents; the rest rotate and encode
+  int row_ctas;                  // CTAs that rotate and encode; the rest normalise latents
   LatentStatus* status;
 };
 
@@ -231,7 +231,7 @@ cudaError_t launch_latent_attn(const LatentMaps& m, const LatentAttnParams& p, c
 // Trees of more than 64 rows a sequence (p.n = 128): runs of pairs of CTAs.
 cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t s);
-cudaError_t launch_encode(EncodeParams p, cudaStream_t s);
+cudaError_t launch_encode(const EncodeParams& p, cudaStream_t s);
 cudaError_t launch_append(AppendParams p, cudaStream_t s);
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t s);
 // Tensor maps of the expanded form: q [Tq, H, 192], k_nope and v [Tk, H, 128],

@@ -13,9 +13,13 @@
 // row of 128 dims lies in four lanes, lane j with dims 8 j + 32 c + e: 16-byte
 // loads whose four lanes fill two sectors, both halves of every rotated pair in
 // one lane (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and five of the
-// seven Hadamard stages as well; two are shuffles.  Values stay fp32 between the
-// loads and the one rounding at the end.
+// seven Hadamard stages as well; two are shuffles.  Values stay fp32, two to a
+// register pair for the packed arithmetic, between the loads and the one rounding
+// at the end.  CTAs stay and take every so manieth token, the next one's row on its way: with a CTA
+// for each, what starting and ending it costs (the status among it) was half the time.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "latent.h"
 
@@ -24,20 +28,22 @@ namespace dsa {
 namespace {
 constexpr int TE_THREADS = 256;
 constexpr int TE_ROWS = TE_THREADS / 4;  // rows of four lanes per CTA
+constexpr int TE_CTAS = 3;               // per SM
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&y)[8]) {
+// A lane's 32 values of a row: element 4 c + i holds dims 8 j + 32 c + 2 i and the next.
+using Row = uint64_t[16];
+
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t* y) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = __uint_as_float(u[i] << 16);
-    y[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) y[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+__device__ __forceinline__ uint4 pack8(const uint64_t* y) {
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    const float2 f = unpack2(y[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
     u[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
@@ -50,128 +56,150 @@ __device__ __forceinline__ float sum4(float x) {  // over the four lanes of a ro
 // cos and sin of lane j's eight rotated pairs: with `pairs` pair 4 j + i of
 // dims 8 j.. and pair 16 + 4 j + i of dims 32 + 8 j..; else pair 8 j + e.
 struct Angles {
-  float c[8], s[8];
+  float4 c[2], s[2];
+  // where c[0], c[1], s[0] and s[1] (i = 0 .. 3) begin
+  __device__ __forceinline__ static int at(int i, int j, bool pairs) {
+    return (i & 2 ? 32 : 0) + (pairs ? 4 * j + (i & 1 ? 16 : 0) : 8 * j + (i & 1 ? 4 : 0));
+  }
   __device__ __forceinline__ void load(const float* cs, int j, bool pairs) {
-    const int a = pairs ? 4 * j : 8 * j, b = pairs ? 16 + 4 * j : 8 * j + 4;
-    const float4 c0 = *reinterpret_cast<const float4*>(cs + a), c1 = *reinterpret_cast<const float4*>(cs + b);
-    const float4 s0 = *reinterpret_cast<const float4*>(cs + 32 + a), s1 = *reinterpret_cast<const float4*>(cs + 32 + b);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) (i & 2 ? s : c)[i & 1] = *reinterpret_cast<const float4*>(cs + at(i, j, pairs));
   }
 };
+__device__ __forceinline__ uint64_t turn_pair(uint64_t y, float c, float s) {
+  const float2 v = unpack2(y);
+  return pack2(v.x * c - v.y * s, v.x * s + v.y * c);
+}
 // Rotates dims 8 j + e (y0) and 32 + 8 j + e (y1) of a row's 64.
-__device__ __forceinline__ void rotate(float (&y0)[8], float (&y1)[8], const Angles& a, bool pairs) {
+__device__ __forceinline__ void rotate(uint64_t* y0, uint64_t* y1, const Angles& a, bool pairs) {
   if (pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = y0[2 * i], q = y0[2 * i + 1], r = y1[2 * i], s = y1[2 * i + 1];
-      y0[2 * i] = p * a.c[i] - q * a.s[i];
-      y0[2 * i + 1] = p * a.s[i] + q * a.c[i];
-      y1[2 * i] = r * a.c[4 + i] - s * a.s[4 + i];
-      y1[2 * i + 1] = r * a.s[4 + i] + s * a.c[4 + i];
+    for (int h = 0; h < 2; ++h) {
+      uint64_t* y = h ? y1 : y0;
+      y[0] = turn_pair(y[0], a.c[h].x, a.s[h].x);
+      y[1] = turn_pair(y[1], a.c[h].y, a.s[h].y);
+      y[2] = turn_pair(y[2], a.c[h].z, a.s[h].z);
+      y[3] = turn_pair(y[3], a.c[h].w, a.s[h].w);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = y0[i], q = y1[i];
-      y0[i] = p * a.c[i] - q * a.s[i];
-      y1[i] = p * a.s[i] + q * a.c[i];
+    for (int i = 0; i < 4; ++i) {
+      const float4 cc = a.c[i >> 1], ss = a.s[i >> 1];
+      const uint64_t c = i & 1 ? pack2(cc.z, cc.w) : pack2(cc.x, cc.y), s = i & 1 ? pack2(ss.z, ss.w) : pack2(ss.x, ss.y);
+      const uint64_t n = i & 1 ? pack2(-ss.z, -ss.w) : pack2(-ss.x, -ss.y);
+      const uint64_t p = y0[i], q = y1[i];
+      y0[i] = fma2(p, c, fmul2(q, n));
+      y1[i] = fma2(p, s, fmul2(q, c));
     }
   }
 }
 
-// One row's values in place; returns the lane's largest magnitude, without the Hadamard transform's factor.
-__device__ __forceinline__ float encode_values(float (&y)[4][8], const RowEncoding& o, const Angles& a, int j) {
-  if (o.norm_w) {
-    float s = 0.f;
+// max(|a|, |b|, |c|); a NaN is passed over
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// (p, q) -> (p + q, p - q)
+__device__ __forceinline__ void butterfly(uint64_t& p, uint64_t& q) {
+  const uint64_t minus = pack2(-1.f, -1.f), sum = fadd2(p, q);
+  q = fma2(q, minus, p);
+  p = sum;
+}
+
+// One row's norm and rotation in place.
+template <bool NORM>
+__device__ __forceinline__ void norm_rotate(Row& y, const RowEncoding& o, const Angles& a, int j) {
+  if constexpr (NORM) {
+    uint64_t s2 = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += y[i >> 3][i & 7];
-    const float mean = sum4(s) * (1.f / 128);
-    s = 0.f;
+    for (int i = 0; i < 16; ++i) s2 = fadd2(s2, y[i]);
+    const float2 s = unpack2(s2);
+    const float mean = sum4(s.x + s.y) * (1.f / 128);
+    const uint64_t minus = pack2(-mean, -mean);
+    uint64_t q2 = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float d = y[i >> 3][i & 7] - mean;
-      y[i >> 3][i & 7] = d;
-      s = fmaf(d, d, s);
+    for (int i = 0; i < 16; ++i) {
+      y[i] = fadd2(y[i], minus);
+      q2 = fma2(y[i], y[i], q2);
     }
-    const float r = rsqrtf(sum4(s) * (1.f / 128) + o.eps);
+    const float2 q = unpack2(q2);
+    const float r = rsqrtf(sum4(q.x + q.y) * (1.f / 128) + o.eps);
+    const uint64_t r2 = pack2(r, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = i >> 1, d = 8 * j + 32 * c + 4 * (i & 1);
+      const int d = 8 * j + 32 * (i >> 1) + 4 * (i & 1);
       const float4 w = *reinterpret_cast<const float4*>(o.norm_w + d), b = *reinterpret_cast<const float4*>(o.norm_b + d);
-      float* v = &y[c][4 * (i & 1)];
-      v[0] = fmaf(v[0] * r, w.x, b.x);
-      v[1] = fmaf(v[1] * r, w.y, b.y);
-      v[2] = fmaf(v[2] * r, w.z, b.z);
-      v[3] = fmaf(v[3] * r, w.w, b.w);
+      y[2 * i] = fma2(fmul2(y[2 * i], r2), pack2(w.x, w.y), pack2(b.x, b.y));
+      y[2 * i + 1] = fma2(fmul2(y[2 * i + 1], r2), pack2(w.z, w.w), pack2(b.z, b.w));
     }
   }
-  rotate(y[0], y[1], a, o.pairs);
-  if (o.hadamard) {
+  rotate(y, y + 4, a, o.pairs);
+}
+// Its Hadamard transform, without the factor; returns the lane's largest magnitude.
+template <bool HAD>
+__device__ __forceinline__ float transform(Row& y, int j) {
+  if constexpr (HAD) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int i = 0; i < 16; ++i) {
+      const float2 v = unpack2(y[i]);
+      y[i] = pack2(v.x + v.y, v.x - v.y);
+    }
 #pragma unroll
-      for (int h = 1; h < 8; h <<= 1)
+    for (int h = 1; h < 16; h <<= 1)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(e & h)) {
-            const float p = y[c][e], q = y[c][e | h];
-            y[c][e] = p + q;
-            y[c][e | h] = p - q;
-          }
-#pragma unroll
-    for (int h = 1; h < 4; h <<= 1)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (!(c & h))
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float p = y[c][e], q = y[c | h][e];
-            y[c][e] = p + q;
-            y[c | h][e] = p - q;
-          }
+      for (int i = 0; i < 16; ++i)
+        if (!(i & h)) butterfly(y[i], y[i | h]);
 #pragma unroll
     for (int h = 1; h < 4; h <<= 1) {
-      const float sign = j & h ? -1.f : 1.f;  // the lane of the lower dims gets the sum, the other the difference
+      // the lane of the lower dims gets the sum, the other the difference
+      const float sign = j & h ? -1.f : 1.f;
+      const uint64_t sign2 = pack2(sign, sign);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, y[i >> 3][i & 7], h);
-        y[i >> 3][i & 7] = fmaf(sign, y[i >> 3][i & 7], other);
+      for (int i = 0; i < 16; ++i) {
+        const float2 v = unpack2(y[i]);
+        const uint64_t other = pack2(__shfl_xor_sync(0xffffffffu, v.x, h), __shfl_xor_sync(0xffffffffu, v.y, h));
+        y[i] = fma2(sign2, y[i], other);
       }
     }
   }
-  float m = 0.f;
+  float m[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(y[i >> 3][i & 7]));
-  return m;
+  for (int i = 0; i < 16; ++i) {
+    const float2 v = unpack2(y[i]);
+    m[i & 1] = max_abs3(m[i & 1], v.x, v.y);
+  }
+  return fmaxf(m[0], m[1]);
 }
 
 // The scale of a token whose largest magnitude is `amax` (before the Hadamard transform's factor).
-__device__ __forceinline__ float encode_scale(float amax, const RowEncoding& o) {
-  const float s = (o.hadamard ? amax * 0.08838834764831845f : amax) * (1.f / 448);
+template <bool HAD>
+__device__ __forceinline__ float encode_scale(float amax) {
+  const float s = (HAD ? amax * 0.08838834764831845f : amax) * (1.f / 448);
   return s > 0.f ? s : 1.f;
 }
 
 // Rounds a row's values to codes, eight bytes for each of the lane's four runs of dims.
-__device__ __forceinline__ void store_codes(uint8_t* row, const float (&y)[4][8], float amax, int j) {
-  // y / (amax / 448); where the reciprocal would leave the range, by a division
-  const bool far = amax < 1e-30f;
-  const float top = amax > 0.f ? amax * (1.f / 448) : 1.f, inv = far ? 0.f : 448.f / amax;
+__device__ __forceinline__ void store_codes(uint8_t* row, Row& y, float amax, int j) {
+  if (amax < 1e-30f) {  // (448 / amax would leave the range)
+    const float top = amax > 0.f ? amax * (1.f / 448) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 v = unpack2(y[i]);
+      y[i] = pack2(v.x / top, v.y / top);
+    }
+  } else {
+    const float inv = 448.f / amax;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = fmul2(y[i], pack2(inv, inv));
+  }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    uint32_t u[2];
+    uint32_t x[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t x[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 v = make_float2(y[c][4 * h + 2 * e], y[c][4 * h + 2 * e + 1]);
-        v = far ? make_float2(v.x / top, v.y / top) : make_float2(v.x * inv, v.y * inv);
-        x[e] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-      }
-      u[h] = x[0] | x[1] << 16;
-    }
-    *reinterpret_cast<uint2*>(row + 8 * j + 32 * c) = make_uint2(u[0], u[1]);
+    for (int i = 0; i < 4; ++i) x[i] = __nv_cvt_float2_to_fp8x2(unpack2(y[4 * c + i]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(row + 8 * j + 32 * c) = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
   }
 }
 
@@ -181,7 +209,7 @@ __device__ __forceinline__ void load_pe(const __nv_bfloat16* row, int j, uint4 (
   v[1] = *reinterpret_cast<const uint4*>(row + 32 + 8 * j);
 }
 __device__ __forceinline__ void rotate_pe(const uint4 (&v)[2], const Angles& a, bool pairs, uint4 (&r)[2]) {
-  float y0[8], y1[8];
+  uint64_t y0[4], y1[4];
   unpack8(v[0], y0);
   unpack8(v[1], y1);
   rotate(y0, y1, a, pairs);
@@ -194,55 +222,73 @@ __device__ __forceinline__ void store_pe(__nv_bfloat16* row, int j, const uint4 
 }
 }  // namespace
 
-// CTAs [0, index_ctas) encode 64 rows each: with 64 rows a token one token, else 64
-// tokens.  The others rotate 64 rope rows each.
-template <int G>
-__global__ void __launch_bounds__(TE_THREADS) encode_kernel(const EncodeParams p) {
+// CTAs [0, index_ctas): a step is one token of 64 rows (G = 64) or 64 tokens of
+// one (G = 1).  The others rotate rope rows, 64 a step.
+template <int G, bool NORM, bool HAD, bool JOINT>
+__global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const EncodeParams p) {
   pdl_enter();
-  __shared__ float s_max[TE_THREADS / 32];
-  const int tid = threadIdx.x, j = tid & 3, lane = tid & 31;
+  __shared__ float s_max[2][TE_THREADS / 32];
+  constexpr int TOKENS = TE_ROWS / G;  // per step
+  const int tid = threadIdx.x, j = tid & 3, lane = tid & 31, group = tid >> 2;
   bool bad = false;
+  auto position = [&](int64_t t) {  // -1: padding, or nothing
+    const int pos = t < p.T ? p.positions[t] : -1;
+    if (pos < p.max_positions) return pos;
+    bad = true;
+    return -1;
+  };
   if (blockIdx.x < (unsigned)p.index_ctas) {
-    const int64_t row = (int64_t)blockIdx.x * TE_ROWS + (tid >> 2);
-    const int64_t t = G == 1 ? row : blockIdx.x;
-    const int g = G == 1 ? 0 : tid >> 2;
-    int pos = t < p.T ? p.positions[t] : -1;
-    if (pos >= p.max_positions) bad = true, pos = -1;
-    float y[4][8] = {};
-    Angles a = {};
-    if (pos >= 0) {
-      const __nv_bfloat16* x = p.x + t * p.x_token + g * p.x_head + 8 * j;
-      uint4 v[4];
+    const int g = G == 1 ? 0 : group;
+    const int64_t step = (int64_t)p.index_ctas * TOKENS;
+    int64_t t = (int64_t)blockIdx.x * TOKENS + (G == 1 ? group : 0);
+    int pos = position(t);
+    for (int64_t t0 = (int64_t)blockIdx.x * TOKENS, n = 0; t0 < p.T; t0 += step, t += step, ++n) {
+      uint4 v[4] = {};
+      Angles a = {};
+      if (pos >= 0) {
+        const __nv_bfloat16* x = p.x + t * p.x_token + g * p.x_head + 8 * j;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(x + 32 * c);
-      a.load(p.cos_sin + (int64_t)pos * 64, j, p.enc.pairs);
+        for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(x + 32 * c);
+        a.load(p.cos_sin + (int64_t)pos * 64, j, p.enc.pairs);
+      }
+      uint4 e[2] = {};
+      if (JOINT && pos >= 0) load_pe(p.pe + t * p.pe_token, j, e);
+      const int next = position(t + step);
+      Row y;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) unpack8(v[c], y[c]);
-    }
-    float m = encode_values(y, p.enc, a, j);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if constexpr (G > 1) {
+      for (int c = 0; c < 4; ++c) unpack8(v[c], y + 4 * c);
+      norm_rotate<NORM>(y, p.enc, a, j);
+      float m = transform<HAD>(y, j);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      if constexpr (G > 1) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) s_max[tid >> 5] = m;
-      __syncthreads();
+        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) s_max[n & 1][tid >> 5] = m;
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < TE_THREADS / 32; ++i) m = fmaxf(m, s_max[i]);
-    }
-    if (pos >= 0) {
-      store_codes(p.codes + (t * G + g) * 128, y, m, j);
-      if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale(m, p.enc);
+        for (int i = 0; i < TE_THREADS / 32; ++i) m = fmaxf(m, s_max[n & 1][i]);
+      }
+      if (JOINT && pos >= 0) {
+        if (p.pe_pairs != p.enc.pairs) a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
+        uint4 r[2];
+        rotate_pe(e, a, p.pe_pairs, r);
+        store_pe(p.pe_out + t * p.po_token, j, r);
+      }
+      if (pos >= 0) {
+        store_codes(p.codes + (t * G + g) * 128, y, m, j);
+        if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale<HAD>(m);
+      }
+      pos = next;
     }
   } else {
-    const int64_t row = ((int64_t)blockIdx.x - p.index_ctas) * TE_ROWS + (tid >> 2);
-    const int64_t t = row / p.H;
-    const int h = (int)(row % p.H);
-    int pos = t < p.T ? p.positions[t] : -1;
-    if (pos >= p.max_positions) bad = true, pos = -1;
-    if (pos >= 0) {
+    const int64_t rows = (int64_t)p.T * p.H, step = (int64_t)(gridDim.x - p.index_ctas) * TE_ROWS;
+    for (int64_t row = (int64_t)(blockIdx.x - p.index_ctas) * TE_ROWS + group; row < rows; row += step) {
+      const int64_t t = rows < (1ll << 31) ? (int)row / p.H : row / p.H;
+      const int h = (int)(row - t * p.H), pos = position(t);
       uint4 v[2], r[2];
       load_pe(p.pe + t * p.pe_token + h * p.pe_head, j, v);
+      if (pos < 0) continue;
       Angles a;
       a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
       rotate_pe(v, a, p.pe_pairs, r);
@@ -252,13 +298,26 @@ __global__ void __launch_bounds__(TE_THREADS) encode_kernel(const EncodeParams p
   last_cta(p.status, bad);
 }
 
-cudaError_t launch_encode(EncodeParams p, cudaStream_t s) {
-  p.index_ctas = !p.x ? 0 : p.G == 1 ? (p.T + TE_ROWS - 1) / TE_ROWS : p.T;
-  const int64_t pe_rows = p.pe ? (int64_t)p.T * p.H : 0;
-  const unsigned ctas = (unsigned)(p.index_ctas + (pe_rows + TE_ROWS - 1) / TE_ROWS);
+template <int G, bool NORM, bool HAD, bool JOINT>
+static cudaError_t launch_encode_as(EncodeParams p, cudaStream_t s) {
+  // both kinds of CTAs at once, in shares that end together
+  const int all = TE_CTAS * option_grid(), steps = !p.x ? 0 : G == 1 ? ceil_div(p.T, TE_ROWS) : p.T;
+  const int64_t pe_rows = p.pe && !JOINT ? (int64_t)p.T * p.H : 0, pe_steps = (pe_rows + TE_ROWS - 1) / TE_ROWS;
+  const int64_t share = 4 * (int64_t)steps + 3 * pe_steps;
+  const int pe_ctas = (int)std::min<int64_t>(pe_steps, std::max<int64_t>(pe_steps > 0, all * 3 * pe_steps / share));
+  p.index_ctas = min(steps, max(1, all - pe_ctas));
   count_launch();
-  return p.G == 1 ? launch_pdl(encode_kernel<1>, dim3(ctas), dim3(TE_THREADS), 0, s, p)
-                  : launch_pdl(encode_kernel<64>, dim3(ctas), dim3(TE_THREADS), 0, s, p);
+  return launch_pdl(encode_kernel<G, NORM, HAD, JOINT>, dim3(p.index_ctas + pe_ctas), dim3(TE_THREADS), 0, s, p);
+}
+template <int G, bool JOINT>
+static cudaError_t launch_encode_g(const EncodeParams& p, cudaStream_t s) {
+  if (p.enc.norm_w)
+    return p.enc.hadamard ? launch_encode_as<G, true, true, JOINT>(p, s) : launch_encode_as<G, true, false, JOINT>(p, s);
+  return p.enc.hadamard ? launch_encode_as<G, false, true, JOINT>(p, s) : launch_encode_as<G, false, false, JOINT>(p, s);
+}
+cudaError_t launch_encode(const EncodeParams& p, cudaStream_t s) {
+  if (p.G > 1) return launch_encode_g<64, false>(p, s);
+  return p.x && p.pe && p.H == 1 ? launch_encode_g<1, true>(p, s) : launch_encode_g<1, false>(p, s);
 }
 
 // ---------------------------------------------------------------- append --
@@ -276,7 +335,7 @@ __device__ __forceinline__ bool valid_sequence(const AppendParams& p, int b, int
   n = (int)end - first;
   return (int64_t)len + n <= (int64_t)p.max_pages * PAGE;
 }
-__device__ __forceinline__ Place place_token(const AppendParams& p, int t, bool& bad) {
+__device__ __forceinline__ Place place_token(const AppendParams& p, int64_t t, bool& bad) {
   Place r{-1, 0};
   if (t >= p.T) return r;
   int lo = 0, hi = p.B;  // the first sequence that ends behind t
@@ -287,7 +346,7 @@ __device__ __forceinline__ Place place_token(const AppendParams& p, int t, bool&
   }
   int first, n, len;
   if (lo == p.B || !valid_sequence(p, lo, first, n, len) || first > t) return r;
-  const int s = len + t - first;
+  const int s = len + (int)t - first;
   const int page = p.block_table[(int64_t)lo * p.max_pages + s / PAGE];
   r.pos = p.positions ? p.positions[t] : s;
   if (page < 0 || page >= p.num_pages || r.pos < 0 || r.pos >= p.max_positions) bad = true;
@@ -296,87 +355,92 @@ __device__ __forceinline__ Place place_token(const AppendParams& p, int t, bool&
 }
 }  // namespace
 
-// CTAs [0, latent_ctas): a warp per token normalises its latent, 16 dims per
-// lane.  The others: four lanes per token rotate the rope part and encode the
-// index key.
-__global__ void __launch_bounds__(TE_THREADS) append_kernel(const AppendParams p) {
+// CTAs [0, row_ctas): four lanes per token rotate the rope part and encode the
+// index key.  The others: a warp normalises the latents of AP_TOKENS tokens at a time, 16 dims
+// per lane, so that enough loads are in flight.
+constexpr int AP_TOKENS = 4;
+template <bool NORM, bool HAD>
+__global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const AppendParams p) {
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
-  if (blockIdx.x < (unsigned)p.latent_ctas) {
-    const int64_t t = (int64_t)blockIdx.x * (TE_THREADS / 32) + (tid >> 5);
-    if (t < p.T) {
-      uint4 v[2];
+  if (blockIdx.x >= (unsigned)p.row_ctas) {
+    const int64_t step = (int64_t)(gridDim.x - p.row_ctas) * (TE_THREADS / 32) * AP_TOKENS;
+    for (int64_t t0 = ((int64_t)(blockIdx.x - p.row_ctas) * (TE_THREADS / 32) + (tid >> 5)) * AP_TOKENS; t0 < p.T; t0 += step) {
+      uint4 v[AP_TOKENS][2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) v[k] = *reinterpret_cast<const uint4*>(p.c + t * p.c_stride + 256 * k + 8 * lane);
-      const Place at = place_token(p, (int)t, bad);
-      if (p.c_norm) {
-        float y[2][8];
-        unpack8(v[0], y[0]);
-        unpack8(v[1], y[1]);
-        float s = 0.f;
+      for (int i = 0; i < AP_TOKENS; ++i)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s = fmaf(y[i >> 3][i & 7], y[i >> 3][i & 7], s);
+        for (int k = 0; k < 2; ++k)
+          if (t0 + i < p.T) v[i][k] = *reinterpret_cast<const uint4*>(p.c + (t0 + i) * p.c_stride + 256 * k + 8 * lane);
+      int64_t slot = lane < AP_TOKENS ? place_token(p, t0 + lane, bad).slot : -1;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float r = rsqrtf(s * (1.f / LA_DC) + p.c_eps);
+      for (int i = 0; i < AP_TOKENS; ++i) {
+        const int64_t at = __shfl_sync(0xffffffffu, slot, i);
+        if (at < 0) continue;  // (the same in the whole warp)
+        if (p.c_norm) {
+          uint64_t y[8], s2 = 0;
+          unpack8(v[i][0], y);
+          unpack8(v[i][1], y + 4);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+          for (int x = 0; x < 8; ++x) s2 = fma2(y[x], y[x], s2);
+          const float2 ss = unpack2(s2);
+          float s = ss.x + ss.y;
 #pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 g = *reinterpret_cast<const float4*>(p.c_norm + 256 * k + 8 * lane + e);
-            y[k][e] *= r * g.x;
-            y[k][e + 1] *= r * g.y;
-            y[k][e + 2] *= r * g.z;
-            y[k][e + 3] *= r * g.w;
+          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          const float r = rsqrtf(s * (1.f / LA_DC) + p.c_eps);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 g = *reinterpret_cast<const float4*>(p.c_norm + 256 * (x >> 1) + 8 * lane + 4 * (x & 1));
+            y[2 * x] = fmul2(y[2 * x], fmul2(pack2(r, r), pack2(g.x, g.y)));
+            y[2 * x + 1] = fmul2(y[2 * x + 1], fmul2(pack2(r, r), pack2(g.z, g.w)));
           }
-          v[k] = pack8(y[k]);
+          v[i][0] = pack8(y);
+          v[i][1] = pack8(y + 4);
         }
-      }
-      if (at.slot >= 0) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          *reinterpret_cast<uint4*>(p.ckv + at.slot * p.ckv_stride + 256 * k + 8 * lane) = v[k];
-          if (p.c_out) *reinterpret_cast<uint4*>(p.c_out + t * p.c_out_stride + 256 * k + 8 * lane) = v[k];
+          *reinterpret_cast<uint4*>(p.ckv + at * p.ckv_stride + 256 * k + 8 * lane) = v[i][k];
+          if (p.c_out) *reinterpret_cast<uint4*>(p.c_out + (t0 + i) * p.c_out_stride + 256 * k + 8 * lane) = v[i][k];
         }
       }
     }
   } else {
-    const int64_t t = ((int64_t)blockIdx.x - p.latent_ctas) * TE_ROWS + (tid >> 2);
     const int j = tid & 3;
-    float y[4][8] = {};
-    Angles a = {};
-    uint4 e[2] = {};
-    Place at{-1, 0};
-    if (t < p.T) {
-      load_pe(p.k_pe + t * p.kp_stride, j, e);
-      uint4 v[4];
-      if (p.index_k) {
+    // (every lane takes part in the shuffles)
+    for (int64_t t0 = (int64_t)blockIdx.x * TE_ROWS; t0 < p.T; t0 += (int64_t)p.row_ctas * TE_ROWS) {
+      const int64_t t = t0 + (tid >> 2);
+      uint4 e[2] = {}, v[4] = {};
+      if (t < p.T) {
+        load_pe(p.k_pe + t * p.kp_stride, j, e);
+        if (p.index_k) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(p.index_k + t * p.ik_stride + 32 * c + 8 * j);
+          for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(p.index_k + t * p.ik_stride + 32 * c + 8 * j);
+        }
       }
-      at = place_token(p, (int)t, bad);
-      if (p.index_k) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) unpack8(v[c], y[c]);
-      }
-    }
-    const float* cs = p.cos_sin + (int64_t)at.pos * 64;
-    if (at.slot >= 0) {
-      uint4 r[2];
-      a.load(cs, j, p.pe_pairs);
-      rotate_pe(e, a, p.pe_pairs, r);
-      store_pe(p.kpe + at.slot * p.kpe_stride, j, r);
-      if (p.k_pe_out) store_pe(p.k_pe_out + t * p.kp_out_stride, j, r);
-    }
-    if (p.index_k) {
-      if (at.slot >= 0 && p.enc.pairs != p.pe_pairs) a.load(cs, j, p.enc.pairs);
-      float m = encode_values(y, p.enc, a, j);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const Place at = place_token(p, t, bad);
+      const float* cs = p.cos_sin + (int64_t)at.pos * 64;
+      Angles a = {};
       if (at.slot >= 0) {
-        store_codes(p.k_cache + at.slot * 128, y, m, j);
-        if (j == 0) p.k_scale[at.slot] = encode_scale(m, p.enc);
+        uint4 r[2];
+        a.load(cs, j, p.pe_pairs);
+        rotate_pe(e, a, p.pe_pairs, r);
+        store_pe(p.kpe + at.slot * p.kpe_stride, j, r);
+        if (p.k_pe_out) store_pe(p.k_pe_out + t * p.kp_out_stride, j, r);
+      }
+      if (p.index_k) {
+        if (at.slot >= 0 && p.enc.pairs != p.pe_pairs) a.load(cs, j, p.enc.pairs);
+        Row y;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) unpack8(v[c], y + 4 * c);
+        norm_rotate<NORM>(y, p.enc, a, j);
+        float m = transform<HAD>(y, j);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (at.slot >= 0) {
+          store_codes(p.k_cache + at.slot * 128, y, m, j);
+          if (j == 0) p.k_scale[at.slot] = encode_scale<HAD>(m);
+        }
       }
     }
   }
@@ -394,10 +458,16 @@ __global__ void __launch_bounds__(TE_THREADS) append_kernel(const AppendParams p
 }
 
 cudaError_t launch_append(AppendParams p, cudaStream_t s) {
-  p.latent_ctas = (p.T + TE_THREADS / 32 - 1) / (TE_THREADS / 32);
-  const unsigned ctas = (unsigned)(p.latent_ctas + (p.T + TE_ROWS - 1) / TE_ROWS);
+  // both kinds of CTAs at once, in shares that end together
+  const int all = TE_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS), latents = ceil_div(p.T, TE_THREADS / 32 * AP_TOKENS);
+  p.row_ctas = min(rows, max(1, all / 3));
+  const dim3 ctas(p.row_ctas + min(latents, max(1, all - p.row_ctas))), threads(TE_THREADS);
   count_launch();
-  return launch_pdl(append_kernel, dim3(ctas), dim3(TE_THREADS), 0, s, p);
+  if (p.enc.norm_w)
+    return p.enc.hadamard ? launch_pdl(append_kernel<true, true>, ctas, threads, 0, s, p)
+                          : launch_pdl(append_kernel<true, false>, ctas, threads, 0, s, p);
+  return p.enc.hadamard ? launch_pdl(append_kernel<false, true>, ctas, threads, 0, s, p)
+                        : launch_pdl(append_kernel<false, false>, ctas, threads, 0, s, p);
 }
 
 }  // namespace dsa
