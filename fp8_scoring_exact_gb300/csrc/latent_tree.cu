@@ -53,9 +53,9 @@ constexpr int T_KF = 0, T_KE = T_KF + TP_SLOTS, T_VF = T_KE + TP_SLOTS, T_RF = T
 constexpr uint32_t TP_OFF_STAT = TP_OFF_MISC + (T_BARS * 8 + 127) / 128 * 128;
 constexpr uint32_t TP_OFF_FLAG = TP_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t TP_OFF_SEEN = TP_OFF_FLAG + 16;   // [parity][warp] keys that some row of the block sees
-constexpr uint32_t TP_OFF_NOTE = TP_OFF_SEEN + 2 * 8 * 8;  // 16 bytes that the odd CTA's copies read and write
+constexpr uint32_t TP_OFF_NOTE = TP_OFF_SEEN + 2 * 8 * 8;  // [warp] 16 bytes that the odd CTA's copies read and write
 // per group of 32 rows: a masked tile's bits [row][page], then [part][row] maxima or sums
-constexpr uint32_t TP_OFF_ROW = TP_OFF_SEEN + 2 * 8 * 8 + 112;
+constexpr uint32_t TP_OFF_ROW = (TP_OFF_NOTE + 8 * 16 + 127) / 128 * 128;
 constexpr uint32_t TP_SMEM = TP_OFF_ROW + 2 * 512 + 1024;  // + alignment
 static_assert(TP_SMEM <= 227 * 1024 && sizeof(Stats) <= 128 && TP_OFF_ROW % 128 == 0, "shared memory per CTA");
 
@@ -288,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
     uint64_t* s_bits = reinterpret_cast<uint64_t*>(smem + TP_OFF_ROW + 512 * g);  // [lane][page]
     float* s_red = reinterpret_cast<float*>(smem + TP_OFF_ROW + 512 * g);         // [part][lane]
     const uint32_t lead_s = lead_bar(T_SE), lead_p = lead_bar(T_PF + part), lead_o = lead_bar(T_OE);
-    const uint32_t lead_note = cluster_addr(sbase + TP_OFF_NOTE, 0);
+    const uint32_t note = sbase + TP_OFF_NOTE + 16 * sw, lead_note = cluster_addr(note, 0);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     uint32_t masked = 0;  // masked tiles so far
     bool ok = true;
@@ -335,6 +335,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
             for (int e = tid; e < 4 * 64 * 8; e += TP_SOFTMAX)
               if (hidden >> (e >> 3 & 63) & 1) v[e] = make_uint4(0, 0, 0, 0);
           }
+          // (any 32 keys' product may start once their own warps have arrived: the others' writes are ready for it at
+          // the vote, which comes before every arrival)
+          fence_proxy_async_smem();
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -394,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         __syncwarp();
         if (lane == 0 && ok) {
           if (rank == 0) mbar_arrive_expect_tx(bar(T_PF + part), 16);
-          else note_cluster(lead_note, sbase + TP_OFF_NOTE, lead_p);
+          else note_cluster(lead_note, note, lead_p);
         }
       }
       // ---- the piece's result: the row's sum, then O out of TMEM
@@ -496,31 +499,44 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnP
   // the runs of its first and its last tile
   const int c0 = s1 > s0 ? (s0 + p.item_units) / per : 0, n = s1 > s0 ? (s1 - 1) / per - c0 + 1 : 0;
   if (n == 1) return;  // (its only piece wrote the result)
-  float m = neg_inf();
-  for (int j = 0; j < n; ++j) m = fmaxf(m, row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i].x : 0.f);
-  const float mm = m == neg_inf() ? 0.f : m;
-  float sum = 0.f, o[16];
+  // a row's maximum first where its pieces go to several warps; else the pieces in turn, rescaled as the maximum moves,
+  // so that their values are on the way together with their maxima
+  auto stats = [&](int j) { return row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i] : make_float2(neg_inf(), 0.f); };
+  float m = neg_inf(), sum = 0.f, o[16];
 #pragma unroll
   for (int d = 0; d < 16; ++d) o[d] = 0.f;
+  if constexpr (PARTS > 1) {
+    for (int j = 0; j < n; ++j) m = fmaxf(m, stats(j).x);
+  }
 #pragma unroll 2
   for (int j = 0; j < n; ++j) {
-    const float2 ml = row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i] : make_float2(0.f, 0.f);
-    const float x = ex2(ml.x - mm);
-    sum += x * ml.y;
-    if (PARTS > 1 && j % PARTS != part) continue;
+    const float2 ml = stats(j);
+    if constexpr (PARTS > 1) {
+      const float x = ml.y == 0.f ? 0.f : ex2(ml.x - m);
+      sum += x * ml.y;
+      if (j % PARTS != part) continue;
+    }
     const int64_t piece = 2 * (int64_t)(c0 + j) + (j == 0 ? 1 : 0);
     const float4* src = reinterpret_cast<const float4*>(p.part_o) + (piece * (LA_DC / 4) + d0 / 4) * TP_ROWS + i;
     float4 v[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) v[d] = row ? __ldcs(src + d * TP_ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ml.y == 0.f) continue;  // a piece without a visible key adds nothing
+    float a = 1.f;
+    if constexpr (PARTS == 1) {
+      const float top = fmaxf(m, ml.x);
+      a = ex2(m - top);  // 0 from no piece
+      m = top;
+    }
+    const float x = ex2(ml.x - m);
+    if constexpr (PARTS == 1) sum = sum * a + x * ml.y;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
-      if (ml.y != 0.f) {  // a piece without a visible key adds nothing
-        o[4 * d] += x * v[d].x;
-        o[4 * d + 1] += x * v[d].y;
-        o[4 * d + 2] += x * v[d].z;
-        o[4 * d + 3] += x * v[d].w;
-      }
+    for (int d = 0; d < 4; ++d) {
+      o[4 * d] = o[4 * d] * a + x * v[d].x;
+      o[4 * d + 1] = o[4 * d + 1] * a + x * v[d].y;
+      o[4 * d + 2] = o[4 * d + 2] * a + x * v[d].z;
+      o[4 * d + 3] = o[4 * d + 3] * a + x * v[d].w;
+    }
   }
   if constexpr (PARTS > 1) {
     if (part) {
@@ -546,7 +562,7 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnP
   uint4* dst = reinterpret_cast<uint4*>(p.out + at * LA_DC + d0);
   dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
   dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (d0 == 0) p.lse[at] = sum == 0.f ? neg_inf() : mm + log2f(sum);
+  if (d0 == 0) p.lse[at] = sum == 0.f ? neg_inf() : m + log2f(sum);
 }
 
 cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cudaStream_t s) {

@@ -182,7 +182,7 @@ __device__ __forceinline__ float encode_scale(float amax) {
 
 // Rounds a row's values to codes, eight bytes for each of the lane's four runs of dims.
 __device__ __forceinline__ void store_codes(uint8_t* row, Row& y, float amax, int j) {
-  if (amax < 1e-30f) {  // (448 / amax would leave the range)
+  if (!(amax >= 1e-30f && amax <= 1e30f)) {  // (448 / amax would leave the range, or __fdividef's)
     const float top = amax > 0.f ? amax * (1.f / 448) : 1.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -190,7 +190,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, Row& y, float amax, in
       y[i] = pack2(v.x / top, v.y / top);
     }
   } else {
-    const float inv = 448.f / amax;
+    const float inv = __fdividef(448.f, amax);
 #pragma unroll
     for (int i = 0; i < 16; ++i) y[i] = fmul2(y[i], pack2(inv, inv));
   }

@@ -101,7 +101,7 @@ def test_encode_matches_oracle(B, T, G, H, norm, had, inter, pe_inter):  # noqa:
 
 
 @pytest.mark.parametrize("G", [64, 1])
-@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e30])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e30, 3e37])
 def test_encode_ends_of_the_range(B, G, scale):  # noqa: F811
     """Scales below fp32's normal range, large ones, and a token of zeros."""
     g = torch.Generator().manual_seed(5)
