@@ -9,7 +9,8 @@
 // steps lie behind all targets of this one.
 //
 // A few keys of 1284 bytes per sequence: one CTA per sequence, one warp per key,
-// all of a step's loads in flight at once.
+// all of a step's loads in flight at once.  Bound by latency, some five dependent
+// accesses: 4 us for one sequence, 5 for 64 with trees of 64 nodes (0.8 MB).
 #include "latent.h"
 
 namespace dsa {

@@ -172,6 +172,13 @@ int run_cached(LatentAttnParams& p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.B * R;
   // the rows of a block: a prefix gathers the rows of the whole batch, so its
   // blocks are full; else the smallest block that holds a sequence's rows
+  // A tree's blocks: 128 rows of a pair of CTAs where a sequence has more than 64 rows (us in a graph; 48, 64, 80 and 128
+  // rows in blocks of 64, and by pairs):
+  //     1 sequence of 2048 keys    15  14  15  15     15  15  15  15
+  //     1 of 32768                 19  18  22  22     21  22  22  21
+  //     8 of 8192                  24  24  32  34     29  30  31  32
+  //     16 of 32768               112 107 207 197    113 114 114 116
+  //     64 of 8192                121 119 222 220    117 121 122 126
   const bool pairs = p.tree_mask && R > 64;
   p.n = pairs ? 128 : p.prefix_table || R > 32 ? 64 : R > 16 ? 32 : 16;
   p.blocks = ceil_div(R, p.n);

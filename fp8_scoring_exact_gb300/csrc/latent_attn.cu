@@ -5,7 +5,8 @@
 // + 1) of its sequence; with u_s = scale_log2 * (q_nope . ckv[s] + q_pe .
 // kpe[s]) its output is sum_s 2^(u_s - lse) ckv[s], lse = log2(sum_s 2^u_s).
 // A row that sees no key gets zeros and lse = -inf.  Of a tree of drafted tokens
-// node i sees the keys before the nodes, and the nodes that its bits name.
+// node i sees the keys before the nodes, and the nodes that its bits name (here
+// for up to 64 rows a sequence; latent_tree.cu for more).
 //
 // A key is 1152 bytes and costs a row 2176 operations, so up to about 128
 // rows a sequence the cache's bandwidth bounds the call, beyond that (a

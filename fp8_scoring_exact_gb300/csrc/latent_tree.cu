@@ -21,7 +21,22 @@
 // Warps: 0 copies K, 3 copies V (a copy takes a warp some 225 cycles to issue),
 // 1 and 2 issue S and O (even CTA), 4-11 softmax, four threads per row.  As in
 // latent_attn.cu a row's reference moves only when a logit passes it by 8, which
-// a vote of the row's four warps finds out.
+// a vote of the row's four warps finds out.  Weights are handed over and multiplied 32 keys at
+// a time, so that one buffer serves: with a barrier per tile the next tile's
+// weights waited for the product (3310 cycles a tile).  The odd CTA announces its
+// weights by a copy of 16 bytes that counts on the even one's barrier; an arrival with
+// release at cluster scope took 1500 to 4000 cycles (3300 to 4500 a tile; 2490
+// this way).
+//
+// Four sequences of up to 16384 keys, 16 nodes of 128 heads (194 GFLOP): 113 us,
+// the tensor cores 76% busy, and 10 to join the pieces; in long runs, which meet
+// the power limit, 132 in all, 1.47 PFLOP/s of the 1.70 that a library product
+// sustains.  64 sequences of up to 32768 keys, 8 nodes of 16 heads (1.31 GB, read from
+// DRAM once): 230 us, 5.7 TB/s, and 9; in long runs 262.  Prefetching the keys of the tiles
+// 1, 2, 3 or 4 ahead into the L2 made both slower (268, 275, 281, 313 for 264).
+// Seven sequences with up to 64 nodes of 16 heads (46 GFLOP): 42 and 8 us, 18
+// tiles per pair of CTAs.  In all of them the blocks of 64 rows of latent_attn.cu took 1.5
+// times as long (208, 411 and 77 us).
 #include "latent_items.cuh"
 
 namespace dsa {
@@ -478,15 +493,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
   }
 }
 
-// The call's last kernel: joins the pieces of cut items, in their order, and
+// The call's last kernel: joins the pieces of cut items, in a fixed order, and
 // gives the rows of items without a key their zeros.  CTA (item, 32 rows, 8 /
 // PARTS strips of 16 dims): a lane per row, a strip per warp, or, with PARTS = 8, one
-// strip of which each warp takes every eighth piece.
+// strip of which each warp takes every eighth piece.  A warp takes its pieces in
+// turn, rescaling as the maximum moves, so that their values are on the way together
+// with their maxima (four at a time).
 constexpr int TJ_THREADS = 256;
 template <int PARTS>
 __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnParams p) {
   pdl_enter();
-  __shared__ float s_o[PARTS > 1 ? PARTS - 1 : 1][16][32];
+  __shared__ float s_part[PARTS > 1 ? PARTS - 1 : 1][18][32];  // maximum, sum and 16 dims
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) {
     p.status->last = p.status->now;
     p.status->now = 0;
@@ -499,56 +516,54 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnP
   // the runs of its first and its last tile
   const int c0 = s1 > s0 ? (s0 + p.item_units) / per : 0, n = s1 > s0 ? (s1 - 1) / per - c0 + 1 : 0;
   if (n == 1) return;  // (its only piece wrote the result)
-  // a row's maximum first where its pieces go to several warps; else the pieces in turn, rescaled as the maximum moves,
-  // so that their values are on the way together with their maxima
-  auto stats = [&](int j) { return row ? p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i] : make_float2(neg_inf(), 0.f); };
   float m = neg_inf(), sum = 0.f, o[16];
 #pragma unroll
   for (int d = 0; d < 16; ++d) o[d] = 0.f;
-  if constexpr (PARTS > 1) {
-    for (int j = 0; j < n; ++j) m = fmaxf(m, stats(j).x);
-  }
-#pragma unroll 2
-  for (int j = 0; j < n; ++j) {
-    const float2 ml = stats(j);
-    if constexpr (PARTS > 1) {
-      const float x = ml.y == 0.f ? 0.f : ex2(ml.x - m);
-      sum += x * ml.y;
-      if (j % PARTS != part) continue;
-    }
-    const int64_t piece = 2 * (int64_t)(c0 + j) + (j == 0 ? 1 : 0);
-    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (piece * (LA_DC / 4) + d0 / 4) * TP_ROWS + i;
-    float4 v[4];
+  // adds what a piece (or another warp's pieces) has; nothing with a sum of 0, whatever its values
+  auto add = [&](float pm, float ps, const float* v) {
+    if (ps == 0.f) return;
+    const float top = fmaxf(m, pm), a = ex2(m - top), x = ex2(pm - top);  // (a = 0 from no piece)
+    m = top;
+    sum = sum * a + x * ps;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] = row ? __ldcs(src + d * TP_ROWS) : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ml.y == 0.f) continue;  // a piece without a visible key adds nothing
-    float a = 1.f;
-    if constexpr (PARTS == 1) {
-      const float top = fmaxf(m, ml.x);
-      a = ex2(m - top);  // 0 from no piece
-      m = top;
-    }
-    const float x = ex2(ml.x - m);
-    if constexpr (PARTS == 1) sum = sum * a + x * ml.y;
+    for (int d = 0; d < 16; ++d) o[d] = o[d] * a + x * v[d];
+  };
+  constexpr int BATCH = PARTS > 1 ? 4 : 2;
+  for (int j0 = part; j0 < n; j0 += BATCH * PARTS) {
+    float2 ml[BATCH];
+    float4 v[BATCH][4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      o[4 * d] = o[4 * d] * a + x * v[d].x;
-      o[4 * d + 1] = o[4 * d + 1] * a + x * v[d].y;
-      o[4 * d + 2] = o[4 * d + 2] * a + x * v[d].z;
-      o[4 * d + 3] = o[4 * d + 3] * a + x * v[d].w;
+    for (int k = 0; k < BATCH; ++k) {
+      const int j = j0 + k * PARTS;
+      if (j < n && row) {
+        const int64_t piece = 2 * (int64_t)(c0 + j) + (j == 0 ? 1 : 0);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o) + (piece * (LA_DC / 4) + d0 / 4) * TP_ROWS + i;
+        ml[k] = p.part_ml[(int64_t)(w + c0 + j) * TP_ROWS + i];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[k][d] = __ldcs(src + d * TP_ROWS);
+      } else {
+        ml[k] = make_float2(neg_inf(), 0.f);
+      }
     }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) add(ml[k].x, ml[k].y, &v[k][0].x);
   }
   if constexpr (PARTS > 1) {
     if (part) {
+      s_part[part - 1][0][lane] = m;
+      s_part[part - 1][1][lane] = sum;
 #pragma unroll
-      for (int d = 0; d < 16; ++d) s_o[part - 1][d][lane] = o[d];
+      for (int d = 0; d < 16; ++d) s_part[part - 1][2 + d][lane] = o[d];
     }
     __syncthreads();
     if (part) return;
+#pragma unroll 1
+    for (int k = 0; k < PARTS - 1; ++k) {
+      float v[16];
 #pragma unroll
-    for (int j = 0; j < PARTS - 1; ++j)
-#pragma unroll
-      for (int d = 0; d < 16; ++d) o[d] += s_o[j][d][lane];
+      for (int d = 0; d < 16; ++d) v[d] = s_part[k][2 + d][lane];
+      add(s_part[k][0][lane], s_part[k][1][lane], v);
+    }
   }
   if (!row) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -808,3 +808,19 @@ def test_a_drafted_step_as_a_server_runs_it(B):  # noqa: F811
     for b in range(nb):
         slots, scores, E = o.row_scores(b, 0)
         assert not checks.check_row(top[b, 0], slots, scores, E, K, order_key=np.arange(len(slots)))
+
+
+def test_example_runs(B):  # noqa: F811
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_tree.py")
+    spec = importlib.util.spec_from_file_location("draft_tree", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    said = []
+    lens, out, lse, chosen, status = m.main(say=said.append)
+    assert status == 0 and len(said) == 6 and all(n > p for n, p in zip(lens, (300, 61, 700)))
+    assert bool(torch.isfinite(out.float()).all()) and bool(torch.isfinite(lse).all())
+    for b, n in enumerate(lens):
+        row = chosen[b, 0].tolist()
+        assert sum(c >= 0 for c in row) == min(128, n) and len(set(c for c in row if c >= 0)) == min(128, n)
