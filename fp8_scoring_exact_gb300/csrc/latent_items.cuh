@@ -119,7 +119,7 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
   bool bad = false;
   const int pre = p.prefix_items ? valid_len(*p.prefix_len, p.prefix_pages, bad) : 0;
   if (bad) atomicOr(status, ST_RANGE);
-  int base = 0;
+  int base = 0, mine = 0, mine_end = 0;  // this thread's last item
   for (int i0 = 0; i0 < p.items; i0 += THREADS) {
     const int w = i0 + tid;
     int units = 0;
@@ -149,7 +149,9 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
       before += i < warp ? v : 0;
       all += v;
     }
-    if (w < p.items) start[w] = base + before + x - units;
+    mine = base + before + x - units;
+    mine_end = mine + units;
+    if (w < p.items) start[w] = mine;
     base += all;
   }
   const int per = max(p.item_units + 2, ceil_div(base, p.grid));
@@ -160,8 +162,12 @@ __device__ __forceinline__ Runs plan_runs(const LatentAttnParams& p, int* tmp, i
     if (blockIdx.x == 0) *p.per = per;
   }
   __syncthreads();
-  for (int w = tid; w < p.items; w += THREADS)
-    if (start[w] <= t && t < start[w + 1]) tmp[33] = w;  // one item at most
+  if (p.items <= THREADS) {  // (start[] need not be read back)
+    if (tid < p.items && mine <= t && t < mine_end) tmp[33] = tid;
+  } else {
+    for (int w = tid; w < p.items; w += THREADS)
+      if (start[w] <= t && t < start[w + 1]) tmp[33] = w;  // one item at most
+  }
   __syncthreads();
   return Runs{start, t, (int)min((int64_t)base, (int64_t)t + per), tmp[33], p.item_units};
 }

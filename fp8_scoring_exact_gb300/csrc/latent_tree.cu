@@ -32,10 +32,12 @@
 // the tensor cores 76% busy, and 10 to join the pieces; in long runs, which meet
 // the power limit, 132 in all, 1.47 PFLOP/s of the 1.70 that a library product
 // sustains.  64 sequences of up to 32768 keys, 8 nodes of 16 heads (1.31 GB, read from
-// DRAM once): 230 us, 5.7 TB/s, and 9; in long runs 262.  Prefetching the keys of the tiles
+// DRAM once): 230 us, 5.7 TB/s, and 9; in long runs 253.  Prefetching the keys of the tiles
 // 1, 2, 3 or 4 ahead into the L2 made both slower (268, 275, 281, 313 for 264).
-// Seven sequences with up to 64 nodes of 16 heads (46 GFLOP): 42 and 8 us, 18
-// tiles per pair of CTAs.  In all of them the blocks of 64 rows of latent_attn.cu took 1.5
+// Seven sequences with up to 64 nodes of 16 heads (46 GFLOP): 42 and 8 us; the 17
+// tiles of a pair of CTAs take 2200 cycles each, the way to the first logits 12000, a
+// piece's end 13000 (its masked tiles wait for values to be cleared, then the
+// last product, then 4300 for O's way out).  In all of them the blocks of 64 rows of latent_attn.cu took 1.5
 // times as long (208, 411 and 77 us).
 #include "latent_items.cuh"
 
@@ -68,9 +70,9 @@ constexpr int T_KF = 0, T_KE = T_KF + TP_SLOTS, T_VF = T_KE + TP_SLOTS, T_RF = T
 constexpr uint32_t TP_OFF_STAT = TP_OFF_MISC + (T_BARS * 8 + 127) / 128 * 128;
 constexpr uint32_t TP_OFF_FLAG = TP_OFF_STAT + 128;  // abort, TMEM base
 constexpr uint32_t TP_OFF_SEEN = TP_OFF_FLAG + 16;   // [parity][warp] keys that some row of the block sees
-constexpr uint32_t TP_OFF_NOTE = TP_OFF_SEEN + 2 * 8 * 8;  // [warp] 16 bytes that the odd CTA's copies read and write
+constexpr uint32_t TP_OFF_NOTE = TP_OFF_SEEN + 2 * 8 * 8;  // [softmax warp, O issuer] 16 bytes that note_cluster copies
 // per group of 32 rows: a masked tile's bits [row][page], then [part][row] maxima or sums
-constexpr uint32_t TP_OFF_ROW = (TP_OFF_NOTE + 8 * 16 + 127) / 128 * 128;
+constexpr uint32_t TP_OFF_ROW = (TP_OFF_NOTE + 9 * 16 + 127) / 128 * 128;
 constexpr uint32_t TP_SMEM = TP_OFF_ROW + 2 * 512 + 1024;  // + alignment
 static_assert(TP_SMEM <= 227 * 1024 && sizeof(Stats) <= 128 && TP_OFF_ROW % 128 == 0, "shared memory per CTA");
 
@@ -91,12 +93,11 @@ __device__ __forceinline__ int load_pages(const LatentAttnParams& p, const Item&
   return page;
 }
 
-// Tells a barrier of another CTA that this warp's weights are in this CTA's
-// shared memory: a copy of 16 bytes that counts on the barrier there.  It comes
-// behind the warp's fences from generic to async proxy, and its completion releases what precedes it to
-// the cluster; an arrival with release at cluster scope does so by a fence that
-// waits on all of the SM's traffic (1500 to 4000 cycles beside the copies of
-// keys).
+// Tells a barrier of another CTA what this warp has done: a copy of 16 bytes
+// that counts on the barrier there.  It comes behind the warp's fences from generic
+// to async proxy, and its completion releases what precedes it to the cluster; an
+// arrival with release at cluster scope does so by a fence that waits on all of
+// the SM's traffic (1500 to 4000 cycles beside the copies of keys).
 __device__ __forceinline__ void note_cluster(uint32_t dst, uint32_t src, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
                "r"(src), "r"(bar)
@@ -153,6 +154,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
     bool ok = true;
     while (ok && runs.next(w, k0, k1, whole)) {
       const Item im = load_item<true>(p, w);
+      bool bad = false;
+      int pages = load_pages(p, im, k0 & ~15, lane, bad);  // (on their way while the queries' copies are issued)
       if (!(ok = mbar_wait_warp(bar(T_QE), (seg & 1) ^ 1, abort_flag, stats))) break;
       if (lane == 0) {
         if (rank == 0) mbar_arrive_expect_tx(bar(T_QF), 2 * 9 * TP_CHUNK);
@@ -160,13 +163,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         tma_load_2d_pair(sbase + TP_OFF_Q + 8 * TP_CHUNK, &maps.q_pe, 0, im.row0 + 64 * rank, lead_bar(T_QF));
       }
       ++seg;
-      int pages = 0;
       for (int k = k0; ok && k < k1; ++k, ++it) {
-        if (k == k0 || (k & 15) == 0) {
-          bool bad = false;
-          pages = load_pages(p, im, k & ~15, lane, bad);
-          if (__ballot_sync(0xffffffffu, bad) && lane == 0) atomicOr(&stats->status, ST_RANGE);
-        }
+        if (k > k0 && (k & 15) == 0) pages = load_pages(p, im, k, lane, bad);
         const int slot = __shfl_sync(0xffffffffu, pages, 2 * (k & 15) + rank) * PAGE;
         if (!(ok = mbar_wait_warp(bar(T_RE), (it & 1) ^ 1, abort_flag, stats))) break;
         if (lane == 0 && !(p.withhold && it == 0)) {
@@ -181,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
           }
         }
       }
+      if (__ballot_sync(0xffffffffu, bad) && lane == 0) atomicOr(&stats->status, ST_RANGE);
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------- values --
@@ -257,7 +256,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
           if (!ok) break;
           if (leader) {  // (the lane that acquired them)
             mbar_arrive(bar(T_Z));
-            mbar_arrive_cluster<true>(cluster_addr(bar(T_Z), 1));
+            const uint32_t note = sbase + TP_OFF_NOTE + 16 * 8;
+            note_cluster(cluster_addr(note, 1), note, cluster_addr(bar(T_Z), 1));
           }
           __syncwarp();
         }
@@ -313,6 +313,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
       uint64_t l[2] = {0, 0};  // this thread's part of the row's sum, in four parts
       for (int k = k0; k < k1; ++k, ++it) {
         const uint32_t sb = it & 1;
+        const bool cut = (k + 1) * TP_KEYS > im.ctx;  // some of the tile's keys are nodes, or behind the last
+        uint64_t* seen = s_seen + 8 * (masked & 1);
+        if (cut) {
+          // Bits of the block's 128 rows, two pages, on their way while the logits are made: this CTA's are kept (a
+          // row's by a warp of the group that reads them), and all of them added up, since both CTAs' rows read the
+          // values that are cleared.
+          const int i = tid & 127, page = tid >> 7;
+          const uint64_t bits = tree_bits(p, im, im.r0 + i, 2 * k + page);
+          if (i >> 6 == rank) s_bits[2 * lane + page] = bits;
+          const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+          const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+          // (two parities: a group may come here for the next masked tile while the other still reads)
+          if (lane == 0) seen[sw] = (uint64_t)hi << 32 | lo;
+          if (rank == 1 && sw == 0 && lane == 0 && ok) mbar_arrive_expect_tx(bar(T_Z), 16);
+        }
         ok &= mbar_wait_warp(bar(T_SF + sb), (it >> 1) & 1, abort_flag, stats);
         tc_fence_after();
         uint32_t s[32];
@@ -321,17 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster<false>(lead_s + 8 * sb);
-        if ((k + 1) * TP_KEYS > im.ctx) {
-          // Bits of the block's 128 rows, two pages: this CTA's are kept (a row's by a warp of the group that reads
-          // them), and all of them added up, since both CTAs' rows read the values that are cleared.
-          const int i = tid & 127, page = tid >> 7;
-          const uint64_t bits = tree_bits(p, im, im.r0 + i, 2 * k + page);
-          if (i >> 6 == rank) s_bits[2 * lane + page] = bits;
-          const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
-          const uint32_t hi = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
-          // (two parities: a group may come here for the next masked tile while the other still reads)
-          uint64_t* seen = s_seen + 8 * (masked & 1);
-          if (lane == 0) seen[sw] = (uint64_t)hi << 32 | lo;
+        if (cut) {
           named_bar_sync(1, TP_SOFTMAX);
           const uint32_t mine = (uint32_t)(s_bits[2 * lane + h] >> (32 * ch));
 #pragma unroll
@@ -423,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
       const int i = 64 * rank + r;  // row of the block
       const bool row = i < im.nrows, node = row && im.r0 + i < im.nodes * p.H;
       if (!node) sum = 0.f;
-      const int64_t piece = (int64_t)w + pair, cut = 2 * (int64_t)pair + (k0 == 0 ? 1 : 0);
+      const int64_t piece = (int64_t)w + pair, part_at = 2 * (int64_t)pair + (k0 == 0 ? 1 : 0);
       if (part == 0) {
         if (!whole) p.part_ml[piece * TP_ROWS + i] = make_float2(sum == 0.f ? neg_inf() : ref, sum);
         else if (row) p.lse[im.row0 + i] = sum == 0.f ? neg_inf() : ref + log2f(sum);
@@ -456,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
           }
         } else if (row) {
           // [piece][dim / 4][row][4]: lanes are rows
-          float4* dst = reinterpret_cast<float4*>(p.part_o) + (cut * (LA_DC / 4) + (dim + 32 * c) / 4) * TP_ROWS + i;
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + (part_at * (LA_DC / 4) + (dim + 32 * c) / 4) * TP_ROWS + i;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             dst[j * TP_ROWS] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
