@@ -810,6 +810,138 @@ def test_a_drafted_step_as_a_server_runs_it(B):  # noqa: F811
         assert not checks.check_row(top[b, 0], slots, scores, E, K, order_key=np.arange(len(slots)))
 
 
+@pytest.fixture(params=[1, 2, 7, 40])
+def few_ctas(request, B):  # noqa: F811
+    """The kernels' CTAs limited, so that each takes many tokens, items and pieces in turn."""
+    B.set_option("grid_ctas", request.param)
+    yield request.param
+    B.set_option("grid_ctas", 0)  # the SM count again
+
+
+@pytest.mark.parametrize("G,H,T,norm,had", [(64, 16, 40, False, True), (64, 100, 21, True, True), (64, 3, 33, False, False),
+                                            (1, 1, 1500, True, True), (1, 2, 700, False, True), (1, None, 900, True, False)])
+def test_encode_by_few_ctas(B, few_ctas, G, H, T, norm, had):  # noqa: F811
+    g = torch.Generator().manual_seed(T)
+    table, x, pe = _table(), _normal(g, T, G, 128), None if H is None else _normal(g, T, H, 64)
+    pos = torch.randint(-MAXPOS // 4, MAXPOS, (T,), generator=g, dtype=torch.int32)  # some are padding
+    nm = _norm(g) if norm else None
+    codes, scale = torch.zeros((T, G, 128), dtype=torch.uint8, device="cuda"), torch.full((T,), -1.0, device="cuda")
+    out = None if H is None else torch.full((T, H, 64), 5.0, dtype=BF16, device="cuda")
+    B.indexer_encode(x.cuda(), table.cuda(), pos.cuda(), norm=None if nm is None else (nm[0].cuda(), nm[1].cuda(), nm[2]),
+                     hadamard=had, pe=None if H is None else pe.cuda(), codes=codes, scale=scale, pe_out=out)
+    assert B.latent_last_status() == 0
+    keep = (pos >= 0).numpy()
+    kd = torch.from_numpy(keep).cuda()
+    cs = _np(table)[pos.numpy()[keep]]
+    y, reach = te.index_rows(_np(x)[keep], cs, _np_norm(nm), False, had)
+    check_codes(codes[kd], scale[kd], y, reach)
+    assert torch.all(codes[~kd] == 0) and torch.all(scale[~kd] == -1.0)
+    if H is not None:
+        check_rope(out[kd], _np(pe)[keep], cs[:, None], True)
+        assert torch.all(out[~kd] == 5.0)
+
+
+@pytest.mark.parametrize("index", [False, True])
+def test_append_by_few_ctas(B, few_ctas, index):  # noqa: F811
+    g = torch.Generator().manual_seed(70)
+    new, lens, table = [130, 0, 1, 600, 33, 64], [3, 9, 63, 0, 200, 64], _table()
+    T = sum(new) + 5
+    p = Pages([a + b for a, b in zip(new, lens)], seed=71, joint=index)
+    c, k_pe = _tokens(g, T)
+    cu, cn, nm, ix = np.concatenate([[0], np.cumsum(new)]), (torch.rand(512, generator=g), 1e-6), _norm(g), _normal(g, T, 128)
+    dl = _ints(lens)
+    B.latent_cache_append(c.cuda().contiguous(), k_pe.cuda().contiguous(), table.cuda(), _ints(cu), p.table.cuda(), dl, p.ckv,
+                          p.kpe, c_norm=(cn[0].cuda(), cn[1]), index_k=ix.cuda() if index else None,
+                          index_norm=(nm[0].cuda(), nm[1].cuda(), nm[2]) if index else None, hadamard=index,
+                          k_cache=p.kc if index else None, k_cache_scale=p.ks if index else None, new_lens=dl)
+    assert B.latent_last_status() == 0 and dl.tolist() == [a + b for a, b in zip(new, lens)]
+    check_appended(p, cu, lens, c, k_pe, table, cn, index=(ix, nm, False, True) if index else None)
+
+
+@pytest.mark.parametrize("nn,H,seqs", [
+    (8, 16, [(1500, 8), (9, 8), (130, 3), (0, 0), (700, 8), (64, 8)]), (20, 16, [(300, 20), (2000, 11), (20, 20), (128, 1)]),
+    (65, 3, [(500, 65), (65, 65), (190, 64)]), (3, 16, [(400, 3), (2, 2), (65, 3)])])
+def test_tree_by_few_ctas(B, few_ctas, nn, H, seqs):  # noqa: F811
+    """Runs of many items and pieces: whole items, cut ones, and ones that start and end in a run."""
+    rng = np.random.default_rng(few_ctas + nn)
+    lens, drafts = [a for a, _ in seqs], [n for _, n in seqs]
+    c = Cache(lens, seed=nn)
+    seen = [_seen_of(_random_tree(rng, n)) for n in drafts]
+    qn, qp = _queries(len(lens), nn, H, seed=H)
+    for b, n in enumerate(drafts):
+        qn[b, n:] = float("nan")
+    out, lse = _tree(B, c, qn, qp, _mask(seen, nn), drafts)
+    assert B.latent_last_status() == 0
+    _check_tree(c, qn, qp, out, lse, seen)
+
+
+def test_binding_refuses_what_does_not_fit(B):  # noqa: F811
+    """Wrong types, shapes, strides and combinations: an exception, and nothing is written."""
+    def z(*shape, dtype=BF16):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    i32 = dict(dtype=torch.int32)
+    table, pos = z(100, 64, dtype=torch.float32), z(4, **i32)
+    x, pe = z(4, 64, 128), z(4, 16, 64)
+    norm = z(128, dtype=torch.float32), z(128, dtype=torch.float32), 1e-6
+    ckv, kpe, kc, ks = z(3, 64, 512), z(3, 64, 64), z(3, 64, 128, dtype=torch.uint8), z(3, 64, dtype=torch.float32)
+    bt, lens, cu = z(2, 2, **i32), z(2, **i32), z(3, **i32)
+    c, kp, ik = z(4, 512), z(4, 64), z(4, 128)
+    cn = z(512, dtype=torch.float32), 1e-6
+    qn, qp, mask = z(2, 3, 16, 512), z(2, 3, 16, 64), z(2, 3, 1, dtype=torch.int64)
+    path, n2 = z(2, 5, **i32), z(2, **i32)
+    bad = [
+        lambda: B.indexer_encode(z(4, 2, 128), table, pos), lambda: B.indexer_encode(z(5, 64, 128), table, pos),
+        lambda: B.indexer_encode(x.float(), table, pos), lambda: B.indexer_encode(x, table.double(), pos),
+        lambda: B.indexer_encode(x, z(100, 32, dtype=torch.float32), pos), lambda: B.indexer_encode(x, table, pos.long()),
+        lambda: B.indexer_encode(x, table, pos, norm=(norm[0][:64], norm[1], 1e-6)),
+        lambda: B.indexer_encode(x, table, pos, norm=(norm[0], norm[1], -1.0)),
+        lambda: B.indexer_encode(None, table, pos), lambda: B.indexer_encode(None, table, pos, pe=pe, norm=norm),
+        lambda: B.indexer_encode(x, table, pos, pe_out=pe), lambda: B.indexer_encode(x, table, pos, pe=pe[..., :32]),
+        lambda: B.indexer_encode(x, table, pos, pe=z(4, 16, 128)[..., ::2]),
+        lambda: B.indexer_encode(x, table, pos, pe=z(4, 16, 68)[..., :64]),       # head stride no multiple of 8
+        lambda: B.indexer_encode(x, table, pos, pe=z(4, 1, 64).expand(4, 16, 64)),  # head stride 0
+        lambda: B.indexer_encode(x, table, pos, pe=z(4, 16, 72)[..., 4:68]),       # not 16-byte aligned
+        lambda: B.indexer_encode(x, table, pos, codes=z(4, 64, 64, dtype=torch.uint8)),
+        lambda: B.indexer_encode(x, table, pos, scale=z(5, dtype=torch.float32)),
+        lambda: B.indexer_encode(x[:0], table, pos[:0]), lambda: B.indexer_encode(x.cpu(), table, pos),
+        lambda: B.latent_cache_append(c, kp[:3], table, cu, bt, lens, ckv, kpe),
+        lambda: B.latent_cache_append(c, kp, table, cu[:2], bt, lens, ckv, kpe),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens[:1], ckv, kpe),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv[:2], kpe),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, index_k=ik),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, k_cache=kc, k_cache_scale=ks),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, index_k=ik, k_cache=kc),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, index_norm=norm),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, c_norm=(cn[0][:128], 1e-6)),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, positions=pos[:3]),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, c_out=z(4, 576)),
+        lambda: B.latent_cache_append(c, kp, table, cu, bt, lens, ckv, kpe, new_lens=z(3, **i32)),
+        lambda: B.latent_cache_append(z(1, 512).expand(4, 512), kp, table, cu, bt, lens, ckv, kpe),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt, lens, z(2, 3, 2, dtype=torch.int64), SCALE),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt, lens, mask.int(), SCALE),
+        lambda: B.latent_attention_tree(qn, qp[:, :2], ckv, kpe, bt, lens, mask, SCALE),
+        lambda: B.latent_attention_tree(qn[0], qp, ckv, kpe, bt, lens, mask, SCALE),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt[:1], lens, mask, SCALE),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt, lens, mask, 0.0),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt, lens, mask, SCALE, draft_lens=n2[:1]),
+        lambda: B.latent_attention_tree(qn, qp, ckv, kpe, bt, lens, mask, SCALE, out=qn.float()),
+        lambda: B.latent_attention_tree(qn.transpose(1, 2), qp, ckv, kpe, bt, lens, mask, SCALE),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path[0], n2),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path[:, :0], n2),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path.long(), n2),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2[:1], path, n2),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path, n2, k_cache=kc),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path, n2, k_cache=kc[:2], k_cache_scale=ks),
+        lambda: B.latent_cache_accept(ckv, kpe, bt, lens, n2, path.t(), n2)]
+    before = B.launch_count()
+    for k, call in enumerate(bad):
+        with pytest.raises((TypeError, ValueError, B.IndexerError)):
+            call()
+            pytest.fail(f"call {k} was taken")
+    assert B.launch_count() == before
+
+
 def test_example_runs(B):  # noqa: F811
     import importlib.util
     import os
