@@ -32,7 +32,7 @@
 // the tensor cores 76% busy, and 10 to join the pieces; in long runs, which meet
 // the power limit, 132 in all, 1.47 PFLOP/s of the 1.70 that a library product
 // sustains.  64 sequences of up to 32768 keys, 8 nodes of 16 heads (1.31 GB, read from
-// DRAM once): 230 us, 5.7 TB/s, and 9; in long runs 253.  Prefetching the keys of the tiles
+// DRAM once): 230 us, 5.7 TB/s, and 9; in long runs 253 to 265.  Prefetching the keys of the tiles
 // 1, 2, 3 or 4 ahead into the L2 made both slower (268, 275, 281, 313 for 264).
 // Seven sequences with up to 64 nodes of 16 heads (46 GFLOP): 42 and 8 us; the 17
 // tiles of a pair of CTAs take 2200 cycles each, the way to the first logits 12000, a
@@ -128,7 +128,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TP_THREADS, 1)
     tma_prefetch_desc(&maps.q_pe);
     tma_prefetch_desc(&maps.ckv);
     tma_prefetch_desc(&maps.kpe);
-    for (int i = 0; i < T_BARS; ++i) mbar_init(bar(i), i == T_SE || i == T_SE + 1 || i == T_OE ? 16 : i >= T_PF && i < T_PD ? 2 : 1);
+    for (int i = 0; i < T_BARS; ++i)
+      mbar_init(bar(i), i == T_SE || i == T_SE + 1 || i == T_OE ? 16 : i >= T_PF && i < T_PD ? 2 : 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -516,7 +517,8 @@ __global__ void __launch_bounds__(TJ_THREADS) tree_join_kernel(const LatentAttnP
   const int w = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s0 = p.start[w], s1 = p.start[w + 1], per = *p.per;
   const int b = w / p.blocks, R = p.next_n * p.H, r0 = w % p.blocks * TP_ROWS;
-  const int i = 32 * blockIdx.y + lane, d0 = 16 * (PARTS > 1 ? blockIdx.z : 8 * blockIdx.z + warp), part = PARTS > 1 ? warp : 0;
+  const int i = 32 * blockIdx.y + lane, part = PARTS > 1 ? warp : 0;
+  const int d0 = 16 * (PARTS > 1 ? blockIdx.z : 8 * blockIdx.z + warp);
   const bool row = r0 + i < R;
   // the runs of its first and its last tile
   const int c0 = s1 > s0 ? (s0 + p.item_units) / per : 0, n = s1 > s0 ? (s1 - 1) / per - c0 + 1 : 0;

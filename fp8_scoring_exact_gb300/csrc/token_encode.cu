@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
   bool bad = false;
   if (blockIdx.x >= (unsigned)p.row_ctas) {
     const int64_t step = (int64_t)(gridDim.x - p.row_ctas) * (TE_THREADS / 32) * AP_TOKENS;
-    for (int64_t t0 = ((int64_t)(blockIdx.x - p.row_ctas) * (TE_THREADS / 32) + (tid >> 5)) * AP_TOKENS; t0 < p.T; t0 += step) {
+    const int64_t first = ((int64_t)(blockIdx.x - p.row_ctas) * (TE_THREADS / 32) + (tid >> 5)) * AP_TOKENS;
+    for (int64_t t0 = first; t0 < p.T; t0 += step) {
       uint4 v[AP_TOKENS][2];
 #pragma unroll
       for (int i = 0; i < AP_TOKENS; ++i)
@@ -469,7 +470,8 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
 
 cudaError_t launch_append(AppendParams p, cudaStream_t s) {
   // both kinds of CTAs at once, in shares that end together
-  const int all = TE_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS), latents = ceil_div(p.T, TE_THREADS / 32 * AP_TOKENS);
+  const int all = TE_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS);
+  const int latents = ceil_div(p.T, TE_THREADS / 32 * AP_TOKENS);
   p.row_ctas = min(rows, max(1, all / 3));
   const dim3 ctas(p.row_ctas + min(latents, max(1, all - p.row_ctas))), threads(TE_THREADS);
   count_launch();
