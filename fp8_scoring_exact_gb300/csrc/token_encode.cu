@@ -183,21 +183,27 @@ __device__ __forceinline__ float transform(Row& y, int j) {
   return fmaxf(m[0], m[1]);
 }
 
-// The scale of a token whose largest magnitude is `amax` (before the Hadamard transform's factor).
+// The Hadamard transform's factor, 1 / sqrt(128).
+template <bool HAD>
+constexpr float FACTOR = HAD ? 0.08838834764831845f : 1.f;
+
+// The scale of a token whose largest magnitude is `amax` (before the factor); 1 where it is 0, or rounds to it.
 template <bool HAD>
 __device__ __forceinline__ float encode_scale(float amax) {
-  const float s = (HAD ? amax * 0.08838834764831845f : amax) * (1.f / 448);
+  const float s = amax * FACTOR<HAD> * (1.f / 448);
   return s > 0.f ? s : 1.f;
 }
 
 // Rounds a row's values to codes, eight bytes for each of the lane's four runs of dims.
+template <bool HAD>
 __device__ __forceinline__ void store_codes(uint8_t* row, Row& y, float amax, int j) {
-  if (!(amax >= 1e-30f && amax <= 1e30f)) {  // (448 / amax would leave the range, or __fdividef's)
-    const float top = amax > 0.f ? amax * (1.f / 448) : 1.f;
+  if (!(amax >= 1e-30f && amax <= 1e30f)) {
+    // 448 / amax would leave the range, or __fdividef's; and below it a scale has few bits, or is 1
+    const float top = encode_scale<HAD>(amax);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float2 v = unpack2(y[i]);
-      y[i] = pack2(v.x / top, v.y / top);
+      y[i] = pack2(v.x * FACTOR<HAD> / top, v.y * FACTOR<HAD> / top);
     }
   } else {
     const float inv = __fdividef(448.f, amax);
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const Encod
         store_pe(p.pe_out + t * p.po_token, j, r);
       }
       if (pos >= 0) {
-        store_codes(p.codes + (t * G + g) * 128, y, m, j);
+        store_codes<HAD>(p.codes + (t * G + g) * 128, y, m, j);
         if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale<HAD>(m);
       }
       pos = next;
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         if (at.slot >= 0) {
-          store_codes(p.k_cache + at.slot * 128, y, m, j);
+          store_codes<HAD>(p.k_cache + at.slot * 128, y, m, j);
           if (j == 0) p.k_scale[at.slot] = encode_scale<HAD>(m);
         }
       }

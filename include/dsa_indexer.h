@@ -338,8 +338,9 @@ DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uin
  * keys before the nodes and node j where bit j % 64 of tree_mask[b, i, j / 64] is
  * set (its ancestors and itself, or whatever is wanted); otherwise as
  * dsa_latent_attention_paged.  A node that no query sees may hold anything.
- * Queries i >= draft_lens[b] are padding: their rows get zeros and lse = -inf.  A number of nodes below 0, above next_n or above
- * seq_lens[b] is DSA_ERR_RANGE, and the sequence counts as empty.
+ * Queries i >= draft_lens[b] are padding: their rows get zeros and lse = -inf.
+ * A number of nodes below 0, above next_n or above seq_lens[b] is DSA_ERR_RANGE,
+ * and the sequence counts as empty.
  *
  *   tree_mask [B, next_n, ceil(next_n / 64)] uint64, 8-byte aligned   draft_lens [B] int32 or null
  */
@@ -386,13 +387,14 @@ typedef enum {
  *     y[g] = (x[t, g] - mean) / sqrt(var + norm_eps) * norm_weight + norm_bias   over its 128 dims (null: y = x)
  *     pair i of dims [0, 64): (a, b) -> (a cos_i - b sin_i, a sin_i + b cos_i)
  *     y[g] = H y[g] / sqrt(128), H[d, e] = (-1)^popcount(d & e)   (with DSA_ENCODE_HADAMARD)
- *     scale[t] = max over g, d of |y| / 448, or 1 where all are 0;   codes[t, g] = e4m3(y / scale[t])
+ *     scale[t] = max over g, d of |y| / 448, or 1 where that is 0;   codes[t, g] = e4m3(y / scale[t])
  *
  * in fp32 with one rounding, to nearest even.  The rope parts pe[t, h] (64 dims)
  * turn by the same angles and are rounded to bf16.  A token whose position is
  * negative is padding, and one at or past max_positions is DSA_ERR_RANGE
- * (dsa_latent_last_status): their outputs stay as they were.  x must be finite; a
- * token with an infinity or NaN has undefined codes and scale.
+ * (dsa_latent_last_status): their outputs stay as they were.  x must be finite, and
+ * y below 2^120 in magnitude before a Hadamard transform; a token with more, an
+ * infinity or NaN has undefined codes and scale.
  *
  *   x [T, G, 128] bf16, G = 64 or 1, or null        codes [T, G, 128] e4m3   scale [T] fp32
  *   pe [T, H, 64] bf16, or null                     pe_out [T, H, 64] bf16 (may be pe, with its strides)

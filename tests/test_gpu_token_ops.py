@@ -127,6 +127,35 @@ def test_encode_ends_of_the_range(B, G, scale):  # noqa: F811
     assert got[4, -1, 127] == 448
 
 
+@pytest.mark.parametrize("had", [False, True])
+@pytest.mark.parametrize("G", [64, 1])
+@pytest.mark.parametrize("steps", [3, 50, 100, 3000, 10 ** 6])
+def test_encode_scales_of_few_bits(B, G, steps, had):  # noqa: F811
+    """Values of some `steps` of 2^-149, by a norm's weights: a scale that rounds to 0 is 1, and the codes are of the
+    scale that is stored."""
+    g, step, T = torch.Generator().manual_seed(steps), 2.0 ** -149, 70
+    x, pos, table = _normal(g, T, G, 128), torch.arange(T, dtype=torch.int32), _table()
+    nm = torch.full((128,), steps * step, dtype=torch.float64).float(), torch.zeros(128), 1e-6
+    assert float(nm[0][0]) == steps * step
+    codes, s, _ = B.indexer_encode(x.cuda(), table.cuda(), pos.cuda(), norm=(nm[0].cuda(), nm[1].cuda(), nm[2]),
+                                   hadamard=had)
+    y, reach = te.index_rows(_np(x), _np(table)[:T], _np_norm(nm), False, had)
+    got, s = te.values(codes.view(torch.uint8).cpu().numpy()), _np(s)
+    # a normalised value is off by half a step and turned to half of sqrt(2), each of a rotation's two products by half:
+    # below 2; the transform adds 128 of those and multiplies by 1 / sqrt(128), and rounds: below 24
+    off = (24 if had else 2) * step + VALUE * reach
+    assert np.all(np.abs(np.where(s == 1, 0, s) - _top(y)) <= step / 2 + off.max((1, 2)) / 448 + 2.0 ** -22 * _top(y))
+    assert np.all(got[s == 1] == 0)
+    s = np.where(s == 1, 0, s)[:, None, None]
+    # a code is off by 2^-4 or 2^-10 of the scale; a scale by half a step, which 448 times is what is cut off at most
+    tol = np.maximum(2.0 ** -4 * (np.abs(y) + off), 2.0 ** -10 * s) + off + 224 * step + off.max((1, 2), keepdims=True)
+    assert np.all(np.abs(got * s - y) <= tol)
+
+
+def _top(y):
+    return np.abs(y).max((1, 2)) / 448
+
+
 @pytest.mark.parametrize("G", [64, 1])
 def test_encode_padding_strides_and_in_place(B, G):  # noqa: F811
     """Positions below 0 are padding, at or past the table's end an error: outputs stay as they were.  Rows are parts of
