@@ -10,23 +10,25 @@
 // cache slot, behind the block table.
 //
 // What it cannot do without are bytes: a query token reads 16 KB and writes 8 KB.  A
-// row of 128 dims lies in four lanes, lane j with dims 8 j + 32 c + e: 16-byte
-// loads whose four lanes fill two sectors, both halves of every rotated pair in
-// one lane (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and five of the
-// seven Hadamard stages as well; two are shuffles.  Values stay fp32, two to a
+// row of 128 dims lies in L lanes, lane j with dims 32 / L j + 32 c + e: 16-byte
+// loads that fill whole sectors, both halves of every rotated pair in
+// one lane (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and the
+// Hadamard stages but log2 L as well, which are shuffles.  The 64 rows of a query
+// token take two lanes each, which halves the shuffles (4096 tokens 30.3 us, 32.0 with
+// four), single rows four (131072 keys 28.6 us; 42 with two, whose norm and rope part spill).
+// Values stay fp32, two to a
 // register pair for the packed arithmetic, between the loads and the one rounding
 // at the end.  CTAs stay and take every so manieth token: with a CTA for each, what
 // starting and ending it costs (the status among it) was a third of the time.
 //
-// 4096 query tokens with 16 rope rows each (118 MB): 32 us, 3.7 TB/s; the index
-// rows alone 28, without the Hadamard transform 21, which is the memory's pace and a start of
-// 4 us.  The transform's 470 instructions per warp and token do not hide behind
-// it: the issue slots are 38% used, the shared-memory path (shuffles) 54%, and a
-// fourth CTA per SM changed nothing.  Slower or no faster were: rows fetched ahead by
-// cp.async (30.8 us), the exchange of the last two stages through shared memory
-// (32.3), those stages on mma.sync with values in three bf16 parts (27.3).
-// 131072 keys with norm and rope part (118 MB): 31 us; 16384 tokens appended (48
-// MB): 14 us.
+// On the device, in a graph: 4096 query tokens with 16 rope rows each (118 MB) 30.3 us,
+// 3.9 TB/s; the index rows alone 27.0, without the Hadamard transform 21.9, the rope
+// rows alone 7.7.  CTAs per SM: three 33.7, five 32.3; a rope row counted as 2, 4 or 6
+// quarters of an index row instead of 3: 31.9, 32.4, 34.4.  Slower were also: the next token's
+// rows in registers (33.8), rows fetched ahead by cp.async, the exchange of the last stages through shared
+// memory; those stages on mma.sync with values in three bf16 parts gained 3%.
+// 131072 keys with norm and rope part (118 MB): 28.6 us; the index rows alone 21.4, 16.5 without
+// the norm, 13.7 without both.  16384 tokens appended (48 MB): 14 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -36,12 +38,34 @@
 namespace dsa {
 
 namespace {
-constexpr int TE_THREADS = 256;
-constexpr int TE_ROWS = TE_THREADS / 4;  // rows of four lanes per CTA
-constexpr int TE_CTAS = 3;               // per SM
+constexpr int TE_ROWS = 64;  // per CTA
+// Lanes of a row of encode_kernel, the threads of a CTA and the CTAs per SM.
+template <int G>
+constexpr int LANES = G > 1 ? 2 : 4;
+template <int G>
+constexpr int THREADS = TE_ROWS * LANES<G>;
+template <int G>
+constexpr int CTAS = G > 1 ? 4 : 3;
 
-// A lane's 32 values of a row: element 4 c + i holds dims 8 j + 32 c + 2 i and the next.
-using Row = uint64_t[16];
+// A lane's values of a row, of L lanes: element (16 / L) c + i holds dims (32 / L) j + 32 c + 2 i and the next.
+template <int L>
+using Row = uint64_t[64 / L];
+
+// Where a lane's `n`-th 16 bytes of bf16 begin.
+template <int L>
+__device__ __forceinline__ int dim8(int n, int j) {
+  return 32 * (n / (4 / L)) + 8 * (n % (4 / L)) + 32 / L * j;
+}
+template <int L, int N>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* row, int j, uint4 (&v)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = *reinterpret_cast<const uint4*>(row + dim8<L>(n, j));
+}
+template <int L, int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int j, const uint4 (&v)[N]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) *reinterpret_cast<uint4*>(row + dim8<L>(n, j)) = v[n];
+}
 
 __device__ __forceinline__ void unpack8(const uint4& v, uint64_t* y) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -58,34 +82,44 @@ __device__ __forceinline__ uint4 pack8(const uint64_t* y) {
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ float sum4(float x) {  // over the four lanes of a row
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+template <int L>
+__device__ __forceinline__ float sum_row(float x) {
+#pragma unroll
+  for (int h = 1; h < L; h <<= 1) x += __shfl_xor_sync(0xffffffffu, x, h);
+  return x;
+}
+template <int N>
+__device__ __forceinline__ float max_lanes(float x) {  // over every N lanes
+#pragma unroll
+  for (int h = 1; h < N; h <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, h));
+  return x;
 }
 
-// cos and sin of lane j's eight rotated pairs: with `pairs` pair 4 j + i of
-// dims 8 j.. and pair 16 + 4 j + i of dims 32 + 8 j..; else pair 8 j + e.
+// cos and sin of lane j's 32 / L rotated pairs: with `pairs` those from 16 / L j on,
+// of its dims below 32, and from 16 + 16 / L j on, of the others; else those from 32 / L j on.
+template <int L>
 struct Angles {
-  float4 c[2], s[2];
-  // where c[0], c[1], s[0] and s[1] (i = 0 .. 3) begin
-  __device__ __forceinline__ static int at(int i, int j, bool pairs) {
-    return (i & 2 ? 32 : 0) + (pairs ? 4 * j + (i & 1 ? 16 : 0) : 8 * j + (i & 1 ? 4 : 0));
-  }
+  static constexpr int HALF = 4 / L;  // of them, in fours, in dims below 32
+  float4 c[2 * HALF], s[2 * HALF];
   __device__ __forceinline__ void load(const float* cs, int j, bool pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) (i & 2 ? s : c)[i & 1] = *reinterpret_cast<const float4*>(cs + at(i, j, pairs));
+    for (int i = 0; i < 2 * HALF; ++i) {
+      const int at = 4 * i + (pairs ? 4 * HALF * j + (i < HALF ? 0 : 16 - 4 * HALF) : 8 * HALF * j);
+      c[i] = *reinterpret_cast<const float4*>(cs + at);
+      s[i] = *reinterpret_cast<const float4*>(cs + 32 + at);
+    }
   }
 };
 __device__ __forceinline__ uint64_t turn_pair(uint64_t y, float c, float s) {
   const float2 v = unpack2(y);
   return pack2(v.x * c - v.y * s, v.x * s + v.y * c);
 }
-// Rotates dims 8 j + e (y0) and 32 + 8 j + e (y1) of a row's 64.
-__device__ __forceinline__ void rotate(uint64_t* y0, uint64_t* y1, const Angles& a, bool pairs) {
+// Rotates a lane's dims below 64.
+template <int L>
+__device__ __forceinline__ void rotate(uint64_t* y, const Angles<L>& a, bool pairs) {
   if (pairs) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint64_t* y = h ? y1 : y0;
+    for (int h = 0; h < 8 / L; ++h, y += 4) {
       y[0] = turn_pair(y[0], a.c[h].x, a.s[h].x);
       y[1] = turn_pair(y[1], a.c[h].y, a.s[h].y);
       y[2] = turn_pair(y[2], a.c[h].z, a.s[h].z);
@@ -93,13 +127,13 @@ __device__ __forceinline__ void rotate(uint64_t* y0, uint64_t* y1, const Angles&
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 16 / L; ++i) {
       const float4 cc = a.c[i >> 1], ss = a.s[i >> 1];
       const uint64_t c = i & 1 ? pack2(cc.z, cc.w) : pack2(cc.x, cc.y), s = i & 1 ? pack2(ss.z, ss.w) : pack2(ss.x, ss.y);
       const uint64_t n = i & 1 ? pack2(-ss.z, -ss.w) : pack2(-ss.x, -ss.y);
-      const uint64_t p = y0[i], q = y1[i];
-      y0[i] = fma2(p, c, fmul2(q, n));
-      y1[i] = fma2(p, s, fmul2(q, c));
+      const uint64_t p = y[i], q = y[16 / L + i];
+      y[i] = fma2(p, c, fmul2(q, n));
+      y[16 / L + i] = fma2(p, s, fmul2(q, c));
     }
   }
 }
@@ -119,55 +153,55 @@ __device__ __forceinline__ void butterfly(uint64_t& p, uint64_t& q) {
 }
 
 // One row's norm and rotation in place.
-template <bool NORM>
-__device__ __forceinline__ void norm_rotate(Row& y, const RowEncoding& o, const Angles& a, int j) {
+template <int L, bool NORM>
+__device__ __forceinline__ void norm_rotate(Row<L>& y, const RowEncoding& o, const Angles<L>& a, int j) {
   if constexpr (NORM) {
     uint64_t s2 = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s2 = fadd2(s2, y[i]);
+    for (int i = 0; i < 64 / L; ++i) s2 = fadd2(s2, y[i]);
     const float2 s = unpack2(s2);
-    const float mean = sum4(s.x + s.y) * (1.f / 128);
+    const float mean = sum_row<L>(s.x + s.y) * (1.f / 128);
     const uint64_t minus = pack2(-mean, -mean);
     uint64_t q2 = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 64 / L; ++i) {
       y[i] = fadd2(y[i], minus);
       q2 = fma2(y[i], y[i], q2);
     }
     const float2 q = unpack2(q2);
-    const float r = rsqrtf(sum4(q.x + q.y) * (1.f / 128) + o.eps);
+    const float r = rsqrtf(sum_row<L>(q.x + q.y) * (1.f / 128) + o.eps);
     const uint64_t r2 = pack2(r, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int d = 8 * j + 32 * (i >> 1) + 4 * (i & 1);
+    for (int i = 0; i < 32 / L; ++i) {
+      const int d = dim8<L>(i >> 1, j) + 4 * (i & 1);
       const float4 w = *reinterpret_cast<const float4*>(o.norm_w + d), b = *reinterpret_cast<const float4*>(o.norm_b + d);
       y[2 * i] = fma2(fmul2(y[2 * i], r2), pack2(w.x, w.y), pack2(b.x, b.y));
       y[2 * i + 1] = fma2(fmul2(y[2 * i + 1], r2), pack2(w.z, w.w), pack2(b.z, b.w));
     }
   }
-  rotate(y, y + 4, a, o.pairs);
+  rotate<L>(y, a, o.pairs);
 }
 // Its Hadamard transform, without the factor; returns the lane's largest magnitude.
-template <bool HAD>
-__device__ __forceinline__ float transform(Row& y, int j) {
+template <int L, bool HAD>
+__device__ __forceinline__ float transform(Row<L>& y, int j) {
   if constexpr (HAD) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 64 / L; ++i) {
       const float2 v = unpack2(y[i]);
       y[i] = pack2(v.x + v.y, v.x - v.y);
     }
 #pragma unroll
-    for (int h = 1; h < 16; h <<= 1)
+    for (int h = 1; h < 64 / L; h <<= 1)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 64 / L; ++i)
         if (!(i & h)) butterfly(y[i], y[i | h]);
 #pragma unroll
-    for (int h = 1; h < 4; h <<= 1) {
+    for (int h = 1; h < L; h <<= 1) {
       // the lane of the lower dims gets the sum, the other the difference
       const float sign = j & h ? -1.f : 1.f;
       const uint64_t sign2 = pack2(sign, sign);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 64 / L; ++i) {
         const float2 v = unpack2(y[i]);
         const uint64_t other = pack2(__shfl_xor_sync(0xffffffffu, v.x, h), __shfl_xor_sync(0xffffffffu, v.y, h));
         y[i] = fma2(sign2, y[i], other);
@@ -176,7 +210,7 @@ __device__ __forceinline__ float transform(Row& y, int j) {
   }
   float m[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 64 / L; ++i) {
     const float2 v = unpack2(y[i]);
     m[i & 1] = max_abs3(m[i & 1], v.x, v.y);
   }
@@ -194,58 +228,57 @@ __device__ __forceinline__ float encode_scale(float amax) {
   return s > 0.f ? s : 1.f;
 }
 
-// Rounds a row's values to codes, eight bytes for each of the lane's four runs of dims.
-template <bool HAD>
-__device__ __forceinline__ void store_codes(uint8_t* row, Row& y, float amax, int j) {
+// Rounds a row's values to codes, 32 / L bytes for each of the lane's four runs of dims.
+template <int L, bool HAD>
+__device__ __forceinline__ void store_codes(uint8_t* row, Row<L>& y, float amax, int j) {
   if (!(amax >= 1e-30f && amax <= 1e30f)) {
     // 448 / amax would leave the range, or __fdividef's; and below it a scale has few bits, or is 1
     const float top = encode_scale<HAD>(amax);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 64 / L; ++i) {
       const float2 v = unpack2(y[i]);
       y[i] = pack2(v.x * FACTOR<HAD> / top, v.y * FACTOR<HAD> / top);
     }
   } else {
     const float inv = __fdividef(448.f, amax);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = fmul2(y[i], pack2(inv, inv));
+    for (int i = 0; i < 64 / L; ++i) y[i] = fmul2(y[i], pack2(inv, inv));
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    uint32_t x[4];
+    uint32_t x[8 / L];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __nv_cvt_float2_to_fp8x2(unpack2(y[4 * c + i]), __NV_SATFINITE, __NV_E4M3);
-    *reinterpret_cast<uint2*>(row + 8 * j + 32 * c) = make_uint2(x[0] | x[1] << 16, x[2] | x[3] << 16);
+    for (int i = 0; i < 8 / L; ++i) {
+      const uint64_t* p = y + 16 / L * c + 2 * i;
+      x[i] = __nv_cvt_float2_to_fp8x2(unpack2(p[0]), __NV_SATFINITE, __NV_E4M3) |
+             (uint32_t)__nv_cvt_float2_to_fp8x2(unpack2(p[1]), __NV_SATFINITE, __NV_E4M3) << 16;
+    }
+    uint8_t* to = row + 32 * c + 32 / L * j;
+    if constexpr (L == 4) *reinterpret_cast<uint2*>(to) = make_uint2(x[0], x[1]);
+    else *reinterpret_cast<uint4*>(to) = make_uint4(x[0], x[1], x[2], x[3]);
   }
 }
 
-// Rope part of one row: lane j of four reads 16 bytes at dims 8 j and 32 + 8 j, and writes them rotated.
-__device__ __forceinline__ void load_pe(const __nv_bfloat16* row, int j, uint4 (&v)[2]) {
-  v[0] = *reinterpret_cast<const uint4*>(row + 8 * j);
-  v[1] = *reinterpret_cast<const uint4*>(row + 32 + 8 * j);
-}
-__device__ __forceinline__ void rotate_pe(const uint4 (&v)[2], const Angles& a, bool pairs, uint4 (&r)[2]) {
-  uint64_t y0[4], y1[4];
-  unpack8(v[0], y0);
-  unpack8(v[1], y1);
-  rotate(y0, y1, a, pairs);
-  r[0] = pack8(y0);
-  r[1] = pack8(y1);
-}
-__device__ __forceinline__ void store_pe(__nv_bfloat16* row, int j, const uint4 (&v)[2]) {
-  *reinterpret_cast<uint4*>(row + 8 * j) = v[0];
-  *reinterpret_cast<uint4*>(row + 32 + 8 * j) = v[1];
+// A lane's share of a rope part, rotated.
+template <int L>
+__device__ __forceinline__ void rotate_pe(uint4 (&v)[8 / L], const Angles<L>& a, bool pairs) {
+  uint64_t y[32 / L];
+#pragma unroll
+  for (int i = 0; i < 8 / L; ++i) unpack8(v[i], y + 4 * i);
+  rotate<L>(y, a, pairs);
+#pragma unroll
+  for (int i = 0; i < 8 / L; ++i) v[i] = pack8(y + 4 * i);
 }
 }  // namespace
 
 // CTAs [0, index_ctas): a step is one token of 64 rows (G = 64) or 64 tokens of
 // one (G = 1).  The others rotate rope rows, 64 a step.
 template <int G, bool NORM, bool HAD, bool JOINT>
-__global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const EncodeParams p) {
+__global__ void __launch_bounds__(THREADS<G>, CTAS<G>) encode_kernel(const EncodeParams p) {
   pdl_enter();
-  __shared__ float s_max[2][TE_THREADS / 32];
-  constexpr int TOKENS = TE_ROWS / G;  // per step
-  const int tid = threadIdx.x, j = tid & 3, lane = tid & 31, group = tid >> 2;
+  constexpr int L = LANES<G>, WARPS = THREADS<G> / 32, TOKENS = TE_ROWS / G;  // per step
+  __shared__ float s_max[2][WARPS];
+  const int tid = threadIdx.x, j = tid % L, lane = tid & 31, group = tid / L;
   bool bad = false;
   auto position = [&](int64_t t) {  // -1: padding, or nothing
     const int pos = t < p.T ? p.positions[t] : -1;
@@ -259,40 +292,33 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const Encod
     int64_t t = (int64_t)blockIdx.x * TOKENS + (G == 1 ? group : 0);
     int pos = position(t);
     for (int64_t t0 = (int64_t)blockIdx.x * TOKENS, n = 0; t0 < p.T; t0 += step, t += step, ++n) {
-      uint4 v[4] = {};
-      Angles a = {};
+      uint4 v[16 / L] = {};
+      Angles<L> a = {};
       if (pos >= 0) {
-        const __nv_bfloat16* x = p.x + t * p.x_token + g * p.x_head + 8 * j;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(x + 32 * c);
+        load_row<L>(p.x + t * p.x_token + g * p.x_head, j, v);
         a.load(p.cos_sin + (int64_t)pos * 64, j, p.enc.pairs);
       }
-      uint4 e[2] = {};
-      if (JOINT && pos >= 0) load_pe(p.pe + t * p.pe_token, j, e);
+      uint4 e[8 / L] = {};
+      if (JOINT && pos >= 0) load_row<L>(p.pe + t * p.pe_token, j, e);
       const int next = position(t + step);
-      Row y;
+      Row<L> y;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) unpack8(v[c], y + 4 * c);
-      norm_rotate<NORM>(y, p.enc, a, j);
-      float m = transform<HAD>(y, j);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
+      norm_rotate<L, NORM>(y, p.enc, a, j);
+      float m = max_lanes<G == 1 ? L : 32>(transform<L, HAD>(y, j));
       if constexpr (G > 1) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) s_max[n & 1][tid >> 5] = m;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < TE_THREADS / 32; ++i) m = fmaxf(m, s_max[n & 1][i]);
+        for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_max[n & 1][i]);
       }
       if (JOINT && pos >= 0) {
         if (p.pe_pairs != p.enc.pairs) a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
-        uint4 r[2];
-        rotate_pe(e, a, p.pe_pairs, r);
-        store_pe(p.pe_out + t * p.po_token, j, r);
+        rotate_pe<L>(e, a, p.pe_pairs);
+        store_row<L>(p.pe_out + t * p.po_token, j, e);
       }
       if (pos >= 0) {
-        store_codes<HAD>(p.codes + (t * G + g) * 128, y, m, j);
+        store_codes<L, HAD>(p.codes + (t * G + g) * 128, y, m, j);
         if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale<HAD>(m);
       }
       pos = next;
@@ -302,13 +328,13 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const Encod
     for (int64_t row = (int64_t)(blockIdx.x - p.index_ctas) * TE_ROWS + group; row < rows; row += step) {
       const int64_t t = rows < (1ll << 31) ? (int)row / p.H : row / p.H;
       const int h = (int)(row - t * p.H), pos = position(t);
-      uint4 v[2], r[2];
-      load_pe(p.pe + t * p.pe_token + h * p.pe_head, j, v);
+      uint4 v[8 / L];
+      load_row<L>(p.pe + t * p.pe_token + h * p.pe_head, j, v);
       if (pos < 0) continue;
-      Angles a;
+      Angles<L> a;
       a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
-      rotate_pe(v, a, p.pe_pairs, r);
-      store_pe(p.pe_out + t * p.po_token + h * p.po_head, j, r);
+      rotate_pe<L>(v, a, p.pe_pairs);
+      store_row<L>(p.pe_out + t * p.po_token + h * p.po_head, j, v);
     }
   }
   last_cta(p.status, bad);
@@ -317,13 +343,13 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) encode_kernel(const Encod
 template <int G, bool NORM, bool HAD, bool JOINT>
 static cudaError_t launch_encode_as(EncodeParams p, cudaStream_t s) {
   // both kinds of CTAs at once, in shares that end together
-  const int all = TE_CTAS * option_grid(), steps = !p.x ? 0 : G == 1 ? ceil_div(p.T, TE_ROWS) : p.T;
+  const int all = CTAS<G> * option_grid(), steps = !p.x ? 0 : G == 1 ? ceil_div(p.T, TE_ROWS) : p.T;
   const int64_t pe_rows = p.pe && !JOINT ? (int64_t)p.T * p.H : 0, pe_steps = (pe_rows + TE_ROWS - 1) / TE_ROWS;
   const int64_t share = 4 * (int64_t)steps + 3 * pe_steps;
   const int pe_ctas = (int)std::min<int64_t>(pe_steps, std::max<int64_t>(pe_steps > 0, all * 3 * pe_steps / share));
   p.index_ctas = min(steps, max(1, all - pe_ctas));
   count_launch();
-  return launch_pdl(encode_kernel<G, NORM, HAD, JOINT>, dim3(p.index_ctas + pe_ctas), dim3(TE_THREADS), 0, s, p);
+  return launch_pdl(encode_kernel<G, NORM, HAD, JOINT>, dim3(p.index_ctas + pe_ctas), dim3(THREADS<G>), 0, s, p);
 }
 template <int G, bool JOINT>
 static cudaError_t launch_encode_g(const EncodeParams& p, cudaStream_t s) {
@@ -374,15 +400,15 @@ __device__ __forceinline__ Place place_token(const AppendParams& p, int64_t t, b
 // CTAs [0, row_ctas): four lanes per token rotate the rope part and encode the
 // index key.  The others: a warp normalises the latents of AP_TOKENS tokens at a time, 16 dims
 // per lane, so that enough loads are in flight.
-constexpr int AP_TOKENS = 4;
+constexpr int AP_TOKENS = 4, AP_LANES = LANES<1>, AP_THREADS = THREADS<1>, AP_CTAS = CTAS<1>;
 template <bool NORM, bool HAD>
-__global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const AppendParams p) {
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31;
   bool bad = false;
   if (blockIdx.x >= (unsigned)p.row_ctas) {
-    const int64_t step = (int64_t)(gridDim.x - p.row_ctas) * (TE_THREADS / 32) * AP_TOKENS;
-    const int64_t first = ((int64_t)(blockIdx.x - p.row_ctas) * (TE_THREADS / 32) + (tid >> 5)) * AP_TOKENS;
+    const int64_t step = (int64_t)(gridDim.x - p.row_ctas) * (AP_THREADS / 32) * AP_TOKENS;
+    const int64_t first = ((int64_t)(blockIdx.x - p.row_ctas) * (AP_THREADS / 32) + (tid >> 5)) * AP_TOKENS;
     for (int64_t t0 = first; t0 < p.T; t0 += step) {
       uint4 v[AP_TOKENS][2];
 #pragma unroll
@@ -423,39 +449,34 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
       }
     }
   } else {
-    const int j = tid & 3;
+    constexpr int L = AP_LANES;
+    const int j = tid % L;
     // (every lane takes part in the shuffles)
     for (int64_t t0 = (int64_t)blockIdx.x * TE_ROWS; t0 < p.T; t0 += (int64_t)p.row_ctas * TE_ROWS) {
-      const int64_t t = t0 + (tid >> 2);
-      uint4 e[2] = {}, v[4] = {};
+      const int64_t t = t0 + tid / L;
+      uint4 e[8 / L] = {}, v[16 / L] = {};
       if (t < p.T) {
-        load_pe(p.k_pe + t * p.kp_stride, j, e);
-        if (p.index_k) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(p.index_k + t * p.ik_stride + 32 * c + 8 * j);
-        }
+        load_row<L>(p.k_pe + t * p.kp_stride, j, e);
+        if (p.index_k) load_row<L>(p.index_k + t * p.ik_stride, j, v);
       }
       const Place at = place_token(p, t, bad);
       const float* cs = p.cos_sin + (int64_t)at.pos * 64;
-      Angles a = {};
+      Angles<L> a = {};
       if (at.slot >= 0) {
-        uint4 r[2];
         a.load(cs, j, p.pe_pairs);
-        rotate_pe(e, a, p.pe_pairs, r);
-        store_pe(p.kpe + at.slot * p.kpe_stride, j, r);
-        if (p.k_pe_out) store_pe(p.k_pe_out + t * p.kp_out_stride, j, r);
+        rotate_pe<L>(e, a, p.pe_pairs);
+        store_row<L>(p.kpe + at.slot * p.kpe_stride, j, e);
+        if (p.k_pe_out) store_row<L>(p.k_pe_out + t * p.kp_out_stride, j, e);
       }
       if (p.index_k) {
         if (at.slot >= 0 && p.enc.pairs != p.pe_pairs) a.load(cs, j, p.enc.pairs);
-        Row y;
+        Row<L> y;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) unpack8(v[c], y + 4 * c);
-        norm_rotate<NORM>(y, p.enc, a, j);
-        float m = transform<HAD>(y, j);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
+        norm_rotate<L, NORM>(y, p.enc, a, j);
+        const float m = max_lanes<L>(transform<L, HAD>(y, j));
         if (at.slot >= 0) {
-          store_codes<HAD>(p.k_cache + at.slot * 128, y, m, j);
+          store_codes<L, HAD>(p.k_cache + at.slot * 128, y, m, j);
           if (j == 0) p.k_scale[at.slot] = encode_scale<HAD>(m);
         }
       }
@@ -464,7 +485,7 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
   // new_lens may be seq_lens itself: it is written where every CTA has read what it needs
   if (last_cta(p.status, bad)) {
     bool wrong = false;
-    for (int b = tid; b < p.B; b += TE_THREADS) {
+    for (int b = tid; b < p.B; b += AP_THREADS) {
       int first, n, len;
       const bool ok = valid_sequence(p, b, first, n, len);
       wrong |= !ok;
@@ -476,10 +497,10 @@ __global__ void __launch_bounds__(TE_THREADS, TE_CTAS) append_kernel(const Appen
 
 cudaError_t launch_append(AppendParams p, cudaStream_t s) {
   // both kinds of CTAs at once, in shares that end together
-  const int all = TE_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS);
-  const int latents = ceil_div(p.T, TE_THREADS / 32 * AP_TOKENS);
+  const int all = AP_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS);
+  const int latents = ceil_div(p.T, AP_THREADS / 32 * AP_TOKENS);
   p.row_ctas = min(rows, max(1, all / 3));
-  const dim3 ctas(p.row_ctas + min(latents, max(1, all - p.row_ctas))), threads(TE_THREADS);
+  const dim3 ctas(p.row_ctas + min(latents, max(1, all - p.row_ctas))), threads(AP_THREADS);
   count_launch();
   if (p.enc.norm_w)
     return p.enc.hadamard ? launch_pdl(append_kernel<true, true>, ctas, threads, 0, s, p)
