@@ -11,24 +11,27 @@
 //
 // What it cannot do without are bytes: a query token reads 16 KB and writes 8 KB.  A
 // row of 128 dims lies in L lanes, lane j with dims 32 / L j + 32 c + e: 16-byte
-// loads that fill whole sectors, both halves of every rotated pair in
-// one lane (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and the
-// Hadamard stages but log2 L as well, which are shuffles.  The 64 rows of a query
-// token take two lanes each, which halves the shuffles (4096 tokens 30.3 us, 32.0 with
-// four), single rows four (131072 keys 28.6 us; 42 with two, whose norm and rope part spill).
-// Values stay fp32, two to a
-// register pair for the packed arithmetic, between the loads and the one rounding
-// at the end.  CTAs stay and take every so manieth token: with a CTA for each, what
-// starting and ending it costs (the status among it) was a third of the time.
+// loads that fill whole sectors, both halves of every rotated pair in one lane
+// (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and all Hadamard stages
+// but log2 L, which are shuffles.  The 64 rows of a query token take two lanes
+// each, which halves the shuffles (4096 tokens 30.3 us, 32.0 with four), single
+// rows four (131072 keys 28.6 us; 42 with two, whose norm and rope part spill).
+// Values stay fp32, two to a register pair for the packed arithmetic, between
+// the loads and the one rounding at the end.  CTAs stay and take every so manieth
+// token: with a CTA for each, what starting and ending it costs (the status among
+// it) was a third of the time.
 //
-// On the device, in a graph: 4096 query tokens with 16 rope rows each (118 MB) 30.3 us,
-// 3.9 TB/s; the index rows alone 27.0, without the Hadamard transform 21.9, the rope
-// rows alone 7.7.  CTAs per SM: three 33.7, five 32.3; a rope row counted as 2, 4 or 6
-// quarters of an index row instead of 3: 31.9, 32.4, 34.4.  Slower were also: the next token's
-// rows in registers (33.8), rows fetched ahead by cp.async, the exchange of the last stages through shared
-// memory; those stages on mma.sync with values in three bf16 parts gained 3%.
-// 131072 keys with norm and rope part (118 MB): 28.6 us; the index rows alone 21.4, 16.5 without
-// the norm, 13.7 without both.  16384 tokens appended (48 MB): 14 us.
+// On the device, in a graph: 4096 query tokens with 16 rope rows each (118 MB)
+// 30.3 us, 3.9 TB/s, of which a start of 4; the index rows alone 27.0, without the
+// Hadamard transform 21.9; the rope rows alone 7.7.  The shared-memory path is 58%
+// busy, issue 31%.  CTAs per SM: three 33.7, five 32.3; a rope row counted as 2, 4
+// or 6 quarters of an index row instead of 3: 31.9, 32.4, 34.4.  Slower were also
+// the next token's rows in registers (33.8), rows fetched ahead by cp.async, and
+// the exchange of the last stages through shared memory; those stages on mma.sync
+// with values in three bf16 parts gained 3%, rows copied ahead by TMA 4% (with a
+// norm they lost 5%): neither was worth its code.
+// 131072 keys with norm and rope part (118 MB): 28.6 us; the index rows alone 21.4,
+// 16.5 without the norm, 13.7 without both.  16384 tokens appended (48 MB): 14 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
