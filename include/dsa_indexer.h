@@ -432,7 +432,9 @@ DSA_API int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_
  * A sequence whose border, length or new length does not fit the arrays or its
  * table is skipped (new_lens[b] = seq_lens[b]); a token whose position is outside
  * [0, max_positions), or whose page is outside the cache, is not written.  Both
- * are DSA_ERR_RANGE.  No two sequences may write one page.
+ * are DSA_ERR_RANGE, and so are borders that do not ascend: a sequence beside them may
+ * be skipped too, but one whose length moves has all of its tokens, and no
+ * token goes to two.  No two sequences may write one page.
  */
 DSA_API int dsa_latent_cache_append(const uint16_t* c, int64_t c_stride, const uint16_t* k_pe, int64_t k_pe_stride,
                                     const uint16_t* index_k, int64_t index_k_stride,
