@@ -279,10 +279,9 @@ DSA_API int dsa_sparse_attention_last_status(dsa_stream_t stream);
  * capture goes on without it): run one of the same sizes on the stream first.
  * Calls on one stream, graphs captured on it, and their replays on whatever
  * stream, share that stream's scratch and status: they have to run one after
- * the other.  Two at a time overwrite each other's partial results, and
- * nothing reports it (after an encode, append or accept that ran so, later
- * ones' status and new_lens may be wrong as well, until dsa_indexer_release).
- * Graphs that are to run side by side are captured on a stream each.
+ * the other.  Two at a time overwrite each other's partial results and new_lens,
+ * and nothing reports it; calls behind them are sound again.  Graphs that are to
+ * run side by side are captured on a stream each.
  */
 
 /*

@@ -58,3 +58,56 @@ def test_append_with_any_borders(B):  # noqa: F811
         else:
             moved += sum(a != b for a, b in zip(new, lens))
     assert moved > 100  # (sequences are written beside borders that do not ascend, so the rule above is tried)
+
+
+# ----------------------------------------------------------- calls and ends --
+def test_replays_beside_each_other_leave_nothing_behind(B):  # noqa: F811
+    """Graphs captured on one stream share its status, and have to be replayed in turn.  Two that are not, of grids of
+    different sizes, spoil no call behind them: its lengths, rows and status are its own."""
+    g, table, s = torch.Generator().manual_seed(9), _table().cuda(), torch.cuda.Stream()
+    new, lens = [40 * i % 97 for i in range(64)], [i % 70 for i in range(64)]
+    cu, after = np.concatenate([[0], np.cumsum(new)]), [a + b for a, b in zip(new, lens)]
+    T = sum(new)
+    p = Pages(after, seed=10)
+    c, k_pe = (x.cuda() for x in _tokens(g, T, joint=False))
+    dcu, bt, before, dl = _ints(cu), p.table.cuda(), _ints(lens), _ints(lens)
+    x, pos = _normal(g, 3, 64, 128).cuda(), _ints([1, 2, 3])
+    codes, scale = torch.empty((3, 64, 128), dtype=torch.uint8, device="cuda"), torch.empty(3, device="cuda")
+
+    def append():
+        dl.copy_(before)
+        B.latent_cache_append(c, k_pe, table, dcu, bt, dl, p.ckv, p.kpe, new_lens=dl)
+
+    def encode():
+        B.indexer_encode(x, table, pos, codes=codes, scale=scale)
+
+    graphs = []
+    torch.cuda.synchronize()
+    for call in (append, encode):
+        with torch.cuda.stream(s):
+            call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            call()
+    want = codes.clone()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    slots = [torch.from_numpy(p.slots(b, lens[b], new[b])).cuda() for b in range(64)]
+    for _ in range(60):
+        for _ in range(8):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        p.ckv.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):  # in turn, on the stream that they shared
+            append()
+            ok, got = B.latent_last_status(), dl.tolist()
+            B.indexer_encode(x, table, _ints([1, MAXPOS, 3]), codes=codes, scale=scale)
+            bad = B.latent_last_status()
+            encode()
+            again = B.latent_last_status()
+        assert got == after and (ok, bad, again) == (0, B.DSA_ERR_RANGE, 0) and torch.equal(codes, want)
+        for b in range(64):
+            assert torch.equal(p.ckv.view(-1, 512)[slots[b]], c[int(cu[b]):int(cu[b + 1])])
