@@ -506,12 +506,15 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const Appen
   }
   // new_lens may be seq_lens itself: it is written where every CTA has read what it needs
   if (last_cta(p.status, bad)) {
-    bool wrong = false;
+    bool wrong = false, falls = false;
+    for (int b = tid; b < p.B; b += AP_THREADS) falls |= (p.cu_new[b + 1] < p.cu_new[b]) | (p.seq_lens[b] < 0);
+    falls = __syncthreads_or(falls);  // (where borders ascend no search need be made: 64 sequences 6.9 us, 7.6 with it)
     for (int b = tid; b < p.B; b += AP_THREADS) {
       Search at(p.B);
-      at.run(p, [&](int mid, int) { return mid >= b; });
+      if (falls) at.run(p, [&](int mid, int) { return mid >= b; });
+      else at.lo = b;
       int first, n, len;
-      const bool ok = valid_sequence(p, at, first, n, len);
+      const bool ok = valid_sequence(p, at, first, n, len);  // (from the L1: a length has been read above, too)
       wrong |= !ok;
       p.new_lens[b] = ok ? len + n : len;
     }
