@@ -27,6 +27,8 @@ struct Scratch {
   size_t cap = 0;
   std::vector<uint8_t*> outgrown;
 };
+// Held from the lookup of a call's scratch until its kernels are launched: a release on another thread comes before, or
+// waits for them.
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
 
@@ -100,13 +102,6 @@ bool usable_encoding(RowEncoding& e, const float* w, const float* b, float eps, 
   return true;
 }
 constexpr int ENCODE_FLAGS = DSA_ENCODE_PAIRS | DSA_ENCODE_HADAMARD | DSA_ENCODE_PE_HALVES;
-
-// Status of the calls on a stream, for operators that need no other scratch; null on an error.
-LatentStatus* get_status(cudaStream_t stream) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  const Scratch* s = get_scratch(stream, 0);
-  return s ? s->status : nullptr;
-}
 
 // Arguments shared by the forms of cached attention.
 int check_cached(const LatentAttnParams& p) {
@@ -373,7 +368,10 @@ int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_t x_head
   p.pe_out = reinterpret_cast<__nv_bfloat16*>(pe_out);
   p.po_token = po_token_stride;
   p.po_head = po_head_stride;
-  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const Scratch* scratch = get_scratch(stream, 0);
+  if (!scratch) return DSA_ERR_CUDA;
+  p.status = scratch->status;
   return launch_encode(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 } catch (...) {
   return DSA_ERR_CUDA;
@@ -439,7 +437,10 @@ int dsa_latent_cache_append(const uint16_t* c, int64_t c_stride, const uint16_t*
   p.c_out_stride = c_out_stride;
   p.kp_out_stride = k_pe_out_stride;
   p.new_lens = new_lens;
-  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const Scratch* scratch = get_scratch(stream, 0);
+  if (!scratch) return DSA_ERR_CUDA;
+  p.status = scratch->status;
   return launch_append(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 } catch (...) {
   return DSA_ERR_CUDA;
@@ -476,7 +477,10 @@ int dsa_latent_cache_accept(uint16_t* ckv, int64_t ckv_stride, uint16_t* kpe, in
   p.num_pages = num_pages;
   p.max_path = max_path;
   p.new_lens = new_lens;
-  if (!(p.status = get_status(stream))) return DSA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_mu);
+  const Scratch* scratch = get_scratch(stream, 0);
+  if (!scratch) return DSA_ERR_CUDA;
+  p.status = scratch->status;
   return launch_accept(p, stream) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 } catch (...) {
   return DSA_ERR_CUDA;

@@ -111,3 +111,43 @@ def test_replays_beside_each_other_leave_nothing_behind(B):  # noqa: F811
         assert got == after and (ok, bad, again) == (0, B.DSA_ERR_RANGE, 0) and torch.equal(codes, want)
         for b in range(64):
             assert torch.equal(p.ckv.view(-1, 512)[slots[b]], c[int(cu[b]):int(cu[b + 1])])
+
+
+def test_calls_beside_releases(B):  # noqa: F811
+    """dsa_indexer_release on one thread while others call: a call's status is not freed before its kernels are done."""
+    from concurrent.futures import ThreadPoolExecutor
+    g, table = torch.Generator().manual_seed(11), _table().cuda()
+    x, pos = _normal(g, 40, 64, 128).cuda(), _ints(range(40))
+    c, k_pe = (t.cuda() for t in _tokens(g, 8, joint=False))
+    want = B.indexer_encode(x, table, pos, hadamard=True)
+    cu, tables = _ints([0, 8]), [_ints([[2 * k, 2 * k + 1]]) for k in range(3)]
+    ckv, kpe = (torch.zeros((6, 64, d), dtype=BF16, device="cuda") for d in (512, 64))
+    lens, drafts, path, plens = _ints([60]), _ints([8]), _ints([[0, 3, 7]]), _ints([3])
+    torch.cuda.synchronize()
+
+    def calls(k):
+        s = torch.cuda.Stream()
+        codes, scale = torch.empty((40, 64, 128), dtype=torch.uint8, device="cuda"), torch.empty(40, device="cuda")
+        n1, n2 = torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(300):
+            B.indexer_encode(x, table, pos, hadamard=True, codes=codes, scale=scale, stream=s)
+            B.latent_cache_append(c, k_pe, table, cu, tables[k], lens, ckv, kpe, new_lens=n1, stream=s)
+            B.latent_cache_accept(ckv, kpe, tables[k], n1, drafts, path, plens, new_lens=n2, stream=s)
+        s.synchronize()
+        return codes, scale, n1.tolist(), n2.tolist(), tables[k][0].tolist()
+
+    def releases():
+        for _ in range(150):
+            B.release()
+
+    with ThreadPoolExecutor(4) as pool:
+        done = [pool.submit(calls, k) for k in range(3)]
+        pool.submit(releases).result()
+        done = [d.result() for d in done]
+    torch.cuda.synchronize()
+    for codes, scale, n1, n2, pages in done:
+        assert torch.equal(codes, want[0].view(torch.uint8)) and torch.equal(scale, want[1])
+        assert n1 == [68] and n2 == [63]
+        flat = ckv[pages].view(-1, 512)
+        assert torch.equal(flat[60:63], c[[0, 3, 7]]) and torch.equal(flat[63:68], c[3:8])
