@@ -104,7 +104,7 @@ struct Arena {
   bool used = false;
 };
 
-std::map<std::pair<int, cudaStream_t>, Arena> g_arenas;
+std::map<std::pair<int, uint64_t>, Arena> g_arenas;
 
 // Returns the arena of (current device, stream) with room for `need` bytes.
 Arena* get_arena(cudaStream_t stream, const Layout& L, int* err) {
@@ -113,7 +113,7 @@ Arena* get_arena(cudaStream_t stream, const Layout& L, int* err) {
     *err = DSA_ERR_CUDA;
     return nullptr;
   }
-  Arena& a = g_arenas[{dev, stream}];
+  Arena& a = g_arenas[{dev, stream_key(stream)}];
   if (a.cap < L.total) {
     if (a.base) {
       cudaDeviceSynchronize();
@@ -517,7 +517,7 @@ struct AuxScratch {
   uint8_t* base = nullptr;
   size_t cap = 0;
 };
-std::map<std::pair<int, cudaStream_t>, AuxScratch> g_aux;  // guarded by g_mu
+std::map<std::pair<int, uint64_t>, AuxScratch> g_aux;  // guarded by g_mu
 
 uint8_t* aux_scratch(cudaStream_t stream, size_t need, int* err) {
   int dev = 0;
@@ -525,7 +525,7 @@ uint8_t* aux_scratch(cudaStream_t stream, size_t need, int* err) {
     *err = DSA_ERR_CUDA;
     return nullptr;
   }
-  AuxScratch& a = g_aux[{dev, stream}];
+  AuxScratch& a = g_aux[{dev, stream_key(stream)}];
   if (a.cap < need) {
     if (a.base) {
       cudaDeviceSynchronize();
@@ -588,7 +588,7 @@ struct HostStage {
 };
 
 std::mutex g_host_mu;  // one host-buffer call at a time (it synchronises before returning)
-std::map<std::pair<int, cudaStream_t>, HostStage> g_host;
+std::map<std::pair<int, uint64_t>, HostStage> g_host;
 
 // Rows per chunk: the option when set, else half of the rows but at least
 // 2048 (every chunk pays the fused call's fixed launch sequence and its
@@ -612,7 +612,7 @@ Stats* arena_stats(cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_arenas.find({dev, stream});
+  auto it = g_arenas.find({dev, stream_key(stream)});
   if (it == g_arenas.end() || !it->second.base) return nullptr;
   return reinterpret_cast<Stats*>(it->second.base + it->second.L.stats);
 }
@@ -691,7 +691,7 @@ int dsa_indexer_topk_host(const uint8_t* q_fp8, const float* q_scale, const uint
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> hl(g_host_mu);
-  HostStage& hs = g_host[{dev, stream}];
+  HostStage& hs = g_host[{dev, stream_key(stream)}];
   int rc = host_stage_init(hs, L, stream);
   if (rc != DSA_OK) {
     cudaGetLastError();
@@ -1211,7 +1211,7 @@ int dsa_sparse_attention_last_status(dsa_stream_t stream_) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_aux.find({dev, stream});
+  auto it = g_aux.find({dev, stream_key(stream)});
   if (it == g_aux.end() || !it->second.base) return DSA_OK;
   int st = 0;
   if (cudaMemcpy(&st, it->second.base, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;
@@ -1224,7 +1224,7 @@ int dsa_indexer_last_device_status(dsa_stream_t stream_, int32_t* failures_out) 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_arenas.find({dev, stream});
+  auto it = g_arenas.find({dev, stream_key(stream)});
   if (it == g_arenas.end() || !it->second.used) {
     if (failures_out) memset(failures_out, 0, 4 * sizeof(int32_t));
     return DSA_OK;
@@ -1250,7 +1250,7 @@ int dsa_indexer_last_repaired_rows(dsa_stream_t stream_, int32_t* rows_out, int 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_arenas.find({dev, stream});
+  auto it = g_arenas.find({dev, stream_key(stream)});
   if (it == g_arenas.end() || !it->second.used) return 0;
   Stats st;
   const Arena& a = it->second;
@@ -1343,7 +1343,7 @@ float dsa_indexer_profiled_main_ms(dsa_stream_t stream_) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1.f;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_arenas.find({dev, stream});
+  auto it = g_arenas.find({dev, stream_key(stream)});
   if (it == g_arenas.end() || !it->second.profiled) return -1.f;
   if (cudaEventSynchronize(it->second.ev1) != cudaSuccess) return -1.f;
   float ms = -1.f;

@@ -286,6 +286,14 @@ struct SparseAttnParams {
   int* status;                  // ST_RANGE: a slot >= num_slots was named (read as padding)
 };
 
+// What a stream's scratch is kept under: its handle, but for cudaStreamPerThread, one handle for a stream per thread, that
+// stream's id.  (Where that cannot be had no call can be made either.)
+inline uint64_t stream_key(cudaStream_t s) {
+  unsigned long long id = 0;
+  if (s != cudaStreamPerThread || cudaStreamGetId(s, &id) != cudaSuccess) return reinterpret_cast<uintptr_t>(s);
+  return id | 1ull << 63;
+}
+
 // One bit per device (0..63) for a per-device, once-only host action.
 struct DeviceFlags {
   std::atomic<uint64_t> bits{0};

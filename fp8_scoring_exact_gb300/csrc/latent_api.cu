@@ -30,7 +30,7 @@ struct Scratch {
 // Held from the lookup of a call's scratch until its kernels are launched: a release on another thread comes before, or
 // waits for them.
 std::mutex g_mu;
-std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
+std::map<std::pair<int, uint64_t>, Scratch> g_scratch;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -41,7 +41,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 const Scratch* get_scratch(cudaStream_t stream, size_t need) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  Scratch& a = g_scratch[{dev, stream}];
+  Scratch& a = g_scratch[{dev, stream_key(stream)}];
   if (!a.status || a.cap < need) {
     cudaStreamCaptureStatus capturing;
     if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
@@ -619,7 +619,7 @@ int dsa_latent_last_status(dsa_stream_t stream_) try {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
-  auto it = g_scratch.find({dev, stream});
+  auto it = g_scratch.find({dev, stream_key(stream)});
   if (it == g_scratch.end() || !it->second.status) return DSA_OK;
   LatentStatus s;
   if (cudaMemcpy(&s, it->second.status, sizeof(s), cudaMemcpyDeviceToHost) != cudaSuccess) return DSA_ERR_CUDA;

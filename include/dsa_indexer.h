@@ -33,7 +33,8 @@
  *     candidate buffers, repair scores), allocated on first use and grown on
  *     demand; growing synchronises the device once.  Calls on the same stream
  *     are serialised by the stream; calls on different streams use different
- *     scratch.  The scratch is released by dsa_indexer_release() or at exit.
+ *     scratch (cudaStreamPerThread is another stream on every thread).  The
+ *     scratch is released by dsa_indexer_release() or at exit.
  *   - Fixed geometry: 64 heads, head dimension 128 (section 2.3); 1 <= K <=
  *     DSA_MAX_K.
  *

@@ -151,3 +151,60 @@ def test_calls_beside_releases(B):  # noqa: F811
         assert n1 == [68] and n2 == [63]
         flat = ckv[pages].view(-1, 512)
         assert torch.equal(flat[60:63], c[[0, 3, 7]]) and torch.equal(flat[63:68], c[3:8])
+
+
+class PerThread:
+    """cudaStreamPerThread: one handle, of a stream of its own on every thread."""
+    cuda_stream = 2
+
+
+def test_the_streams_of_threads_are_apart(B):  # noqa: F811
+    from concurrent.futures import ThreadPoolExecutor
+    s, table, x = PerThread(), _table().cuda(), torch.zeros((1, 64, 128), dtype=BF16, device="cuda")
+    codes, scale = torch.empty((1, 64, 128), dtype=torch.uint8, device="cuda"), torch.empty(1, device="cuda")
+    good, bad = _ints([0]), _ints([MAXPOS])
+    torch.cuda.synchronize()
+
+    def encode(pos):
+        B.indexer_encode(x, table, pos, codes=codes, scale=scale, stream=s)
+        return B.latent_last_status(s)
+
+    with ThreadPoolExecutor(1) as first, ThreadPoolExecutor(1) as second:
+        assert first.submit(encode, bad).result() == B.DSA_ERR_RANGE
+        assert second.submit(B.latent_last_status, s).result() == 0  # (nothing has run on this thread's)
+        assert second.submit(encode, good).result() == 0
+        assert first.submit(B.latent_last_status, s).result() == B.DSA_ERR_RANGE
+        assert first.submit(encode, good).result() == 0
+
+
+def test_threads_append_on_their_streams_at_once(B):  # noqa: F811
+    """Calls of different sizes, in place, on four threads' own streams."""
+    from concurrent.futures import ThreadPoolExecutor
+    s, table = PerThread(), _table().cuda()
+
+    def work(k):
+        g = torch.Generator().manual_seed(20 + k)
+        new = [(k + 1) * 37 % 61 + 300 * k, 5, 64 * k]
+        lens, T = [3, 60, 64], sum(new)
+        p = Pages([a + b for a, b in zip(new, lens)], seed=k)
+        c, k_pe = (t.cuda() for t in _tokens(g, T, joint=False))
+        cu, bt, dl, before = _ints(np.concatenate([[0], np.cumsum(new)])), p.table.cuda(), _ints(lens), _ints(lens)
+        x, pos = _normal(g, 5 + 90 * k, 64, 128).cuda(), _ints(range(5 + 90 * k))
+        codes = torch.empty((len(pos), 64, 128), dtype=torch.uint8, device="cuda")
+        scale = torch.empty(len(pos), device="cuda")
+        out = torch.empty(3, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(100):
+            B.latent_cache_append(c, k_pe, table, cu, bt, before, p.ckv, p.kpe, new_lens=out, stream=s)
+            B.indexer_encode(x, table, pos, hadamard=True, codes=codes, scale=scale, stream=s)
+        B.latent_cache_append(c, k_pe, table, cu, bt, dl, p.ckv, p.kpe, new_lens=dl, stream=s)
+        status = B.latent_last_status(s)
+        flat = p.ckv.view(-1, 512)
+        for b, (a, n) in enumerate(zip(lens, new)):
+            lo = sum(new[:b])
+            assert torch.equal(flat[torch.from_numpy(p.slots(b, a, n)).cuda()], c[lo:lo + n])
+        assert out.tolist() == dl.tolist() == [a + n for a, n in zip(lens, new)]
+        return status
+
+    with ThreadPoolExecutor(4) as pool:
+        assert list(pool.map(work, range(4))) == [0] * 4
