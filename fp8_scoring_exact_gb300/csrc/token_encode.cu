@@ -93,6 +93,12 @@ __device__ __forceinline__ float sum_row(float x) {
   for (int h = 1; h < L; h <<= 1) x += __shfl_xor_sync(0xffffffffu, x, h);
   return x;
 }
+__device__ __forceinline__ float sum_warp(float2 v) {
+  float x = v.x + v.y;
+#pragma unroll
+  for (int h = 16; h; h >>= 1) x += __shfl_xor_sync(0xffffffffu, x, h);
+  return x;
+}
 template <int N>
 __device__ __forceinline__ float max_lanes(float x) {  // over every N lanes
 #pragma unroll
@@ -157,10 +163,34 @@ __device__ __forceinline__ void butterfly(uint64_t& p, uint64_t& q) {
   p = sum;
 }
 
-// One row's norm and rotation in place.
-template <int L, bool NORM>
-__device__ __forceinline__ void norm_rotate(Row<L>& y, const RowEncoding& o, const Angles<L>& a, int j) {
+// A power of two that brings `top`, the largest magnitude of what is squared, to [1, 4) (and what is below fp32's normal
+// range as far up as it can).
+__device__ __forceinline__ float unit_scale(float top) {
+  const int e = (int)(__float_as_uint(top) >> 23) - 127;
+  return __uint_as_float((uint32_t)(127 - min(max(e, -126), 126)) << 23);
+}
+// Whether a mean square (with eps) was formed without overflow, and is large enough that no square has lost bits that it
+// still has: 2^-90 is 2^59 steps of fp32's lower end.
+__device__ __forceinline__ bool sound_square(float t) { return t >= 0x1p-90f && t <= 3.402823466e38f; }
+
+// One row's norm and rotation in place.  False: the row is too large (from 2e18 on) or too small to be squared, and
+// has to be taken SCALED: times a power of two, with eps times its square.
+template <int L, bool NORM, bool SCALED>
+__device__ __forceinline__ bool norm_rotate(Row<L>& y, const RowEncoding& o, const Angles<L>& a, int j) {
+  bool sound = true;
   if constexpr (NORM) {
+    float k = 1.f;
+    if constexpr (SCALED) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64 / L; ++i) {
+        const float2 x = unpack2(y[i]);
+        m = max_abs3(m, x.x, x.y);
+      }
+      k = unit_scale(fmaxf(max_lanes<L>(m), sqrtf(o.eps)));
+#pragma unroll
+      for (int i = 0; i < 64 / L; ++i) y[i] = fmul2(y[i], pack2(k, k));
+    }
     uint64_t s2 = 0;
 #pragma unroll
     for (int i = 0; i < 64 / L; ++i) s2 = fadd2(s2, y[i]);
@@ -174,7 +204,9 @@ __device__ __forceinline__ void norm_rotate(Row<L>& y, const RowEncoding& o, con
       q2 = fma2(y[i], y[i], q2);
     }
     const float2 q = unpack2(q2);
-    const float r = rsqrtf(sum_row<L>(q.x + q.y) * (1.f / 128) + o.eps);
+    const float t = sum_row<L>(q.x + q.y) * (1.f / 128) + (SCALED ? o.eps * k * k : o.eps);
+    sound = SCALED || sound_square(t);
+    const float r = rsqrtf(t);
     const uint64_t r2 = pack2(r, r);
 #pragma unroll
     for (int i = 0; i < 32 / L; ++i) {
@@ -185,6 +217,7 @@ __device__ __forceinline__ void norm_rotate(Row<L>& y, const RowEncoding& o, con
     }
   }
   rotate<L>(y, a, o.pairs);
+  return sound;
 }
 // Its Hadamard transform, without the factor; returns the lane's largest magnitude.
 template <int L, bool HAD>
@@ -274,65 +307,81 @@ __device__ __forceinline__ void rotate_pe(uint4 (&v)[8 / L], const Angles<L>& a,
 #pragma unroll
   for (int i = 0; i < 8 / L; ++i) v[i] = pack8(y + 4 * i);
 }
+
+// What a thread notes: a position past the table; a row that has to be taken SCALED.  (In one register: with one each
+// 4096 query tokens with a norm took 42.7 us.)
+constexpr int TE_BAD = 1, TE_UNSOUND = 2;
+
+// The position of token t; -1: padding, or nothing.
+__device__ __forceinline__ int token_position(const EncodeParams& p, int64_t t, int& flags) {
+  const int pos = t < p.T ? p.positions[t] : -1;
+  if (pos < p.max_positions) return pos;
+  flags |= TE_BAD;
+  return -1;
+}
+
+// The index rows of a CTA's tokens, and with JOINT their rope parts: a step is one token of 64 rows (G = 64) or 64 tokens
+// of one (G = 1).
+template <int G, bool NORM, bool HAD, bool JOINT, bool SCALED>
+__device__ __forceinline__ void encode_rows(const EncodeParams& p, float (*s_max)[THREADS<G> / 32], int& flags) {
+  constexpr int L = LANES<G>, WARPS = THREADS<G> / 32, TOKENS = TE_ROWS / G;  // per step
+  const int tid = threadIdx.x, j = tid % L, lane = tid & 31, group = tid / L, g = G == 1 ? 0 : group;
+  const int64_t step = (int64_t)p.index_ctas * TOKENS;
+  int64_t t = (int64_t)blockIdx.x * TOKENS + (G == 1 ? group : 0);
+  int pos = token_position(p, t, flags);
+  for (int64_t t0 = (int64_t)blockIdx.x * TOKENS, n = 0; t0 < p.T; t0 += step, t += step, ++n) {
+    uint4 v[16 / L] = {};
+    Angles<L> a = {};
+    if (pos >= 0) {
+      load_row<L>(p.x + t * p.x_token + g * p.x_head, j, v);
+      a.load(p.cos_sin + (int64_t)pos * 64, j, p.enc.pairs);
+    }
+    uint4 e[8 / L] = {};
+    if (JOINT && pos >= 0) load_row<L>(p.pe + t * p.pe_token, j, e);
+    const int next = token_position(p, t + step, flags);
+    Row<L> y;
+#pragma unroll
+    for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
+    if (!norm_rotate<L, NORM, SCALED>(y, p.enc, a, j) && pos >= 0) flags |= TE_UNSOUND;
+    float m = max_lanes<G == 1 ? L : 32>(transform<L, HAD>(y, j));
+    if constexpr (G > 1) {
+      if (lane == 0) s_max[n & 1][tid >> 5] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_max[n & 1][i]);
+    }
+    if (JOINT && pos >= 0) {
+      if (p.pe_pairs != p.enc.pairs) a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
+      rotate_pe<L>(e, a, p.pe_pairs);
+      store_row<L>(p.pe_out + t * p.po_token, j, e);
+    }
+    if (pos >= 0) {
+      store_codes<L, HAD>(p.codes + (t * G + g) * 128, y, m, j);
+      if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale<HAD>(m);
+    }
+    pos = next;
+  }
+}
 }  // namespace
 
-// CTAs [0, index_ctas): a step is one token of 64 rows (G = 64) or 64 tokens of
-// one (G = 1).  The others rotate rope rows, 64 a step.
+// CTAs [0, index_ctas) encode rows, the others rotate rope rows, 64 a step.
 template <int G, bool NORM, bool HAD, bool JOINT>
 __global__ void __launch_bounds__(THREADS<G>, CTAS<G>) encode_kernel(const EncodeParams p) {
   pdl_enter();
-  constexpr int L = LANES<G>, WARPS = THREADS<G> / 32, TOKENS = TE_ROWS / G;  // per step
-  __shared__ float s_max[2][WARPS];
-  const int tid = threadIdx.x, j = tid % L, lane = tid & 31, group = tid / L;
-  bool bad = false;
-  auto position = [&](int64_t t) {  // -1: padding, or nothing
-    const int pos = t < p.T ? p.positions[t] : -1;
-    if (pos < p.max_positions) return pos;
-    bad = true;
-    return -1;
-  };
+  constexpr int L = LANES<G>;
+  __shared__ float s_max[2][THREADS<G> / 32];
+  int flags = 0;
   if (blockIdx.x < (unsigned)p.index_ctas) {
-    const int g = G == 1 ? 0 : group;
-    const int64_t step = (int64_t)p.index_ctas * TOKENS;
-    int64_t t = (int64_t)blockIdx.x * TOKENS + (G == 1 ? group : 0);
-    int pos = position(t);
-    for (int64_t t0 = (int64_t)blockIdx.x * TOKENS, n = 0; t0 < p.T; t0 += step, t += step, ++n) {
-      uint4 v[16 / L] = {};
-      Angles<L> a = {};
-      if (pos >= 0) {
-        load_row<L>(p.x + t * p.x_token + g * p.x_head, j, v);
-        a.load(p.cos_sin + (int64_t)pos * 64, j, p.enc.pairs);
-      }
-      uint4 e[8 / L] = {};
-      if (JOINT && pos >= 0) load_row<L>(p.pe + t * p.pe_token, j, e);
-      const int next = position(t + step);
-      Row<L> y;
-#pragma unroll
-      for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
-      norm_rotate<L, NORM>(y, p.enc, a, j);
-      float m = max_lanes<G == 1 ? L : 32>(transform<L, HAD>(y, j));
-      if constexpr (G > 1) {
-        if (lane == 0) s_max[n & 1][tid >> 5] = m;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < WARPS; ++i) m = fmaxf(m, s_max[n & 1][i]);
-      }
-      if (JOINT && pos >= 0) {
-        if (p.pe_pairs != p.enc.pairs) a.load(p.cos_sin + (int64_t)pos * 64, j, p.pe_pairs);
-        rotate_pe<L>(e, a, p.pe_pairs);
-        store_row<L>(p.pe_out + t * p.po_token, j, e);
-      }
-      if (pos >= 0) {
-        store_codes<L, HAD>(p.codes + (t * G + g) * 128, y, m, j);
-        if (G == 1 ? j == 0 : tid == 0) p.scale[t] = encode_scale<HAD>(m);
-      }
-      pos = next;
-    }
+    encode_rows<G, NORM, HAD, JOINT, false>(p, s_max, flags);
+    // a CTA that has met a row too large or too small to be squared takes its tokens once more, whose rope parts are done
+    // (a vote on every row instead made 131072 keys 31.7 us)
+    if (NORM && __syncthreads_or(flags & TE_UNSOUND)) encode_rows<G, NORM, HAD, false, true>(p, s_max, flags);
   } else {
+    const int j = threadIdx.x % L, group = threadIdx.x / L;
     const int64_t rows = (int64_t)p.T * p.H, step = (int64_t)(gridDim.x - p.index_ctas) * TE_ROWS;
     for (int64_t row = (int64_t)(blockIdx.x - p.index_ctas) * TE_ROWS + group; row < rows; row += step) {
       const int64_t t = rows < (1ll << 31) ? (int)row / p.H : row / p.H;
-      const int h = (int)(row - t * p.H), pos = position(t);
+      const int h = (int)(row - t * p.H), pos = token_position(p, t, flags);
       uint4 v[8 / L];
       load_row<L>(p.pe + t * p.pe_token + h * p.pe_head, j, v);
       if (pos < 0) continue;
@@ -342,7 +391,7 @@ __global__ void __launch_bounds__(THREADS<G>, CTAS<G>) encode_kernel(const Encod
       store_row<L>(p.pe_out + t * p.po_token + h * p.po_head, j, v);
     }
   }
-  last_cta(p.status, bad);
+  last_cta(p.status, flags & TE_BAD);
 }
 
 template <int G, bool NORM, bool HAD, bool JOINT>
@@ -417,12 +466,55 @@ __device__ __forceinline__ Place place_token(const AppendParams& p, int64_t t, b
   else r.slot = (int64_t)page * PAGE + s % PAGE;
   return r;
 }
+constexpr int AP_TOKENS = 4, AP_LANES = LANES<1>, AP_THREADS = THREADS<1>, AP_CTAS = CTAS<1>;
+
+// The rope parts (but for SCALED, where they are done) and index keys of a CTA's tokens, four lanes each.  True: some key
+// of this thread has to be taken SCALED.
+template <bool NORM, bool HAD, bool SCALED>
+__device__ __forceinline__ bool append_rows(const AppendParams& p, bool& bad) {
+  constexpr int L = AP_LANES;
+  const int tid = threadIdx.x, j = tid % L;
+  bool unsound = false;
+  // (every lane takes part in the shuffles)
+  for (int64_t t0 = (int64_t)blockIdx.x * TE_ROWS; t0 < p.T; t0 += (int64_t)p.row_ctas * TE_ROWS) {
+    const int64_t t = t0 + tid / L;
+    uint4 e[8 / L] = {}, v[16 / L] = {};
+    if (t < p.T) {
+      if (!SCALED) load_row<L>(p.k_pe + t * p.kp_stride, j, e);
+      if (p.index_k) load_row<L>(p.index_k + t * p.ik_stride, j, v);
+    }
+    const Place at = place_token(p, t, bad);
+    const float* cs = p.cos_sin + (int64_t)at.pos * 64;
+    Angles<L> a = {};
+    if (at.slot >= 0) {
+      a.load(cs, j, p.pe_pairs);
+      if (!SCALED) {
+        rotate_pe<L>(e, a, p.pe_pairs);
+        store_row<L>(p.kpe + at.slot * p.kpe_stride, j, e);
+        if (p.k_pe_out) store_row<L>(p.k_pe_out + t * p.kp_out_stride, j, e);
+      }
+    }
+    if (p.index_k) {
+      if (at.slot >= 0 && p.enc.pairs != p.pe_pairs) a.load(cs, j, p.enc.pairs);
+      Row<L> y;
+#pragma unroll
+      for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
+      const bool sound = norm_rotate<L, NORM, SCALED>(y, p.enc, a, j);
+      unsound |= at.slot >= 0 && !sound;
+      const float m = max_lanes<L>(transform<L, HAD>(y, j));
+      if (at.slot >= 0) {
+        store_codes<L, HAD>(p.k_cache + at.slot * 128, y, m, j);
+        if (j == 0) p.k_scale[at.slot] = encode_scale<HAD>(m);
+      }
+    }
+  }
+  return unsound;
+}
 }  // namespace
 
 // CTAs [0, row_ctas): four lanes per token rotate the rope part and encode the
 // index key.  The others: a warp normalises the latents of AP_TOKENS tokens at a time, 16 dims
 // per lane, so that enough loads are in flight.
-constexpr int AP_TOKENS = 4, AP_LANES = LANES<1>, AP_THREADS = THREADS<1>, AP_CTAS = CTAS<1>;
 template <bool NORM, bool HAD>
 __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const AppendParams p) {
   pdl_enter();
@@ -449,11 +541,24 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const Appen
           unpack8(v[i][1], y + 4);
 #pragma unroll
           for (int x = 0; x < 8; ++x) s2 = fma2(y[x], y[x], s2);
-          const float2 ss = unpack2(s2);
-          float s = ss.x + ss.y;
+          float t = sum_warp(unpack2(s2)) * (1.f / LA_DC) + p.c_eps;
+          if (!sound_square(t)) {  // (the same in the whole warp) too large or too small to be squared
+            float m = 0.f;
 #pragma unroll
-          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          const float r = rsqrtf(s * (1.f / LA_DC) + p.c_eps);
+            for (int x = 0; x < 8; ++x) {
+              const float2 u = unpack2(y[x]);
+              m = max_abs3(m, u.x, u.y);
+            }
+            const float k = unit_scale(fmaxf(max_lanes<32>(m), sqrtf(p.c_eps)));
+            s2 = 0;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              y[x] = fmul2(y[x], pack2(k, k));
+              s2 = fma2(y[x], y[x], s2);
+            }
+            t = sum_warp(unpack2(s2)) * (1.f / LA_DC) + p.c_eps * k * k;
+          }
+          const float r = rsqrtf(t);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float4 g = *reinterpret_cast<const float4*>(p.c_norm + 256 * (x >> 1) + 8 * lane + 4 * (x & 1));
@@ -471,38 +576,8 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const Appen
       }
     }
   } else {
-    constexpr int L = AP_LANES;
-    const int j = tid % L;
-    // (every lane takes part in the shuffles)
-    for (int64_t t0 = (int64_t)blockIdx.x * TE_ROWS; t0 < p.T; t0 += (int64_t)p.row_ctas * TE_ROWS) {
-      const int64_t t = t0 + tid / L;
-      uint4 e[8 / L] = {}, v[16 / L] = {};
-      if (t < p.T) {
-        load_row<L>(p.k_pe + t * p.kp_stride, j, e);
-        if (p.index_k) load_row<L>(p.index_k + t * p.ik_stride, j, v);
-      }
-      const Place at = place_token(p, t, bad);
-      const float* cs = p.cos_sin + (int64_t)at.pos * 64;
-      Angles<L> a = {};
-      if (at.slot >= 0) {
-        a.load(cs, j, p.pe_pairs);
-        rotate_pe<L>(e, a, p.pe_pairs);
-        store_row<L>(p.kpe + at.slot * p.kpe_stride, j, e);
-        if (p.k_pe_out) store_row<L>(p.k_pe_out + t * p.kp_out_stride, j, e);
-      }
-      if (p.index_k) {
-        if (at.slot >= 0 && p.enc.pairs != p.pe_pairs) a.load(cs, j, p.enc.pairs);
-        Row<L> y;
-#pragma unroll
-        for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
-        norm_rotate<L, NORM>(y, p.enc, a, j);
-        const float m = max_lanes<L>(transform<L, HAD>(y, j));
-        if (at.slot >= 0) {
-          store_codes<L, HAD>(p.k_cache + at.slot * 128, y, m, j);
-          if (j == 0) p.k_scale[at.slot] = encode_scale<HAD>(m);
-        }
-      }
-    }
+    const bool unsound = append_rows<NORM, HAD, false>(p, bad);
+    if (NORM && __syncthreads_or(unsound)) append_rows<NORM, HAD, true>(p, bad);
   }
   // new_lens may be seq_lens itself: it is written where every CTA has read what it needs
   if (last_cta(p.status, bad)) {

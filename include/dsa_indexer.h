@@ -394,7 +394,8 @@ typedef enum {
  * negative is padding, and one at or past max_positions is DSA_ERR_RANGE
  * (dsa_latent_last_status): their outputs stay as they were.  x must be finite, and
  * y below 2^120 in magnitude before a Hadamard transform; a token with more, an
- * infinity or NaN has undefined codes and scale.
+ * infinity or NaN has undefined codes and scale, and so has one whose row is
+ * constant under a norm with norm_eps = 0.
  *
  *   x [T, G, 128] bf16, G = 64 or 1, or null        codes [T, G, 128] e4m3   scale [T] fp32
  *   pe [T, H, 64] bf16, or null                     pe_out [T, H, 64] bf16 (may be pe, with its strides)

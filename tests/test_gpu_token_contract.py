@@ -4,7 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_token_ops import B, BF16, MAXPOS, Pages, _ints, _normal, _np, _table, _tokens  # noqa: F401
+from oracle import token_encode as te
+from test_gpu_token_ops import (B, BF, BF16, MAXPOS, Pages, _ints, _normal, _np, _np_norm, _table, _tokens,  # noqa: F401
+                                check_codes)
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +210,51 @@ def test_threads_append_on_their_streams_at_once(B):  # noqa: F811
 
     with ThreadPoolExecutor(4) as pool:
         assert list(pool.map(work, range(4))) == [0] * 4
+
+
+# ------------------------------------------------------------------- norms --
+SIZES = [1e-38, 1e-30, 1e-22, 1e-12, 1e15, 3e18, 1e25, 1e38]
+
+
+def _sized(g, size, *shape):
+    """Normal values times `size`, as far as bf16 goes."""
+    return (torch.randn(shape, generator=g, dtype=torch.float64) * size).clamp(-3.3e38, 3.3e38).to(BF16)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-6, 1e20])
+@pytest.mark.parametrize("G,had", [(64, True), (1, False)])
+def test_layer_norm_of_rows_of_any_size(B, G, had, eps):  # noqa: F811
+    """A norm's result does not depend on whether the squares of its row fit fp32; rows of all sizes in one call, so that
+    warps and tokens mix them.  The bounds are those of every encoding, relative to the norm's own terms: a power of two
+    loses nothing, and eps times two of them one rounding, or all of what is below 2^-149 of a sum of at least 1/128."""
+    g, table, T = torch.Generator().manual_seed(31), _table(), 8 * len(SIZES)
+    x = torch.stack([_sized(g, SIZES[t % len(SIZES)], G, 128) for t in range(T)])
+    x[5] = torch.stack([_sized(g, SIZES[(3 * r) % len(SIZES)], 128) for r in range(G)])  # and one token that has them all
+    pos, nm = torch.arange(T, dtype=torch.int32), (torch.randn(128, generator=g), torch.randn(128, generator=g), eps)
+    codes, s, _ = B.indexer_encode(x.cuda(), table.cuda(), pos.cuda(), norm=(nm[0].cuda(), nm[1].cuda(), eps), hadamard=had)
+    # (the oracle works out the square of eps' fp32 value)
+    y, reach = te.index_rows(_np(x), _np(table)[:T], (_np(nm[0]), _np(nm[1]), float(np.float32(eps))), False, had)
+    assert B.latent_last_status() == 0
+    check_codes(codes, s, y, reach)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-6, 1e20])
+def test_append_norms_of_any_size(B, eps):  # noqa: F811
+    g, table, T = torch.Generator().manual_seed(32), _table(), 8 * len(SIZES) + 3
+    c = torch.stack([_sized(g, SIZES[t % len(SIZES)], 512) for t in range(T)])
+    ik = torch.stack([_sized(g, SIZES[t % len(SIZES)], 128) for t in range(T)])
+    k_pe, p = _normal(g, T, 64), Pages([T + 9], seed=33)
+    # (weights that keep the smallest results in bf16's normal range: x / sqrt(eps) is 1e-48 and more of 1e-38 and 1e20)
+    w = (1 + 0.3 * torch.rand(512, generator=g)) * (1e20 if eps > 1 else 1.0)
+    nm = torch.randn(128, generator=g), torch.randn(128, generator=g), float(np.float32(eps))
+    B.latent_cache_append(c.cuda(), k_pe.cuda(), table.cuda(), _ints([0, T]), p.table.cuda(), _ints([9]), p.ckv, p.kpe,
+                          c_norm=(w.cuda(), eps), index_k=ik.cuda(), index_norm=(nm[0].cuda(), nm[1].cuda(), eps),
+                          hadamard=True, k_cache=p.kc, k_cache_scale=p.ks)
+    assert B.latent_last_status() == 0
+    s = p.slots(0, 9, T)
+    want, got = te.rms_norm(_np(c), _np(w), float(np.float32(eps))), _np(p.ckv).reshape(-1, 512)[s]
+    # below bf16's normal range a step is 2^-133, and below fp32's a product's half a step of 2^-149 comes before it
+    assert np.all(np.abs(got - want) <= (BF + 2.0 ** -18) * np.abs(want) + 2.0 ** -133)
+    at = torch.from_numpy(s).cuda()
+    check_codes(p.kc.view(-1, 128)[at][:, None], p.ks.view(-1)[at],
+                *te.index_rows(_np(ik)[:, None], _np(table)[9:9 + T], _np_norm(nm), False, True))
