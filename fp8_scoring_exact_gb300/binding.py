@@ -367,8 +367,9 @@ def _latent_cache(ckv, kpe):
     """(ckv, its slot stride, kpe, its slot stride), pages of a cache [P,64,512] and [P,64,64]; either
     may be part of a wider array (slots evenly spaced)."""
     pages = ckv.shape[0] if isinstance(ckv, torch.Tensor) and ckv.dim() else 0
-    if (isinstance(kpe, torch.Tensor) and ckv.is_cuda and kpe.is_cuda and ckv.dtype is kpe.dtype is _BF16 and
-            ckv.shape == (pages, 64, LATENT_DC) and kpe.shape == (pages, 64, LATENT_DP)):  # (nothing to refuse, in short)
+    if (isinstance(ckv, torch.Tensor) and isinstance(kpe, torch.Tensor) and ckv.is_cuda and kpe.is_cuda and
+            ckv.dtype is kpe.dtype is _BF16 and ckv.shape == (pages, 64, LATENT_DC) and
+            kpe.shape == (pages, 64, LATENT_DP)):  # (nothing to refuse, in short)
         (a0, a1, a2), (b0, b1, b2) = ckv.stride(), kpe.stride()
         if a2 == b2 == 1 and a0 == 64 * a1 and b0 == 64 * b1:
             return (ckv.data_ptr(), a1, kpe.data_ptr(), b1), pages
