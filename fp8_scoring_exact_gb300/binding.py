@@ -473,6 +473,15 @@ def _rows_here(t, name, shape, dev):
     raise _refusal(t, name, shape, _BF16, dev)
 
 
+def _axes(t, name, layout):
+    """Shape of a tensor of as many axes as `layout` names."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != layout.count(",") + 1:
+        raise ValueError(f"{name} must be [{layout}], got {list(t.shape)}")
+    return t.shape
+
+
 def _current_device(t):
     """Index of the current device; `t`: some tensor of the call (without a CUDA tensor CUDA is not asked)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -485,9 +494,7 @@ def _pages_here(ckv, kpe, block_table, seq_lens, dev):
     cache, pages = _latent_cache(ckv, kpe)
     if not ckv.get_device() == kpe.get_device() == dev:
         raise ValueError(f"the caches must be on the current device, {dev}")
-    shape = block_table.shape
-    if len(shape) != 2:
-        raise ValueError(f"block_table must be [B,max_pages], got {list(shape)}")
+    shape = _axes(block_table, "block_table", "B,max_pages")
     return (cache, (_here(block_table, "block_table", shape, _I32, dev),
                     _here(seq_lens, "seq_lens", shape[:1], _I32, dev)), (*shape, pages))
 
@@ -515,7 +522,7 @@ def latent_attention_tree(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_l
     draft_lens[b] are padding: zeros and lse -inf."""
     dev = _current_device(q_nope)
     cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
-    nn, H = q_nope.shape[1:3] if q_nope.dim() == 4 else (0, 0)
+    nn, H = _axes(q_nope, "q_nope", "B,next_n,H,512")[1:3]
     shape, rows = (B, nn, H, LATENT_DC), (B, nn, H)
     queries = _here(q_nope, "q_nope", shape, _BF16, dev), _here(q_pe, "q_pe", (B, nn, H, LATENT_DP), _BF16, dev)
     mask = _here(tree_mask, "tree_mask", (B, nn, (nn + 63) // 64), torch.int64, dev)
@@ -542,7 +549,7 @@ def latent_cache_accept(ckv_cache, kpe_cache, block_table, seq_lens, draft_lens,
     dev = _current_device(ckv_cache)
     cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
     keys = _index_cache(k_cache, k_cache_scale, pages, dev)
-    width = path.shape[-1] if path.dim() else 0
+    width = _axes(path, "path", "B,max_path")[1]
     nodes = _here(path, "path", (B, width), _I32, dev)
     if new_lens is None:
         new_lens = _new((B,), _I32, ckv_cache.device, stream)
@@ -572,7 +579,7 @@ def _layer_norm(norm, name, dev):
 
 
 def _rotation_table(cos_sin, dev):
-    n = cos_sin.shape[0] if cos_sin.dim() else 0
+    n = _axes(cos_sin, "cos_sin", "max_positions,64")[0]
     return _here(cos_sin, "cos_sin", (n, LATENT_DP), _F32, dev), n
 
 
@@ -592,7 +599,7 @@ def indexer_encode(x, cos_sin, positions, norm=None, interleaved=False, hadamard
     rows = parts = out = (None, 0, 0)
     to = (None, None)
     if x is not None:
-        G = x.shape[1] if x.dim() == 3 else 0
+        G = _axes(x, "x", "T,G,128")[1]
         if G != HEADS and G != 1:
             raise ValueError(f"x must be [T,64,128] or [T,1,128], got {list(x.shape)}")
         shape = (T, G, HEAD_DIM)
@@ -609,7 +616,7 @@ def indexer_encode(x, cos_sin, positions, norm=None, interleaved=False, hadamard
     elif norm is not None or codes is not None or scale is not None:
         raise ValueError("norm, codes and scale go with x")
     if pe is not None:
-        H = pe.shape[1] if pe.dim() == 3 else 0
+        H = _axes(pe, "pe", "T,H,64")[1]
         shape = (T, H, LATENT_DP)
         parts = _rows_here(pe, "pe", shape, dev)
         if pe_out is None:
@@ -636,7 +643,7 @@ def latent_cache_append(c, k_pe, cos_sin, cu_new, block_table, seq_lens, ckv_cac
     [P,64].  positions int32 [T]: of the angles, by default a token's place in its sequence.  c_out and k_pe_out get
     what the cache gets.  Returns new_lens int32 [B], which may be seq_lens itself."""
     dev = _current_device(c)
-    T = c.shape[0]
+    T = _axes(c, "c", "T,512")[0]
     rows, parts = _rows_here(c, "c", (T, LATENT_DC), dev), _rows_here(k_pe, "k_pe", (T, LATENT_DP), dev)
     cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
     keys = _index_cache(k_cache, k_cache_scale, pages, dev)

@@ -258,3 +258,47 @@ def test_append_norms_of_any_size(B, eps):  # noqa: F811
     at = torch.from_numpy(s).cuda()
     check_codes(p.kc.view(-1, 128)[at][:, None], p.ks.view(-1)[at],
                 *te.index_rows(_np(ik)[:, None], _np(table)[9:9 + T], _np_norm(nm), False, True))
+
+
+# --------------------------------------------------------------- refusals --
+def test_arguments_of_any_kind_are_refused_not_taken(B):  # noqa: F811
+    """Every tensor argument in turn as something else: an exception of the bindings' own kinds, and nothing launched."""
+    def z(*shape, dtype=BF16):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    i32, f32 = dict(dtype=torch.int32), dict(dtype=torch.float32)
+    table, norm = z(100, 64, **f32), (z(128, **f32), z(128, **f32), 1e-6)
+    cache = dict(ckv_cache=z(3, 64, 512), kpe_cache=z(3, 64, 64), block_table=z(2, 2, **i32), seq_lens=z(2, **i32))
+    keys = dict(k_cache=z(3, 64, 128, dtype=torch.uint8), k_cache_scale=z(3, 64, **f32))
+    calls = {
+        B.indexer_encode: dict(x=z(4, 64, 128), cos_sin=table, positions=z(4, **i32), pe=z(4, 2, 64), pe_out=z(4, 2, 64),
+                               codes=z(4, 64, 128, dtype=torch.uint8), scale=z(4, **f32), norm=norm),
+        B.latent_cache_append: dict(c=z(4, 512), k_pe=z(4, 64), cos_sin=table, cu_new=z(3, **i32), **cache, **keys,
+                                    c_norm=(z(512, **f32), 1e-6), index_k=z(4, 128), index_norm=norm,
+                                    positions=z(4, **i32), c_out=z(4, 512), k_pe_out=z(4, 64), new_lens=z(2, **i32)),
+        B.latent_attention_tree: dict(q_nope=z(2, 3, 16, 512), q_pe=z(2, 3, 16, 64), **cache, sm_scale=0.1,
+                                      tree_mask=z(2, 3, 1, dtype=torch.int64), draft_lens=z(2, **i32),
+                                      out=z(2, 3, 16, 512), lse=z(2, 3, 16, **f32)),
+        B.latent_cache_accept: dict(**cache, **keys, draft_lens=z(2, **i32), path=z(2, 5, **i32), path_lens=z(2, **i32),
+                                    new_lens=z(2, **i32))}
+    optional = {"pe_out", "codes", "scale", "norm", "positions", "c_norm", "index_norm", "c_out", "k_pe_out", "new_lens",
+                "draft_lens", "out", "lse"}
+    before = B.launch_count()
+    for fn, args in calls.items():
+        for name, value in args.items():
+            if isinstance(value, float):
+                continue
+            if isinstance(value, tuple):
+                wrong = [(None, *value[1:]), (value[0].cpu(), *value[1:]), (value[0][None], *value[1:])]
+            else:
+                wrong = [3, [1, 2], "x", value.cpu(), value[0], value[None], value.double(), value.reshape(-1)[:1]]
+                if name not in optional or (fn is B.indexer_encode and name == "positions") or (
+                        fn is B.latent_cache_accept and name == "draft_lens"):
+                    wrong.append(None)
+            for v in wrong:
+                if fn is B.indexer_encode and name in ("x", "pe") and v is None:
+                    continue  # (optional, but for what goes with them)
+                with pytest.raises((TypeError, ValueError, B.IndexerError)):
+                    fn(**dict(args, **{name: v}))
+                    pytest.fail(f"{fn.__name__}: {name} was taken")
+    assert B.launch_count() == before
