@@ -91,6 +91,15 @@ bool usable_stride(int64_t& stride, int64_t extent, int64_t instead) {
   return stride > 0 && !(stride & 7) && stride < (1ll << 38);
 }
 
+// Whether rows that are written lie apart: [n1, n2] of them, of `row` elements, one axis within the other's stride.
+bool rows_apart(int64_t s1, int64_t n1, int64_t s2, int64_t n2, int64_t row) {
+  auto within = [&](int64_t outer, int64_t n_outer, int64_t inner, int64_t n_inner) {
+    if (n_inner > 1 && inner < row) return false;
+    return n_outer == 1 || (outer >= row && (n_inner == 1 || (outer - row) / inner >= n_inner - 1));
+  };
+  return within(s1, n1, s2, n2) || within(s2, n2, s1, n1);
+}
+
 // Index rows' LayerNorm and order of pairs.
 bool usable_encoding(RowEncoding& e, const float* w, const float* b, float eps, int flags) {
   if (!w != !b || !aligned16(w) || !aligned16(b) || (w && !(eps >= 0.f && eps <= 3.4e38f))) return false;
@@ -344,7 +353,8 @@ int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_t x_head
             !usable_stride(x_head_stride, G, DSA_HEAD_DIM)))
     return DSA_ERR_ARG;
   if (pe && (H <= 0 || !usable_stride(pe_token_stride, T, LA_DP) || !usable_stride(pe_head_stride, H, LA_DP) ||
-             !usable_stride(po_token_stride, T, LA_DP) || !usable_stride(po_head_stride, H, LA_DP)))
+             !usable_stride(po_token_stride, T, LA_DP) || !usable_stride(po_head_stride, H, LA_DP) ||
+             !rows_apart(po_token_stride, T, po_head_stride, H, LA_DP)))
     return DSA_ERR_ARG;
   // in place only element by element
   if (pe && pe == pe_out && (pe_token_stride != po_token_stride || pe_head_stride != po_head_stride)) return DSA_ERR_ARG;
@@ -394,6 +404,7 @@ int dsa_latent_cache_append(const uint16_t* c, int64_t c_stride, const uint16_t*
       (index_k && !usable_stride(index_k_stride, T, DSA_HEAD_DIM)) || (c_out && !usable_stride(c_out_stride, T, LA_DC)) ||
       (k_pe_out && !usable_stride(k_pe_out_stride, T, LA_DP)))
     return DSA_ERR_ARG;
+  if ((c_out && c_out_stride < LA_DC) || (k_pe_out && k_pe_out_stride < LA_DP)) return DSA_ERR_ARG;
   if (ckv_stride < LA_DC || kpe_stride < LA_DP || (ckv_stride & 7) || (kpe_stride & 7)) return DSA_ERR_ARG;
   for (const void* q : {(const void*)c, (const void*)k_pe, (const void*)index_k, (const void*)c_norm,
                         (const void*)cos_sin, (const void*)ckv, (const void*)kpe, (const void*)k_cache,

@@ -402,8 +402,8 @@ typedef enum {
  *   norm_weight, norm_bias [128] fp32, or both null
  *   cos_sin [max_positions, 64] fp32: 32 cosines, then 32 sines, of each position's angles
  *   positions [T] int32
- *   token and head strides in elements, positive multiples of 8, of an axis of one element anything;
- *   all arrays but scale and positions 16-byte aligned
+ *   token and head strides in elements, positive multiples of 8, of an axis of one element anything; pe_out's rows
+ *   lie apart, one axis within the other's stride; all arrays but scale and positions 16-byte aligned
  */
 DSA_API int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_t x_head_stride, int G,
                                const float* norm_weight, const float* norm_bias, float norm_eps,
@@ -428,7 +428,8 @@ DSA_API int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_
  *   c_norm [512] fp32 or null        index_norm_weight, index_norm_bias [128] fp32, or both null
  *   cu_new [B + 1] int32, ascending, within [0, T]; tokens outside every sequence are padding
  *   positions [T] int32 or null      c_out [T, 512], k_pe_out [T, 64] bf16 or null (may be c and k_pe)
- *   strides in elements, as in dsa_indexer_encode    new_lens [B] int32 (may be seq_lens itself)
+ *   strides in elements, as in dsa_indexer_encode, of c_out and k_pe_out at least a row
+ *   new_lens [B] int32 (may be seq_lens itself)
  *
  * A sequence whose border, length or new length does not fit the arrays or its
  * table is skipped (new_lens[b] = seq_lens[b]); a token whose position is outside
