@@ -4,9 +4,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import latent_attention as la
 from oracle import token_encode as te
-from test_gpu_token_ops import (B, BF, BF16, MAXPOS, Pages, _ints, _normal, _np, _np_norm, _table, _tokens,  # noqa: F401
-                                check_codes)
+from test_gpu_token_ops import (B, BF, BF16, MAXPOS, Cache, Pages, _check_tree, _ints, _mask, _normal, _np,  # noqa: F401
+                                _np_norm, _queries, _random_tree, _seen_of, _table, _tokens, _tree, check_codes)
 
 pytestmark = pytest.mark.gpu
 
@@ -302,3 +303,49 @@ def test_arguments_of_any_kind_are_refused_not_taken(B):  # noqa: F811
                     fn(**dict(args, **{name: v}))
                     pytest.fail(f"{fn.__name__}: {name} was taken")
     assert B.launch_count() == before
+
+
+# ------------------------------------------- more work than threads or CTAs --
+def _tree_call(B, nn, H, seqs, seed):  # noqa: F811
+    """A tree's call over sequences of (length, nodes), one node of each that nobody sees holding NaN or infinity,
+    padding queries NaN; held against the oracle, and run again for the same bits."""
+    rng = np.random.default_rng(seed)
+    lens, drafts = [a for a, _ in seqs], [n for _, n in seqs]
+    c = Cache(lens, seed=seed)
+    seen = [_seen_of(_random_tree(rng, n)) for n in drafts]
+    for b, n in enumerate(drafts):
+        if n > 2:
+            j = int(rng.integers(1, n))
+            seen[b] = [s - {j} for s in seen[b]]
+            slot = la.slots_of(c.table[b].numpy(), lens[b])[lens[b] - n + j]
+            c.data.view(-1, 576)[slot] = float("nan") if b % 2 else float("inf")
+    qn, qp = _queries(len(lens), nn, H, seed=seed + 1)
+    for b, n in enumerate(drafts):
+        qn[b, n:] = float("nan")
+    mask = _mask(seen, nn)
+    out, lse = _tree(B, c, qn, qp, mask, drafts)
+    assert B.latent_last_status() == 0
+    again, lse2 = _tree(B, c, qn, qp, mask, drafts)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16)) and torch.equal(lse2, lse)
+    c.data = torch.nan_to_num(c.data, nan=0.0, posinf=0.0)
+    _check_tree(c, qn, qp, out, lse, seen)
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 7, 40])
+@pytest.mark.parametrize("nn,H,n", [(5, 16, 450), (5, 30, 260), (3, 16, 700)])
+def test_tree_of_more_items_than_threads(B, nn, H, n, ctas):  # noqa: F811
+    """Items are numbered in rounds of a CTA's threads (384, or 352): one or two blocks of 128 rows a sequence, and
+    blocks of 64; many items a run, and whole ones, or without a key."""
+    seqs = [(i * 7 % 301, min(i * 7 % 301, i * 5 % (nn + 1))) for i in range(n)]
+    B.set_option("grid_ctas", ctas)
+    try:
+        _tree_call(B, nn, H, seqs, seed=n + ctas)
+    finally:
+        B.set_option("grid_ctas", 0)
+
+
+@pytest.mark.parametrize("nn,H,seqs", [(8, 16, [(33000, 8)]), (5, 16, [(131080, 5)]), (2, 16, [(131080, 2)]),
+                                       (40, 16, [(70000, 33), (300, 40)])])
+def test_tree_behind_long_histories(B, nn, H, seqs):  # noqa: F811
+    """Rows cut into a piece for nearly every pair of CTAs, which are joined by eight warps in several rounds."""
+    _tree_call(B, nn, H, seqs, seed=nn)
