@@ -595,7 +595,13 @@ cudaError_t launch_tree_pair(const LatentMaps& m, const LatentAttnParams& p, cud
   e = launch_pdl(tree_pair_kernel, dim3(2 * p.grid), dim3(TP_THREADS), TP_SMEM, s, m, p);
   if (e != cudaSuccess) return e;
   count_launch();
-  if (p.grid > 8 * p.items)  // rows of many pieces
+  // Eight warps a strip where rows have many pieces.  The whole call, us in a graph by eight warps and by one, 76 pairs:
+  //     blocks      1           2           4           5           6           7           8           16
+  //     keys 4096                       21  22      22  22      23  23      24  23
+  //         16384                       28  36      36  38      41  43      45  45
+  //         32768   21  50      24  43      46  53                  60  62                  78  75      130 120
+  // (40 pairs, 16384 keys: 2 blocks 25  28, 3 28  28, 4 32  32, 5 41  39.)
+  if (p.grid > 12 * p.items)
     return launch_pdl(tree_join_kernel<8>, dim3(p.items, 4, 32), dim3(TJ_THREADS), 0, s, p);
   return launch_pdl(tree_join_kernel<1>, dim3(p.items, 4, 4), dim3(TJ_THREADS), 0, s, p);
 }
