@@ -308,27 +308,24 @@ __device__ __forceinline__ void rotate_pe(uint4 (&v)[8 / L], const Angles<L>& a,
   for (int i = 0; i < 8 / L; ++i) v[i] = pack8(y + 4 * i);
 }
 
-// What a thread notes: a position past the table; a row that has to be taken SCALED.  (In one register: with one each
-// 4096 query tokens with a norm took 42.7 us.)
-constexpr int TE_BAD = 1, TE_UNSOUND = 2;
-
 // The position of token t; -1: padding, or nothing.
-__device__ __forceinline__ int token_position(const EncodeParams& p, int64_t t, int& flags) {
+__device__ __forceinline__ int token_position(const EncodeParams& p, int64_t t, bool& bad) {
   const int pos = t < p.T ? p.positions[t] : -1;
   if (pos < p.max_positions) return pos;
-  flags |= TE_BAD;
+  bad = true;
   return -1;
 }
 
 // The index rows of a CTA's tokens, and with JOINT their rope parts: a step is one token of 64 rows (G = 64) or 64 tokens
-// of one (G = 1).
+// of one (G = 1).  s_unsound (in shared memory: a register more made 4096 query tokens with a norm 41.6 us instead of
+// 40.8): some row has to be taken SCALED.
 template <int G, bool NORM, bool HAD, bool JOINT, bool SCALED>
-__device__ __forceinline__ void encode_rows(const EncodeParams& p, float (*s_max)[THREADS<G> / 32], int& flags) {
+__device__ __forceinline__ void encode_rows(const EncodeParams& p, float (*s_max)[THREADS<G> / 32], int& s_unsound, bool& bad) {
   constexpr int L = LANES<G>, WARPS = THREADS<G> / 32, TOKENS = TE_ROWS / G;  // per step
   const int tid = threadIdx.x, j = tid % L, lane = tid & 31, group = tid / L, g = G == 1 ? 0 : group;
   const int64_t step = (int64_t)p.index_ctas * TOKENS;
   int64_t t = (int64_t)blockIdx.x * TOKENS + (G == 1 ? group : 0);
-  int pos = token_position(p, t, flags);
+  int pos = token_position(p, t, bad);
   for (int64_t t0 = (int64_t)blockIdx.x * TOKENS, n = 0; t0 < p.T; t0 += step, t += step, ++n) {
     uint4 v[16 / L] = {};
     Angles<L> a = {};
@@ -338,11 +335,11 @@ __device__ __forceinline__ void encode_rows(const EncodeParams& p, float (*s_max
     }
     uint4 e[8 / L] = {};
     if (JOINT && pos >= 0) load_row<L>(p.pe + t * p.pe_token, j, e);
-    const int next = token_position(p, t + step, flags);
+    const int next = token_position(p, t + step, bad);
     Row<L> y;
 #pragma unroll
     for (int c = 0; c < 16 / L; ++c) unpack8(v[c], y + 4 * c);
-    if (!norm_rotate<L, NORM, SCALED>(y, p.enc, a, j) && pos >= 0) flags |= TE_UNSOUND;
+    if (!norm_rotate<L, NORM, SCALED>(y, p.enc, a, j) && pos >= 0) s_unsound = 1;
     float m = max_lanes<G == 1 ? L : 32>(transform<L, HAD>(y, j));
     if constexpr (G > 1) {
       if (lane == 0) s_max[n & 1][tid >> 5] = m;
@@ -370,18 +367,26 @@ __global__ void __launch_bounds__(THREADS<G>, CTAS<G>) encode_kernel(const Encod
   pdl_enter();
   constexpr int L = LANES<G>;
   __shared__ float s_max[2][THREADS<G> / 32];
-  int flags = 0;
+  __shared__ int s_unsound;
+  bool bad = false;
   if (blockIdx.x < (unsigned)p.index_ctas) {
-    encode_rows<G, NORM, HAD, JOINT, false>(p, s_max, flags);
+    if constexpr (NORM) {
+      if (threadIdx.x == 0) s_unsound = 0;
+      __syncthreads();
+    }
+    encode_rows<G, NORM, HAD, JOINT, false>(p, s_max, s_unsound, bad);
     // a CTA that has met a row too large or too small to be squared takes its tokens once more, whose rope parts are done
     // (a vote on every row instead made 131072 keys 31.7 us)
-    if (NORM && __syncthreads_or(flags & TE_UNSOUND)) encode_rows<G, NORM, HAD, false, true>(p, s_max, flags);
+    if constexpr (NORM) {
+      __syncthreads();
+      if (s_unsound) encode_rows<G, NORM, HAD, false, true>(p, s_max, s_unsound, bad);
+    }
   } else {
     const int j = threadIdx.x % L, group = threadIdx.x / L;
     const int64_t rows = (int64_t)p.T * p.H, step = (int64_t)(gridDim.x - p.index_ctas) * TE_ROWS;
     for (int64_t row = (int64_t)(blockIdx.x - p.index_ctas) * TE_ROWS + group; row < rows; row += step) {
       const int64_t t = rows < (1ll << 31) ? (int)row / p.H : row / p.H;
-      const int h = (int)(row - t * p.H), pos = token_position(p, t, flags);
+      const int h = (int)(row - t * p.H), pos = token_position(p, t, bad);
       uint4 v[8 / L];
       load_row<L>(p.pe + t * p.pe_token + h * p.pe_head, j, v);
       if (pos < 0) continue;
@@ -391,12 +396,18 @@ __global__ void __launch_bounds__(THREADS<G>, CTAS<G>) encode_kernel(const Encod
       store_row<L>(p.pe_out + t * p.po_token + h * p.po_head, j, v);
     }
   }
-  last_cta(p.status, flags & TE_BAD);
+  last_cta(p.status, bad);
 }
 
 template <int G, bool NORM, bool HAD, bool JOINT>
 static cudaError_t launch_encode_as(EncodeParams p, cudaStream_t s) {
-  // both kinds of CTAs at once, in shares that end together
+  // Both kinds of CTAs at once; a rope row counts 3 quarters of an index row.  us in a graph with 1, 2, 3, 4 and 6:
+  //     tokens    16 heads                        5 heads                         64 heads
+  //     1000      15.1  11.4  11.0  12.5  13.1    15.1  10.9  10.7  10.6  10.7    17.4  14.1  13.9  15.8  17.3
+  //     2500      30.0  21.7  20.4  22.4  23.1    30.0  20.5  20.0  20.2  20.2    35.0  27.5  28.5  29.2  36.1
+  //     4096      46.2  32.0  30.4  32.8  34.7    45.6  30.2  28.1  29.4  29.6    54.2  41.2  42.2  44.6  54.7
+  //     6000      65.4  43.9  42.8  45.1  48.1    65.2  42.4  39.4  39.6  40.1    77.4  57.4  59.5  61.8  78.3
+  // (128 heads: 2 is faster by 3 to 7%)
   const int all = CTAS<G> * option_grid(), steps = !p.x ? 0 : G == 1 ? ceil_div(p.T, TE_ROWS) : p.T;
   const int64_t pe_rows = p.pe && !JOINT ? (int64_t)p.T * p.H : 0, pe_steps = (pe_rows + TE_ROWS - 1) / TE_ROWS;
   const int64_t share = 4 * (int64_t)steps + 3 * pe_steps;
@@ -598,7 +609,14 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) append_kernel(const Appen
 }
 
 cudaError_t launch_append(AppendParams p, cudaStream_t s) {
-  // both kinds of CTAs at once, in shares that end together
+  // Both kinds of CTAs at once.  us in a graph, CTAs for rope parts and index keys a sixth, a quarter, a third, 10/24 and
+  // a half of all:
+  //     tokens    with an index key               without
+  //     7000      12.7  10.0  10.0  10.0  10.0     9.0   8.9   8.7   8.8   8.8
+  //     16384     21.1  18.2  15.8  15.5  16.5    14.5  13.5  14.1  14.0  15.1
+  //     20000     24.7  19.8  18.5  18.4  18.2    16.2  14.6  16.2  16.6  16.2
+  //     30000     32.7  26.6  24.1  22.9  24.1    22.3  19.9  20.9  20.9  20.7
+  // (between 9000 and 60000 tokens without a key a quarter and a third are within 3%, either way)
   const int all = AP_CTAS * option_grid(), rows = ceil_div(p.T, TE_ROWS);
   const int latents = ceil_div(p.T, AP_THREADS / 32 * AP_TOKENS);
   p.row_ctas = min(rows, max(1, all / 3));
