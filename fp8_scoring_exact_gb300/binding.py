@@ -519,7 +519,7 @@ def latent_attention_tree(q_nope, q_pe, ckv_cache, kpe_cache, block_table, seq_l
     """latent_attention_paged for drafted tokens that form a tree: the last draft_lens[b] (int32 [B]; without it
     next_n, or all keys if there are fewer) of a sequence's keys are its nodes; query i sees the keys before them and
     node j where bit j % 64 of tree_mask[b, i, j // 64] is set (int64 [B, next_n, ceil(next_n / 64)]).  Queries past
-    draft_lens[b] are padding: zeros and lse -inf."""
+    draft_lens[b] are padding: zeros and lse -inf.  A node that any query sees has to be finite.  No key weights."""
     dev = _current_device(q_nope)
     cache, tables, (B, maxp, pages) = _pages_here(ckv_cache, kpe_cache, block_table, seq_lens, dev)
     nn, H = _axes(q_nope, "q_nope", "B,next_n,H,512")[1:3]

@@ -55,11 +55,13 @@ __device__ __forceinline__ bool last_cta(LatentStatus* st, bool bad) {
 }
 #endif
 
-// Row blocks of cached attention: an item is a block of up to n rows (16, 32 or
-// 64) with the keys its rows see, cut into tiles of one page.  An item with
+// Row blocks of cached attention: an item is a block of up to n rows with the keys
+// its rows see, cut into tiles: 16, 32 or 64 rows and tiles of one page, or, of
+// trees with more rows a sequence, 128 rows and tiles of two pages.  An item with
 // tiles counts item_units units and one per tile; the items' units are
-// numbered through, and CTA c of the grid takes units [c per, (c + 1) per): its
-// tiles in one item are a piece, whose id is item + c.
+// numbered through, and run c takes units [c per, (c + 1) per): its tiles in one item
+// are a piece, whose id is item + c.  A run is a CTA's, or, with 128 rows, that of a
+// pair of CTAs (cta_group::2).
 // What starting and ending a piece costs, in tiles: 2 without a prefix (128 rows of seven sequences: 70.2 us; 70.7 with
 // 4); 4 with one, where most of a sequence's own items are short and their pages cold (64 sequences behind 32768 shared
 // keys: 171 us with 2, 163 with 3, 159 with 4, 163 with 8).
@@ -94,11 +96,11 @@ struct LatentAttnParams {
   float* weights;               // [B, ld_weights] or null: += the softmax weight of every key
   int64_t ld_weights;
   LatentStatus* status;
-  // the call's row blocks and scratch
   // a tree of drafted tokens: the sequence's last keys (null tree_mask: next_n tokens in a row)
   const uint64_t* tree_mask;    // [B, next_n, mask_words]: node i sees node j where bit j % 64 of word j / 64 is set
   const int32_t* draft_lens;    // [B] nodes of a sequence, or null: next_n, or all its keys if it has fewer
   int mask_words;
+  // the call's row blocks and scratch
   int n;                        // rows per block (128: of a pair of CTAs; grid then counts pairs)
   int prefix_items, blocks;     // row blocks over the prefix (all sequences' rows), and per sequence
   int items, grid, item_units;
@@ -107,8 +109,9 @@ struct LatentAttnParams {
   int32_t* per;                 // [1] units per CTA
   // [grid, items + 1] ([2 grid, items + 1] for pairs of CTAs) first unit of each item, worked out by every CTA for itself
   int32_t* start;
-  // unnormalised outputs of the pieces ([128 / 4 dims, 128 rows, 4] each where they are a pair's): with a prefix all of them, [items + grid, n, 512]; without one those of cut
-  // items, of which a CTA has two at most, [2 grid, n, 512] (1: the one that starts with its item's first tile)
+  // unnormalised outputs of the pieces: with a prefix all of them, [items + grid, n, 512]; without one those of cut items,
+  // of which a run has two at most, [2 grid, n, 512] (1: the one that starts with its item's first tile); a pair's pieces
+  // are [512 / 4 dims, 128 rows, 4] each
   float* part_o;
   float2* part_ml;              // [items + grid, n]: reference maximum (base-2 units) and sum
   float* logits;                // [B, blocks, max_pages, 64, n] unscaled logits (-inf: not seen), for the key weights

@@ -15,23 +15,24 @@
 // (pairs (2 i, 2 i + 1) in e, pairs (i, i + 32) in c), and all Hadamard stages
 // but log2 L, which are shuffles.  The 64 rows of a query token take two lanes
 // each, which halves the shuffles (4096 tokens 30.3 us, 32.0 with four), single
-// rows four (131072 keys 28.6 us; 42 with two, whose norm and rope part spill).
+// rows four (131072 keys 28.6 us, and 42 with two, whose norm and rope part spill;
+// with four 8 or 22 bytes of a norm's builds do, or none).
 // Values stay fp32, two to a register pair for the packed arithmetic, between
 // the loads and the one rounding at the end.  CTAs stay and take every so manieth
 // token: with a CTA for each, what starting and ending it costs (the status among
 // it) was a third of the time.
 //
 // On the device, in a graph: 4096 query tokens with 16 rope rows each (118 MB)
-// 30.3 us, 3.9 TB/s, of which a start of 4; the index rows alone 27.0, without the
-// Hadamard transform 21.9; the rope rows alone 7.7.  The shared-memory path is 58%
-// busy, issue 31%.  CTAs per SM: three 33.7, five 32.3; a rope row counted as 2, 4
-// or 6 quarters of an index row instead of 3: 31.9, 32.4, 34.4.  Slower were also
+// 30.4 us, 3.9 TB/s, of which a start of 4; the index rows alone 27.1, without the
+// Hadamard transform 22.0, with a norm 36.6 (40.8 with the rope rows; a row's weights
+// are 16 loads a lane); the rope rows alone 7.7.  The shared-memory path is 58%
+// busy, issue 31%.  CTAs per SM: three 33.7, five 32.3.  Slower were also
 // the next token's rows in registers (33.8), rows fetched ahead by cp.async, and
 // the exchange of the last stages through shared memory; those stages on mma.sync
 // with values in three bf16 parts gained 3%, rows copied ahead by TMA 4% (with a
 // norm they lost 5%): neither was worth its code.
-// 131072 keys with norm and rope part (118 MB): 28.6 us; the index rows alone 21.4,
-// 16.5 without the norm, 13.7 without both.  16384 tokens appended (48 MB): 14 us.
+// 131072 keys with norm and rope part (118 MB): 28.0 us; the index rows alone 21.8,
+// 16.5 without the norm, 13.7 without both.  16384 tokens appended (48 MB): 16.2 us.
 #include <cuda_fp8.h>
 
 #include <limits.h>

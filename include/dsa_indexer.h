@@ -337,7 +337,10 @@ DSA_API int dsa_latent_attention_shared_prefix(const uint16_t* q_nope, const uin
  * them, or all its keys if it has fewer).  Query i, for every head, sees the
  * keys before the nodes and node j where bit j % 64 of tree_mask[b, i, j / 64] is
  * set (its ancestors and itself, or whatever is wanted); otherwise as
- * dsa_latent_attention_paged.  A node that no query sees may hold anything.
+ * dsa_latent_attention_paged.  A node that no query sees may hold anything; one that
+ * some query sees has to be finite, or the others of its sequence may get NaN too.
+ * There are no key weights for dsa_latent_cache_evict: a cache that is evicted by
+ * weight is decoded by dsa_latent_attention_paged.
  * Queries i >= draft_lens[b] are padding: their rows get zeros and lse = -inf.
  * A number of nodes below 0, above next_n or above seq_lens[b] is DSA_ERR_RANGE,
  * and the sequence counts as empty.
@@ -359,7 +362,8 @@ DSA_API int dsa_latent_attention_tree(const uint16_t* q_nope, const uint16_t* q_
  * names nodes in [0, draft_lens[b]); one that does not, or lengths that do not
  * fit, is DSA_ERR_RANGE and leaves the sequence as it is (new_lens[b] =
  * seq_lens[b]).  A node whose page or target page is outside the cache is not
- * moved.  No two sequences may share the pages of their nodes.
+ * moved.  No two sequences may share the pages of their nodes, and none may have
+ * one of them twice.
  *
  *   path [B, max_path] int32   path_lens, draft_lens [B] int32
  *   k_cache, k_cache_scale: the indexer's keys and scales, moved along, or both null
@@ -389,16 +393,18 @@ typedef enum {
  *     y[g] = H y[g] / sqrt(128), H[d, e] = (-1)^popcount(d & e)   (with DSA_ENCODE_HADAMARD)
  *     scale[t] = max over g, d of |y| / 448, or 1 where that is 0;   codes[t, g] = e4m3(y / scale[t])
  *
- * in fp32 with one rounding, to nearest even.  The rope parts pe[t, h] (64 dims)
+ * in fp32, rounded to codes once, to nearest even; y / scale is a product with a
+ * reciprocal, off by some 2^-22 of itself, so that a value as near as that to the
+ * middle between two codes may get either.  The rope parts pe[t, h] (64 dims)
  * turn by the same angles and are rounded to bf16.  A token whose position is
  * negative is padding, and one at or past max_positions is DSA_ERR_RANGE
  * (dsa_latent_last_status): their outputs stay as they were.  x must be finite, and
- * y below 2^120 in magnitude before a Hadamard transform; a token with more, an
- * infinity or NaN has undefined codes and scale, and so has one whose row is
- * constant under a norm with norm_eps = 0.
+ * y below 2^127 in magnitude, below 2^120 before a Hadamard transform; a token with
+ * more, an infinity or NaN has undefined codes and scale, and so has one whose row is
+ * constant under a norm with norm_eps = 0.  (Under a norm x may be of any size.)
  *
  *   x [T, G, 128] bf16, G = 64 or 1, or null        codes [T, G, 128] e4m3   scale [T] fp32
- *   pe [T, H, 64] bf16, or null                     pe_out [T, H, 64] bf16 (may be pe, with its strides)
+ *   pe [T, H, 64] bf16, or null                     pe_out [T, H, 64] bf16 (may be pe, with its strides; no part of x)
  *   norm_weight, norm_bias [128] fp32, or both null
  *   cos_sin [max_positions, 64] fp32: 32 cosines, then 32 sines, of each position's angles
  *   positions [T] int32
@@ -427,7 +433,8 @@ DSA_API int dsa_indexer_encode(const uint16_t* x, int64_t x_token_stride, int64_
  *   c [T, 512], k_pe [T, 64] bf16    index_k [T, 128] bf16 or null, with k_cache and k_cache_scale
  *   c_norm [512] fp32 or null        index_norm_weight, index_norm_bias [128] fp32, or both null
  *   cu_new [B + 1] int32, ascending, within [0, T]; tokens outside every sequence are padding
- *   positions [T] int32 or null      c_out [T, 512], k_pe_out [T, 64] bf16 or null (may be c and k_pe)
+ *   positions [T] int32 or null      c_out [T, 512], k_pe_out [T, 64] bf16 or null (may be c and k_pe, with
+ *   their strides; no part of another input)
  *   strides in elements, as in dsa_indexer_encode, of c_out and k_pe_out at least a row
  *   new_lens [B] int32 (may be seq_lens itself)
  *
