@@ -239,6 +239,32 @@ def test_layer_norm_of_rows_of_any_size(B, G, had, eps):  # noqa: F811
     check_codes(codes, s, y, reach)
 
 
+@pytest.mark.parametrize("ctas", [0, 3])
+@pytest.mark.parametrize("G,H,T", [(64, 4, 300), (1, 1, 5000), (1, 3, 900)])
+def test_a_large_row_changes_no_other(B, G, H, T, ctas):  # noqa: F811
+    """Tokens beside one that is taken again are taken again with it: with the same bits, and rope parts in place are
+    rotated once."""
+    g, table = torch.Generator().manual_seed(34), _table(T).cuda()
+    x, pe, pos = _normal(g, T, G, 128), _normal(g, T, H, 64), torch.arange(T, dtype=torch.int32).cuda()
+    nm = (torch.randn(128, generator=g).cuda(), torch.randn(128, generator=g).cuda(), 1e-6)
+    large = torch.randperm(T, generator=g)[:T // 40]
+    x2 = x.clone()
+    x2[large, -1] = _sized(g, 1e38, len(large), 128)
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[large] = False
+    rest = rest.cuda()
+    B.set_option("grid_ctas", ctas)
+    try:
+        codes, scale, out = B.indexer_encode(x.cuda(), table, pos, norm=nm, hadamard=True, pe=pe.cuda())
+        there = pe.cuda()
+        codes2, scale2, _ = B.indexer_encode(x2.cuda(), table, pos, norm=nm, hadamard=True, pe=there, pe_out=there)
+        assert B.latent_last_status() == 0
+    finally:
+        B.set_option("grid_ctas", 0)
+    assert torch.equal(there, out) and torch.equal(scale[rest], scale2[rest])
+    assert torch.equal(codes.view(torch.uint8)[rest], codes2.view(torch.uint8)[rest])
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-42, 1e-6, 1e20])
 def test_append_norms_of_any_size(B, eps):  # noqa: F811
     g, table, T = torch.Generator().manual_seed(32), _table(), 8 * len(SIZES) + 3
