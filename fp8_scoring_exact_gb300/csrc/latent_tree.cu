@@ -105,13 +105,14 @@ __device__ __forceinline__ int load_pages(const LatentAttnParams& p, const Item&
 //   3. the copy's bytes land in the other CTA and count on its barrier, whose phase ends
 //   4. the lane there that issues the MMA waits for that phase (acquire), then
 //      tcgen05.fence::after_thread_sync, and issues
-// Steps 1, 2 and 4 are the PTX model's own.  That 3 comes after 1 is not: the model
-// does not say that the completion of a bulk copy releases what other lanes wrote
-// before it was issued.  It rests on the copy being issued after writes that have been
-// done, in the SM whose shared memory and TMEM the MMA reads them from, and has been tried with
-// 35000 random trees, 16 runs each, all bits alike.  The other way, from the issuer that
-// has seen both CTAs' values arrive to the odd CTA's warps, which clear some, is the same
-// with the arrival of the values (their copies' completion, acquired) as step 1.
+// Steps 1, 2 and 4 are the PTX model's own.  The one between 2 and 3 is a reading: the
+// model does not spell out whether writes of other lanes, before a bulk copy was
+// issued, are among what its completion releases.  It rests on those writes having
+// been done when the copy is issued, in the SM whose shared memory and TMEM the MMA reads
+// them from; 35000 random trees, 16 runs each, gave the same bits.  The other way, from
+// the issuer that has seen both CTAs' values arrive to the odd CTA's warps, which clear
+// some, is alike, with the arrival of the values (their copies' completion, acquired)
+// as step 1.
 __device__ __forceinline__ void note_cluster(uint32_t dst, uint32_t src, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
                "r"(src), "r"(bar)
